@@ -412,6 +412,158 @@ kdn_status kdn_gain_scan_static(int variant, int B, int T, int H, int dk, int io
                                 const float* r, const float* var0, float* kappa, float* var_T,
                                 void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The operators around the mixer in its layer: layer norm, the short causal
+ * convolution that feeds q, k and v, and a gated recurrence per channel (the
+ * memory recurrence S <- D S + ... without keys).  Conventions as above, with
+ * these differences:
+ *   - io dtype KDN_F32 or KDN_BF16 (no flags); parameters (weight, bias),
+ *     statistics and recurrent states are fp32; all arithmetic is fp32 and a
+ *     value is rounded once, when it is stored.
+ *   - Any channel count D >= 1.  Pointers need only their element's alignment
+ *     (workspaces: 16 bytes); 16-byte alignment and D a multiple of 8 run
+ *     fastest.
+ *   - Inputs marked "rows of D, `stride` apart" may be slices of wider rows
+ *     (one third of a fused projection, say): row i starts at element
+ *     i * stride, stride >= D.  Everything else is dense.
+ *   - No output may overlap any other buffer, unless a call says so.
+ *   - Packed sequences: with `cu_seqlens` (device, int32 [N+1], N >= 1) B must
+ *     be 1, and sequence n is the tokens cu_seqlens[n] .. cu_seqlens[n+1] - 1
+ *     of the row.  Offsets start at 0, never decrease and end at or before T;
+ *     a sequence may be empty.  Tokens from cu_seqlens[N] on belong to no
+ *     sequence: nothing of an output is written there, and they add to no
+ *     gradient.  Without cu_seqlens (NULL, N ignored) each of the B rows is one
+ *     sequence and N below means B.  Offsets are not checked; bad ones give
+ *     unspecified values, but no access outside the tensors.
+ *   - Infinities and NaN of one sequence never reach another one.
+ *   - Deterministic, capturable into a HIP graph; two calls that may run at
+ *     the same time need a workspace each.
+ */
+
+/*
+ * Layer norm over the last axis: rows of D,
+ *   mean = sum(x) / D, rstd = 1 / sqrt(sum((x - mean)^2) / D + eps)
+ *   y = (x - mean) rstd weight + bias
+ *   x      rows of D, x_stride apart, io dtype     y [rows, D] io dtype
+ *   weight, bias [D] fp32, each nullable (ones, zeros)
+ *   mean, rstd   [rows] fp32, written; each nullable
+ *   eps    finite, >= 0
+ * The variance is taken around the mean, in a second pass over the row.
+ */
+kdn_status kdn_layer_norm_fwd(int rows, int D, int io_dtype, float eps, const void* x,
+                              long long x_stride, const float* weight, const float* bias,
+                              void* y, float* mean, float* rstd, void* stream);
+
+/*
+ * Backward of kdn_layer_norm_fwd.  With g = dy weight and xh = (x - mean) rstd:
+ *   dx = rstd (g - mean(g) - xh mean(g xh)),
+ *   dweight = sum over rows of dy xh, dbias = sum over rows of dy
+ *   dy [rows, D] io dtype; x as in the forward; mean, rstd [rows] from it
+ *   dx [rows, D] io dtype; dweight, dbias [D] fp32, each nullable
+ * The workspace (kdn_layer_norm_bwd_workspace_size bytes) holds partial sums
+ * of dweight and dbias; it is not needed when both are NULL.
+ */
+size_t kdn_layer_norm_bwd_workspace_size(int rows, int D);
+kdn_status kdn_layer_norm_bwd(int rows, int D, int io_dtype, const void* dy, const void* x,
+                              long long x_stride, const float* mean, const float* rstd,
+                              const float* weight, void* dx, float* dweight, float* dbias,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Activation of the convolution's output. */
+typedef enum { KDN_ACT_NONE = 0, KDN_ACT_SILU = 1 } kdn_activation;
+
+/*
+ * Short causal convolution, one filter of W taps (2 <= W <= 4) per channel:
+ *   z_t = bias + sum_{j < W} weight[W-1-j] x_{t-j},   y = z, or z sigmoid(z)
+ * where the W - 1 inputs before a sequence's first token are its state0 (oldest
+ * first; zeros when NULL).
+ *   x [B,T,D] rows x_stride apart, y [B,T,D] io dtype
+ *   weight [W,D] fp32 (the last row multiplies the current token),
+ *   bias [D] fp32, nullable
+ *   state0, state_T [N,W-1,D] io dtype, nullable: the last W - 1 inputs before
+ *   the sequence and at its end (with state0 moved up for a sequence that is
+ *   shorter).  They must not overlap.
+ */
+kdn_status kdn_conv_fwd(int B, int T, int D, int W, int io_dtype, int activation, const void* x,
+                        long long x_stride, const float* weight, const float* bias,
+                        const void* state0, const int* cu_seqlens, int N, void* y, void* state_T,
+                        void* stream);
+
+/*
+ * Backward of kdn_conv_fwd (z is formed again from x).  dy [B,T,D] and
+ * dstate_T [N,W-1,D] (nullable: zeros) in the io dtype are the gradients by y
+ * and state_T; dx [B,T,D] (rows of a dense tensor), dstate0 [N,W-1,D] (nullable) io dtype,
+ * dweight [W,D] and dbias [D] (nullable) fp32 are written in full, but for dx
+ * of tokens behind the last sequence.
+ */
+size_t kdn_conv_bwd_workspace_size(int B, int T, int D, int W);
+kdn_status kdn_conv_bwd(int B, int T, int D, int W, int io_dtype, int activation, const void* dy,
+                        const void* x, long long x_stride, const float* weight, const float* bias,
+                        const void* state0, const int* cu_seqlens, int N, const void* dstate_T,
+                        void* dx, float* dweight, float* dbias, void* dstate0, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * One token of kdn_conv_fwd for each of B sequences: x (rows of D, x_stride
+ * apart) and y [B,D]; state [B,W-1,D] is read and moved on in place.
+ */
+kdn_status kdn_conv_step(int B, int D, int W, int io_dtype, int activation, const void* x,
+                         long long x_stride, const float* weight, const float* bias, void* state,
+                         void* y, void* stream);
+
+/* How the recurrence gets its decay: alpha itself, or its pre-activation. */
+typedef enum { KDN_GATE_ALPHA = 0, KDN_GATE_PREACT = 1 } kdn_gate;
+
+/* Tokens between the states that the recurrence's forward keeps for its
+ * backward. */
+enum { KDN_REC_CHECKPOINT = 64 };
+
+/*
+ * Gated recurrence per channel:
+ *   h_t = alpha_t h_{t-1} + u_t,   u_t = x_t, or (1 - alpha_t) x_t with `blend`
+ *   x     [B,T,D] rows x_stride apart, io dtype
+ *   a     [B,T,D] rows a_stride apart: alpha in fp32 (KDN_GATE_ALPHA, 0 <=
+ *         alpha <= 1), or a_pre in the io dtype with alpha = sigmoid(a_pre)
+ *         (KDN_GATE_PREACT; 1 - alpha is then formed without cancellation)
+ *   h0    [N,D] fp32 state before each sequence, nullable (zeros)
+ *   h     [B,T,D] io dtype;  h_T [N,D] fp32, nullable: the state after each
+ *         sequence (h0 for an empty one)
+ *   checkpoints  [B, ceil(T / KDN_REC_CHECKPOINT), D] fp32, nullable: the state
+ *         before every 64th token of the row, for kdn_rec_bwd
+ *   workspace    kdn_rec_fwd_workspace_size bytes (0 for short rows)
+ */
+size_t kdn_rec_fwd_workspace_size(int B, int T, int D);
+kdn_status kdn_rec_fwd(int B, int T, int D, int io_dtype, int gate, int blend, const void* x,
+                       long long x_stride, const void* a, long long a_stride, const float* h0,
+                       const int* cu_seqlens, int N, void* h, float* h_T, float* checkpoints,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Backward of kdn_rec_fwd, for dh [B,T,D] (io dtype) = dL/dh and dh_T [N,D]
+ * (fp32, nullable: zeros) = dL/dh_T.  The states are formed again in fp32 from
+ * the forward's checkpoints.  With lam_t = dh_t + alpha_{t+1} lam_{t+1} (dh_T in
+ * place of the second term at a sequence's end):
+ *   dx = lam, or (1 - alpha) lam with `blend`           [B,T,D] io dtype
+ *   da = lam h_{t-1}, or lam (h_{t-1} - x_t), by alpha  [B,T,D] fp32; times
+ *        alpha (1 - alpha) by a_pre                     [B,T,D] io dtype
+ *   dh0 = alpha_1 lam_1 (dh_T for an empty sequence)    [N,D] fp32, nullable
+ */
+size_t kdn_rec_bwd_workspace_size(int B, int T, int D);
+kdn_status kdn_rec_bwd(int B, int T, int D, int io_dtype, int gate, int blend, const void* dh,
+                       const void* x, long long x_stride, const void* a, long long a_stride,
+                       const float* checkpoints, const float* h0, const int* cu_seqlens, int N,
+                       const float* dh_T, void* dx, void* da, float* dh0, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * One token of kdn_rec_fwd for each of B sequences: x, a (rows of D, x_stride
+ * and a_stride apart), h [B,D]; state [B,D] fp32 is read and overwritten.
+ */
+kdn_status kdn_rec_step(int B, int D, int io_dtype, int gate, int blend, const void* x,
+                        long long x_stride, const void* a, long long a_stride, float* state,
+                        void* h, void* stream);
+
 const char* kdn_status_string(int status);
 const char* kdn_last_error_message(void);
 

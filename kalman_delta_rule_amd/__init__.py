@@ -14,6 +14,14 @@ from .api import (  # noqa: F401
     KDN_OUT_F32,
     KdnError,
     fwd_launcher,
+    kdn_conv_bwd,
+    kdn_conv_fwd,
+    kdn_conv_step,
+    kdn_layer_norm_bwd,
+    kdn_layer_norm_fwd,
+    kdn_rec_bwd,
+    kdn_rec_fwd,
+    kdn_rec_step,
     kdn_diag_fwd,
     kdn_bwd,
     kdn_bwd_preact,
@@ -39,6 +47,14 @@ __all__ = [
     "kdn_bwd",
     "kdn_bwd_preact",
     "kdn_gain_scan",
+    "kdn_layer_norm_fwd",
+    "kdn_layer_norm_bwd",
+    "kdn_conv_fwd",
+    "kdn_conv_bwd",
+    "kdn_conv_step",
+    "kdn_rec_fwd",
+    "kdn_rec_bwd",
+    "kdn_rec_step",
     "kdn_fwd_workspace_size",
     "kdn_version",
     "fwd_launcher",

@@ -16,6 +16,9 @@ KDN_F32, KDN_BF16 = 0, 1
 KDN_DIAG, KDN_ISO = 0, 1
 KDN_MATH_BF16 = 0x100  # OR-ed into io_dtype: single bf16 products in the Diagonal bf16 forward
 KDN_OUT_F32 = 0x200    # OR-ed into io_dtype: fp32 o from bf16 q, k, v (Diagonal, split products)
+KDN_ACT_NONE, KDN_ACT_SILU = 0, 1
+KDN_GATE_ALPHA, KDN_GATE_PREACT = 0, 1
+KDN_REC_CHECKPOINT = 64  # tokens between the states the recurrence's forward keeps
 
 _lib = None
 
@@ -84,6 +87,34 @@ def lib():
     L.kdn_gain_scan_static_max_bytes.argtypes = []
     L.kdn_gain_scan_static.restype = i
     L.kdn_gain_scan_static.argtypes = [i] * 6 + [f] + [vp] + [fp] * 4 + [fp, fp, vp]
+    ll = ctypes.c_longlong
+    L.kdn_layer_norm_fwd.restype = i
+    L.kdn_layer_norm_fwd.argtypes = [i] * 3 + [f, vp, ll] + [fp] * 2 + [vp] + [fp] * 2 + [vp]
+    L.kdn_layer_norm_bwd_workspace_size.restype = sz
+    L.kdn_layer_norm_bwd_workspace_size.argtypes = [i] * 2
+    L.kdn_layer_norm_bwd.restype = i
+    L.kdn_layer_norm_bwd.argtypes = ([i] * 3 + [vp] * 2 + [ll] + [fp] * 3 + [vp] + [fp] * 2
+                                     + [vp, sz, vp])
+    L.kdn_conv_fwd.restype = i
+    L.kdn_conv_fwd.argtypes = [i] * 6 + [vp, ll] + [fp] * 2 + [vp] * 2 + [i] + [vp] * 3
+    L.kdn_conv_bwd_workspace_size.restype = sz
+    L.kdn_conv_bwd_workspace_size.argtypes = [i] * 4
+    L.kdn_conv_bwd.restype = i
+    L.kdn_conv_bwd.argtypes = ([i] * 6 + [vp] * 2 + [ll] + [fp] * 2 + [vp] * 2 + [i] + [vp] * 2
+                               + [fp] * 2 + [vp] * 2 + [sz, vp])
+    L.kdn_conv_step.restype = i
+    L.kdn_conv_step.argtypes = [i] * 5 + [vp, ll] + [fp] * 2 + [vp] * 3
+    for name in ("kdn_rec_fwd_workspace_size", "kdn_rec_bwd_workspace_size"):
+        fn = getattr(L, name)
+        fn.restype = sz
+        fn.argtypes = [i] * 3
+    L.kdn_rec_fwd.restype = i
+    L.kdn_rec_fwd.argtypes = ([i] * 6 + [vp, ll] * 2 + [fp, vp, i, vp] + [fp] * 2 + [vp, sz, vp])
+    L.kdn_rec_bwd.restype = i
+    L.kdn_rec_bwd.argtypes = ([i] * 6 + [vp] + [vp, ll] * 2 + [fp] * 2 + [vp, i, fp] + [vp] * 2
+                              + [fp, vp, sz, vp])
+    L.kdn_rec_step.restype = i
+    L.kdn_rec_step.argtypes = [i] * 5 + [vp, ll] * 2 + [fp, vp, vp]
     L.kdn_status_string.restype = ctypes.c_char_p
     L.kdn_status_string.argtypes = [i]
     L.kdn_last_error_message.restype = ctypes.c_char_p
@@ -99,7 +130,10 @@ EXPORTED = ("kdn_fwd_workspace_size", "kdn_diag_fwd", "kdn_iso_fwd", "kdn_step",
             "kdn_fwd_preact_workspace_size", "kdn_fwd_preact", "kdn_gates_from_preact",
             "kdn_bwd_preact_workspace_size", "kdn_bwd_preact",
             "kdn_gain_workspace_size", "kdn_gain_scan", "kdn_gain_scan_static_max_bytes",
-            "kdn_gain_scan_static", "kdn_status_string",
+            "kdn_gain_scan_static", "kdn_layer_norm_fwd", "kdn_layer_norm_bwd_workspace_size",
+            "kdn_layer_norm_bwd", "kdn_conv_fwd", "kdn_conv_bwd_workspace_size", "kdn_conv_bwd",
+            "kdn_conv_step", "kdn_rec_fwd_workspace_size", "kdn_rec_fwd",
+            "kdn_rec_bwd_workspace_size", "kdn_rec_bwd", "kdn_rec_step", "kdn_status_string",
             "kdn_last_error_message", "kdn_version")
 
 

@@ -507,3 +507,342 @@ def kdn_fwd_workspace_size(variant: str, B, T, H, dk, dv, io_dtype: torch.dtype)
 
 def kdn_version() -> str:
     return _lib.lib().kdn_version().decode()
+
+
+# ---- the operators around the mixer ---------------------------------------
+
+_ACT = {None: 0, "silu": 1}
+_GATE = {"alpha": 0, "preact": 1}
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between the rows of t's last axis: t may be a slice of wider
+    rows, but its channels lie side by side and its rows an equal way apart."""
+    D = t.shape[-1]
+    if t.is_contiguous():
+        return D
+    if D > 1 and t.stride(-1) != 1:
+        raise ValueError("%s must have its channels side by side (stride 1)" % name)
+    step = D
+    rows = 0  # rows collapsed so far, from the innermost axis outwards
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if rows == 0:
+            step, rows = stride, size
+        elif stride == step * rows:
+            rows *= size
+        else:
+            raise ValueError("%s must have its rows evenly spaced" % name)
+    if step < D:
+        raise ValueError("%s has rows that overlap" % name)
+    return step
+
+
+def _need_rows(t, name, shape, dtype, device) -> int:
+    """_need for a tensor that may be a slice of wider rows; the row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    return _row_stride(t, name)
+
+
+def _first(t, name, dims):
+    """Device and io code of a call's first tensor, [.., D] with ``dims`` axes
+    (None: any number)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dim() != dims if dims is not None else t.dim() < 1:
+        raise ValueError("%s must have %s, got shape %s" % (
+            name, "at least one axis" if dims is None else "%d axes" % dims, tuple(t.shape)))
+    if t.device.type != "cuda":
+        raise ValueError("tensors must be on a HIP device")
+    if t.dtype == torch.bfloat16:
+        return t.device, KDN_BF16
+    if t.dtype == torch.float32:
+        return t.device, KDN_F32
+    raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype))
+
+
+def _optional(dev, *tensors):
+    for t, name, shape, dtype in tensors:
+        if t is not None:
+            _need(t, name, shape, dtype, dev)
+
+
+def _given(t, name, shape, dtype, dev):
+    """The caller's output tensor, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(t, name, shape, dtype, dev)
+    return t
+
+
+def _sequences(cu_seqlens, B, dev) -> int:
+    """Number of sequences: the rows, or the packed ones of a single row."""
+    if cu_seqlens is None:
+        return B
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be a tensor [N+1] of offsets, N >= 1")
+    _need(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, dev)
+    if B != 1:
+        raise ValueError("packed sequences (cu_seqlens) need one row, got %d" % B)
+    return cu_seqlens.numel() - 1
+
+
+def _workspace(workspace, need: int, dev):
+    if workspace is not None:
+        if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise TypeError("workspace must be contiguous uint8")
+        if workspace.device != dev:
+            raise ValueError("workspace is on %s, expected %s" % (workspace.device, dev))
+        return workspace, workspace.numel()
+    return (torch.empty(need, dtype=torch.uint8, device=dev), need) if need else (None, 0)
+
+
+def kdn_layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, y=None,
+                       want_stats: bool = False):
+    """Layer norm over the last axis of x [..., D] (a slice of wider rows is
+    fine).  Returns (y, mean, rstd): y in x's dtype, and with ``want_stats``
+    the fp32 statistics [...] that kdn_layer_norm_bwd reads (None, None
+    otherwise).  weight, bias: [D] fp32, each optional."""
+    L = _lib.lib()
+    dev, io = _first(x, "x", None)
+    D = x.shape[-1]
+    stride = _row_stride(x, "x")
+    f32 = torch.float32
+    _optional(dev, (weight, "weight", (D,), f32), (bias, "bias", (D,), f32))
+    y = _given(y, "y", x.shape, x.dtype, dev)
+    mean = rstd = None
+    if want_stats:
+        mean = torch.empty(x.shape[:-1], dtype=f32, device=dev)
+        rstd = torch.empty(x.shape[:-1], dtype=f32, device=dev)
+    with torch.cuda.device(dev):
+        st = L.kdn_layer_norm_fwd(x.numel() // D if D else 0, D, io, float(eps), x.data_ptr(),
+                                  stride, _ptr(weight), _ptr(bias), y.data_ptr(), _ptr(mean),
+                                  _ptr(rstd), _stream(dev))
+    _lib.check(st)
+    return y, mean, rstd
+
+
+def kdn_layer_norm_bwd(dy, x, mean, rstd, weight=None, want_param_grads: bool = True, dx=None,
+                       workspace=None) -> dict:
+    """Backward of kdn_layer_norm_fwd with its mean and rstd.  Returns a dict
+    with dx (x's dtype) and, with ``want_param_grads``, dweight and dbias [D]
+    (fp32, summed over every row)."""
+    L = _lib.lib()
+    dev, io = _first(x, "x", None)
+    D = x.shape[-1]
+    stride = _row_stride(x, "x")
+    f32 = torch.float32
+    _need(dy, "dy", x.shape, x.dtype, dev)
+    _need(mean, "mean", x.shape[:-1], f32, dev)
+    _need(rstd, "rstd", x.shape[:-1], f32, dev)
+    _optional(dev, (weight, "weight", (D,), f32))
+    rows = x.numel() // D if D else 0
+    g = {"dx": _given(dx, "dx", x.shape, x.dtype, dev)}
+    ws, ws_bytes = None, 0
+    if want_param_grads:
+        g["dweight"] = torch.empty(D, dtype=f32, device=dev)
+        g["dbias"] = torch.empty(D, dtype=f32, device=dev)
+        ws, ws_bytes = _workspace(workspace, L.kdn_layer_norm_bwd_workspace_size(rows, D), dev)
+    with torch.cuda.device(dev):
+        st = L.kdn_layer_norm_bwd(rows, D, io, dy.data_ptr(), x.data_ptr(), stride,
+                                  mean.data_ptr(), rstd.data_ptr(), _ptr(weight),
+                                  g["dx"].data_ptr(), _ptr(g.get("dweight")),
+                                  _ptr(g.get("dbias")), _ptr(ws), ws_bytes, _stream(dev))
+    _lib.check(st)
+    return g
+
+
+def _activation(activation) -> int:
+    if activation not in _ACT:
+        raise ValueError("activation must be None or 'silu', got %r" % (activation,))
+    return _ACT[activation]
+
+
+def _taps(weight, D) -> int:
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a tensor [W, D]")
+    return weight.shape[0]
+
+
+def kdn_conv_fwd(x, weight, bias=None, state0=None, cu_seqlens=None, activation=None,
+                 want_state: bool = False, y=None, state_T=None):
+    """Short causal convolution per channel over x [B,T,D] (a slice of wider
+    rows is fine) with weight [W,D] (its last row multiplies the current
+    token; W from 2 to 4) and bias [D], fp32; ``activation`` None or "silu".
+    state0 [N,W-1,D] (x's dtype) holds the inputs before each sequence, zeros
+    without; cu_seqlens (int32 [N+1]) packs N sequences into one row.  Returns
+    (y, state_T): state_T [N,W-1,D], the last inputs of each sequence, if
+    given or with ``want_state`` (None otherwise)."""
+    L = _lib.lib()
+    dev, io = _first(x, "x", 3)
+    B, T, D = x.shape
+    stride = _row_stride(x, "x")
+    W = _taps(weight, D)
+    N = _sequences(cu_seqlens, B, dev)
+    f32 = torch.float32
+    _need(weight, "weight", (W, D), f32, dev)
+    _optional(dev, (bias, "bias", (D,), f32), (state0, "state0", (N, W - 1, D), x.dtype))
+    act = _activation(activation)
+    y = _given(y, "y", x.shape, x.dtype, dev)
+    if want_state or state_T is not None:
+        state_T = _given(state_T, "state_T", (N, max(W - 1, 0), D), x.dtype, dev)
+    with torch.cuda.device(dev):
+        st = L.kdn_conv_fwd(B, T, D, W, io, act, x.data_ptr(), stride, weight.data_ptr(),
+                            _ptr(bias), _ptr(state0), _ptr(cu_seqlens), N, y.data_ptr(),
+                            _ptr(state_T), _stream(dev))
+    _lib.check(st)
+    return y, state_T
+
+
+def kdn_conv_bwd(dy, x, weight, bias=None, state0=None, cu_seqlens=None, activation=None,
+                 dstate_T=None, dx=None, workspace=None) -> dict:
+    """Backward of kdn_conv_fwd given by the same arguments, for dL/dy = dy and
+    dL/dstate_T = dstate_T (optional).  Returns a dict with dx (x's dtype),
+    dweight [W,D] (fp32), dbias [D] (fp32) where bias is given and dstate0
+    (x's dtype) where state0 is given."""
+    L = _lib.lib()
+    dev, io = _first(x, "x", 3)
+    B, T, D = x.shape
+    stride = _row_stride(x, "x")
+    W = _taps(weight, D)
+    N = _sequences(cu_seqlens, B, dev)
+    f32 = torch.float32
+    _need(dy, "dy", x.shape, x.dtype, dev)
+    _need(weight, "weight", (W, D), f32, dev)
+    _optional(dev, (bias, "bias", (D,), f32), (state0, "state0", (N, W - 1, D), x.dtype),
+              (dstate_T, "dstate_T", (N, W - 1, D), x.dtype))
+    act = _activation(activation)
+    g = {"dx": _given(dx, "dx", x.shape, x.dtype, dev),
+         "dweight": torch.empty((W, D), dtype=f32, device=dev)}
+    if bias is not None:
+        g["dbias"] = torch.empty(D, dtype=f32, device=dev)
+    if state0 is not None:
+        g["dstate0"] = torch.empty_like(state0)
+    ws, ws_bytes = _workspace(workspace, L.kdn_conv_bwd_workspace_size(B, T, D, W), dev)
+    with torch.cuda.device(dev):
+        st = L.kdn_conv_bwd(B, T, D, W, io, act, dy.data_ptr(), x.data_ptr(), stride,
+                            weight.data_ptr(), _ptr(bias), _ptr(state0), _ptr(cu_seqlens), N,
+                            _ptr(dstate_T), g["dx"].data_ptr(), g["dweight"].data_ptr(),
+                            _ptr(g.get("dbias")), _ptr(g.get("dstate0")), _ptr(ws), ws_bytes,
+                            _stream(dev))
+    _lib.check(st)
+    return g
+
+
+def kdn_conv_step(x, weight, state, bias=None, activation=None, y=None) -> torch.Tensor:
+    """One token of kdn_conv_fwd: x [B,D]; state [B,W-1,D] (x's dtype) is moved
+    on in place.  Returns y [B,D]."""
+    L = _lib.lib()
+    dev, io = _first(x, "x", 2)
+    B, D = x.shape
+    stride = _row_stride(x, "x")
+    W = _taps(weight, D)
+    _need(weight, "weight", (W, D), torch.float32, dev)
+    _need(state, "state", (B, W - 1, D), x.dtype, dev)
+    if bias is not None:
+        _need(bias, "bias", (D,), torch.float32, dev)
+    y = _given(y, "y", (B, D), x.dtype, dev)
+    with torch.cuda.device(dev):
+        st = L.kdn_conv_step(B, D, W, io, _activation(activation), x.data_ptr(), stride,
+                             weight.data_ptr(), _ptr(bias), state.data_ptr(), y.data_ptr(),
+                             _stream(dev))
+    _lib.check(st)
+    return y
+
+
+def _gate(gate, io_dtype):
+    """The gate's code and the dtype of its tensor."""
+    if gate not in _GATE:
+        raise ValueError("gate must be 'alpha' or 'preact', got %r" % (gate,))
+    return _GATE[gate], io_dtype if gate == "preact" else torch.float32
+
+
+def kdn_rec_fwd(x, a, h0=None, cu_seqlens=None, gate: str = "preact", blend: bool = False,
+                want_checkpoints: bool = False, h=None, h_T=None, workspace=None):
+    """Gated recurrence per channel, h_t = alpha_t h_{t-1} + x_t (with
+    ``blend``: (1 - alpha_t) x_t), over x [B,T,D].  ``a`` [B,T,D] holds
+    pre-activations in x's dtype, alpha = sigmoid(a) (gate="preact"), or alpha
+    itself in fp32 (gate="alpha"); x and a may be slices of wider rows.  h0
+    [N,D] fp32 is the state before each sequence (zeros without); cu_seqlens
+    (int32 [N+1]) packs N sequences into one row.  Returns (h, h_T,
+    checkpoints): h in x's dtype, h_T [N,D] fp32 and, with
+    ``want_checkpoints``, the states that kdn_rec_bwd starts from (None
+    otherwise)."""
+    L = _lib.lib()
+    dev, io = _first(x, "x", 3)
+    B, T, D = x.shape
+    stride = _row_stride(x, "x")
+    code, adt = _gate(gate, x.dtype)
+    a_stride = _need_rows(a, "a", x.shape, adt, dev)
+    N = _sequences(cu_seqlens, B, dev)
+    f32 = torch.float32
+    _optional(dev, (h0, "h0", (N, D), f32))
+    h = _given(h, "h", x.shape, x.dtype, dev)
+    h_T = _given(h_T, "h_T", (N, D), f32, dev)
+    chk = None
+    if want_checkpoints:
+        chk = torch.empty((B, -(-T // _lib.KDN_REC_CHECKPOINT), D), dtype=f32, device=dev)
+    ws, ws_bytes = _workspace(workspace, L.kdn_rec_fwd_workspace_size(B, T, D), dev)
+    with torch.cuda.device(dev):
+        st = L.kdn_rec_fwd(B, T, D, io, code, int(bool(blend)), x.data_ptr(), stride, a.data_ptr(),
+                           a_stride, _ptr(h0), _ptr(cu_seqlens), N, h.data_ptr(), h_T.data_ptr(),
+                           _ptr(chk), _ptr(ws), ws_bytes, _stream(dev))
+    _lib.check(st)
+    return h, h_T, chk
+
+
+def kdn_rec_bwd(dh, x, a, checkpoints, h0=None, dh_T=None, cu_seqlens=None, gate: str = "preact",
+                blend: bool = False, dx=None, workspace=None) -> dict:
+    """Backward of kdn_rec_fwd given by the same arguments and its checkpoints,
+    for dL/dh = dh and dL/dh_T = dh_T (optional).  Returns a dict with dx (x's
+    dtype), da (a's dtype: the gradient by alpha or by its pre-activation)
+    and dh0 [N,D] fp32."""
+    L = _lib.lib()
+    dev, io = _first(x, "x", 3)
+    B, T, D = x.shape
+    stride = _row_stride(x, "x")
+    code, adt = _gate(gate, x.dtype)
+    a_stride = _need_rows(a, "a", x.shape, adt, dev)
+    N = _sequences(cu_seqlens, B, dev)
+    f32 = torch.float32
+    _need(dh, "dh", x.shape, x.dtype, dev)
+    _need(checkpoints, "checkpoints", (B, -(-T // _lib.KDN_REC_CHECKPOINT), D), f32, dev)
+    _optional(dev, (h0, "h0", (N, D), f32), (dh_T, "dh_T", (N, D), f32))
+    g = {"dx": _given(dx, "dx", x.shape, x.dtype, dev),
+         "da": torch.empty(x.shape, dtype=adt, device=dev),
+         "dh0": torch.empty((N, D), dtype=f32, device=dev)}
+    ws, ws_bytes = _workspace(workspace, L.kdn_rec_bwd_workspace_size(B, T, D), dev)
+    with torch.cuda.device(dev):
+        st = L.kdn_rec_bwd(B, T, D, io, code, int(bool(blend)), dh.data_ptr(), x.data_ptr(),
+                           stride, a.data_ptr(), a_stride, checkpoints.data_ptr(), _ptr(h0),
+                           _ptr(cu_seqlens), N, _ptr(dh_T), g["dx"].data_ptr(),
+                           g["da"].data_ptr(), g["dh0"].data_ptr(), _ptr(ws), ws_bytes,
+                           _stream(dev))
+    _lib.check(st)
+    return g
+
+
+def kdn_rec_step(x, a, state, gate: str = "preact", blend: bool = False, h=None) -> torch.Tensor:
+    """One token of kdn_rec_fwd: x, a [B,D]; state [B,D] fp32 is updated in
+    place.  Returns h [B,D]."""
+    L = _lib.lib()
+    dev, io = _first(x, "x", 2)
+    B, D = x.shape
+    stride = _row_stride(x, "x")
+    code, adt = _gate(gate, x.dtype)
+    a_stride = _need_rows(a, "a", x.shape, adt, dev)
+    _need(state, "state", (B, D), torch.float32, dev)
+    h = _given(h, "h", (B, D), x.dtype, dev)
+    with torch.cuda.device(dev):
+        st = L.kdn_rec_step(B, D, io, code, int(bool(blend)), x.data_ptr(), stride, a.data_ptr(),
+                            a_stride, state.data_ptr(), h.data_ptr(), _stream(dev))
+    _lib.check(st)
+    return h

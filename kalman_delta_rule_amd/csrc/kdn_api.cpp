@@ -13,9 +13,9 @@
 #include "kdn_internal.h"
 #include "kdn_ops.h"
 
-namespace {
+namespace kdn {
 
-thread_local char g_msg[512] = "";
+static thread_local char g_msg[512] = "";
 
 kdn_status fail(kdn_status st, const char* fmt, ...)
 {
@@ -31,6 +31,13 @@ kdn_status ok()
     g_msg[0] = '\0';
     return KDN_OK;
 }
+
+}  // namespace kdn
+
+namespace {
+
+using kdn::fail;
+using kdn::ok;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -942,7 +949,7 @@ const char* kdn_status_string(int status)
     }
 }
 
-const char* kdn_last_error_message(void) { return g_msg; }
+const char* kdn_last_error_message(void) { return kdn::g_msg; }
 
 const char* kdn_version(void) { return "kdn-mi355x 0.1.0 gfx950"; }
 
