@@ -421,12 +421,12 @@ kdn_status kdn_gain_scan_static(int variant, int B, int T, int H, int dk, int io
  *   - io dtype KDN_F32 or KDN_BF16 (no flags); parameters (weight, bias),
  *     statistics and recurrent states are fp32; all arithmetic is fp32 and a
  *     value is rounded once, when it is stored.
- *   - Any channel count D >= 1.  Pointers need only their element's alignment
+ *   - Any channel count D from 1 to 2^20.  Pointers need only their element's alignment
  *     (workspaces: 16 bytes); 16-byte alignment and D a multiple of 8 run
  *     fastest.
  *   - Inputs marked "rows of D, `stride` apart" may be slices of wider rows
  *     (one third of a fused projection, say): row i starts at element
- *     i * stride, stride >= D.  Everything else is dense.
+ *     i * stride, D <= stride <= 2^22.  Everything else is dense.
  *   - No output may overlap any other buffer, unless a call says so.
  *   - Packed sequences: with `cu_seqlens` (device, int32 [N+1], N >= 1) B must
  *     be 1, and sequence n is the tokens cu_seqlens[n] .. cu_seqlens[n+1] - 1

@@ -16,7 +16,7 @@ using kdn::fail;
 using kdn::ok;
 
 constexpr long long kMaxElems = 1ll << 31;  // of every dense tensor
-constexpr long long kMaxSpan = 1ll << 46;   // elements a strided input may span
+constexpr long long kMaxStride = 1ll << 22;  // kernels step over a tile of rows with 32-bit byte offsets
 constexpr int kMaxD = 1 << 20;
 
 // One buffer of a call: its bytes (0: not given) and what the call does to it.
@@ -75,8 +75,8 @@ kdn_status check_rows(long long rows, int D, long long stride, const char* name,
 {
     if (stride < D)
         return fail(KDN_ERR_INVALID_ARG, "%s_stride must be at least D = %d, got %lld", name, D, stride);
-    if (rows > 1 && stride > kMaxSpan / rows)
-        return fail(KDN_ERR_UNSUPPORTED, "%s spans more than 2^46 elements", name);
+    if (stride > kMaxStride)
+        return fail(KDN_ERR_UNSUPPORTED, "%s_stride is at most 2^22, got %lld", name, stride);
     span = rows ? (rows - 1) * stride + D : 0;
     return KDN_OK;
 }

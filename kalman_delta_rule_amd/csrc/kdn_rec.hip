@@ -1,5 +1,29 @@
 // kdn_rec.hip -- gated recurrence per channel, forward, backward and
 // single-token step, gfx950.
+//
+//   h_t = alpha_t h_{t-1} + u_t         u = x, or (1 - alpha) x ("blend")
+//   lam_t = dh_t + g_{t+1},  g_t = alpha_t lam_t  (g behind a sequence: dh_T)
+//   dx = lam (1 - alpha if blend),  dalpha = lam (h_{t-1} - x if blend)
+//
+// Both recurrences are affine in what they carry: over any span of tokens
+// carry -> A carry + U with A the product of the decays.  So a workgroup takes a
+// tile of 128 tokens and 64 channels, each half-wave of it a run of tokens (two
+// channels a lane): the run's (A, U) first, from registers; then one wave joins
+// the runs in order, gets what the tile starts from, and hands every run its own
+// start; then the runs are walked again, from the same registers, with their
+// outputs stored.  Inputs are read once and outputs written once.
+//
+// Tiles of the same channels are chained through the workspace (tile_carry):
+// each publishes its (A, U), and the last of 16 the value behind it.  A tile's
+// start is that value of the group before, with the (A, U) of the tiles between
+// applied in token order: always the same operations, so results do not depend
+// on timing.  A word is 4 or 8 bytes, stored and loaded whole (relaxed, agent
+// scope: it may cross to another XCD's L2), and is its own flag: a launch before
+// sets them to all ones, which no published word is (a NaN is made canonical).
+//
+// Where a sequence starts (forward) or ends (backward) inside a span, A is 0, and
+// a span with A = 0 gives U whatever it is handed: nothing, infinities and
+// NaN included, passes from one sequence to another.
 #include "kdn.h"
 #include "kdn_block_device.h"
 
@@ -8,148 +32,700 @@ namespace kdn {
 namespace {
 
 constexpr int kChk = KDN_REC_CHECKPOINT;
+constexpr int kTile = 128;   // tokens of a tile
+constexpr int kGroup = 16;   // tiles of a group of the chain
+constexpr int kPolls = 1 << 21;
 
-// alpha and 1 - alpha of a gate value; from a pre-activation both without
-// cancellation: with e = exp(-a), 1 / (1 + e) and e / (1 + e)
-__device__ __forceinline__ void gate_of(float a, bool preact, float& alpha, float& rest)
+// ---- the chain through the workspace ----------------------------------------
+
+struct Chain {
+    uint32_t* ticket;
+    unsigned long long* spans;  // [tiles][columns]: (A, U) of a tile
+    uint32_t* starts;           // [groups][columns]: the value behind a group
+    int tiles, columns;
+};
+
+__host__ __device__ inline Chain chain_at(void* ws, int tiles, int columns)
 {
-    if (!preact) {
+    Chain c;
+    c.tiles = tiles;
+    c.columns = columns;
+    c.ticket = static_cast<uint32_t*>(ws);
+    c.spans = reinterpret_cast<unsigned long long*>(static_cast<char*>(ws) + 16);
+    c.starts = reinterpret_cast<uint32_t*>(c.spans + (size_t)tiles * columns);
+    return c;
+}
+
+// bytes behind the ticket
+inline size_t chain_words(int tiles, int columns)
+{
+    const size_t groups = (tiles + kGroup - 1) / kGroup;
+    return ((size_t)tiles * columns * 2 + groups * columns + 3) / 4 * 4;
+}
+
+__global__ __launch_bounds__(256) void rec_clear_kernel(uint4* ws, size_t n)
+{
+    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < n)
+        ws[i] = i ? uint4{~0u, ~0u, ~0u, ~0u} : uint4{0, 0, 0, 0};
+}
+
+__device__ __forceinline__ uint32_t word_of(float v)
+{
+    return v != v ? 0x7FC00000u : __float_as_uint(v);
+}
+
+__device__ __forceinline__ void publish(uint32_t* p, float v)
+{
+    __hip_atomic_store(p, word_of(v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ void publish(unsigned long long* p, float A, float U)
+{
+    __hip_atomic_store(p, (unsigned long long)word_of(U) << 32 | word_of(A), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+}
+
+template <typename Word>
+__device__ __forceinline__ Word peek(const Word* p)
+{
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Wait for a word.  Tiles are handed out by ticket in the order of their
+// dependences, so the tile that publishes it has its workgroup running already
+// and waits for earlier ones only: the wait ends.  Were the workspace shared
+// with another call against the rules, the bound on the polls ends it, with NaN.
+template <typename Word>
+__device__ __forceinline__ Word await(const Word* p, Word v)
+{
+    for (int k = 0; v == ~Word(0) && k < kPolls; ++k) {
+        __builtin_amdgcn_s_sleep(1);
+        v = peek(p);
+    }
+    return v;
+}
+
+__device__ __forceinline__ float apply(float A, float U, float carry)
+{
+    return A == 0.f ? U : fmaf(A, carry, U);
+}
+
+// What tile `k` in chain order starts from, for the column `col` of this lane,
+// whose own span is (A, U); publishes what later tiles need.
+__device__ __forceinline__ float tile_carry(const Chain& ch, int k, int col, float A, float U)
+{
+    const int g = k / kGroup, j = k - g * kGroup;
+    const bool last = j == kGroup - 1;
+    unsigned long long* spans = ch.spans + (size_t)g * kGroup * ch.columns + col;
+    if (!last && k + 1 < ch.tiles)
+        publish(spans + (size_t)j * ch.columns, A, U);
+    unsigned long long w[kGroup - 1];
+#pragma unroll
+    for (int i = 0; i < kGroup - 1; ++i)
+        w[i] = i < j ? peek(spans + (size_t)i * ch.columns) : 0;
+    float carry = 0.f;
+    if (g) {
+        const uint32_t* p = ch.starts + (size_t)(g - 1) * ch.columns + col;
+        carry = __uint_as_float(await(p, peek(p)));
+    }
+#pragma unroll
+    for (int i = 0; i < kGroup - 1; ++i) {
+        if (i < j) {
+            const unsigned long long v = await(spans + (size_t)i * ch.columns, w[i]);
+            carry = apply(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)), carry);
+        }
+    }
+    if (last && k + 1 < ch.tiles)
+        publish(ch.starts + (size_t)g * ch.columns + col, apply(A, U, carry));
+    return carry;
+}
+
+// ---- values ------------------------------------------------------------------
+
+// V adjacent values as they are in memory (any alignment of their elements)
+template <typename E, int V>
+struct __attribute__((packed, aligned(sizeof(E)))) Pack {
+    E v[V];
+};
+
+template <typename E, int V>
+__device__ __forceinline__ Pack<E, V> load_at(const char* base, uint32_t off)
+{
+    return *reinterpret_cast<const Pack<E, V>*>(base + off);
+}
+
+template <typename E, int V>
+__device__ __forceinline__ void store_at(char* base, uint32_t off, const float (&v)[V])
+{
+    Pack<E, V> p;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        p.v[i] = from_f32<E>(v[i]);
+    *reinterpret_cast<Pack<E, V>*>(base + off) = p;
+}
+
+// alpha and 1 - alpha.  From a pre-activation the smaller of the two is formed
+// as e / (1 + e), e = exp(-|a|) <= 1, with full relative accuracy, the larger
+// as one minus it, off by half a step: with alpha near one its error is
+// carried through hundreds of products.
+template <bool PRE>
+__device__ __forceinline__ void gate_of(float a, float& alpha, float& rest)
+{
+    if constexpr (PRE) {
+        const float e = __builtin_amdgcn_exp2f(fabsf(a) * -kLog2e);
+        const float s = e * rcp(1.f + e), l = 1.f - s;
+        alpha = a >= 0.f ? l : a < 0.f ? s : a;
+        rest = a >= 0.f ? s : a < 0.f ? l : a;
+    } else {
         alpha = a;
         rest = 1.f - a;
-        return;
     }
-    alpha = gate_sigmoid(a);
-    rest = gate_sigmoid(-a);
 }
 
-__device__ __forceinline__ float load_gate(const void* a, size_t i, bool preact, bool bf)
-{
-    return preact && bf ? to_f32(static_cast<const bf16*>(a)[i]) : static_cast<const float*>(a)[i];
-}
+// Marks of a tile's tokens: the sequence that starts or ends at each, or -1.
+struct Marks {
+    int start[kTile], end[kTile];
+};
 
-// one lane walks one channel of one row
-template <typename IO>
-__global__ __launch_bounds__(64) void rec_fwd_kernel(RecArgs a)
+// Fills them (all threads of the workgroup); the offsets may be anything.
+template <int THREADS>
+__device__ __forceinline__ void mark_tile(Marks& m, const RecArgs& a, int b, int t0)
 {
-    constexpr bool bf = sizeof(IO) == 2;
-    const int c = blockIdx.y * 64 + threadIdx.x, b = blockIdx.x;
-    if (c >= a.D)
-        return;
-    for (int n = a.cu ? 0 : b; n < (a.cu ? a.N : b + 1); ++n) {
-        const int p = a.cu ? a.cu[n] : 0, q = a.cu ? a.cu[n + 1] : a.T;
-        if (p < 0 || q > a.T)
-            continue;
-        float h = a.h0 ? a.h0[(size_t)n * a.D + c] : 0.f;
-        for (int t = p; t < q; ++t) {
-            const size_t r = (size_t)b * a.T + t;
-            if (a.ckpt && t % kChk == 0)
-                a.ckpt[((size_t)b * ((a.T + kChk - 1) / kChk) + t / kChk) * a.D + c] = h;
-            float alpha, rest;
-            gate_of(load_gate(a.a, r * a.as + c, a.preact, bf), a.preact, alpha, rest);
-            const float x = to_f32(static_cast<const IO*>(a.x)[r * a.xs + c]);
-            h = fmaf(alpha, h, a.blend ? rest * x : x);
-            static_cast<IO*>(a.h)[r * a.D + c] = from_f32<IO>(h);
+    for (int i = threadIdx.x; i < kTile; i += THREADS)
+        m.start[i] = m.end[i] = -1;
+    __syncthreads();
+    if (a.cu) {
+        for (int n = threadIdx.x; n < a.N; n += THREADS) {
+            const int p = a.cu[n], q = a.cu[n + 1];
+            if (p < q && p >= t0 && p - t0 < kTile)
+                m.start[p - t0] = n;
+            if (p < q && q > t0 && q - 1 - t0 < kTile)
+                m.end[q - 1 - t0] = n;
         }
-        if (a.h_T)
-            a.h_T[(size_t)n * a.D + c] = h;
+    } else if (threadIdx.x == 0 && a.T) {
+        if (t0 == 0)
+            m.start[0] = b;
+        if (a.T - 1 - t0 < kTile)
+            m.end[a.T - 1 - t0] = b;
     }
+    __syncthreads();
 }
 
-template <typename IO>
-__global__ __launch_bounds__(64) void rec_bwd_kernel(RecArgs a)
+// bits of a half-wave's L tokens whose mark is set
+template <int L>
+__device__ __forceinline__ uint32_t marked(const int* marks)
 {
-    constexpr bool bf = sizeof(IO) == 2;
-    __shared__ float prev[kChk][64];  // the state before each token of a block
-    const int c = blockIdx.y * 64 + threadIdx.x, b = blockIdx.x;
-    if (c >= a.D)
-        return;
-    const int blocks = (a.T + kChk - 1) / kChk;
-    for (int n = a.cu ? a.N - 1 : b; n >= (a.cu ? 0 : b); --n) {
-        const int p = a.cu ? a.cu[n] : 0, q = a.cu ? a.cu[n + 1] : a.T;
-        if (p < 0 || q > a.T)
-            continue;
-        const float h0 = a.h0 ? a.h0[(size_t)n * a.D + c] : 0.f;
-        float g = a.dh_T ? a.dh_T[(size_t)n * a.D + c] : 0.f;  // alpha lam of the next token
-        int end = q;
-        while (end > p) {
-            const int blk = (end - 1) / kChk, begin = max(p, blk * kChk);
-            float h = begin == p ? h0 : a.ckpt[((size_t)b * blocks + blk) * a.D + c];
-            for (int t = begin; t < end; ++t) {
-                const size_t r = (size_t)b * a.T + t;
-                float alpha, rest;
-                gate_of(load_gate(a.a, r * a.as + c, a.preact, bf), a.preact, alpha, rest);
-                const float x = to_f32(static_cast<const IO*>(a.x)[r * a.xs + c]);
-                prev[t - begin][threadIdx.x] = h;
-                h = fmaf(alpha, h, a.blend ? rest * x : x);
-            }
-            for (int t = end - 1; t >= begin; --t) {
-                const size_t r = (size_t)b * a.T + t;
-                float alpha, rest;
-                gate_of(load_gate(a.a, r * a.as + c, a.preact, bf), a.preact, alpha, rest);
-                const float x = to_f32(static_cast<const IO*>(a.x)[r * a.xs + c]);
-                const float lam = to_f32(static_cast<const IO*>(a.dh)[r * a.D + c]) + g;
-                const float hp = prev[t - begin][threadIdx.x];
-                const float da = lam * (a.blend ? hp - x : hp);
-                static_cast<IO*>(a.dx)[r * a.D + c] = from_f32<IO>(a.blend ? lam * rest : lam);
-                if (a.preact)
-                    static_cast<IO*>(a.da)[r * a.D + c] = from_f32<IO>(da * alpha * rest);
-                else
-                    static_cast<float*>(a.da)[r * a.D + c] = da;
-                g = alpha * lam;
-            }
-            end = begin;
+    const int l = threadIdx.x & 31;
+    const unsigned long long w = __ballot(l < L && marks[l < L ? l : 0] >= 0);
+    return (uint32_t)((threadIdx.x & 32) ? w >> 32 : w);
+}
+
+// tokens of the row that belong to a sequence
+__device__ __forceinline__ int token_limit(const RecArgs& a)
+{
+    return a.cu ? min(max(a.cu[a.N], 0), a.T) : a.T;
+}
+
+struct Tile {
+    int k;   // in chain order
+    int b, t0, c0;  // row, first token, first channel
+    int col;        // first column of the chain
+};
+
+// The tile of this workgroup: by ticket where tiles are chained.
+template <int CT>
+__device__ __forceinline__ Tile take_tile(const RecArgs& a, const Chain& ch, int ctiles, bool backward)
+{
+    __shared__ uint32_t s_ticket;
+    uint32_t id = blockIdx.x;
+    if (ch.tiles > 1) {
+        if (threadIdx.x == 0)
+            s_ticket = __hip_atomic_fetch_add(ch.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        id = s_ticket;
+    }
+    const int per = a.B * ctiles;  // all tiles of a time come before the next time's
+    Tile t;
+    t.k = id / per;
+    const int r = id - t.k * per;
+    t.b = r / ctiles;
+    t.c0 = (r - t.b * ctiles) * CT;
+    t.col = r * CT;
+    t.t0 = (backward ? ch.tiles - 1 - t.k : t.k) * kTile;
+    return t;
+}
+
+// ---- forward -------------------------------------------------------------------
+
+// 256 threads: eight half-waves of 16 tokens.
+template <typename IO, bool PRE, bool BLEND, int V>
+__global__ __launch_bounds__(256, 4) void rec_fwd_kernel(RecArgs a, Chain ch, int ctiles)
+{
+    typedef typename std::conditional<PRE, IO, float>::type GT;
+    constexpr int L = 16, RUNS = 8, CT = 32 * V;
+    __shared__ Marks marks;
+    __shared__ float2 spans[RUNS][CT];
+    __shared__ float starts[RUNS][CT];
+
+    const Tile tile = take_tile<CT>(a, ch, ctiles, false);
+    const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
+    // lanes behind the last channel repeat the last ones
+    const int c = min(tile.c0 + lane * V, a.D - V);
+    const int first = run * L;  // of the run, in the tile
+    const size_t row0 = (size_t)tile.b * a.T + tile.t0;
+
+    Pack<GT, V> ra[L];
+    Pack<IO, V> rx[L];
+    if (a.T) {
+        // rows behind the last one repeat it
+        const char* pa = static_cast<const char*>(a.a) + row0 * a.as * sizeof(GT);
+        const char* px = static_cast<const char*>(a.x) + row0 * a.xs * sizeof(IO);
+        const uint32_t sa = (uint32_t)a.as * sizeof(GT), sx = (uint32_t)a.xs * sizeof(IO);
+        const uint32_t last = min(a.T - 1 - tile.t0, kTile - 1);
+        const uint32_t ea = last * sa + c * sizeof(GT), ex = last * sx + c * sizeof(IO);
+        uint32_t oa = min(first * sa + c * (uint32_t)sizeof(GT), ea);
+        uint32_t ox = min(first * sx + c * (uint32_t)sizeof(IO), ex);
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            ra[i] = load_at<GT, V>(pa, oa);
+            rx[i] = load_at<IO, V>(px, ox);
+            oa = min(oa + sa, ea);
+            ox = min(ox + sx, ex);
         }
-        if (a.dh0)
-            a.dh0[(size_t)n * a.D + c] = g;
+    }
+
+    mark_tile<256>(marks, a, tile.b, tile.t0);
+    const int valid = token_limit(a) - (tile.t0 + first);  // tokens of the run, if positive
+    const uint32_t start = marked<L>(marks.start + first), end = marked<L>(marks.end + first);
+    const bool plain = __all(valid >= L && !start && !end);
+
+    float al[L][V], u[L][V];
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float rest;
+            gate_of<PRE>(to_f32(ra[i].v[v]), al[i][v], rest);
+            const float x = to_f32(rx[i].v[v]);
+            u[i][v] = BLEND ? rest * x : x;
+        }
+
+    float A[V], U[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        A[v] = 1.f, U[v] = 0.f;
+    if (plain) {
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                U[v] = fmaf(al[i][v], U[v], u[i][v]);
+                A[v] *= al[i][v];
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            if (i >= valid)
+                continue;
+            const bool s = start >> i & 1;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (s) {
+                    A[v] = 0.f;
+                    U[v] = a.h0 ? a.h0[(size_t)marks.start[first + i] * a.D + c + v] : 0.f;
+                }
+                U[v] = fmaf(al[i][v], U[v], u[i][v]);
+                A[v] *= al[i][v];
+            }
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        spans[run][lane * V + v] = float2{A[v], U[v]};
+    __syncthreads();
+
+    if (threadIdx.x < CT) {
+        const int s = threadIdx.x;
+        float2 g[RUNS];
+        float TA = 1.f, TU = 0.f;
+#pragma unroll
+        for (int r = 0; r < RUNS; ++r) {
+            g[r] = spans[r][s];
+            TU = apply(g[r].x, g[r].y, TU);
+            TA = g[r].x == 0.f ? 0.f : TA * g[r].x;
+        }
+        float carry = ch.tiles > 1 ? tile_carry(ch, tile.k, tile.col + s, TA, TU) : 0.f;
+#pragma unroll
+        for (int r = 0; r < RUNS; ++r) {
+            starts[r][s] = carry;
+            carry = apply(g[r].x, g[r].y, carry);
+        }
+    }
+    __syncthreads();
+
+    float h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        h[v] = starts[run][lane * V + v];
+    if (a.ckpt && first % kChk == 0 && valid > 0) {
+        const int blocks = (a.T + kChk - 1) / kChk;
+        float* p = a.ckpt + ((size_t)tile.b * blocks + (tile.t0 + first) / kChk) * a.D + c;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            p[v] = !(start & 1) ? h[v] : a.h0 ? a.h0[(size_t)marks.start[first] * a.D + c + v] : 0.f;
+    }
+    char* ph = static_cast<char*>(a.h) + row0 * a.D * sizeof(IO);
+    const uint32_t sh = (uint32_t)a.D * sizeof(IO);
+    uint32_t oh = first * sh + c * (uint32_t)sizeof(IO);
+    if (plain) {
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                h[v] = fmaf(al[i][v], h[v], u[i][v]);
+            store_at<IO, V>(ph, oh, h);
+            oh += sh;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            if (i >= valid)
+                continue;
+            const bool s = start >> i & 1, e = end >> i & 1;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (s)
+                    h[v] = a.h0 ? a.h0[(size_t)marks.start[first + i] * a.D + c + v] : 0.f;
+                h[v] = fmaf(al[i][v], h[v], u[i][v]);
+                if (e && a.h_T)
+                    a.h_T[(size_t)marks.end[first + i] * a.D + c + v] = h[v];
+            }
+            store_at<IO, V>(ph, oh, h);
+            oh += sh;
+        }
+    }
+
+    // empty sequences keep their state
+    if (tile.k == 0 && a.h_T) {
+        for (int n = a.cu ? run : tile.b; n < (a.cu ? a.N : tile.b + 1); n += RUNS) {
+            if (a.cu ? a.cu[n] < a.cu[n + 1] : a.T > 0 || run > 0)
+                continue;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                a.h_T[(size_t)n * a.D + c + v] = a.h0 ? a.h0[(size_t)n * a.D + c + v] : 0.f;
+        }
     }
 }
 
-template <typename IO>
+// ---- backward ------------------------------------------------------------------
+
+// 512 threads: sixteen half-waves of 8 tokens (the inputs, the decays and the
+// states of 16 tokens would not fit the registers of two workgroups a CU).  The
+// states before the runs come from the forward's checkpoints, so only the
+// adjoint is chained, in reverse.
+template <typename IO, bool PRE, bool BLEND, int V>
+__global__ __launch_bounds__(512, 4) void rec_bwd_kernel(RecArgs a, Chain ch, int ctiles)
+{
+    typedef typename std::conditional<PRE, IO, float>::type GT;
+    constexpr int L = 8, RUNS = 16, CT = 32 * V, PER = kChk / L;  // runs of a checkpoint
+    __shared__ Marks marks;
+    __shared__ float2 spans[RUNS][CT], rspans[RUNS][CT];
+    __shared__ float starts[RUNS][CT], rstarts[RUNS][CT];
+
+    const Tile tile = take_tile<CT>(a, ch, ctiles, true);
+    const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
+    const int c = min(tile.c0 + lane * V, a.D - V);
+    const int first = run * L;
+    const size_t row0 = (size_t)tile.b * a.T + tile.t0;
+
+    Pack<GT, V> ra[L];
+    Pack<IO, V> rx[L], rd[L];
+    if (a.T) {
+        const char* pa = static_cast<const char*>(a.a) + row0 * a.as * sizeof(GT);
+        const char* px = static_cast<const char*>(a.x) + row0 * a.xs * sizeof(IO);
+        const char* pd = static_cast<const char*>(a.dh) + row0 * a.D * sizeof(IO);
+        const uint32_t sa = (uint32_t)a.as * sizeof(GT), sx = (uint32_t)a.xs * sizeof(IO),
+                       sd = (uint32_t)a.D * sizeof(IO);
+        const uint32_t last = min(a.T - 1 - tile.t0, kTile - 1);
+        const uint32_t ea = last * sa + c * sizeof(GT), ex = last * sx + c * sizeof(IO),
+                       ed = last * sd + c * sizeof(IO);
+        uint32_t oa = min(first * sa + c * (uint32_t)sizeof(GT), ea);
+        uint32_t ox = min(first * sx + c * (uint32_t)sizeof(IO), ex);
+        uint32_t od = min(first * sd + c * (uint32_t)sizeof(IO), ed);
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            ra[i] = load_at<GT, V>(pa, oa);
+            rx[i] = load_at<IO, V>(px, ox);
+            rd[i] = load_at<IO, V>(pd, od);
+            oa = min(oa + sa, ea);
+            ox = min(ox + sx, ex);
+            od = min(od + sd, ed);
+        }
+    }
+
+    mark_tile<512>(marks, a, tile.b, tile.t0);
+    const int valid = token_limit(a) - (tile.t0 + first);
+    const uint32_t start = marked<L>(marks.start + first), end = marked<L>(marks.end + first);
+    const bool plain = __all(valid >= L && !start && !end);
+
+    float al[L][V], rest[L][V];
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            gate_of<PRE>(to_f32(ra[i].v[v]), al[i][v], rest[i][v]);
+
+    float A[V], U[V], RA[V], RU[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        A[v] = RA[v] = 1.f, U[v] = RU[v] = 0.f;
+    if (plain) {
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float x = to_f32(rx[i].v[v]);
+                U[v] = fmaf(al[i][v], U[v], BLEND ? rest[i][v] * x : x);
+                A[v] *= al[i][v];
+            }
+#pragma unroll
+        for (int i = L - 1; i >= 0; --i)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                RU[v] = al[i][v] * (to_f32(rd[i].v[v]) + RU[v]);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            RA[v] = A[v];
+    } else {
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            if (i >= valid)
+                continue;
+            const bool s = start >> i & 1;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (s) {
+                    A[v] = 0.f;
+                    U[v] = a.h0 ? a.h0[(size_t)marks.start[first + i] * a.D + c + v] : 0.f;
+                }
+                const float x = to_f32(rx[i].v[v]);
+                U[v] = fmaf(al[i][v], U[v], BLEND ? rest[i][v] * x : x);
+                A[v] *= al[i][v];
+            }
+        }
+#pragma unroll
+        for (int i = L - 1; i >= 0; --i) {
+            if (i >= valid)
+                continue;
+            const bool e = end >> i & 1;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (e) {
+                    RA[v] = 0.f;
+                    RU[v] = a.dh_T ? a.dh_T[(size_t)marks.end[first + i] * a.D + c + v] : 0.f;
+                }
+                RU[v] = al[i][v] * (to_f32(rd[i].v[v]) + RU[v]);
+                RA[v] *= al[i][v];
+            }
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        spans[run][lane * V + v] = float2{A[v], U[v]};
+        rspans[run][lane * V + v] = float2{RA[v], RU[v]};
+    }
+    __syncthreads();
+
+    const int wave = threadIdx.x >> 6, s = threadIdx.x & 63;
+    if (wave == 0 && s < CT) {
+        float TA = 1.f, TU = 0.f;
+#pragma unroll
+        for (int r = RUNS - 1; r >= 0; --r) {
+            const float2 g = rspans[r][s];
+            TU = apply(g.x, g.y, TU);
+            TA = g.x == 0.f ? 0.f : TA * g.x;
+        }
+        float carry = ch.tiles > 1 ? tile_carry(ch, tile.k, tile.col + s, TA, TU) : 0.f;
+#pragma unroll
+        for (int r = RUNS - 1; r >= 0; --r) {
+            const float2 g = rspans[r][s];
+            rstarts[r][s] = carry;
+            carry = apply(g.x, g.y, carry);
+        }
+    } else if ((wave == 1 || wave == 2) && s < CT) {
+        // the states before the runs of checkpoint `wave` - 1 of the tile
+        const int blocks = (a.T + kChk - 1) / kChk, blk = tile.t0 / kChk + wave - 1;
+        const int cs = min(tile.c0 + s / V * V, a.D - V) + s % V;
+        float h = blk < blocks ? a.ckpt[((size_t)tile.b * blocks + blk) * a.D + cs] : 0.f;
+#pragma unroll
+        for (int r = 0; r < PER; ++r) {
+            const float2 g = spans[(wave - 1) * PER + r][s];
+            starts[(wave - 1) * PER + r][s] = h;
+            h = apply(g.x, g.y, h);
+        }
+    }
+    __syncthreads();
+
+    float h[V], prev[L][V], g[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        h[v] = starts[run][lane * V + v];
+        g[v] = rstarts[run][lane * V + v];
+    }
+    char* px = static_cast<char*>(a.dx) + row0 * a.D * sizeof(IO);
+    char* pa = static_cast<char*>(a.da) + row0 * a.D * sizeof(GT);
+    const uint32_t sx = (uint32_t)a.D * sizeof(IO), sa = (uint32_t)a.D * sizeof(GT);
+    const uint32_t ox = c * (uint32_t)sizeof(IO), oa = c * (uint32_t)sizeof(GT);
+    // the outputs of token i, from its adjoint
+    auto token = [&](int i) {
+        float dx[V], da[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float lam = to_f32(rd[i].v[v]) + g[v];
+            const float part = BLEND ? prev[i][v] - to_f32(rx[i].v[v]) : prev[i][v];
+            dx[v] = BLEND ? lam * rest[i][v] : lam;
+            da[v] = lam * part;
+            if constexpr (PRE)
+                da[v] *= al[i][v] * rest[i][v];
+            g[v] = al[i][v] * lam;
+        }
+        store_at<IO, V>(px, (first + i) * sx + ox, dx);
+        store_at<GT, V>(pa, (first + i) * sa + oa, da);
+    };
+    if (plain) {
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                prev[i][v] = h[v];
+                const float x = to_f32(rx[i].v[v]);
+                h[v] = fmaf(al[i][v], h[v], BLEND ? rest[i][v] * x : x);
+            }
+#pragma unroll
+        for (int i = L - 1; i >= 0; --i)
+            token(i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (start >> i & 1)
+                    h[v] = a.h0 ? a.h0[(size_t)marks.start[first + i] * a.D + c + v] : 0.f;
+                prev[i][v] = h[v];
+                const float x = to_f32(rx[i].v[v]);
+                h[v] = fmaf(al[i][v], h[v], BLEND ? rest[i][v] * x : x);
+            }
+#pragma unroll
+        for (int i = L - 1; i >= 0; --i) {
+            if (i >= valid)
+                continue;
+            if (end >> i & 1) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    g[v] = a.dh_T ? a.dh_T[(size_t)marks.end[first + i] * a.D + c + v] : 0.f;
+            }
+            token(i);
+            if ((start >> i & 1) && a.dh0) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    a.dh0[(size_t)marks.start[first + i] * a.D + c + v] = g[v];
+            }
+        }
+    }
+
+    if (tile.k == 0 && a.dh0) {
+        for (int n = a.cu ? run : tile.b; n < (a.cu ? a.N : tile.b + 1); n += RUNS) {
+            if (a.cu ? a.cu[n] < a.cu[n + 1] : a.T > 0 || run > 0)
+                continue;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                a.dh0[(size_t)n * a.D + c + v] = a.dh_T ? a.dh_T[(size_t)n * a.D + c + v] : 0.f;
+        }
+    }
+}
+
+// ---- one token ---------------------------------------------------------------------
+
+template <typename IO, bool PRE>
 __global__ __launch_bounds__(256) void rec_step_kernel(RecArgs a)
 {
-    constexpr bool bf = sizeof(IO) == 2;
+    typedef typename std::conditional<PRE, IO, float>::type GT;
     const int c = blockIdx.y * 256 + threadIdx.x, b = blockIdx.x;
     if (c >= a.D)
         return;
     float alpha, rest;
-    gate_of(load_gate(a.a, (size_t)b * a.as + c, a.preact, bf), a.preact, alpha, rest);
+    gate_of<PRE>(to_f32(static_cast<const GT*>(a.a)[(size_t)b * a.as + c]), alpha, rest);
     const float x = to_f32(static_cast<const IO*>(a.x)[(size_t)b * a.xs + c]);
     const float h = fmaf(alpha, a.h_T[(size_t)b * a.D + c], a.blend ? rest * x : x);
     a.h_T[(size_t)b * a.D + c] = h;
     static_cast<IO*>(a.h)[(size_t)b * a.D + c] = from_f32<IO>(h);
 }
 
+int tiles_of(int T) { return T > kTile ? (T + kTile - 1) / kTile : 1; }
+
+template <typename IO, bool PRE, bool BLEND, int V>
+hipError_t launch(const RecArgs& a, bool backward, hipStream_t stream)
+{
+    const int ctiles = (a.D + 32 * V - 1) / (32 * V), tiles = tiles_of(a.T);
+    const int columns = a.B * ctiles * 32 * V;
+    const Chain ch = chain_at(a.ws, tiles, columns);
+    if (tiles > 1) {
+        const size_t n = 1 + chain_words(tiles, columns) / 4;
+        rec_clear_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(static_cast<uint4*>(a.ws), n);
+    }
+    const unsigned grid = (unsigned)((size_t)tiles * a.B * ctiles);
+    if (backward)
+        rec_bwd_kernel<IO, PRE, BLEND, V><<<grid, 512, 0, stream>>>(a, ch, ctiles);
+    else
+        rec_fwd_kernel<IO, PRE, BLEND, V><<<grid, 256, 0, stream>>>(a, ch, ctiles);
+    return hipGetLastError();
+}
+
+template <typename IO>
+hipError_t launch_io(const RecArgs& a, bool backward, hipStream_t stream)
+{
+    // one channel alone is half a lane's pair
+    if (a.D == 1)
+        return a.preact ? (a.blend ? launch<IO, true, true, 1>(a, backward, stream)
+                                   : launch<IO, true, false, 1>(a, backward, stream))
+                        : (a.blend ? launch<IO, false, true, 1>(a, backward, stream)
+                                   : launch<IO, false, false, 1>(a, backward, stream));
+    return a.preact ? (a.blend ? launch<IO, true, true, 2>(a, backward, stream)
+                               : launch<IO, true, false, 2>(a, backward, stream))
+                    : (a.blend ? launch<IO, false, true, 2>(a, backward, stream)
+                               : launch<IO, false, false, 2>(a, backward, stream));
+}
+
 }  // namespace
 
-size_t rec_workspace_bytes(int B, int T, int D) { return 0; }
+size_t rec_workspace_bytes(int B, int T, int D)
+{
+    const int tiles = tiles_of(T), ct = D == 1 ? 32 : 64;
+    if (tiles == 1)
+        return 0;
+    return 16 + chain_words(tiles, B * ((D + ct - 1) / ct) * ct) * 4;
+}
 
 hipError_t launch_rec_fwd(const RecArgs& a, bool bf, hipStream_t stream)
 {
-    const dim3 grid(a.B, (a.D + 63) / 64);
-    if (bf)
-        rec_fwd_kernel<bf16><<<grid, 64, 0, stream>>>(a);
-    else
-        rec_fwd_kernel<float><<<grid, 64, 0, stream>>>(a);
-    return hipGetLastError();
+    return bf ? launch_io<bf16>(a, false, stream) : launch_io<float>(a, false, stream);
 }
 
 hipError_t launch_rec_bwd(const RecArgs& a, bool bf, hipStream_t stream)
 {
-    const dim3 grid(a.B, (a.D + 63) / 64);
-    if (bf)
-        rec_bwd_kernel<bf16><<<grid, 64, 0, stream>>>(a);
-    else
-        rec_bwd_kernel<float><<<grid, 64, 0, stream>>>(a);
-    return hipGetLastError();
+    return bf ? launch_io<bf16>(a, true, stream) : launch_io<float>(a, true, stream);
 }
 
 hipError_t launch_rec_step(const RecArgs& a, bool bf, hipStream_t stream)
 {
     const dim3 grid(a.B, (a.D + 255) / 256);
     if (bf)
-        rec_step_kernel<bf16><<<grid, 256, 0, stream>>>(a);
+        a.preact ? rec_step_kernel<bf16, true><<<grid, 256, 0, stream>>>(a)
+                 : rec_step_kernel<bf16, false><<<grid, 256, 0, stream>>>(a);
     else
-        rec_step_kernel<float><<<grid, 256, 0, stream>>>(a);
+        a.preact ? rec_step_kernel<float, true><<<grid, 256, 0, stream>>>(a)
+                 : rec_step_kernel<float, false><<<grid, 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 

@@ -77,7 +77,7 @@ static void norm_checks()
     BAD(WITH(Norm, c.eps = std::nanf("")).fwd(), KDN_ERR_INVALID_ARG, "eps");
     BAD(WITH(Norm, c.xs = 63).fwd(), KDN_ERR_INVALID_ARG, "x_stride");
     BAD(WITH(Norm, c.xs = -64).fwd(), KDN_ERR_INVALID_ARG, "x_stride");
-    BAD(WITH(Norm, c.xs = LLONG_MAX).fwd(), KDN_ERR_UNSUPPORTED, "2^46");
+    BAD(WITH(Norm, c.xs = LLONG_MAX).fwd(), KDN_ERR_UNSUPPORTED, "2^22");
     BAD(WITH(Norm, c.x = 0).fwd(), KDN_ERR_INVALID_ARG, "x must not be NULL");
     BAD(WITH(Norm, c.y = 0).fwd(), KDN_ERR_INVALID_ARG, "y must not be NULL");
     BAD(WITH(Norm, c.mean = 0).bwd(), KDN_ERR_INVALID_ARG, "mean must not be NULL");
