@@ -1,150 +1,542 @@
 // kdn_conv.hip -- short causal convolution per channel, forward, backward and
 // single-token step, gfx950.
+//
+//   z_t = b + sum_k w_k x_{t-(W-1)+k},  y = z or z sigmoid(z)
+//   g_t = dy_t act'(z_t),  dx_t = sum_k w_k g_{t+(W-1)-k},
+//   dw_k = sum_t g_t x_{t-(W-1)+k},  db = sum_t g_t
+//
+// Bound by HBM.  The rows [B,T] are taken as one row of B T tokens with a
+// sequence starting at every T-th (or where the offsets of packed sequences
+// say).  A thread walks a run of consecutive tokens for VE adjacent channels
+// with the last W - 1 inputs in registers, so that each input is read once (the
+// W - 1 tokens before a run again, from L2); the next rows' loads are issued
+// before the present ones are used.  The backward walks forward too: it keeps
+// the partial dx of the last W - 1 tokens and stores a token's when its last
+// term is added, W - 1 tokens past the run's end.
+//
+// A run without a sequence's border in reach goes the plain way, the others
+// look for a mark at every token: at a sequence's start the last inputs come
+// from its state, at its end they go there.
 #include "kdn_block_device.h"
 
 namespace kdn {
 
 namespace {
 
-// x of the token j before token t of row b, whose sequence is s: from the
-// sequence's state where that is before its first token
-template <typename IO>
-__device__ __forceinline__ float tap(const ConvArgs& a, Span s, int b, int t, int j, int c)
+constexpr int kBatch = 8;     // rows loaded together; a run is a multiple of it
+constexpr int kBatchBwd = 4;  // of two inputs each; at least the W - 1 behind a run
+constexpr int kMostTokens = 32 * 32;  // of a workgroup's tile
+
+// VE adjacent values as they are in memory, at any alignment of an element
+template <typename E, int VE>
+struct __attribute__((packed, aligned(sizeof(E)))) Vec {
+    E v[VE];
+};
+
+template <typename E, int VE>
+__device__ __forceinline__ Vec<E, VE> load_vec(const E* p)
 {
-    if (t - j >= s.p)
-        return to_f32(static_cast<const IO*>(a.x)[((size_t)b * a.T + t - j) * a.xs + c]);
-    const int i = a.W - 1 + t - j - s.p;  // row of the state
-    return a.state0 ? to_f32(static_cast<const IO*>(a.state0)[((size_t)s.n * (a.W - 1) + i) * a.D + c])
-                    : 0.f;
+    return *reinterpret_cast<const Vec<E, VE>*>(p);
 }
 
-template <typename IO>
-__device__ __forceinline__ float conv_z(const ConvArgs& a, Span s, int b, int t, int c)
+template <typename E, int VE>
+__device__ __forceinline__ void store_vec(E* p, const float (&y)[VE])
 {
-    float z = a.bias ? a.bias[c] : 0.f;
-    for (int j = 0; j < a.W; ++j)
-        z = fmaf(a.weight[(size_t)(a.W - 1 - j) * a.D + c], tap<IO>(a, s, b, t, j, c), z);
-    return z;
+    Vec<E, VE> o;
+#pragma unroll
+    for (int j = 0; j < VE; ++j)
+        o.v[j] = from_f32<E>(y[j]);
+    *reinterpret_cast<Vec<E, VE>*>(p) = o;
 }
 
-template <typename IO>
-__global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a)
+template <typename E, int VE>
+__device__ __forceinline__ void widen(const Vec<E, VE>& r, float (&x)[VE])
 {
-    const int c = blockIdx.y * 256 + threadIdx.x;
-    const int b = blockIdx.x / a.T, t = blockIdx.x - b * a.T;
-    if (c >= a.D)
-        return;
-    const Span s = span_of(a.cu, a.N, b, t, a.T);
-    if (s.n < 0)
-        return;
-    const float z = conv_z<IO>(a, s, b, t, c);
-    static_cast<IO*>(a.y)[((size_t)b * a.T + t) * a.D + c] =
-        from_f32<IO>(a.silu ? z * gate_sigmoid(z) : z);
+#pragma unroll
+    for (int j = 0; j < VE; ++j)
+        x[j] = to_f32(r.v[j]);
 }
 
-// Row i of a sequence's state after its last token is the token W-1-i before
-// its end.
-template <typename IO>
-__global__ __launch_bounds__(256) void conv_state_kernel(ConvArgs a)
+// fp32 values [VE] at p, or zeros
+template <typename E, int VE>
+__device__ __forceinline__ void load_or_zero(const E* p, bool given, float (&x)[VE])
 {
-    const int c = blockIdx.y * 256 + threadIdx.x;
-    const int n = blockIdx.x / (a.W - 1), i = blockIdx.x - n * (a.W - 1);
-    if (c >= a.D)
-        return;
-    Span s{n, a.cu ? a.cu[n] : 0, a.cu ? a.cu[n + 1] : a.T};
-    if (s.p < 0 || s.q > a.T || s.q < s.p)
-        return;
-    static_cast<IO*>(a.state_T)[(size_t)blockIdx.x * a.D + c] =
-        from_f32<IO>(tap<IO>(a, s, a.cu ? 0 : n, s.q, a.W - 1 - i, c));
-}
-
-// g_t = dy_t act'(z_t)
-template <typename IO>
-__device__ __forceinline__ float conv_g(const ConvArgs& a, Span s, int b, int t, int c)
-{
-    const float dy = to_f32(static_cast<const IO*>(a.dy)[((size_t)b * a.T + t) * a.D + c]);
-    if (!a.silu)
-        return dy;
-    const float z = conv_z<IO>(a, s, b, t, c), p = gate_sigmoid(z);
-    return dy * (p * (1.f + z * (1.f - p)));
-}
-
-// gradient by the input at place t of the sequence (t < s.p: its state)
-template <typename IO>
-__device__ __forceinline__ float conv_dx(const ConvArgs& a, Span s, int b, int t, int c)
-{
-    float d = 0.f;
-    for (int j = 0; j < a.W; ++j)
-        if (t + j >= s.p && t + j < s.q)
-            d = fmaf(a.weight[(size_t)(a.W - 1 - j) * a.D + c], conv_g<IO>(a, s, b, t + j, c), d);
-    const int i = t - (s.q - (a.W - 1));
-    if (i >= 0 && a.dstate_T)
-        d += to_f32(static_cast<const IO*>(a.dstate_T)[((size_t)s.n * (a.W - 1) + i) * a.D + c]);
-    return d;
-}
-
-template <typename IO>
-__global__ __launch_bounds__(256) void conv_bwd_dx_kernel(ConvArgs a)
-{
-    const int c = blockIdx.y * 256 + threadIdx.x;
-    const int b = blockIdx.x / a.T, t = blockIdx.x - b * a.T;
-    if (c >= a.D)
-        return;
-    const Span s = span_of(a.cu, a.N, b, t, a.T);
-    if (s.n >= 0)
-        static_cast<IO*>(a.dx)[((size_t)b * a.T + t) * a.D + c] =
-            from_f32<IO>(conv_dx<IO>(a, s, b, t, c));
-}
-
-template <typename IO>
-__global__ __launch_bounds__(256) void conv_bwd_state_kernel(ConvArgs a)
-{
-    const int c = blockIdx.y * 256 + threadIdx.x;
-    const int n = blockIdx.x / (a.W - 1), i = blockIdx.x - n * (a.W - 1);
-    if (c >= a.D)
-        return;
-    Span s{n, a.cu ? a.cu[n] : 0, a.cu ? a.cu[n + 1] : a.T};
-    if (s.p < 0 || s.q > a.T || s.q < s.p)
-        return;
-    static_cast<IO*>(a.dstate0)[(size_t)blockIdx.x * a.D + c] =
-        from_f32<IO>(conv_dx<IO>(a, s, a.cu ? 0 : n, s.p - (a.W - 1) + i, c));
-}
-
-template <typename IO>
-__global__ __launch_bounds__(256) void conv_bwd_param_kernel(ConvArgs a)
-{
-    const int c = blockIdx.y * 256 + threadIdx.x;
-    if (c >= a.D)
-        return;
-    float dw[4] = {0.f, 0.f, 0.f, 0.f}, db = 0.f;
-    for (int r = blockIdx.x; r < a.B * a.T; r += gridDim.x) {
-        const int b = r / a.T, t = r - b * a.T;
-        const Span s = span_of(a.cu, a.N, b, t, a.T);
-        if (s.n < 0)
-            continue;
-        const float g = conv_g<IO>(a, s, b, t, c);
-        db += g;
-        for (int j = 0; j < a.W; ++j)
-            dw[a.W - 1 - j] += g * tap<IO>(a, s, b, t, j, c);
+    if (given) {
+        widen<E, VE>(load_vec<E, VE>(p), x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VE; ++j)
+            x[j] = 0.f;
     }
-    for (int j = 0; j < a.W; ++j)
-        a.ws[((size_t)blockIdx.x * (a.W + 1) + j) * a.D + c] = dw[j];
-    a.ws[((size_t)blockIdx.x * (a.W + 1) + a.W) * a.D + c] = db;
 }
 
-__global__ __launch_bounds__(256) void conv_bwd_sum_kernel(ConvArgs a, int groups)
+// Which tokens and channels a workgroup works on.
+struct Plan {
+    int lanes_log2;  // threads side by side on a row: 8 to 64
+    int ctiles;      // tiles of channels
+    int batches;     // of kBatch tokens in a run
+    int tiles;       // tiles of tokens
+};
+
+template <int VE>
+struct Place {
+    int lane, run, runs, length;  // length: tokens of a run
+    int c;                        // first channel
+    long long m0, m;              // first token of the tile, of the run
+
+    __device__ __forceinline__ Place(const Plan& p, int D)
+    {
+        const int tt = blockIdx.x / p.ctiles, ct = blockIdx.x - tt * p.ctiles;
+        lane = threadIdx.x & ((1 << p.lanes_log2) - 1);
+        run = threadIdx.x >> p.lanes_log2;
+        runs = 256 >> p.lanes_log2;
+        length = p.batches * kBatch;
+        // lanes behind the last channel repeat the last ones
+        c = min(((ct << p.lanes_log2) + lane) * VE, D - VE);
+        m0 = (long long)tt * runs * length;
+        m = m0 + (long long)run * length;
+    }
+};
+
+// The sequences that start and end at the tokens m0 - before .. m0 + count - 1
+// (-1 where none does); tokens outside all sequences have neither.
+struct Marks {
+    int start[kMostTokens + 8], end[kMostTokens + 8];
+};
+
+__device__ __forceinline__ void mark_tokens(Marks& k, const ConvArgs& a, long long first, int count)
 {
-    const int c = blockIdx.y * 256 + threadIdx.x, j = blockIdx.x;
-    if (c >= a.D)
-        return;
-    float s = 0.f;
-    for (int g = 0; g < groups; ++g)
-        s += a.ws[((size_t)g * (a.W + 1) + j) * a.D + c];
-    if (j < a.W)
-        a.dweight[(size_t)j * a.D + c] = s;
-    else if (a.dbias)
-        a.dbias[c] = s;
+    const long long M = (long long)a.B * a.T;
+    if (a.cu) {
+        for (int i = threadIdx.x; i < count; i += 256)
+            k.start[i] = k.end[i] = -1;
+        __syncthreads();
+        for (int n = threadIdx.x; n < a.N; n += 256) {
+            const int p = a.cu[n], q = a.cu[n + 1];
+            if (p < q && p >= first && p < first + count)
+                k.start[p - first] = n;
+            if (p < q && q - 1 >= first && q - 1 < first + count)
+                k.end[q - 1 - first] = n;
+        }
+    } else {
+        for (int i = threadIdx.x; i < count; i += 256) {
+            const long long m = first + i;
+            const bool in = m >= 0 && m < M;
+            const uint32_t n = in ? (uint32_t)m / (uint32_t)a.T : 0;  // M < 2^31
+            const int t = in ? (int)((uint32_t)m - n * (uint32_t)a.T) : -1;
+            k.start[i] = t == 0 ? (int)n : -1;
+            k.end[i] = t == a.T - 1 ? (int)n : -1;
+        }
+    }
+    __syncthreads();
 }
+
+// tokens from this one on belong to no sequence
+__device__ __forceinline__ long long token_limit(const ConvArgs& a)
+{
+    return a.cu ? min(max(a.cu[a.N], 0), a.T) : (long long)a.B * a.T;
+}
+
+// whether any of marks [i, i + count) is set, for this thread's run (`lanes`
+// threads side by side look)
+__device__ __forceinline__ bool any_mark(const Marks& k, int i, int count, int lane, int lanes)
+{
+    bool any = false;
+    for (int j = lane; j < count; j += lanes)
+        any |= k.start[i + j] >= 0 || k.end[i + j] >= 0;
+    return any;
+}
+
+// d act(z) / dz and act(z)
+__device__ __forceinline__ float silu(float z) { return z * gate_sigmoid(z); }
+__device__ __forceinline__ float silu_slope(float z)
+{
+    const float p = gate_sigmoid(z);
+    return p * fmaf(z, 1.f - p, 1.f);
+}
+
+// The filter and the last inputs of VE channels.
+template <typename IO, int VE, int W>
+struct Filter {
+    float w[W][VE], b[VE], win[W - 1][VE];
+
+    __device__ __forceinline__ void init(const ConvArgs& a, int c)
+    {
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+            load_or_zero<float, VE>(a.weight + (size_t)k * a.D + c, true, w[k]);
+        load_or_zero<float, VE>(a.bias + c, a.bias, b);
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+            for (int j = 0; j < VE; ++j)
+                win[k][j] = 0.f;
+    }
+
+    __device__ __forceinline__ void from_state(const ConvArgs& a, int n, int c)
+    {
+        const IO* s = static_cast<const IO*>(a.state0) + (size_t)n * (W - 1) * a.D + c;
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+            load_or_zero<IO, VE>(s + (size_t)k * a.D, a.state0, win[k]);
+    }
+
+    __device__ __forceinline__ void z(const float (&x)[VE], float (&out)[VE]) const
+    {
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+            out[j] = b[j];
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k)
+                out[j] = fmaf(w[k][j], win[k][j], out[j]);
+            out[j] = fmaf(w[W - 1][j], x[j], out[j]);
+        }
+    }
+
+    __device__ __forceinline__ void push(const float (&x)[VE])
+    {
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+#pragma unroll
+            for (int k = 0; k + 1 < W - 1; ++k)
+                win[k][j] = win[k + 1][j];
+            win[W - 2][j] = x[j];
+        }
+    }
+};
+
+// Rows of VE channels from token m on, one after another; tokens outside
+// [0, M) repeat the nearest.
+template <typename IO, int VE>
+struct Rows {
+    const IO* p;
+    long long m, M, step;
+
+    __device__ __forceinline__ Rows(const void* base, long long stride, long long first,
+                                    long long total, int c)
+        : m(first), M(total), step(stride)
+    {
+        const long long at = min(max(first, 0ll), total - 1);
+        p = static_cast<const IO*>(base) + at * stride + c;
+    }
+    __device__ __forceinline__ Vec<IO, VE> next()
+    {
+        const Vec<IO, VE> r = load_vec<IO, VE>(p);
+        p += m >= 0 && m + 1 < M ? step : 0;
+        ++m;
+        return r;
+    }
+};
+
+// ---- forward ------------------------------------------------------------------
+
+template <typename IO, int VE, int W>
+__global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, Plan plan)
+{
+    __shared__ Marks marks;
+    const Place<VE> at(plan, a.D);
+    const long long M = (long long)a.B * a.T;
+    Filter<IO, VE, W> f;
+    f.init(a, at.c);
+
+    if (M) {
+        Rows<IO, VE> rows(a.x, a.xs, at.m - (W - 1), M, at.c);
+        Vec<IO, VE> before[W - 1], next[kBatch];
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+            before[k] = rows.next();
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            next[i] = rows.next();
+        mark_tokens(marks, a, at.m0 - (W - 1), at.runs * at.length + W - 1);
+        const int base = at.run * at.length;  // mark of the first token before the run
+        const long long limit = token_limit(a);
+        const bool plain = !__any(at.m + at.length > limit ||
+                                  any_mark(marks, base, at.length + W - 1, at.lane, 1 << plan.lanes_log2));
+        IO* y = static_cast<IO*>(a.y) + at.m * a.D + at.c;
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) {
+            float x[VE];
+            widen<IO, VE>(before[k], x);
+            if (!plain && marks.start[base + k] >= 0)
+                f.from_state(a, marks.start[base + k], at.c);
+            f.push(x);
+        }
+        for (int q = 0; q < plan.batches; ++q) {
+            Vec<IO, VE> now[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                now[i] = next[i];
+            if (q + 1 < plan.batches) {
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+                    next[i] = rows.next();
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int k = base + W - 1 + q * kBatch + i;  // mark of this token
+                float x[VE], z[VE];
+                widen<IO, VE>(now[i], x);
+                if (!plain) {
+                    if (at.m + q * kBatch + i >= limit)
+                        continue;
+                    if (marks.start[k] >= 0)
+                        f.from_state(a, marks.start[k], at.c);
+                }
+                f.z(x, z);
+                if (a.silu) {
+#pragma unroll
+                    for (int j = 0; j < VE; ++j)
+                        z[j] = silu(z[j]);
+                }
+                store_vec<IO, VE>(y + (size_t)(q * kBatch + i) * a.D, z);
+                f.push(x);
+                if (!plain && marks.end[k] >= 0 && a.state_T) {
+                    IO* s = static_cast<IO*>(a.state_T) + (size_t)marks.end[k] * (W - 1) * a.D + at.c;
+#pragma unroll
+                    for (int r = 0; r < W - 1; ++r)
+                        store_vec<IO, VE>(s + (size_t)r * a.D, f.win[r]);
+                }
+            }
+        }
+    }
+
+    // the state of an empty sequence stays what it was
+    if (at.m0 == 0 && a.state_T && (a.cu || !M)) {
+        for (int n = at.run; n < a.N; n += at.runs) {
+            if (a.cu && a.cu[n] < a.cu[n + 1])
+                continue;
+            f.from_state(a, n, at.c);
+            IO* s = static_cast<IO*>(a.state_T) + (size_t)n * (W - 1) * a.D + at.c;
+#pragma unroll
+            for (int r = 0; r < W - 1; ++r)
+                store_vec<IO, VE>(s + (size_t)r * a.D, f.win[r]);
+        }
+    }
+}
+
+// ---- backward -----------------------------------------------------------------
+
+template <typename IO, int VE, int W>
+__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, Plan plan)
+{
+    __shared__ Marks marks;
+    const Place<VE> at(plan, a.D);
+    const long long M = (long long)a.B * a.T;
+    const int lanes = 1 << plan.lanes_log2, batches = at.length / kBatchBwd;
+    Filter<IO, VE, W> f;
+    f.init(a, at.c);
+    float dw[W][VE], db[VE], part[W][VE];  // part[k]: dx of the token W-1-k before this one
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+        db[j] = 0.f;
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+            dw[k][j] = part[k][j] = 0.f;
+    }
+
+    if (M) {
+        Rows<IO, VE> rows(a.x, a.xs, at.m - (W - 1), M, at.c), grads(a.dy, a.D, at.m, M, at.c);
+        Vec<IO, VE> before[W - 1], nx[kBatchBwd], ny[kBatchBwd];
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+            before[k] = rows.next();
+#pragma unroll
+        for (int i = 0; i < kBatchBwd; ++i) {
+            nx[i] = rows.next();
+            ny[i] = grads.next();
+        }
+        mark_tokens(marks, a, at.m0 - (W - 1), at.runs * at.length + 2 * (W - 1));
+        const int base = at.run * at.length;
+        const long long limit = token_limit(a), behind = at.m + at.length;
+        const bool plain = !__any(behind + W - 1 > limit ||
+                                  any_mark(marks, base, at.length + 2 * (W - 1), at.lane, lanes));
+        IO* dx = static_cast<IO*>(a.dx) + at.c;
+        // the sequence that started last within the run, and where
+        int seq = -1;
+        long long began = -1;
+
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) {
+            float x[VE];
+            widen<IO, VE>(before[k], x);
+            if (!plain && marks.start[base + k] >= 0)
+                f.from_state(a, marks.start[base + k], at.c);
+            f.push(x);
+        }
+
+        // a finished gradient: of token m of the run, or of the state's row before `began`
+        auto finish = [&](long long m, const float (&v)[VE]) {
+            if (plain) {
+                if (m >= at.m)
+                    store_vec<IO, VE>(dx + (size_t)m * a.D, v);
+                return;
+            }
+            if (m < began) {
+                if (seq >= 0 && a.dstate0)
+                    store_vec<IO, VE>(static_cast<IO*>(a.dstate0) +
+                                          ((size_t)seq * (W - 1) + (int)(m - began) + W - 1) * a.D + at.c, v);
+            } else if (m >= at.m && m < behind) {
+                store_vec<IO, VE>(dx + (size_t)m * a.D, v);
+            }
+        };
+        // token i of the run (or of the W - 1 behind it)
+        auto token = [&](int i, const Vec<IO, VE>& rx, const Vec<IO, VE>& ry, bool own) {
+            const long long m = at.m + i;
+            const int k = base + W - 1 + i;
+            float x[VE], g[VE], z[VE];
+            widen<IO, VE>(rx, x);
+            widen<IO, VE>(ry, g);
+            if (!plain) {
+                if (m >= limit)
+                    return;
+                if (marks.start[k] >= 0) {
+                    f.from_state(a, marks.start[k], at.c);
+                    seq = own ? marks.start[k] : -1;
+                    began = m;
+                }
+            }
+            if (a.silu) {
+                f.z(x, z);
+#pragma unroll
+                for (int j = 0; j < VE; ++j)
+                    g[j] *= silu_slope(z[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < VE; ++j) {
+                if (own) {
+                    db[j] += g[j];
+#pragma unroll
+                    for (int r = 0; r < W - 1; ++r)
+                        dw[r][j] = fmaf(g[j], f.win[r][j], dw[r][j]);
+                    dw[W - 1][j] = fmaf(g[j], x[j], dw[W - 1][j]);
+                }
+#pragma unroll
+                for (int r = 0; r < W; ++r)
+                    part[r][j] = fmaf(f.w[r][j], g[j], part[r][j]);
+            }
+            f.push(x);
+            finish(m - (W - 1), part[0]);
+#pragma unroll
+            for (int j = 0; j < VE; ++j) {
+#pragma unroll
+                for (int r = 0; r < W - 1; ++r)
+                    part[r][j] = part[r + 1][j];
+                part[W - 1][j] = 0.f;
+            }
+            if (!plain && marks.end[k] >= 0) {
+                // nothing follows in this sequence but its state's gradient
+                const IO* s = static_cast<const IO*>(a.dstate_T) + (size_t)marks.end[k] * (W - 1) * a.D + at.c;
+#pragma unroll
+                for (int r = 0; r < W - 1; ++r) {
+                    float d[VE];
+                    load_or_zero<IO, VE>(s + (size_t)r * a.D, a.dstate_T, d);
+#pragma unroll
+                    for (int j = 0; j < VE; ++j) {
+                        d[j] += part[r][j];
+                        part[r][j] = 0.f;
+                    }
+                    finish(m - (W - 2) + r, d);
+                }
+            }
+        };
+
+        for (int q = 0; q < batches; ++q) {
+            Vec<IO, VE> cx[kBatchBwd], cy[kBatchBwd];
+#pragma unroll
+            for (int i = 0; i < kBatchBwd; ++i)
+                cx[i] = nx[i], cy[i] = ny[i];
+            // behind the last batch come the W - 1 tokens that end the run's dx
+            const bool more = q + 1 < batches;
+#pragma unroll
+            for (int i = 0; i < kBatchBwd; ++i)
+                if (more || i < W - 1) {
+                    nx[i] = rows.next();
+                    ny[i] = grads.next();
+                }
+#pragma unroll
+            for (int i = 0; i < kBatchBwd; ++i)
+                token(q * kBatchBwd + i, cx[i], cy[i], true);
+        }
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i)
+            token(at.length + i, nx[i], ny[i], false);
+    }
+
+    // the gradient by the state of an empty sequence
+    if (at.m0 == 0 && a.dstate0 && (a.cu || !M)) {
+        for (int n = at.run; n < a.N; n += at.runs) {
+            if (a.cu && a.cu[n] < a.cu[n + 1])
+                continue;
+            const size_t o = (size_t)n * (W - 1) * a.D + at.c;
+#pragma unroll
+            for (int r = 0; r < W - 1; ++r) {
+                float d[VE];
+                load_or_zero<IO, VE>(static_cast<const IO*>(a.dstate_T) + o + (size_t)r * a.D, a.dstate_T, d);
+                store_vec<IO, VE>(static_cast<IO*>(a.dstate0) + o + (size_t)r * a.D, d);
+            }
+        }
+    }
+    if (!M)
+        return;
+
+    // sums over the tile: runs within a wave, then the four waves
+    __shared__ float sums[4][64 * VE];
+    const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
+    float* out = a.ws + (size_t)(blockIdx.x / plan.ctiles) * (W + 1) * a.D;
+#pragma unroll
+    for (int k = 0; k <= W; ++k) {
+        float s[VE];
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+            s[j] = k < W ? dw[k < W ? k : 0][j] : db[j];
+            for (int o = lanes; o < 64; o *= 2)
+                s[j] += __shfl_xor(s[j], o);
+        }
+        __syncthreads();
+        if (l < lanes) {
+#pragma unroll
+            for (int j = 0; j < VE; ++j)
+                sums[wave][l * VE + j] = s[j];
+        }
+        __syncthreads();
+        if (threadIdx.x < lanes) {
+#pragma unroll
+            for (int j = 0; j < VE; ++j)
+                s[j] = (sums[0][l * VE + j] + sums[1][l * VE + j]) + (sums[2][l * VE + j] + sums[3][l * VE + j]);
+            store_vec<float, VE>(out + (size_t)k * a.D + at.c, s);
+        }
+    }
+}
+
+// Adds the tiles' sums [tiles][(W+1) D]: 64 columns a workgroup, 16 shares of the
+// tiles each, joined in order.
+__global__ __launch_bounds__(1024) void conv_sum_kernel(ConvArgs a, int tiles)
+{
+    __shared__ float share[16][64];
+    const int l = threadIdx.x & 63, q = threadIdx.x >> 6;
+    const int c = blockIdx.x * 64 + l, n = (a.W + 1) * a.D;
+    float s = 0.f;
+    if (c < n) {
+#pragma unroll 8
+        for (int g = q; g < tiles; g += 16)
+            s += a.ws[(size_t)g * n + c];
+    }
+    share[q][l] = s;
+    __syncthreads();
+    if (q || c >= n)
+        return;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        s += share[i][l];
+    if (c < a.W * a.D)
+        a.dweight[c] = s;
+    else if (a.dbias)
+        a.dbias[c - a.W * a.D] = s;
+}
+
+// ---- one token ---------------------------------------------------------------------
 
 template <typename IO>
 __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a)
@@ -162,51 +554,79 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a)
         st[(size_t)i * a.D] = next;
         next = old;
     }
-    static_cast<IO*>(a.y)[(size_t)b * a.D + c] = from_f32<IO>(a.silu ? z * gate_sigmoid(z) : z);
+    static_cast<IO*>(a.y)[(size_t)b * a.D + c] = from_f32<IO>(a.silu ? silu(z) : z);
+}
+
+// ---- shapes ------------------------------------------------------------------------
+
+// Threads side by side on a row: as many as its vectors, 8 to 64.  Runs as long as
+// leave a workgroup for every compute unit, 8 to 32 tokens: a longer one reads
+// fewer rows twice, and its sums are written once for more tokens.
+Plan plan_of(long long M, int D, int ve)
+{
+    Plan p;
+    const int vecs = (D + ve - 1) / ve;
+    p.lanes_log2 = vecs <= 8 ? 3 : vecs <= 16 ? 4 : vecs <= 32 ? 5 : 6;
+    p.ctiles = (vecs + (1 << p.lanes_log2) - 1) >> p.lanes_log2;
+    const int runs = 256 >> p.lanes_log2;
+    p.batches = 4;
+    while (p.batches > 1 && (M + runs * p.batches * kBatch - 1) / (runs * p.batches * kBatch) * p.ctiles < 512)
+        p.batches /= 2;
+    const long long per = (long long)runs * p.batches * kBatch;
+    p.tiles = M ? (int)((M + per - 1) / per) : 1;
+    return p;
+}
+
+template <typename IO, int VE>
+hipError_t conv_fwd(const ConvArgs& a, hipStream_t stream)
+{
+    const Plan p = plan_of((long long)a.B * a.T, a.D, VE);
+    const unsigned grid = (unsigned)p.tiles * p.ctiles;
+    if (a.W == 2)
+        conv_fwd_kernel<IO, VE, 2><<<grid, 256, 0, stream>>>(a, p);
+    else if (a.W == 3)
+        conv_fwd_kernel<IO, VE, 3><<<grid, 256, 0, stream>>>(a, p);
+    else
+        conv_fwd_kernel<IO, VE, 4><<<grid, 256, 0, stream>>>(a, p);
+    return hipGetLastError();
+}
+
+template <typename IO, int VE>
+hipError_t conv_bwd(const ConvArgs& a, hipStream_t stream)
+{
+    const Plan p = plan_of((long long)a.B * a.T, a.D, VE);
+    const unsigned grid = (unsigned)p.tiles * p.ctiles;
+    if (a.W == 2)
+        conv_bwd_kernel<IO, VE, 2><<<grid, 256, 0, stream>>>(a, p);
+    else if (a.W == 3)
+        conv_bwd_kernel<IO, VE, 3><<<grid, 256, 0, stream>>>(a, p);
+    else
+        conv_bwd_kernel<IO, VE, 4><<<grid, 256, 0, stream>>>(a, p);
+    const int columns = (a.W + 1) * a.D;
+    conv_sum_kernel<<<(columns + 63) / 64, 1024, 0, stream>>>(a, a.T ? p.tiles : 0);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 int conv_bwd_groups(int B, int T, int D)
 {
-    const long long rows = (long long)B * T;
-    return rows < 512 ? (int)rows : 512;
+    return T ? plan_of((long long)B * T, D, D < 4 ? 1 : 4).tiles : 0;
 }
 
-template <typename IO>
-static hipError_t conv_fwd(const ConvArgs& a, hipStream_t stream)
-{
-    const unsigned cols = (a.D + 255) / 256;
-    if (a.T)
-        conv_fwd_kernel<IO><<<dim3((unsigned)(a.B * a.T), cols), 256, 0, stream>>>(a);
-    if (a.state_T)
-        conv_state_kernel<IO><<<dim3((unsigned)(a.N * (a.W - 1)), cols), 256, 0, stream>>>(a);
-    return hipGetLastError();
-}
-
-template <typename IO>
-static hipError_t conv_bwd(const ConvArgs& a, hipStream_t stream)
-{
-    const unsigned cols = (a.D + 255) / 256;
-    const int groups = conv_bwd_groups(a.B, a.T, a.D);
-    if (a.T) {
-        conv_bwd_dx_kernel<IO><<<dim3((unsigned)(a.B * a.T), cols), 256, 0, stream>>>(a);
-        conv_bwd_param_kernel<IO><<<dim3(groups, cols), 256, 0, stream>>>(a);
-    }
-    if (a.dstate0)
-        conv_bwd_state_kernel<IO><<<dim3((unsigned)(a.N * (a.W - 1)), cols), 256, 0, stream>>>(a);
-    conv_bwd_sum_kernel<<<dim3(a.W + 1, cols), 256, 0, stream>>>(a, groups);
-    return hipGetLastError();
-}
-
+// fewer channels than a vector go one a thread
 hipError_t launch_conv_fwd(const ConvArgs& a, bool bf, hipStream_t stream)
 {
-    return bf ? conv_fwd<bf16>(a, stream) : conv_fwd<float>(a, stream);
+    if (bf)
+        return a.D < 8 ? conv_fwd<bf16, 1>(a, stream) : conv_fwd<bf16, 8>(a, stream);
+    return a.D < 4 ? conv_fwd<float, 1>(a, stream) : conv_fwd<float, 4>(a, stream);
 }
 
 hipError_t launch_conv_bwd(const ConvArgs& a, bool bf, hipStream_t stream)
 {
-    return bf ? conv_bwd<bf16>(a, stream) : conv_bwd<float>(a, stream);
+    if (bf)
+        return a.D < 4 ? conv_bwd<bf16, 1>(a, stream) : conv_bwd<bf16, 4>(a, stream);
+    return a.D < 4 ? conv_bwd<float, 1>(a, stream) : conv_bwd<float, 4>(a, stream);
 }
 
 hipError_t launch_conv_step(const ConvArgs& a, bool bf, hipStream_t stream)
