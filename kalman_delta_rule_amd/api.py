@@ -53,8 +53,26 @@ def _math_flag(math: Optional[str]) -> int:
     raise ValueError("math must be None or 'bf16', got %r" % (math,))
 
 
+# torch's own accessor of a device's current stream handle: current_stream()
+# builds a Stream object around it, 1.9 us of a 10 us single-token call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device) -> int:
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
+
+
+def _launch(dev, fn, *args) -> None:
+    """fn(*args, stream) on dev, whichever device is current."""
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(dev))
+    if st != 0:
+        _lib.check(st)
 
 
 def _head_vec(t, name, H, dev):
@@ -575,11 +593,11 @@ def _optional(dev, *tensors):
             _need(t, name, shape, dtype, dev)
 
 
-def _given(t, name, shape, dtype, dev):
-    """The caller's output tensor, or a new one."""
+def _given(t, name, like):
+    """The caller's output tensor, or a new one, as ``like`` but dense."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _need(t, name, shape, dtype, dev)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
+    _need(t, name, like.shape, like.dtype, like.device)
     return t
 
 
@@ -617,16 +635,13 @@ def kdn_layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, y=None,
     stride = _row_stride(x, "x")
     f32 = torch.float32
     _optional(dev, (weight, "weight", (D,), f32), (bias, "bias", (D,), f32))
-    y = _given(y, "y", x.shape, x.dtype, dev)
+    y = _given(y, "y", x)
     mean = rstd = None
     if want_stats:
         mean = torch.empty(x.shape[:-1], dtype=f32, device=dev)
         rstd = torch.empty(x.shape[:-1], dtype=f32, device=dev)
-    with torch.cuda.device(dev):
-        st = L.kdn_layer_norm_fwd(x.numel() // D if D else 0, D, io, float(eps), x.data_ptr(),
-                                  stride, _ptr(weight), _ptr(bias), y.data_ptr(), _ptr(mean),
-                                  _ptr(rstd), _stream(dev))
-    _lib.check(st)
+    _launch(dev, L.kdn_layer_norm_fwd, x.numel() // D if D else 0, D, io, float(eps),
+            x.data_ptr(), stride, _ptr(weight), _ptr(bias), y.data_ptr(), _ptr(mean), _ptr(rstd))
     return y, mean, rstd
 
 
@@ -645,18 +660,15 @@ def kdn_layer_norm_bwd(dy, x, mean, rstd, weight=None, want_param_grads: bool = 
     _need(rstd, "rstd", x.shape[:-1], f32, dev)
     _optional(dev, (weight, "weight", (D,), f32))
     rows = x.numel() // D if D else 0
-    g = {"dx": _given(dx, "dx", x.shape, x.dtype, dev)}
+    g = {"dx": _given(dx, "dx", x)}
     ws, ws_bytes = None, 0
     if want_param_grads:
         g["dweight"] = torch.empty(D, dtype=f32, device=dev)
         g["dbias"] = torch.empty(D, dtype=f32, device=dev)
         ws, ws_bytes = _workspace(workspace, L.kdn_layer_norm_bwd_workspace_size(rows, D), dev)
-    with torch.cuda.device(dev):
-        st = L.kdn_layer_norm_bwd(rows, D, io, dy.data_ptr(), x.data_ptr(), stride,
-                                  mean.data_ptr(), rstd.data_ptr(), _ptr(weight),
-                                  g["dx"].data_ptr(), _ptr(g.get("dweight")),
-                                  _ptr(g.get("dbias")), _ptr(ws), ws_bytes, _stream(dev))
-    _lib.check(st)
+    _launch(dev, L.kdn_layer_norm_bwd, rows, D, io, dy.data_ptr(), x.data_ptr(), stride,
+            mean.data_ptr(), rstd.data_ptr(), _ptr(weight), g["dx"].data_ptr(),
+            _ptr(g.get("dweight")), _ptr(g.get("dbias")), _ptr(ws), ws_bytes)
     return g
 
 
@@ -691,14 +703,13 @@ def kdn_conv_fwd(x, weight, bias=None, state0=None, cu_seqlens=None, activation=
     _need(weight, "weight", (W, D), f32, dev)
     _optional(dev, (bias, "bias", (D,), f32), (state0, "state0", (N, W - 1, D), x.dtype))
     act = _activation(activation)
-    y = _given(y, "y", x.shape, x.dtype, dev)
-    if want_state or state_T is not None:
-        state_T = _given(state_T, "state_T", (N, max(W - 1, 0), D), x.dtype, dev)
-    with torch.cuda.device(dev):
-        st = L.kdn_conv_fwd(B, T, D, W, io, act, x.data_ptr(), stride, weight.data_ptr(),
-                            _ptr(bias), _ptr(state0), _ptr(cu_seqlens), N, y.data_ptr(),
-                            _ptr(state_T), _stream(dev))
-    _lib.check(st)
+    y = _given(y, "y", x)
+    if state_T is not None:
+        _need(state_T, "state_T", (N, W - 1, D), x.dtype, dev)
+    elif want_state:
+        state_T = torch.empty((N, max(W - 1, 0), D), dtype=x.dtype, device=dev)
+    _launch(dev, L.kdn_conv_fwd, B, T, D, W, io, act, x.data_ptr(), stride, weight.data_ptr(),
+            _ptr(bias), _ptr(state0), _ptr(cu_seqlens), N, y.data_ptr(), _ptr(state_T))
     return y, state_T
 
 
@@ -720,20 +731,16 @@ def kdn_conv_bwd(dy, x, weight, bias=None, state0=None, cu_seqlens=None, activat
     _optional(dev, (bias, "bias", (D,), f32), (state0, "state0", (N, W - 1, D), x.dtype),
               (dstate_T, "dstate_T", (N, W - 1, D), x.dtype))
     act = _activation(activation)
-    g = {"dx": _given(dx, "dx", x.shape, x.dtype, dev),
-         "dweight": torch.empty((W, D), dtype=f32, device=dev)}
+    g = {"dx": _given(dx, "dx", x), "dweight": torch.empty((W, D), dtype=f32, device=dev)}
     if bias is not None:
         g["dbias"] = torch.empty(D, dtype=f32, device=dev)
     if state0 is not None:
         g["dstate0"] = torch.empty_like(state0)
     ws, ws_bytes = _workspace(workspace, L.kdn_conv_bwd_workspace_size(B, T, D, W), dev)
-    with torch.cuda.device(dev):
-        st = L.kdn_conv_bwd(B, T, D, W, io, act, dy.data_ptr(), x.data_ptr(), stride,
-                            weight.data_ptr(), _ptr(bias), _ptr(state0), _ptr(cu_seqlens), N,
-                            _ptr(dstate_T), g["dx"].data_ptr(), g["dweight"].data_ptr(),
-                            _ptr(g.get("dbias")), _ptr(g.get("dstate0")), _ptr(ws), ws_bytes,
-                            _stream(dev))
-    _lib.check(st)
+    _launch(dev, L.kdn_conv_bwd, B, T, D, W, io, act, dy.data_ptr(), x.data_ptr(), stride,
+            weight.data_ptr(), _ptr(bias), _ptr(state0), _ptr(cu_seqlens), N, _ptr(dstate_T),
+            g["dx"].data_ptr(), g["dweight"].data_ptr(), _ptr(g.get("dbias")),
+            _ptr(g.get("dstate0")), _ptr(ws), ws_bytes)
     return g
 
 
@@ -749,12 +756,9 @@ def kdn_conv_step(x, weight, state, bias=None, activation=None, y=None) -> torch
     _need(state, "state", (B, W - 1, D), x.dtype, dev)
     if bias is not None:
         _need(bias, "bias", (D,), torch.float32, dev)
-    y = _given(y, "y", (B, D), x.dtype, dev)
-    with torch.cuda.device(dev):
-        st = L.kdn_conv_step(B, D, W, io, _activation(activation), x.data_ptr(), stride,
-                             weight.data_ptr(), _ptr(bias), state.data_ptr(), y.data_ptr(),
-                             _stream(dev))
-    _lib.check(st)
+    y = _given(y, "y", x)
+    _launch(dev, L.kdn_conv_step, B, D, W, io, _activation(activation), x.data_ptr(), stride,
+            weight.data_ptr(), _ptr(bias), state.data_ptr(), y.data_ptr())
     return y
 
 
@@ -785,17 +789,18 @@ def kdn_rec_fwd(x, a, h0=None, cu_seqlens=None, gate: str = "preact", blend: boo
     N = _sequences(cu_seqlens, B, dev)
     f32 = torch.float32
     _optional(dev, (h0, "h0", (N, D), f32))
-    h = _given(h, "h", x.shape, x.dtype, dev)
-    h_T = _given(h_T, "h_T", (N, D), f32, dev)
+    h = _given(h, "h", x)
+    if h_T is not None:
+        _need(h_T, "h_T", (N, D), f32, dev)
+    else:
+        h_T = torch.empty((N, D), dtype=f32, device=dev)
     chk = None
     if want_checkpoints:
         chk = torch.empty((B, -(-T // _lib.KDN_REC_CHECKPOINT), D), dtype=f32, device=dev)
     ws, ws_bytes = _workspace(workspace, L.kdn_rec_fwd_workspace_size(B, T, D), dev)
-    with torch.cuda.device(dev):
-        st = L.kdn_rec_fwd(B, T, D, io, code, int(bool(blend)), x.data_ptr(), stride, a.data_ptr(),
-                           a_stride, _ptr(h0), _ptr(cu_seqlens), N, h.data_ptr(), h_T.data_ptr(),
-                           _ptr(chk), _ptr(ws), ws_bytes, _stream(dev))
-    _lib.check(st)
+    _launch(dev, L.kdn_rec_fwd, B, T, D, io, code, int(bool(blend)), x.data_ptr(), stride,
+            a.data_ptr(), a_stride, _ptr(h0), _ptr(cu_seqlens), N, h.data_ptr(), h_T.data_ptr(),
+            _ptr(chk), _ptr(ws), ws_bytes)
     return h, h_T, chk
 
 
@@ -816,17 +821,14 @@ def kdn_rec_bwd(dh, x, a, checkpoints, h0=None, dh_T=None, cu_seqlens=None, gate
     _need(dh, "dh", x.shape, x.dtype, dev)
     _need(checkpoints, "checkpoints", (B, -(-T // _lib.KDN_REC_CHECKPOINT), D), f32, dev)
     _optional(dev, (h0, "h0", (N, D), f32), (dh_T, "dh_T", (N, D), f32))
-    g = {"dx": _given(dx, "dx", x.shape, x.dtype, dev),
+    g = {"dx": _given(dx, "dx", x),
          "da": torch.empty(x.shape, dtype=adt, device=dev),
          "dh0": torch.empty((N, D), dtype=f32, device=dev)}
     ws, ws_bytes = _workspace(workspace, L.kdn_rec_bwd_workspace_size(B, T, D), dev)
-    with torch.cuda.device(dev):
-        st = L.kdn_rec_bwd(B, T, D, io, code, int(bool(blend)), dh.data_ptr(), x.data_ptr(),
-                           stride, a.data_ptr(), a_stride, checkpoints.data_ptr(), _ptr(h0),
-                           _ptr(cu_seqlens), N, _ptr(dh_T), g["dx"].data_ptr(),
-                           g["da"].data_ptr(), g["dh0"].data_ptr(), _ptr(ws), ws_bytes,
-                           _stream(dev))
-    _lib.check(st)
+    _launch(dev, L.kdn_rec_bwd, B, T, D, io, code, int(bool(blend)), dh.data_ptr(), x.data_ptr(),
+            stride, a.data_ptr(), a_stride, checkpoints.data_ptr(), _ptr(h0), _ptr(cu_seqlens), N,
+            _ptr(dh_T), g["dx"].data_ptr(), g["da"].data_ptr(), g["dh0"].data_ptr(), _ptr(ws),
+            ws_bytes)
     return g
 
 
@@ -840,9 +842,7 @@ def kdn_rec_step(x, a, state, gate: str = "preact", blend: bool = False, h=None)
     code, adt = _gate(gate, x.dtype)
     a_stride = _need_rows(a, "a", x.shape, adt, dev)
     _need(state, "state", (B, D), torch.float32, dev)
-    h = _given(h, "h", (B, D), x.dtype, dev)
-    with torch.cuda.device(dev):
-        st = L.kdn_rec_step(B, D, io, code, int(bool(blend)), x.data_ptr(), stride, a.data_ptr(),
-                            a_stride, state.data_ptr(), h.data_ptr(), _stream(dev))
-    _lib.check(st)
+    h = _given(h, "h", x)
+    _launch(dev, L.kdn_rec_step, B, D, io, code, int(bool(blend)), x.data_ptr(), stride,
+            a.data_ptr(), a_stride, state.data_ptr(), h.data_ptr())
     return h
