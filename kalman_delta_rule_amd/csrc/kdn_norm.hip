@@ -7,11 +7,10 @@
 // Both are bound by HBM.  A row is held in the registers of TPR threads, NV
 // vectors of 16 bytes each, from one load to the store: x is read once, and the
 // variance is taken around the mean without a second read.  A workgroup walks
-// many rows, with w and b (and in the backward the sums dw and db of the
-// thread's columns) in registers all along and the next row's loads issued
-// before the present row is reduced.  The backward's sums are joined over the
-// workgroup at the end and written once a workgroup; a second launch adds those,
-// always in the same order.
+// many rows, with w and b (in the backward w and the sums dw and db of the
+// thread's columns) in registers all along.  The backward's sums are joined over
+// the workgroup at the end and written once a workgroup; a second launch adds
+// those, always in the same order.
 #include "kdn_block_device.h"
 
 namespace kdn {
@@ -58,7 +57,7 @@ __device__ __forceinline__ float2 row_sum(float a, float b, float2* red)
         a = b = 0.f;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            const float2 r = red[w];
+            const float2 r = red[threadIdx.x / TPR * W + w];
             a += r.x;
             b += r.y;
         }
@@ -211,15 +210,19 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArg
     }
 }
 
-// 1024 threads have 128 registers each: there the next row is not loaded ahead,
-// the other waves of the SIMD cover its latency.
+// 1024 threads whatever a row takes: the sums of its columns are written once a
+// workgroup, and few values a thread leave the registers for eight waves a SIMD,
+// which cover the loads better than loading a row ahead does with fewer (32768 rows
+// of 2048 bf16: 84 us; a wave a row with the next one loaded ahead 127 us, 256
+// threads a workgroup 91 us, with four times the sums to write).
+constexpr int kBwdThreads = 1024;
+
 template <typename IO, int TPR, int NV>
-__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormArgs a)
+__global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs a)
 {
     typedef Part<IO, TPR, NV> P;
-    constexpr bool AHEAD = TPR < 1024;
-    constexpr int VE = P::VE, THREADS = TPR > 256 ? TPR : 256, WAVES = THREADS / 64;
-    __shared__ float2 red[TPR > 64 ? TPR / 64 : 1];
+    constexpr int VE = P::VE, THREADS = kBwdThreads, WAVES = THREADS / 64;
+    __shared__ float2 red[WAVES];
     const P part(a.D);
     const int per = THREADS / TPR, step = gridDim.x * per;
     const float inv = 1.f / a.D;
@@ -234,27 +237,12 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormArg
     const IO* x = static_cast<const IO*>(a.x);
     const IO* dy = static_cast<const IO*>(a.dy);
     int row = blockIdx.x * per + row_of_thread<TPR>();
-    Vec<IO, VE> nx[NV], ny[NV];
-    float nmean, nrstd;
-    auto fetch = [&](int r) {
-        const int rr = min(r, a.rows - 1);
-        part.load(x + (size_t)rr * a.xs, nx);
-        part.load(dy + (size_t)rr * a.D, ny);
-        nmean = a.mean[rr];
-        nrstd = a.rstd[rr];
-    };
-    if (AHEAD)
-        fetch(row);
     for (int r0 = blockIdx.x * per; r0 < a.rows; r0 += step, row += step) {
-        if (!AHEAD)
-            fetch(row);
+        const int at = min(row, a.rows - 1);
         Vec<IO, VE> rx[NV], ry[NV];
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-            rx[v] = nx[v], ry[v] = ny[v];
-        const float mean = nmean, rstd = nrstd;
-        if (AHEAD && r0 + step < a.rows)
-            fetch(row + step);
+        part.load(x + (size_t)at * a.xs, rx);
+        part.load(dy + (size_t)at * a.D, ry);
+        const float mean = a.mean[at], rstd = a.rstd[at];
         const bool mine = row < a.rows;
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
@@ -291,11 +279,12 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormArg
 
     if (!a.ws)
         return;
-    // the workgroup's rows: lanes of one column within a wave, then the waves
-    constexpr int LANES = TPR < 64 ? TPR : 64;   // of a row in a wave
-    constexpr int SETS = TPR < 64 ? WAVES : WAVES * 64 / TPR;  // waves that hold the same columns
-    __shared__ float sums[SETS > 1 ? SETS : 1][SETS > 1 ? LANES * VE : 1];
-    const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
+    // the workgroup's rows: lanes of one column within a wave, then the sets of
+    // threads that hold all columns
+    constexpr int SETS = TPR < 64 ? WAVES : THREADS / TPR;
+    __shared__ float sums[SETS > 1 ? SETS : 1][SETS > 1 ? TPR * VE : 1];
+    const int l = threadIdx.x % TPR, set = TPR < 64 ? threadIdx.x >> 6 : threadIdx.x / TPR;
+    const bool first = TPR >= 64 || (threadIdx.x & 63) < TPR;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         float* out = a.ws + ((size_t)blockIdx.x * 2 + k) * a.D;
@@ -306,18 +295,18 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormArg
             for (int j = 0; j < VE; ++j) {
                 s[j] = k ? db[v][j] : dw[v][j];
 #pragma unroll
-                for (int o = LANES; o < 64; o *= 2)
+                for (int o = TPR; o < 64; o *= 2)
                     s[j] += __shfl_xor(s[j], o);
             }
             if constexpr (SETS > 1) {
                 __syncthreads();
-                if (l < LANES) {
+                if (first) {
 #pragma unroll
                     for (int j = 0; j < VE; ++j)
-                        sums[wave][l * VE + j] = s[j];
+                        sums[set][l * VE + j] = s[j];
                 }
                 __syncthreads();
-                for (int i = threadIdx.x; i < LANES * VE; i += THREADS) {
+                for (int i = threadIdx.x; i < TPR * VE; i += THREADS) {
                     const int c = v * TPR * VE + i;
                     if (c < a.D) {
                         float t = 0.f;
@@ -441,7 +430,7 @@ __global__ __launch_bounds__(256) void norm_bwd_wide_sums_kernel(NormArgs a)
 struct Shape {
     int tpr, nv;  // tpr 0: too wide
 };
-Shape shape_of(int D, bool bf)
+Shape fwd_shape(int D, bool bf)
 {
     const int vecs = (D + (bf ? 7 : 3)) / (bf ? 8 : 4);
     if (vecs <= 64)
@@ -458,31 +447,33 @@ Shape shape_of(int D, bool bf)
     return {0, 0};
 }
 
-// calls f(threads, vectors) with the shape as constants
-template <typename F>
-hipError_t with_shape(Shape s, F f)
+// The backward holds x, dy, w and two sums: as many threads as the row has vectors,
+// and two or four each only where 1024 threads do not suffice.
+Shape bwd_shape(int D, bool bf)
 {
-    using std::integral_constant;
-#define KDN_SHAPE(T, N)                                              \
-    if (s.tpr == T && s.nv == N)                                     \
-        return f(integral_constant<int, T>{}, integral_constant<int, N>{});
-    KDN_SHAPE(8, 1)
-    KDN_SHAPE(16, 1)
-    KDN_SHAPE(32, 1)
-    KDN_SHAPE(64, 1)
-    KDN_SHAPE(64, 2)
-    KDN_SHAPE(64, 4)
-    KDN_SHAPE(256, 2)
-    KDN_SHAPE(256, 4)
-    KDN_SHAPE(1024, 2)
-#undef KDN_SHAPE
-    return hipErrorInvalidValue;
+    const int vecs = (D + (bf ? 7 : 3)) / (bf ? 8 : 4);
+    if (vecs > 512)
+        return vecs <= 1024 ? Shape{512, 2} : fwd_shape(D, bf);
+    int t = 8;
+    while (t < vecs)
+        t *= 2;
+    return {t, 1};
+}
+
+// calls f(threads, vectors) with the shape as constants, if it is that one
+template <int T, int N, typename F>
+bool with_shape(Shape s, F f)
+{
+    if (s.tpr != T || s.nv != N)
+        return false;
+    f(std::integral_constant<int, T>{}, std::integral_constant<int, N>{});
+    return true;
 }
 
 template <typename IO>
 hipError_t norm_fwd(const NormArgs& a, hipStream_t stream)
 {
-    const Shape s = shape_of(a.D, sizeof(IO) == 2);
+    const Shape s = fwd_shape(a.D, sizeof(IO) == 2);
     if (!s.tpr) {
         norm_fwd_wide_kernel<IO><<<a.rows, 1024, 0, stream>>>(a);
         return hipGetLastError();
@@ -494,21 +485,22 @@ hipError_t norm_fwd(const NormArgs& a, hipStream_t stream)
     const int grid = groups < 2048 ? groups : 2048;
     auto run = [&](auto t, auto n) {
         norm_fwd_kernel<IO, decltype(t)::value, decltype(n)::value><<<grid, threads, 0, stream>>>(a);
-        return hipGetLastError();
     };
+    with_shape<8, 1>(s, run) || with_shape<16, 1>(s, run) || with_shape<32, 1>(s, run) ||
+        with_shape<64, 1>(s, run) || with_shape<64, 2>(s, run) || with_shape<64, 4>(s, run) ||
+        with_shape<256, 2>(s, run) || with_shape<256, 4>(s, run) || with_shape<1024, 2>(s, run);
     if constexpr (sizeof(IO) == 4)
-        if (s.tpr == 1024 && s.nv == 4)
-            return run(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
-    return with_shape(s, run);
+        with_shape<1024, 4>(s, run);
+    return hipGetLastError();
 }
 
-// workgroups of the backward (and partial sums)
+// workgroups of the backward (and partial sums): two a compute unit, or the one
+// that fits with several vectors a thread
 int bwd_groups(int rows, Shape s)
 {
-    const int threads = s.tpr > 256 ? s.tpr : 256;
-    const int per = s.tpr ? threads / s.tpr : 1;
+    const int per = s.tpr ? kBwdThreads / s.tpr : 1;
     const long long groups = ((long long)rows + per - 1) / per;
-    const int most = threads > 256 || !s.tpr ? 256 : 512;
+    const int most = s.nv == 1 ? 512 : 256;
     return groups < most ? (int)groups : most;
 }
 
@@ -516,7 +508,7 @@ template <typename IO>
 hipError_t norm_bwd(const NormArgs& args, hipStream_t stream)
 {
     NormArgs a = args;
-    const Shape s = shape_of(a.D, sizeof(IO) == 2);
+    const Shape s = bwd_shape(a.D, sizeof(IO) == 2);
     const int groups = bwd_groups(a.rows, s);
     const bool sums = a.dweight || a.dbias;
     if (!sums)
@@ -527,18 +519,14 @@ hipError_t norm_bwd(const NormArgs& args, hipStream_t stream)
             norm_bwd_wide_sums_kernel<IO><<<dim3(groups, (a.D + 255) / 256), 256, 0, stream>>>(a);
     } else if (a.rows) {
         auto run = [&](auto t, auto n) {
-            constexpr int T = decltype(t)::value;
-            norm_bwd_kernel<IO, T, decltype(n)::value><<<groups, T > 256 ? T : 256, 0, stream>>>(a);
-            return hipGetLastError();
+            norm_bwd_kernel<IO, decltype(t)::value, decltype(n)::value>
+                <<<groups, kBwdThreads, 0, stream>>>(a);
         };
-        hipError_t e;
+        with_shape<8, 1>(s, run) || with_shape<16, 1>(s, run) || with_shape<32, 1>(s, run) ||
+            with_shape<64, 1>(s, run) || with_shape<128, 1>(s, run) || with_shape<256, 1>(s, run) ||
+            with_shape<512, 1>(s, run) || with_shape<512, 2>(s, run) || with_shape<1024, 2>(s, run);
         if constexpr (sizeof(IO) == 4)
-            e = s.tpr == 1024 && s.nv == 4 ? run(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{})
-                              : with_shape(s, run);
-        else
-            e = with_shape(s, run);
-        if (e != hipSuccess)
-            return e;
+            with_shape<1024, 4>(s, run);
     }
     if (sums)
         norm_sum_kernel<<<(2 * a.D + 63) / 64, 1024, 0, stream>>>(a, groups);
@@ -550,7 +538,7 @@ hipError_t norm_bwd(const NormArgs& args, hipStream_t stream)
 int norm_bwd_groups(int rows, int D)
 {
     // the larger of the two types' numbers, so that one workspace fits both
-    const int f = bwd_groups(rows, shape_of(D, false)), h = bwd_groups(rows, shape_of(D, true));
+    const int f = bwd_groups(rows, bwd_shape(D, false)), h = bwd_groups(rows, bwd_shape(D, true));
     return f > h ? f : h;
 }
 

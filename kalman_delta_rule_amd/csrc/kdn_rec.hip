@@ -14,10 +14,12 @@
 // outputs stored.  Inputs are read once and outputs written once.
 //
 // Tiles of the same channels are chained through the workspace (tile_carry):
-// each publishes its (A, U), and the last of 16 the value behind it.  A tile's
-// start is that value of the group before, with the (A, U) of the tiles between
-// applied in token order: always the same operations, so results do not depend
-// on timing.  A word is 4 or 8 bytes, stored and loaded whole (relaxed, agent
+// each publishes its (A, U), the last of 8 that of the whole group, and the last
+// of 64 the value behind it.  A tile's start is that value of the 64 before, with
+// the (A, U) of the groups and tiles between applied in token order: always
+// the same operations, so results do not depend on timing, and few steps that
+// wait for one another (one in 64 tiles, about 2 us each, the time of a word
+// from one XCD to the next).  A word is 4 or 8 bytes, stored and loaded whole (relaxed, agent
 // scope: it may cross to another XCD's L2), and is its own flag: a launch before
 // sets them to all ones, which no published word is (a NaN is made canonical).
 //
@@ -33,41 +35,50 @@ namespace {
 
 constexpr int kChk = KDN_REC_CHECKPOINT;
 constexpr int kTile = 128;   // tokens of a tile
-constexpr int kGroup = 16;   // tiles of a group of the chain
+constexpr int kGroup = 8;    // tiles of a group of the chain, groups of a block
+constexpr int kBlock = kGroup * kGroup;
 constexpr int kPolls = 1 << 21;
 
 // ---- the chain through the workspace ----------------------------------------
 
 struct Chain {
-    uint32_t* ticket;
-    unsigned long long* spans;  // [tiles][columns]: (A, U) of a tile
-    uint32_t* starts;           // [groups][columns]: the value behind a group
+    uint32_t* tickets;          // [kQueues], kTicketWords apart
+    unsigned long long* spans;   // [tiles][columns]: (A, U) of a tile
+    unsigned long long* groups;  // [tiles / kGroup][columns]: (A, U) of a group
+    uint32_t* starts;            // [tiles / kBlock][columns]: the value behind a block
     int tiles, columns;
+    int queues;
 };
 
-__host__ __device__ inline Chain chain_at(void* ws, int tiles, int columns)
+constexpr int kQueues = 8;         // one for each XCD
+constexpr int kTicketWords = 32;   // a cache line a counter
+
+inline Chain chain_at(void* ws, int tiles, int columns, int queues)
 {
     Chain c;
     c.tiles = tiles;
     c.columns = columns;
-    c.ticket = static_cast<uint32_t*>(ws);
-    c.spans = reinterpret_cast<unsigned long long*>(static_cast<char*>(ws) + 16);
-    c.starts = reinterpret_cast<uint32_t*>(c.spans + (size_t)tiles * columns);
+    c.queues = queues;
+    c.tickets = static_cast<uint32_t*>(ws);
+    c.spans = reinterpret_cast<unsigned long long*>(c.tickets + kQueues * kTicketWords);
+    c.groups = c.spans + (size_t)tiles * columns;
+    c.starts = reinterpret_cast<uint32_t*>(c.groups + (size_t)(tiles / kGroup) * columns);
     return c;
 }
 
-// bytes behind the ticket
-inline size_t chain_words(int tiles, int columns)
+// 16-byte units of the workspace, and of the tickets at its front
+constexpr size_t kTicketUnits = kQueues * kTicketWords / 4;
+inline size_t chain_units(int tiles, int columns)
 {
-    const size_t groups = (tiles + kGroup - 1) / kGroup;
-    return ((size_t)tiles * columns * 2 + groups * columns + 3) / 4 * 4;
+    const size_t words = ((size_t)tiles + tiles / kGroup) * 2 + tiles / kBlock;
+    return kTicketUnits + (words * columns + 3) / 4;
 }
 
 __global__ __launch_bounds__(256) void rec_clear_kernel(uint4* ws, size_t n)
 {
     const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
     if (i < n)
-        ws[i] = i ? uint4{~0u, ~0u, ~0u, ~0u} : uint4{0, 0, 0, 0};
+        ws[i] = i < kTicketUnits ? uint4{0, 0, 0, 0} : uint4{~0u, ~0u, ~0u, ~0u};
 }
 
 __device__ __forceinline__ uint32_t word_of(float v)
@@ -111,35 +122,118 @@ __device__ __forceinline__ float apply(float A, float U, float carry)
     return A == 0.f ? U : fmaf(A, carry, U);
 }
 
-// What tile `k` in chain order starts from, for the column `col` of this lane,
-// whose own span is (A, U); publishes what later tiles need.
-__device__ __forceinline__ float tile_carry(const Chain& ch, int k, int col, float A, float U)
+// The spans [kGroup - 1][columns] at p up to the n-th, as they are now.
+__device__ __forceinline__ void peek_spans(unsigned long long (&w)[kGroup - 1],
+                                           const unsigned long long* p, int n, int columns)
 {
-    const int g = k / kGroup, j = k - g * kGroup;
-    const bool last = j == kGroup - 1;
-    unsigned long long* spans = ch.spans + (size_t)g * kGroup * ch.columns + col;
-    if (!last && k + 1 < ch.tiles)
-        publish(spans + (size_t)j * ch.columns, A, U);
-    unsigned long long w[kGroup - 1];
 #pragma unroll
     for (int i = 0; i < kGroup - 1; ++i)
-        w[i] = i < j ? peek(spans + (size_t)i * ch.columns) : 0;
+        w[i] = i < n ? peek(p + (size_t)i * columns) : 0;
+}
+
+__device__ __forceinline__ float2 span_of(unsigned long long w)
+{
+    return float2{__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32))};
+}
+
+// span a, then span b
+__device__ __forceinline__ float2 join(float2 a, float2 b)
+{
+    return float2{b.x == 0.f ? 0.f : a.x * b.x, apply(b.x, b.y, a.y)};
+}
+
+// For column `col` of this lane and tile `k` in chain order, whose span is
+// `own`: the tiles before it in its group as one span.  Publishes its own span
+// and, from a group's last tile, the group's.
+__device__ __forceinline__ float2 chain_near(const Chain& ch, int k, int col, float2 own)
+{
+    const int g = k / kGroup, j = k % kGroup;
+    const bool more = k + 1 < ch.tiles;
+    unsigned long long* spans = ch.spans + (size_t)(k - j) * ch.columns + col;
+    if (j != kGroup - 1 && more)
+        publish(spans + (size_t)j * ch.columns, own.x, own.y);
+    unsigned long long w[kGroup - 1];
+    peek_spans(w, spans, j, ch.columns);
+    float2 near{1.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kGroup - 1; ++i)
+        if (i < j)
+            near = join(near, span_of(await(spans + (size_t)i * ch.columns, w[i])));
+    if (j == kGroup - 1 && g % kGroup != kGroup - 1 && more) {
+        const float2 all = join(near, own);
+        publish(ch.groups + (size_t)g * ch.columns + col, all.x, all.y);
+    }
+    return near;
+}
+
+// What the tile's group starts from.
+__device__ __forceinline__ float chain_far(const Chain& ch, int k, int col)
+{
+    const int b = k / kBlock, g = k / kGroup, j = g % kGroup;
+    const unsigned long long* groups = ch.groups + (size_t)(g - j) * ch.columns + col;
+    unsigned long long w[kGroup - 1];
+    peek_spans(w, groups, j, ch.columns);
     float carry = 0.f;
-    if (g) {
-        const uint32_t* p = ch.starts + (size_t)(g - 1) * ch.columns + col;
-        carry = __uint_as_float(await(p, peek(p)));
+    if (b) {
+        const uint32_t* start = ch.starts + (size_t)(b - 1) * ch.columns + col;
+        carry = __uint_as_float(await(start, peek(start)));
     }
 #pragma unroll
-    for (int i = 0; i < kGroup - 1; ++i) {
+    for (int i = 0; i < kGroup - 1; ++i)
         if (i < j) {
-            const unsigned long long v = await(spans + (size_t)i * ch.columns, w[i]);
-            carry = apply(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)), carry);
+            const float2 v = span_of(await(groups + (size_t)i * ch.columns, w[i]));
+            carry = apply(v.x, v.y, carry);
         }
-    }
-    if (last && k + 1 < ch.tiles)
-        publish(ch.starts + (size_t)g * ch.columns + col, apply(A, U, carry));
     return carry;
 }
+
+// From a block's last tile: the value behind it, which starts the next block.
+__device__ __forceinline__ void chain_block(const Chain& ch, int k, int col, float behind)
+{
+    if (k % kBlock == kBlock - 1 && k + 1 < ch.tiles)
+        publish(ch.starts + (size_t)(k / kBlock) * ch.columns + col, behind);
+}
+
+// A tile's part in the chain, by its first two waves, a lane a column; all
+// threads call it.  In: the spans of its runs; out: those of the tile before
+// each run, the span `near` of the tiles before it in the group and the value
+// `far` that the group starts from.  REVERSE: the last run is the first.
+template <int RUNS, int CT, bool REVERSE>
+struct Link {
+    float2 runs[RUNS][CT];
+    float2 near[CT], own[CT];
+    float far[CT];
+
+    __device__ __forceinline__ void work(const Chain& ch, int k, int col)
+    {
+        const int wave = threadIdx.x >> 6, s = threadIdx.x & 63;
+        if (wave == 0 && s < CT) {
+            float2 t{1.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < RUNS; ++i) {
+                float2& r = runs[REVERSE ? RUNS - 1 - i : i][s];
+                const float2 g = r;
+                r = t;
+                t = join(t, g);
+            }
+            own[s] = t;
+            near[s] = ch.tiles > 1 ? chain_near(ch, k, col + s, t) : float2{1.f, 0.f};
+        } else if (wave == 1 && s < CT) {
+            far[s] = ch.tiles > 1 ? chain_far(ch, k, col + s) : 0.f;
+        }
+    }
+    // after a barrier: what run `run` starts from in the tile's column s
+    __device__ __forceinline__ float start(int run, int s) const
+    {
+        return apply(runs[run][s].x, runs[run][s].y, apply(near[s].x, near[s].y, far[s]));
+    }
+    __device__ __forceinline__ void finish(const Chain& ch, int k, int col) const
+    {
+        const int s = threadIdx.x;
+        if (s < CT && ch.tiles > 1)
+            chain_block(ch, k, col + s, apply(own[s].x, own[s].y, apply(near[s].x, near[s].y, far[s])));
+    }
+};
 
 // ---- values ------------------------------------------------------------------
 
@@ -165,6 +259,25 @@ __device__ __forceinline__ void store_at(char* base, uint32_t off, const float (
     *reinterpret_cast<Pack<E, V>*>(base + off) = p;
 }
 
+// V values of each of a run's L tokens: rows `stride` bytes apart from `base`, the
+// run's first at row `first`, the lane's values at byte `col` of a row.  Where the
+// tile reaches behind the row's end (`rows` < kTile), the last row is repeated.
+template <typename E, int V, int L>
+__device__ __forceinline__ void load_run(Pack<E, V> (&r)[L], const char* base, uint32_t stride,
+                                         int first, uint32_t col, int rows)
+{
+    if (rows >= kTile) {
+        const uint32_t off = first * stride + col;
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+            r[i] = load_at<E, V>(base + (size_t)i * stride, off);
+    } else if (rows > 0) {
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+            r[i] = load_at<E, V>(base, min(first + i, rows - 1) * stride + col);
+    }
+}
+
 // alpha and 1 - alpha.  From a pre-activation the smaller of the two is formed
 // as e / (1 + e), e = exp(-|a|) <= 1, with full relative accuracy, the larger
 // as one minus it, off by half a step: with alpha near one its error is
@@ -175,8 +288,8 @@ __device__ __forceinline__ void gate_of(float a, float& alpha, float& rest)
     if constexpr (PRE) {
         const float e = __builtin_amdgcn_exp2f(fabsf(a) * -kLog2e);
         const float s = e * rcp(1.f + e), l = 1.f - s;
-        alpha = a >= 0.f ? l : a < 0.f ? s : a;
-        rest = a >= 0.f ? s : a < 0.f ? l : a;
+        alpha = a < 0.f ? s : l;
+        rest = a < 0.f ? l : s;
     } else {
         alpha = a;
         rest = 1.f - a;
@@ -233,22 +346,42 @@ struct Tile {
     int col;        // first column of the chain
 };
 
-// The tile of this workgroup: by ticket where tiles are chained.
+// The tile of this workgroup.  Chained tiles are taken by ticket, from one queue a
+// XCD (workgroups are dealt to the XCDs in turn), each with its own share of
+// the columns, adjacent ones, so that the pieces of a row that one XCD reads
+// lie together, and its own counter.  Within a queue all tiles of a time come
+// before the next time's.  A workgroup that finds its queue empty goes on to the
+// next one: there are as many workgroups as tiles, so each gets one.
 template <int CT>
 __device__ __forceinline__ Tile take_tile(const RecArgs& a, const Chain& ch, int ctiles, bool backward)
 {
-    __shared__ uint32_t s_ticket;
-    uint32_t id = blockIdx.x;
+    const uint32_t per = a.B * ctiles;
+    uint32_t k = 0, r = blockIdx.x;
     if (ch.tiles > 1) {
-        if (threadIdx.x == 0)
-            s_ticket = __hip_atomic_fetch_add(ch.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __shared__ uint32_t s_queue, s_ticket;
+        if (threadIdx.x == 0) {
+            uint32_t q = blockIdx.x % ch.queues, i = 0;
+            for (int n = 0; n < ch.queues; ++n) {
+                const uint32_t c0 = q * per / ch.queues, c1 = (q + 1) * per / ch.queues;
+                i = __hip_atomic_fetch_add(ch.tickets + q * kTicketWords, 1u, __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_AGENT);
+                if (i < (c1 - c0) * ch.tiles)
+                    break;
+                q = q + 1 == (uint32_t)ch.queues ? 0 : q + 1;
+            }
+            s_queue = q;
+            s_ticket = i;
+        }
         __syncthreads();
-        id = s_ticket;
+        // the same for the whole wave: addresses from here on are scalar
+        const uint32_t q = __builtin_amdgcn_readfirstlane(s_queue);
+        const uint32_t i = __builtin_amdgcn_readfirstlane(s_ticket);
+        const uint32_t c0 = q * per / ch.queues, n = (q + 1) * per / ch.queues - c0;
+        k = i / n;
+        r = c0 + (i - k * n);
     }
-    const int per = a.B * ctiles;  // all tiles of a time come before the next time's
     Tile t;
-    t.k = id / per;
-    const int r = id - t.k * per;
+    t.k = k;
     t.b = r / ctiles;
     t.c0 = (r - t.b * ctiles) * CT;
     t.col = r * CT;
@@ -265,8 +398,7 @@ __global__ __launch_bounds__(256, 4) void rec_fwd_kernel(RecArgs a, Chain ch, in
     typedef typename std::conditional<PRE, IO, float>::type GT;
     constexpr int L = 16, RUNS = 8, CT = 32 * V;
     __shared__ Marks marks;
-    __shared__ float2 spans[RUNS][CT];
-    __shared__ float starts[RUNS][CT];
+    __shared__ Link<RUNS, CT, false> link;
 
     const Tile tile = take_tile<CT>(a, ch, ctiles, false);
     const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
@@ -277,23 +409,11 @@ __global__ __launch_bounds__(256, 4) void rec_fwd_kernel(RecArgs a, Chain ch, in
 
     Pack<GT, V> ra[L];
     Pack<IO, V> rx[L];
-    if (a.T) {
-        // rows behind the last one repeat it
-        const char* pa = static_cast<const char*>(a.a) + row0 * a.as * sizeof(GT);
-        const char* px = static_cast<const char*>(a.x) + row0 * a.xs * sizeof(IO);
-        const uint32_t sa = (uint32_t)a.as * sizeof(GT), sx = (uint32_t)a.xs * sizeof(IO);
-        const uint32_t last = min(a.T - 1 - tile.t0, kTile - 1);
-        const uint32_t ea = last * sa + c * sizeof(GT), ex = last * sx + c * sizeof(IO);
-        uint32_t oa = min(first * sa + c * (uint32_t)sizeof(GT), ea);
-        uint32_t ox = min(first * sx + c * (uint32_t)sizeof(IO), ex);
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            ra[i] = load_at<GT, V>(pa, oa);
-            rx[i] = load_at<IO, V>(px, ox);
-            oa = min(oa + sa, ea);
-            ox = min(ox + sx, ex);
-        }
-    }
+    const int rows = a.T - tile.t0;
+    load_run<GT, V, L>(ra, static_cast<const char*>(a.a) + row0 * a.as * sizeof(GT),
+                       (uint32_t)a.as * sizeof(GT), first, c * sizeof(GT), rows);
+    load_run<IO, V, L>(rx, static_cast<const char*>(a.x) + row0 * a.xs * sizeof(IO),
+                       (uint32_t)a.xs * sizeof(IO), first, c * sizeof(IO), rows);
 
     mark_tile<256>(marks, a, tile.b, tile.t0);
     const int valid = token_limit(a) - (tile.t0 + first);  // tokens of the run, if positive
@@ -342,32 +462,16 @@ __global__ __launch_bounds__(256, 4) void rec_fwd_kernel(RecArgs a, Chain ch, in
     }
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        spans[run][lane * V + v] = float2{A[v], U[v]};
+        link.runs[run][lane * V + v] = float2{A[v], U[v]};
     __syncthreads();
-
-    if (threadIdx.x < CT) {
-        const int s = threadIdx.x;
-        float2 g[RUNS];
-        float TA = 1.f, TU = 0.f;
-#pragma unroll
-        for (int r = 0; r < RUNS; ++r) {
-            g[r] = spans[r][s];
-            TU = apply(g[r].x, g[r].y, TU);
-            TA = g[r].x == 0.f ? 0.f : TA * g[r].x;
-        }
-        float carry = ch.tiles > 1 ? tile_carry(ch, tile.k, tile.col + s, TA, TU) : 0.f;
-#pragma unroll
-        for (int r = 0; r < RUNS; ++r) {
-            starts[r][s] = carry;
-            carry = apply(g[r].x, g[r].y, carry);
-        }
-    }
+    link.work(ch, tile.k, tile.col);
     __syncthreads();
+    link.finish(ch, tile.k, tile.col);
 
     float h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        h[v] = starts[run][lane * V + v];
+        h[v] = link.start(run, lane * V + v);
     if (a.ckpt && first % kChk == 0 && valid > 0) {
         const int blocks = (a.T + kChk - 1) / kChk;
         float* p = a.ckpt + ((size_t)tile.b * blocks + (tile.t0 + first) / kChk) * a.D + c;
@@ -377,15 +481,14 @@ __global__ __launch_bounds__(256, 4) void rec_fwd_kernel(RecArgs a, Chain ch, in
     }
     char* ph = static_cast<char*>(a.h) + row0 * a.D * sizeof(IO);
     const uint32_t sh = (uint32_t)a.D * sizeof(IO);
-    uint32_t oh = first * sh + c * (uint32_t)sizeof(IO);
+    const uint32_t oh = first * sh + c * (uint32_t)sizeof(IO);
     if (plain) {
 #pragma unroll
         for (int i = 0; i < L; ++i) {
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 h[v] = fmaf(al[i][v], h[v], u[i][v]);
-            store_at<IO, V>(ph, oh, h);
-            oh += sh;
+            store_at<IO, V>(ph + (size_t)i * sh, oh, h);
         }
     } else {
 #pragma unroll
@@ -401,8 +504,7 @@ __global__ __launch_bounds__(256, 4) void rec_fwd_kernel(RecArgs a, Chain ch, in
                 if (e && a.h_T)
                     a.h_T[(size_t)marks.end[first + i] * a.D + c + v] = h[v];
             }
-            store_at<IO, V>(ph, oh, h);
-            oh += sh;
+            store_at<IO, V>(ph + (size_t)i * sh, oh, h);
         }
     }
 
@@ -430,8 +532,8 @@ __global__ __launch_bounds__(512, 4) void rec_bwd_kernel(RecArgs a, Chain ch, in
     typedef typename std::conditional<PRE, IO, float>::type GT;
     constexpr int L = 8, RUNS = 16, CT = 32 * V, PER = kChk / L;  // runs of a checkpoint
     __shared__ Marks marks;
-    __shared__ float2 spans[RUNS][CT], rspans[RUNS][CT];
-    __shared__ float starts[RUNS][CT], rstarts[RUNS][CT];
+    __shared__ float2 spans[RUNS][CT];
+    __shared__ Link<RUNS, CT, true> link;
 
     const Tile tile = take_tile<CT>(a, ch, ctiles, true);
     const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
@@ -441,28 +543,13 @@ __global__ __launch_bounds__(512, 4) void rec_bwd_kernel(RecArgs a, Chain ch, in
 
     Pack<GT, V> ra[L];
     Pack<IO, V> rx[L], rd[L];
-    if (a.T) {
-        const char* pa = static_cast<const char*>(a.a) + row0 * a.as * sizeof(GT);
-        const char* px = static_cast<const char*>(a.x) + row0 * a.xs * sizeof(IO);
-        const char* pd = static_cast<const char*>(a.dh) + row0 * a.D * sizeof(IO);
-        const uint32_t sa = (uint32_t)a.as * sizeof(GT), sx = (uint32_t)a.xs * sizeof(IO),
-                       sd = (uint32_t)a.D * sizeof(IO);
-        const uint32_t last = min(a.T - 1 - tile.t0, kTile - 1);
-        const uint32_t ea = last * sa + c * sizeof(GT), ex = last * sx + c * sizeof(IO),
-                       ed = last * sd + c * sizeof(IO);
-        uint32_t oa = min(first * sa + c * (uint32_t)sizeof(GT), ea);
-        uint32_t ox = min(first * sx + c * (uint32_t)sizeof(IO), ex);
-        uint32_t od = min(first * sd + c * (uint32_t)sizeof(IO), ed);
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            ra[i] = load_at<GT, V>(pa, oa);
-            rx[i] = load_at<IO, V>(px, ox);
-            rd[i] = load_at<IO, V>(pd, od);
-            oa = min(oa + sa, ea);
-            ox = min(ox + sx, ex);
-            od = min(od + sd, ed);
-        }
-    }
+    const int rows = a.T - tile.t0;
+    load_run<GT, V, L>(ra, static_cast<const char*>(a.a) + row0 * a.as * sizeof(GT),
+                       (uint32_t)a.as * sizeof(GT), first, c * sizeof(GT), rows);
+    load_run<IO, V, L>(rx, static_cast<const char*>(a.x) + row0 * a.xs * sizeof(IO),
+                       (uint32_t)a.xs * sizeof(IO), first, c * sizeof(IO), rows);
+    load_run<IO, V, L>(rd, static_cast<const char*>(a.dh) + row0 * a.D * sizeof(IO),
+                       (uint32_t)a.D * sizeof(IO), first, c * sizeof(IO), rows);
 
     mark_tile<512>(marks, a, tile.b, tile.t0);
     const int valid = token_limit(a) - (tile.t0 + first);
@@ -533,91 +620,46 @@ __global__ __launch_bounds__(512, 4) void rec_bwd_kernel(RecArgs a, Chain ch, in
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         spans[run][lane * V + v] = float2{A[v], U[v]};
-        rspans[run][lane * V + v] = float2{RA[v], RU[v]};
+        link.runs[run][lane * V + v] = float2{RA[v], RU[v]};
     }
     __syncthreads();
 
-    const int wave = threadIdx.x >> 6, s = threadIdx.x & 63;
-    if (wave == 0 && s < CT) {
-        float TA = 1.f, TU = 0.f;
-#pragma unroll
-        for (int r = RUNS - 1; r >= 0; --r) {
-            const float2 g = rspans[r][s];
-            TU = apply(g.x, g.y, TU);
-            TA = g.x == 0.f ? 0.f : TA * g.x;
-        }
-        float carry = ch.tiles > 1 ? tile_carry(ch, tile.k, tile.col + s, TA, TU) : 0.f;
-#pragma unroll
-        for (int r = RUNS - 1; r >= 0; --r) {
-            const float2 g = rspans[r][s];
-            rstarts[r][s] = carry;
-            carry = apply(g.x, g.y, carry);
-        }
-    } else if ((wave == 1 || wave == 2) && s < CT) {
-        // the states before the runs of checkpoint `wave` - 1 of the tile
-        const int blocks = (a.T + kChk - 1) / kChk, blk = tile.t0 / kChk + wave - 1;
-        const int cs = min(tile.c0 + s / V * V, a.D - V) + s % V;
-        float h = blk < blocks ? a.ckpt[((size_t)tile.b * blocks + blk) * a.D + cs] : 0.f;
-#pragma unroll
-        for (int r = 0; r < PER; ++r) {
-            const float2 g = spans[(wave - 1) * PER + r][s];
-            starts[(wave - 1) * PER + r][s] = h;
-            h = apply(g.x, g.y, h);
-        }
-    }
-    __syncthreads();
+    link.work(ch, tile.k, tile.col);
 
-    float h[V], prev[L][V], g[V];
+    // the states again, meanwhile: from the checkpoint over the runs between, then of
+    // each token only what its gradients take, h_{t-1}, or h_{t-1} - x_t
+    float h[V], part[L][V], g[V];
+    const int blocks = (a.T + kChk - 1) / kChk, blk = min((tile.t0 + first) / kChk, blocks - 1);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        h[v] = starts[run][lane * V + v];
-        g[v] = rstarts[run][lane * V + v];
-    }
+    for (int v = 0; v < V; ++v)
+        h[v] = valid > 0 ? a.ckpt[((size_t)tile.b * blocks + blk) * a.D + c + v] : 0.f;
+    for (int r = run / PER * PER; r < run; ++r)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            h[v] = apply(spans[r][lane * V + v].x, spans[r][lane * V + v].y, h[v]);
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (!plain && (start >> i & 1))
+                h[v] = a.h0 ? a.h0[(size_t)marks.start[first + i] * a.D + c + v] : 0.f;
+            const float x = to_f32(rx[i].v[v]);
+            part[i][v] = BLEND ? h[v] - x : h[v];
+            h[v] = fmaf(al[i][v], h[v], BLEND ? rest[i][v] * x : x);
+        }
+    __syncthreads();
+    link.finish(ch, tile.k, tile.col);
+
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        g[v] = link.start(run, lane * V + v);
     char* px = static_cast<char*>(a.dx) + row0 * a.D * sizeof(IO);
     char* pa = static_cast<char*>(a.da) + row0 * a.D * sizeof(GT);
     const uint32_t sx = (uint32_t)a.D * sizeof(IO), sa = (uint32_t)a.D * sizeof(GT);
-    const uint32_t ox = c * (uint32_t)sizeof(IO), oa = c * (uint32_t)sizeof(GT);
-    // the outputs of token i, from its adjoint
-    auto token = [&](int i) {
-        float dx[V], da[V];
+    const uint32_t ox = first * sx + c * (uint32_t)sizeof(IO), oa = first * sa + c * (uint32_t)sizeof(GT);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float lam = to_f32(rd[i].v[v]) + g[v];
-            const float part = BLEND ? prev[i][v] - to_f32(rx[i].v[v]) : prev[i][v];
-            dx[v] = BLEND ? lam * rest[i][v] : lam;
-            da[v] = lam * part;
-            if constexpr (PRE)
-                da[v] *= al[i][v] * rest[i][v];
-            g[v] = al[i][v] * lam;
-        }
-        store_at<IO, V>(px, (first + i) * sx + ox, dx);
-        store_at<GT, V>(pa, (first + i) * sa + oa, da);
-    };
-    if (plain) {
-#pragma unroll
-        for (int i = 0; i < L; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                prev[i][v] = h[v];
-                const float x = to_f32(rx[i].v[v]);
-                h[v] = fmaf(al[i][v], h[v], BLEND ? rest[i][v] * x : x);
-            }
-#pragma unroll
-        for (int i = L - 1; i >= 0; --i)
-            token(i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < L; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (start >> i & 1)
-                    h[v] = a.h0 ? a.h0[(size_t)marks.start[first + i] * a.D + c + v] : 0.f;
-                prev[i][v] = h[v];
-                const float x = to_f32(rx[i].v[v]);
-                h[v] = fmaf(al[i][v], h[v], BLEND ? rest[i][v] * x : x);
-            }
-#pragma unroll
-        for (int i = L - 1; i >= 0; --i) {
+    for (int i = L - 1; i >= 0; --i) {
+        if (!plain) {
             if (i >= valid)
                 continue;
             if (end >> i & 1) {
@@ -625,12 +667,22 @@ __global__ __launch_bounds__(512, 4) void rec_bwd_kernel(RecArgs a, Chain ch, in
                 for (int v = 0; v < V; ++v)
                     g[v] = a.dh_T ? a.dh_T[(size_t)marks.end[first + i] * a.D + c + v] : 0.f;
             }
-            token(i);
-            if ((start >> i & 1) && a.dh0) {
+        }
+        float dx[V], da[V];
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    a.dh0[(size_t)marks.start[first + i] * a.D + c + v] = g[v];
-            }
+        for (int v = 0; v < V; ++v) {
+            const float lam = to_f32(rd[i].v[v]) + g[v];
+            dx[v] = BLEND ? lam * rest[i][v] : lam;
+            g[v] = al[i][v] * lam;
+            // dalpha times alpha (1 - alpha), of the factors at hand
+            da[v] = PRE ? g[v] * rest[i][v] * part[i][v] : lam * part[i][v];
+        }
+        store_at<IO, V>(px + (size_t)i * sx, ox, dx);
+        store_at<GT, V>(pa + (size_t)i * sa, oa, da);
+        if (!plain && (start >> i & 1) && a.dh0) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                a.dh0[(size_t)marks.start[first + i] * a.D + c + v] = g[v];
         }
     }
 
@@ -669,9 +721,10 @@ hipError_t launch(const RecArgs& a, bool backward, hipStream_t stream)
 {
     const int ctiles = (a.D + 32 * V - 1) / (32 * V), tiles = tiles_of(a.T);
     const int columns = a.B * ctiles * 32 * V;
-    const Chain ch = chain_at(a.ws, tiles, columns);
+    // with fewer columns than XCDs some would have none of their own
+    const Chain ch = chain_at(a.ws, tiles, columns, a.B * ctiles < kQueues ? 1 : kQueues);
     if (tiles > 1) {
-        const size_t n = 1 + chain_words(tiles, columns) / 4;
+        const size_t n = chain_units(tiles, columns);
         rec_clear_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(static_cast<uint4*>(a.ws), n);
     }
     const unsigned grid = (unsigned)((size_t)tiles * a.B * ctiles);
@@ -704,7 +757,7 @@ size_t rec_workspace_bytes(int B, int T, int D)
     const int tiles = tiles_of(T), ct = D == 1 ? 32 : 64;
     if (tiles == 1)
         return 0;
-    return 16 + chain_words(tiles, B * ((D + ct - 1) / ct) * ct) * 4;
+    return chain_units(tiles, B * ((D + ct - 1) / ct) * ct) * 16;
 }
 
 hipError_t launch_rec_fwd(const RecArgs& a, bool bf, hipStream_t stream)
