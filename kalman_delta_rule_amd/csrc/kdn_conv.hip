@@ -82,7 +82,7 @@ template <int VE>
 struct Place {
     int lane, run, runs, length;  // length: tokens of a run
     int c;                        // first channel
-    long long m0, m;              // first token of the tile, of the run
+    int m0, m;                    // first token of the tile, of the run (B T < 2^31)
 
     __device__ __forceinline__ Place(const Plan& p, int D)
     {
@@ -93,8 +93,8 @@ struct Place {
         length = p.batches * kBatch;
         // lanes behind the last channel repeat the last ones
         c = min(((ct << p.lanes_log2) + lane) * VE, D - VE);
-        m0 = (long long)tt * runs * length;
-        m = m0 + (long long)run * length;
+        m0 = tt * runs * length;
+        m = m0 + run * length;
     }
 };
 
@@ -104,37 +104,38 @@ struct Marks {
     int start[kMostTokens + 8], end[kMostTokens + 8];
 };
 
-__device__ __forceinline__ void mark_tokens(Marks& k, const ConvArgs& a, long long first, int count)
+__device__ __forceinline__ void mark_tokens(Marks& k, const ConvArgs& a, int first, int count)
 {
-    const long long M = (long long)a.B * a.T;
+    const int M = a.B * a.T;
     if (a.cu) {
         for (int i = threadIdx.x; i < count; i += 256)
             k.start[i] = k.end[i] = -1;
         __syncthreads();
         for (int n = threadIdx.x; n < a.N; n += 256) {
             const int p = a.cu[n], q = a.cu[n + 1];
-            if (p < q && p >= first && p < first + count)
+            if (p < 0 || p >= q)
+                continue;
+            if (p >= first && p - first < count)
                 k.start[p - first] = n;
-            if (p < q && q - 1 >= first && q - 1 < first + count)
+            if (q - 1 >= first && q - 1 - first < count)
                 k.end[q - 1 - first] = n;
         }
     } else {
         for (int i = threadIdx.x; i < count; i += 256) {
-            const long long m = first + i;
+            const int m = first + i;
             const bool in = m >= 0 && m < M;
-            const uint32_t n = in ? (uint32_t)m / (uint32_t)a.T : 0;  // M < 2^31
-            const int t = in ? (int)((uint32_t)m - n * (uint32_t)a.T) : -1;
-            k.start[i] = t == 0 ? (int)n : -1;
-            k.end[i] = t == a.T - 1 ? (int)n : -1;
+            const int n = in ? (int)((uint32_t)m / (uint32_t)a.T) : 0, t = m - n * a.T;
+            k.start[i] = in && t == 0 ? n : -1;
+            k.end[i] = in && t == a.T - 1 ? n : -1;
         }
     }
     __syncthreads();
 }
 
 // tokens from this one on belong to no sequence
-__device__ __forceinline__ long long token_limit(const ConvArgs& a)
+__device__ __forceinline__ int token_limit(const ConvArgs& a)
 {
-    return a.cu ? min(max(a.cu[a.N], 0), a.T) : (long long)a.B * a.T;
+    return a.cu ? min(max(a.cu[a.N], 0), a.T) : a.B * a.T;
 }
 
 // whether any of marks [i, i + count) is set, for this thread's run (`lanes`
@@ -205,55 +206,51 @@ struct Filter {
     }
 };
 
-// Rows of VE channels from token m on, one after another; tokens outside
-// [0, M) repeat the nearest.
+// Rows of VE channels of [tokens, `stride` apart].
 template <typename IO, int VE>
 struct Rows {
-    const IO* p;
-    long long m, M, step;
+    const IO* base;
+    size_t stride;
+    int last;  // token
 
-    __device__ __forceinline__ Rows(const void* base, long long stride, long long first,
-                                    long long total, int c)
-        : m(first), M(total), step(stride)
+    __device__ __forceinline__ Rows(const void* x, long long stride, int tokens, int c)
+        : base(static_cast<const IO*>(x) + c), stride(stride), last(tokens - 1)
     {
-        const long long at = min(max(first, 0ll), total - 1);
-        p = static_cast<const IO*>(base) + at * stride + c;
     }
-    __device__ __forceinline__ Vec<IO, VE> next()
+    __device__ __forceinline__ const IO* at(int m) const { return base + m * stride; }
+    // tokens outside repeat the nearest
+    __device__ __forceinline__ Vec<IO, VE> near(int m) const
     {
-        const Vec<IO, VE> r = load_vec<IO, VE>(p);
-        p += m >= 0 && m + 1 < M ? step : 0;
-        ++m;
-        return r;
+        return load_vec<IO, VE>(at(min(max(m, 0), last)));
     }
 };
 
 // ---- forward ------------------------------------------------------------------
 
-template <typename IO, int VE, int W>
+template <typename IO, int VE, int W, bool SILU>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, Plan plan)
 {
     __shared__ Marks marks;
     const Place<VE> at(plan, a.D);
-    const long long M = (long long)a.B * a.T;
+    const int M = a.B * a.T;
     Filter<IO, VE, W> f;
     f.init(a, at.c);
 
     if (M) {
-        Rows<IO, VE> rows(a.x, a.xs, at.m - (W - 1), M, at.c);
+        const Rows<IO, VE> rows(a.x, a.xs, M, at.c);
         Vec<IO, VE> before[W - 1], next[kBatch];
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
-            before[k] = rows.next();
+            before[k] = rows.near(at.m - (W - 1) + k);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
-            next[i] = rows.next();
+            next[i] = rows.near(at.m + i);
         mark_tokens(marks, a, at.m0 - (W - 1), at.runs * at.length + W - 1);
         const int base = at.run * at.length;  // mark of the first token before the run
-        const long long limit = token_limit(a);
+        const int limit = token_limit(a);
+        // (a run at the row's front has a mark, so a plain one has tokens all around it)
         const bool plain = !__any(at.m + at.length > limit ||
                                   any_mark(marks, base, at.length + W - 1, at.lane, 1 << plan.lanes_log2));
-        IO* y = static_cast<IO*>(a.y) + at.m * a.D + at.c;
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
             float x[VE];
@@ -262,43 +259,56 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, Plan plan)
                 f.from_state(a, marks.start[base + k], at.c);
             f.push(x);
         }
-        for (int q = 0; q < plan.batches; ++q) {
-            Vec<IO, VE> now[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                now[i] = next[i];
-            if (q + 1 < plan.batches) {
+        auto walk = [&](auto is_plain) {
+            constexpr bool PLAIN = decltype(is_plain)::value;
+            const IO* ahead = rows.at(at.m + kBatch);
+            IO* y = static_cast<IO*>(a.y) + (size_t)at.m * a.D + at.c;
+            for (int q = 0; q < plan.batches; ++q) {
+                Vec<IO, VE> now[kBatch];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i)
-                    next[i] = rows.next();
+                    now[i] = next[i];
+                if (q + 1 < plan.batches) {
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        next[i] = PLAIN ? load_vec<IO, VE>(ahead) : rows.near(at.m + (q + 1) * kBatch + i);
+                        ahead += a.xs;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i, y += a.D) {
+                    const int k = base + W - 1 + q * kBatch + i;  // mark of this token
+                    float x[VE], z[VE];
+                    widen<IO, VE>(now[i], x);
+                    if constexpr (!PLAIN) {
+                        if (at.m + q * kBatch + i >= limit)
+                            continue;
+                        if (marks.start[k] >= 0)
+                            f.from_state(a, marks.start[k], at.c);
+                    }
+                    f.z(x, z);
+                    if constexpr (SILU) {
+#pragma unroll
+                        for (int j = 0; j < VE; ++j)
+                            z[j] = silu(z[j]);
+                    }
+                    store_vec<IO, VE>(y, z);
+                    f.push(x);
+                    if constexpr (!PLAIN) {
+                        if (marks.end[k] >= 0 && a.state_T) {
+                            IO* s = static_cast<IO*>(a.state_T) + (size_t)marks.end[k] * (W - 1) * a.D + at.c;
+#pragma unroll
+                            for (int r = 0; r < W - 1; ++r)
+                                store_vec<IO, VE>(s + (size_t)r * a.D, f.win[r]);
+                        }
+                    }
+                }
             }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int k = base + W - 1 + q * kBatch + i;  // mark of this token
-                float x[VE], z[VE];
-                widen<IO, VE>(now[i], x);
-                if (!plain) {
-                    if (at.m + q * kBatch + i >= limit)
-                        continue;
-                    if (marks.start[k] >= 0)
-                        f.from_state(a, marks.start[k], at.c);
-                }
-                f.z(x, z);
-                if (a.silu) {
-#pragma unroll
-                    for (int j = 0; j < VE; ++j)
-                        z[j] = silu(z[j]);
-                }
-                store_vec<IO, VE>(y + (size_t)(q * kBatch + i) * a.D, z);
-                f.push(x);
-                if (!plain && marks.end[k] >= 0 && a.state_T) {
-                    IO* s = static_cast<IO*>(a.state_T) + (size_t)marks.end[k] * (W - 1) * a.D + at.c;
-#pragma unroll
-                    for (int r = 0; r < W - 1; ++r)
-                        store_vec<IO, VE>(s + (size_t)r * a.D, f.win[r]);
-                }
-            }
-        }
+        };
+        if (plain)
+            walk(std::true_type{});
+        else
+            walk(std::false_type{});
     }
 
     // the state of an empty sequence stays what it was
@@ -317,16 +327,16 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, Plan plan)
 
 // ---- backward -----------------------------------------------------------------
 
-template <typename IO, int VE, int W>
+template <typename IO, int VE, int W, bool SILU>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, Plan plan)
 {
     __shared__ Marks marks;
     const Place<VE> at(plan, a.D);
-    const long long M = (long long)a.B * a.T;
+    const int M = a.B * a.T;
     const int lanes = 1 << plan.lanes_log2, batches = at.length / kBatchBwd;
     Filter<IO, VE, W> f;
     f.init(a, at.c);
-    float dw[W][VE], db[VE], part[W][VE];  // part[k]: dx of the token W-1-k before this one
+    float dw[W][VE], db[VE], part[W][VE];  // part[k]: dx of the token W-1-k before this one, so far
 #pragma unroll
     for (int j = 0; j < VE; ++j) {
         db[j] = 0.f;
@@ -336,26 +346,21 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, Plan plan)
     }
 
     if (M) {
-        Rows<IO, VE> rows(a.x, a.xs, at.m - (W - 1), M, at.c), grads(a.dy, a.D, at.m, M, at.c);
+        const Rows<IO, VE> rows(a.x, a.xs, M, at.c), grads(a.dy, a.D, M, at.c);
         Vec<IO, VE> before[W - 1], nx[kBatchBwd], ny[kBatchBwd];
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
-            before[k] = rows.next();
+            before[k] = rows.near(at.m - (W - 1) + k);
 #pragma unroll
         for (int i = 0; i < kBatchBwd; ++i) {
-            nx[i] = rows.next();
-            ny[i] = grads.next();
+            nx[i] = rows.near(at.m + i);
+            ny[i] = grads.near(at.m + i);
         }
         mark_tokens(marks, a, at.m0 - (W - 1), at.runs * at.length + 2 * (W - 1));
         const int base = at.run * at.length;
-        const long long limit = token_limit(a), behind = at.m + at.length;
+        const int limit = token_limit(a), behind = at.m + at.length;
         const bool plain = !__any(behind + W - 1 > limit ||
                                   any_mark(marks, base, at.length + 2 * (W - 1), at.lane, lanes));
-        IO* dx = static_cast<IO*>(a.dx) + at.c;
-        // the sequence that started last within the run, and where
-        int seq = -1;
-        long long began = -1;
-
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
             float x[VE];
@@ -364,103 +369,124 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, Plan plan)
                 f.from_state(a, marks.start[base + k], at.c);
             f.push(x);
         }
-
-        // a finished gradient: of token m of the run, or of the state's row before `began`
-        auto finish = [&](long long m, const float (&v)[VE]) {
-            if (plain) {
-                if (m >= at.m)
+        auto walk = [&](auto is_plain) {
+            constexpr bool PLAIN = decltype(is_plain)::value;
+            const IO *ax = rows.at(at.m + kBatchBwd), *ay = grads.at(at.m + kBatchBwd);
+            IO* dx = static_cast<IO*>(a.dx) + at.c;
+            IO* out = dx + (size_t)at.m * a.D;  // of the next token to finish, in a plain run
+            // the sequence that started last within the run, and where
+            int seq = -1, began = -1;
+            // a finished gradient: of token m of the run, or of the state's row before `began`
+            auto finish = [&](int m, const float (&v)[VE]) {
+                if (m < began) {
+                    if (seq >= 0 && a.dstate0)
+                        store_vec<IO, VE>(static_cast<IO*>(a.dstate0) +
+                                              ((size_t)seq * (W - 1) + (m - began + W - 1)) * a.D + at.c, v);
+                } else if (m >= at.m && m < behind) {
                     store_vec<IO, VE>(dx + (size_t)m * a.D, v);
-                return;
-            }
-            if (m < began) {
-                if (seq >= 0 && a.dstate0)
-                    store_vec<IO, VE>(static_cast<IO*>(a.dstate0) +
-                                          ((size_t)seq * (W - 1) + (int)(m - began) + W - 1) * a.D + at.c, v);
-            } else if (m >= at.m && m < behind) {
-                store_vec<IO, VE>(dx + (size_t)m * a.D, v);
-            }
-        };
-        // token i of the run (or of the W - 1 behind it)
-        auto token = [&](int i, const Vec<IO, VE>& rx, const Vec<IO, VE>& ry, bool own) {
-            const long long m = at.m + i;
-            const int k = base + W - 1 + i;
-            float x[VE], g[VE], z[VE];
-            widen<IO, VE>(rx, x);
-            widen<IO, VE>(ry, g);
-            if (!plain) {
-                if (m >= limit)
-                    return;
-                if (marks.start[k] >= 0) {
-                    f.from_state(a, marks.start[k], at.c);
-                    seq = own ? marks.start[k] : -1;
-                    began = m;
                 }
-            }
-            if (a.silu) {
-                f.z(x, z);
+            };
+            // token i of the run (or, not its own, of the W - 1 behind it); i < W - 1
+            // only where `early`
+            auto token = [&](int i, const Vec<IO, VE>& rx, const Vec<IO, VE>& ry, bool own, bool early) {
+                const int m = at.m + i, k = base + W - 1 + i;
+                float x[VE], g[VE], z[VE];
+                widen<IO, VE>(rx, x);
+                widen<IO, VE>(ry, g);
+                if constexpr (!PLAIN) {
+                    if (m >= limit)
+                        return;
+                    if (marks.start[k] >= 0) {
+                        f.from_state(a, marks.start[k], at.c);
+                        seq = own ? marks.start[k] : -1;
+                        began = m;
+                    }
+                }
+                if constexpr (SILU) {
+                    f.z(x, z);
 #pragma unroll
-                for (int j = 0; j < VE; ++j)
-                    g[j] *= silu_slope(z[j]);
-            }
+                    for (int j = 0; j < VE; ++j)
+                        g[j] *= silu_slope(z[j]);
+                }
 #pragma unroll
-            for (int j = 0; j < VE; ++j) {
-                if (own) {
-                    db[j] += g[j];
+                for (int j = 0; j < VE; ++j) {
+                    if (own) {
+                        db[j] += g[j];
+#pragma unroll
+                        for (int r = 0; r < W - 1; ++r)
+                            dw[r][j] = fmaf(g[j], f.win[r][j], dw[r][j]);
+                        dw[W - 1][j] = fmaf(g[j], x[j], dw[W - 1][j]);
+                    }
 #pragma unroll
                     for (int r = 0; r < W - 1; ++r)
-                        dw[r][j] = fmaf(g[j], f.win[r][j], dw[r][j]);
-                    dw[W - 1][j] = fmaf(g[j], x[j], dw[W - 1][j]);
+                        part[r][j] = fmaf(f.w[r][j], g[j], part[r][j]);
+                    part[W - 1][j] = f.w[W - 1][j] * g[j];
                 }
-#pragma unroll
-                for (int r = 0; r < W; ++r)
-                    part[r][j] = fmaf(f.w[r][j], g[j], part[r][j]);
-            }
-            f.push(x);
-            finish(m - (W - 1), part[0]);
-#pragma unroll
-            for (int j = 0; j < VE; ++j) {
-#pragma unroll
-                for (int r = 0; r < W - 1; ++r)
-                    part[r][j] = part[r + 1][j];
-                part[W - 1][j] = 0.f;
-            }
-            if (!plain && marks.end[k] >= 0) {
-                // nothing follows in this sequence but its state's gradient
-                const IO* s = static_cast<const IO*>(a.dstate_T) + (size_t)marks.end[k] * (W - 1) * a.D + at.c;
-#pragma unroll
-                for (int r = 0; r < W - 1; ++r) {
-                    float d[VE];
-                    load_or_zero<IO, VE>(s + (size_t)r * a.D, a.dstate_T, d);
-#pragma unroll
-                    for (int j = 0; j < VE; ++j) {
-                        d[j] += part[r][j];
-                        part[r][j] = 0.f;
+                f.push(x);
+                if constexpr (PLAIN) {
+                    if (!early || i >= W - 1) {
+                        store_vec<IO, VE>(out, part[0]);
+                        out += a.D;
                     }
-                    finish(m - (W - 2) + r, d);
+                } else {
+                    finish(m - (W - 1), part[0]);
                 }
-            }
+#pragma unroll
+                for (int j = 0; j < VE; ++j)
+#pragma unroll
+                    for (int r = 0; r < W - 1; ++r)
+                        part[r][j] = part[r + 1][j];
+                if constexpr (!PLAIN) {
+                    if (marks.end[k] >= 0) {
+                        // nothing follows in this sequence but its state's gradient
+                        const IO* s = static_cast<const IO*>(a.dstate_T) +
+                                      (size_t)marks.end[k] * (W - 1) * a.D + at.c;
+#pragma unroll
+                        for (int r = 0; r < W - 1; ++r) {
+                            float d[VE];
+                            load_or_zero<IO, VE>(s + (size_t)r * a.D, a.dstate_T, d);
+#pragma unroll
+                            for (int j = 0; j < VE; ++j) {
+                                d[j] += part[r][j];
+                                part[r][j] = 0.f;
+                            }
+                            finish(m - (W - 2) + r, d);
+                        }
+                    }
+                }
+            };
+            auto batch = [&](int q, bool more, bool early) {
+                Vec<IO, VE> cx[kBatchBwd], cy[kBatchBwd];
+#pragma unroll
+                for (int i = 0; i < kBatchBwd; ++i)
+                    cx[i] = nx[i], cy[i] = ny[i];
+                // behind the last batch come the W - 1 tokens that end the run's dx
+#pragma unroll
+                for (int i = 0; i < kBatchBwd; ++i)
+                    if (more || i < W - 1) {
+                        const int m = at.m + (q + 1) * kBatchBwd + i;
+                        nx[i] = PLAIN ? load_vec<IO, VE>(ax) : rows.near(m);
+                        ny[i] = PLAIN ? load_vec<IO, VE>(ay) : grads.near(m);
+                        ax += a.xs;
+                        ay += a.D;
+                    }
+#pragma unroll
+                for (int i = 0; i < kBatchBwd; ++i)
+                    token(q * kBatchBwd + i, cx[i], cy[i], true, early);
+            };
+            // (a run has at least two batches)
+            batch(0, true, true);
+            for (int q = 1; q + 1 < batches; ++q)
+                batch(q, true, false);
+            batch(batches - 1, false, false);
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i)
+                token(at.length + i, nx[i], ny[i], false, false);
         };
-
-        for (int q = 0; q < batches; ++q) {
-            Vec<IO, VE> cx[kBatchBwd], cy[kBatchBwd];
-#pragma unroll
-            for (int i = 0; i < kBatchBwd; ++i)
-                cx[i] = nx[i], cy[i] = ny[i];
-            // behind the last batch come the W - 1 tokens that end the run's dx
-            const bool more = q + 1 < batches;
-#pragma unroll
-            for (int i = 0; i < kBatchBwd; ++i)
-                if (more || i < W - 1) {
-                    nx[i] = rows.next();
-                    ny[i] = grads.next();
-                }
-#pragma unroll
-            for (int i = 0; i < kBatchBwd; ++i)
-                token(q * kBatchBwd + i, cx[i], cy[i], true);
-        }
-#pragma unroll
-        for (int i = 0; i < W - 1; ++i)
-            token(at.length + i, nx[i], ny[i], false);
+        if (plain)
+            walk(std::true_type{});
+        else
+            walk(std::false_type{});
     }
 
     // the gradient by the state of an empty sequence
@@ -562,7 +588,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a)
 // Threads side by side on a row: as many as its vectors, 8 to 64.  Runs as long as
 // leave a workgroup for every compute unit, 8 to 32 tokens: a longer one reads
 // fewer rows twice, and its sums are written once for more tokens.
-Plan plan_of(long long M, int D, int ve)
+Plan plan_of(int M, int D, int ve)
 {
     Plan p;
     const int vecs = (D + ve - 1) / ve;
@@ -570,40 +596,48 @@ Plan plan_of(long long M, int D, int ve)
     p.ctiles = (vecs + (1 << p.lanes_log2) - 1) >> p.lanes_log2;
     const int runs = 256 >> p.lanes_log2;
     p.batches = 4;
-    while (p.batches > 1 && (M + runs * p.batches * kBatch - 1) / (runs * p.batches * kBatch) * p.ctiles < 512)
+    auto tiles = [&] { return (M + (long long)runs * p.batches * kBatch - 1) / (runs * p.batches * kBatch); };
+    while (p.batches > 1 && tiles() * p.ctiles < 512)
         p.batches /= 2;
-    const long long per = (long long)runs * p.batches * kBatch;
-    p.tiles = M ? (int)((M + per - 1) / per) : 1;
+    p.tiles = M ? (int)tiles() : 1;
     return p;
 }
 
-template <typename IO, int VE>
-hipError_t conv_fwd(const ConvArgs& a, hipStream_t stream)
+template <typename IO, int VE, int W, bool SILU>
+void launch(const ConvArgs& a, bool backward, hipStream_t stream)
 {
-    const Plan p = plan_of((long long)a.B * a.T, a.D, VE);
+    const Plan p = plan_of(a.B * a.T, a.D, VE);
     const unsigned grid = (unsigned)p.tiles * p.ctiles;
-    if (a.W == 2)
-        conv_fwd_kernel<IO, VE, 2><<<grid, 256, 0, stream>>>(a, p);
-    else if (a.W == 3)
-        conv_fwd_kernel<IO, VE, 3><<<grid, 256, 0, stream>>>(a, p);
-    else
-        conv_fwd_kernel<IO, VE, 4><<<grid, 256, 0, stream>>>(a, p);
-    return hipGetLastError();
+    if (!backward) {
+        conv_fwd_kernel<IO, VE, W, SILU><<<grid, 256, 0, stream>>>(a, p);
+        return;
+    }
+    conv_bwd_kernel<IO, VE, W, SILU><<<grid, 256, 0, stream>>>(a, p);
+    conv_sum_kernel<<<((a.W + 1) * a.D + 63) / 64, 1024, 0, stream>>>(a, a.T ? p.tiles : 0);
+}
+
+template <typename IO, int VE, int W>
+void launch_act(const ConvArgs& a, bool backward, hipStream_t stream)
+{
+    a.silu ? launch<IO, VE, W, true>(a, backward, stream) : launch<IO, VE, W, false>(a, backward, stream);
 }
 
 template <typename IO, int VE>
-hipError_t conv_bwd(const ConvArgs& a, hipStream_t stream)
+void launch_taps(const ConvArgs& a, bool backward, hipStream_t stream)
 {
-    const Plan p = plan_of((long long)a.B * a.T, a.D, VE);
-    const unsigned grid = (unsigned)p.tiles * p.ctiles;
-    if (a.W == 2)
-        conv_bwd_kernel<IO, VE, 2><<<grid, 256, 0, stream>>>(a, p);
-    else if (a.W == 3)
-        conv_bwd_kernel<IO, VE, 3><<<grid, 256, 0, stream>>>(a, p);
-    else
-        conv_bwd_kernel<IO, VE, 4><<<grid, 256, 0, stream>>>(a, p);
-    const int columns = (a.W + 1) * a.D;
-    conv_sum_kernel<<<(columns + 63) / 64, 1024, 0, stream>>>(a, a.T ? p.tiles : 0);
+    a.W == 2   ? launch_act<IO, VE, 2>(a, backward, stream)
+    : a.W == 3 ? launch_act<IO, VE, 3>(a, backward, stream)
+               : launch_act<IO, VE, 4>(a, backward, stream);
+}
+
+// Four channels a thread (8 bytes of bf16: eight would take the registers of twice
+// the waves, 60 us against 52 at 32768 x 2048); fewer than four go one a thread.
+int vector_of(int D) { return D < 4 ? 1 : 4; }
+
+template <typename IO>
+hipError_t launch_io(const ConvArgs& a, bool backward, hipStream_t stream)
+{
+    vector_of(a.D) == 1 ? launch_taps<IO, 1>(a, backward, stream) : launch_taps<IO, 4>(a, backward, stream);
     return hipGetLastError();
 }
 
@@ -611,22 +645,17 @@ hipError_t conv_bwd(const ConvArgs& a, hipStream_t stream)
 
 int conv_bwd_groups(int B, int T, int D)
 {
-    return T ? plan_of((long long)B * T, D, D < 4 ? 1 : 4).tiles : 0;
+    return T ? plan_of(B * T, D, vector_of(D)).tiles : 0;
 }
 
-// fewer channels than a vector go one a thread
 hipError_t launch_conv_fwd(const ConvArgs& a, bool bf, hipStream_t stream)
 {
-    if (bf)
-        return a.D < 8 ? conv_fwd<bf16, 1>(a, stream) : conv_fwd<bf16, 8>(a, stream);
-    return a.D < 4 ? conv_fwd<float, 1>(a, stream) : conv_fwd<float, 4>(a, stream);
+    return bf ? launch_io<bf16>(a, false, stream) : launch_io<float>(a, false, stream);
 }
 
 hipError_t launch_conv_bwd(const ConvArgs& a, bool bf, hipStream_t stream)
 {
-    if (bf)
-        return a.D < 4 ? conv_bwd<bf16, 1>(a, stream) : conv_bwd<bf16, 4>(a, stream);
-    return a.D < 4 ? conv_bwd<float, 1>(a, stream) : conv_bwd<float, 4>(a, stream);
+    return bf ? launch_io<bf16>(a, true, stream) : launch_io<float>(a, true, stream);
 }
 
 hipError_t launch_conv_step(const ConvArgs& a, bool bf, hipStream_t stream)
