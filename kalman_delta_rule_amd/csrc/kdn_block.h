@@ -77,7 +77,7 @@ struct RecArgs {
     float* dh0;  // nullable [N,D]
     void* ws;
 };
-size_t rec_workspace_bytes(int B, int T, int D);
+size_t rec_workspace_bytes(int B, int T, int D, bool backward);
 hipError_t launch_rec_fwd(const RecArgs& a, bool bf, hipStream_t stream);
 hipError_t launch_rec_bwd(const RecArgs& a, bool bf, hipStream_t stream);
 hipError_t launch_rec_step(const RecArgs& a, bool bf, hipStream_t stream);

@@ -326,14 +326,15 @@ kdn_status kdn_conv_step(int B, int D, int W, int io_dtype, int activation, cons
                     "kdn_conv_step");
 }
 
-size_t kdn_rec_fwd_workspace_size(int B, int T, int D)
+static size_t rec_workspace_size(int B, int T, int D, bool backward)
 {
     if (B < 1 || T < 0 || D < 1 || D > kMaxD || (__int128)B * T * D >= kMaxElems)
         return 0;
-    return kdn::rec_workspace_bytes(B, T, D);
+    return kdn::rec_workspace_bytes(B, T, D, backward);
 }
 
-size_t kdn_rec_bwd_workspace_size(int B, int T, int D) { return kdn_rec_fwd_workspace_size(B, T, D); }
+size_t kdn_rec_fwd_workspace_size(int B, int T, int D) { return rec_workspace_size(B, T, D, false); }
+size_t kdn_rec_bwd_workspace_size(int B, int T, int D) { return rec_workspace_size(B, T, D, true); }
 
 kdn_status kdn_rec_fwd(int B, int T, int D, int io_dtype, int gate, int blend, const void* x,
                        long long x_stride, const void* a, long long a_stride, const float* h0,

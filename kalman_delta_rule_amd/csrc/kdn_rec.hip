@@ -34,7 +34,6 @@ namespace kdn {
 namespace {
 
 constexpr int kChk = KDN_REC_CHECKPOINT;
-constexpr int kTile = 128;   // tokens of a tile
 constexpr int kGroup = 8;    // tiles of a group of the chain, groups of a block
 constexpr int kBlock = kGroup * kGroup;
 constexpr int kPolls = 1 << 21;
@@ -261,12 +260,12 @@ __device__ __forceinline__ void store_at(char* base, uint32_t off, const float (
 
 // V values of each of a run's L tokens: rows `stride` bytes apart from `base`, the
 // run's first at row `first`, the lane's values at byte `col` of a row.  Where the
-// tile reaches behind the row's end (`rows` < kTile), the last row is repeated.
-template <typename E, int V, int L>
+// tile reaches behind the row's end (`rows` < TILE), the last row is repeated.
+template <int TILE, typename E, int V, int L>
 __device__ __forceinline__ void load_run(Pack<E, V> (&r)[L], const char* base, uint32_t stride,
                                          int first, uint32_t col, int rows)
 {
-    if (rows >= kTile) {
+    if (rows >= TILE) {
         const uint32_t off = first * stride + col;
 #pragma unroll
         for (int i = 0; i < L; ++i)
@@ -296,42 +295,63 @@ __device__ __forceinline__ void gate_of(float a, float& alpha, float& rest)
     }
 }
 
-// Marks of a tile's tokens: the sequence that starts or ends at each, or -1.
+// The sequences that start and end in a tile.  Of packed ones the offsets (which
+// may be anything) are looked through for marks, a token each; otherwise the row is
+// one sequence.
+template <int TILE, int L, int THREADS>
 struct Marks {
-    int start[kTile], end[kTile];
-};
+    int start[TILE], end[TILE];  // the sequence that starts or ends at the token, or -1
 
-// Fills them (all threads of the workgroup); the offsets may be anything.
-template <int THREADS>
-__device__ __forceinline__ void mark_tile(Marks& m, const RecArgs& a, int b, int t0)
-{
-    for (int i = threadIdx.x; i < kTile; i += THREADS)
-        m.start[i] = m.end[i] = -1;
-    __syncthreads();
-    if (a.cu) {
+    // all threads of the workgroup
+    __device__ __forceinline__ void fill(const RecArgs& a, int t0)
+    {
+        if (!a.cu)
+            return;
+        for (int i = threadIdx.x; i < TILE; i += THREADS)
+            start[i] = end[i] = -1;
+        __syncthreads();
         for (int n = threadIdx.x; n < a.N; n += THREADS) {
             const int p = a.cu[n], q = a.cu[n + 1];
-            if (p < q && p >= t0 && p - t0 < kTile)
-                m.start[p - t0] = n;
-            if (p < q && q > t0 && q - 1 - t0 < kTile)
-                m.end[q - 1 - t0] = n;
+            if (p < 0 || p >= q)
+                continue;
+            if (p >= t0 && p - t0 < TILE)
+                start[p - t0] = n;
+            if (q > t0 && q - 1 - t0 < TILE)
+                end[q - 1 - t0] = n;
         }
-    } else if (threadIdx.x == 0 && a.T) {
-        if (t0 == 0)
-            m.start[0] = b;
-        if (a.T - 1 - t0 < kTile)
-            m.end[a.T - 1 - t0] = b;
+        __syncthreads();
     }
-    __syncthreads();
-}
+    // bits of the L tokens from `first` on, where a sequence starts or ends
+    __device__ __forceinline__ uint32_t starts(const RecArgs& a, int t0, int first) const
+    {
+        return a.cu ? bits(start + first) : t0 + first == 0 && a.T > 0;
+    }
+    __device__ __forceinline__ uint32_t ends(const RecArgs& a, int t0, int first) const
+    {
+        const int last = a.T - 1 - t0 - first;
+        return a.cu ? bits(end + first) : last >= 0 && last < L ? 1u << last : 0u;
+    }
+    // the sequence at a token of the tile whose bit is set
+    __device__ __forceinline__ int starting(const RecArgs& a, int b, int i) const { return a.cu ? start[i] : b; }
+    __device__ __forceinline__ int ending(const RecArgs& a, int b, int i) const { return a.cu ? end[i] : b; }
 
-// bits of a half-wave's L tokens whose mark is set
-template <int L>
-__device__ __forceinline__ uint32_t marked(const int* marks)
+private:
+    // of a half-wave's tokens
+    __device__ __forceinline__ static uint32_t bits(const int* marks)
+    {
+        const int l = threadIdx.x & 31;
+        const unsigned long long w = __ballot(l < L && marks[l < L ? l : 0] >= 0);
+        return (uint32_t)((threadIdx.x & 32) ? w >> 32 : w);
+    }
+};
+
+// values [V] of a state [N,D] at sequence n, channel c, or zeros where it is not given
+template <int V>
+__device__ __forceinline__ void state_at(const float* s, int n, int D, int c, float (&h)[V])
 {
-    const int l = threadIdx.x & 31;
-    const unsigned long long w = __ballot(l < L && marks[l < L ? l : 0] >= 0);
-    return (uint32_t)((threadIdx.x & 32) ? w >> 32 : w);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        h[v] = s ? s[(size_t)n * D + c + v] : 0.f;
 }
 
 // tokens of the row that belong to a sequence
@@ -352,55 +372,64 @@ struct Tile {
 // lie together, and its own counter.  Within a queue all tiles of a time come
 // before the next time's.  A workgroup that finds its queue empty goes on to the
 // next one: there are as many workgroups as tiles, so each gets one.
-template <int CT>
+template <int TILE, int CT>
 __device__ __forceinline__ Tile take_tile(const RecArgs& a, const Chain& ch, int ctiles, bool backward)
 {
     const uint32_t per = a.B * ctiles;
-    uint32_t k = 0, r = blockIdx.x;
-    if (ch.tiles > 1) {
-        __shared__ uint32_t s_queue, s_ticket;
-        if (threadIdx.x == 0) {
-            uint32_t q = blockIdx.x % ch.queues, i = 0;
+    __shared__ int s_tile[3];
+    if (threadIdx.x == 0) {
+        uint32_t k = 0, r = blockIdx.x;
+        if (ch.tiles > 1) {
+            uint32_t q = blockIdx.x % ch.queues;
             for (int n = 0; n < ch.queues; ++n) {
-                const uint32_t c0 = q * per / ch.queues, c1 = (q + 1) * per / ch.queues;
-                i = __hip_atomic_fetch_add(ch.tickets + q * kTicketWords, 1u, __ATOMIC_RELAXED,
-                                           __HIP_MEMORY_SCOPE_AGENT);
-                if (i < (c1 - c0) * ch.tiles)
+                const uint32_t c0 = q * per / ch.queues, own = (q + 1) * per / ch.queues - c0;
+                const uint32_t i = __hip_atomic_fetch_add(ch.tickets + q * kTicketWords, 1u,
+                                                          __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                if (i < own * ch.tiles) {
+                    k = i / own;
+                    r = c0 + (i - k * own);
                     break;
+                }
                 q = q + 1 == (uint32_t)ch.queues ? 0 : q + 1;
             }
-            s_queue = q;
-            s_ticket = i;
         }
-        __syncthreads();
-        // the same for the whole wave: addresses from here on are scalar
-        const uint32_t q = __builtin_amdgcn_readfirstlane(s_queue);
-        const uint32_t i = __builtin_amdgcn_readfirstlane(s_ticket);
-        const uint32_t c0 = q * per / ch.queues, n = (q + 1) * per / ch.queues - c0;
-        k = i / n;
-        r = c0 + (i - k * n);
+        const uint32_t b = r / ctiles;
+        s_tile[0] = k;
+        s_tile[1] = b;
+        s_tile[2] = r - b * ctiles;
     }
+    __syncthreads();
+    // the same for the whole wave: addresses from here on are scalar
     Tile t;
-    t.k = k;
-    t.b = r / ctiles;
-    t.c0 = (r - t.b * ctiles) * CT;
-    t.col = r * CT;
-    t.t0 = (backward ? ch.tiles - 1 - t.k : t.k) * kTile;
+    t.k = __builtin_amdgcn_readfirstlane(s_tile[0]);
+    t.b = __builtin_amdgcn_readfirstlane(s_tile[1]);
+    const int ct = __builtin_amdgcn_readfirstlane(s_tile[2]);
+    t.c0 = ct * CT;
+    t.col = (t.b * ctiles + ct) * CT;
+    t.t0 = (backward ? ch.tiles - 1 - t.k : t.k) * TILE;
     return t;
 }
 
 // ---- forward -------------------------------------------------------------------
 
-// 256 threads: eight half-waves of 16 tokens.
+#ifndef FL
+#define FL 16
+#define FR 8
+#define FW 4
+#define BL 8
+#define BR 16
+#define BW 4
+#endif
+constexpr int kFwdL = FL, kFwdRuns = FR, kBwdL = BL, kBwdRuns = BR;
 template <typename IO, bool PRE, bool BLEND, int V>
-__global__ __launch_bounds__(256, 4) void rec_fwd_kernel(RecArgs a, Chain ch, int ctiles)
+__global__ __launch_bounds__(kFwdRuns * 32, FW) void rec_fwd_kernel(RecArgs a, Chain ch, int ctiles)
 {
     typedef typename std::conditional<PRE, IO, float>::type GT;
-    constexpr int L = 16, RUNS = 8, CT = 32 * V;
-    __shared__ Marks marks;
+    constexpr int L = kFwdL, RUNS = kFwdRuns, TILE = L * RUNS, CT = 32 * V;
+    __shared__ Marks<TILE, L, RUNS * 32> marks;
     __shared__ Link<RUNS, CT, false> link;
 
-    const Tile tile = take_tile<CT>(a, ch, ctiles, false);
+    const Tile tile = take_tile<TILE, CT>(a, ch, ctiles, false);
     const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
     // lanes behind the last channel repeat the last ones
     const int c = min(tile.c0 + lane * V, a.D - V);
@@ -410,14 +439,14 @@ __global__ __launch_bounds__(256, 4) void rec_fwd_kernel(RecArgs a, Chain ch, in
     Pack<GT, V> ra[L];
     Pack<IO, V> rx[L];
     const int rows = a.T - tile.t0;
-    load_run<GT, V, L>(ra, static_cast<const char*>(a.a) + row0 * a.as * sizeof(GT),
+    load_run<TILE, GT, V, L>(ra, static_cast<const char*>(a.a) + row0 * a.as * sizeof(GT),
                        (uint32_t)a.as * sizeof(GT), first, c * sizeof(GT), rows);
-    load_run<IO, V, L>(rx, static_cast<const char*>(a.x) + row0 * a.xs * sizeof(IO),
+    load_run<TILE, IO, V, L>(rx, static_cast<const char*>(a.x) + row0 * a.xs * sizeof(IO),
                        (uint32_t)a.xs * sizeof(IO), first, c * sizeof(IO), rows);
 
-    mark_tile<256>(marks, a, tile.b, tile.t0);
+    marks.fill(a, tile.t0);
     const int valid = token_limit(a) - (tile.t0 + first);  // tokens of the run, if positive
-    const uint32_t start = marked<L>(marks.start + first), end = marked<L>(marks.end + first);
+    const uint32_t start = marks.starts(a, tile.t0, first), end = marks.ends(a, tile.t0, first);
     const bool plain = __all(valid >= L && !start && !end);
 
     float al[L][V], u[L][V];
@@ -448,13 +477,14 @@ __global__ __launch_bounds__(256, 4) void rec_fwd_kernel(RecArgs a, Chain ch, in
         for (int i = 0; i < L; ++i) {
             if (i >= valid)
                 continue;
-            const bool s = start >> i & 1;
+            if (start >> i & 1) {
+                state_at<V>(a.h0, marks.starting(a, tile.b, first + i), a.D, c, U);
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    A[v] = 0.f;
+            }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                if (s) {
-                    A[v] = 0.f;
-                    U[v] = a.h0 ? a.h0[(size_t)marks.start[first + i] * a.D + c + v] : 0.f;
-                }
                 U[v] = fmaf(al[i][v], U[v], u[i][v]);
                 A[v] *= al[i][v];
             }
@@ -472,12 +502,14 @@ __global__ __launch_bounds__(256, 4) void rec_fwd_kernel(RecArgs a, Chain ch, in
 #pragma unroll
     for (int v = 0; v < V; ++v)
         h[v] = link.start(run, lane * V + v);
-    if (a.ckpt && first % kChk == 0 && valid > 0) {
+    if (a.ckpt && (tile.t0 + first) % kChk == 0 && valid > 0) {
         const int blocks = (a.T + kChk - 1) / kChk;
         float* p = a.ckpt + ((size_t)tile.b * blocks + (tile.t0 + first) / kChk) * a.D + c;
+        if (start & 1)
+            state_at<V>(a.h0, marks.starting(a, tile.b, first), a.D, c, h);
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            p[v] = !(start & 1) ? h[v] : a.h0 ? a.h0[(size_t)marks.start[first] * a.D + c + v] : 0.f;
+            p[v] = h[v];
     }
     char* ph = static_cast<char*>(a.h) + row0 * a.D * sizeof(IO);
     const uint32_t sh = (uint32_t)a.D * sizeof(IO);
@@ -495,14 +527,16 @@ __global__ __launch_bounds__(256, 4) void rec_fwd_kernel(RecArgs a, Chain ch, in
         for (int i = 0; i < L; ++i) {
             if (i >= valid)
                 continue;
-            const bool s = start >> i & 1, e = end >> i & 1;
+            if (start >> i & 1)
+                state_at<V>(a.h0, marks.starting(a, tile.b, first + i), a.D, c, h);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (s)
-                    h[v] = a.h0 ? a.h0[(size_t)marks.start[first + i] * a.D + c + v] : 0.f;
+            for (int v = 0; v < V; ++v)
                 h[v] = fmaf(al[i][v], h[v], u[i][v]);
-                if (e && a.h_T)
-                    a.h_T[(size_t)marks.end[first + i] * a.D + c + v] = h[v];
+            if ((end >> i & 1) && a.h_T) {
+                float* p = a.h_T + (size_t)marks.ending(a, tile.b, first + i) * a.D + c;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    p[v] = h[v];
             }
             store_at<IO, V>(ph + (size_t)i * sh, oh, h);
         }
@@ -527,15 +561,16 @@ __global__ __launch_bounds__(256, 4) void rec_fwd_kernel(RecArgs a, Chain ch, in
 // states before the runs come from the forward's checkpoints, so only the
 // adjoint is chained, in reverse.
 template <typename IO, bool PRE, bool BLEND, int V>
-__global__ __launch_bounds__(512, 4) void rec_bwd_kernel(RecArgs a, Chain ch, int ctiles)
+__global__ __launch_bounds__(kBwdRuns * 32, BW) void rec_bwd_kernel(RecArgs a, Chain ch, int ctiles)
 {
     typedef typename std::conditional<PRE, IO, float>::type GT;
-    constexpr int L = 8, RUNS = 16, CT = 32 * V, PER = kChk / L;  // runs of a checkpoint
-    __shared__ Marks marks;
+    constexpr int L = kBwdL, RUNS = kBwdRuns, TILE = L * RUNS, CT = 32 * V;
+    constexpr int PER = kChk / L;  // runs of a checkpoint
+    __shared__ Marks<TILE, L, RUNS * 32> marks;
     __shared__ float2 spans[RUNS][CT];
     __shared__ Link<RUNS, CT, true> link;
 
-    const Tile tile = take_tile<CT>(a, ch, ctiles, true);
+    const Tile tile = take_tile<TILE, CT>(a, ch, ctiles, true);
     const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
     const int c = min(tile.c0 + lane * V, a.D - V);
     const int first = run * L;
@@ -544,16 +579,16 @@ __global__ __launch_bounds__(512, 4) void rec_bwd_kernel(RecArgs a, Chain ch, in
     Pack<GT, V> ra[L];
     Pack<IO, V> rx[L], rd[L];
     const int rows = a.T - tile.t0;
-    load_run<GT, V, L>(ra, static_cast<const char*>(a.a) + row0 * a.as * sizeof(GT),
+    load_run<TILE, GT, V, L>(ra, static_cast<const char*>(a.a) + row0 * a.as * sizeof(GT),
                        (uint32_t)a.as * sizeof(GT), first, c * sizeof(GT), rows);
-    load_run<IO, V, L>(rx, static_cast<const char*>(a.x) + row0 * a.xs * sizeof(IO),
+    load_run<TILE, IO, V, L>(rx, static_cast<const char*>(a.x) + row0 * a.xs * sizeof(IO),
                        (uint32_t)a.xs * sizeof(IO), first, c * sizeof(IO), rows);
-    load_run<IO, V, L>(rd, static_cast<const char*>(a.dh) + row0 * a.D * sizeof(IO),
+    load_run<TILE, IO, V, L>(rd, static_cast<const char*>(a.dh) + row0 * a.D * sizeof(IO),
                        (uint32_t)a.D * sizeof(IO), first, c * sizeof(IO), rows);
 
-    mark_tile<512>(marks, a, tile.b, tile.t0);
+    marks.fill(a, tile.t0);
     const int valid = token_limit(a) - (tile.t0 + first);
-    const uint32_t start = marked<L>(marks.start + first), end = marked<L>(marks.end + first);
+    const uint32_t start = marks.starts(a, tile.t0, first), end = marks.ends(a, tile.t0, first);
     const bool plain = __all(valid >= L && !start && !end);
 
     float al[L][V], rest[L][V];
@@ -589,13 +624,14 @@ __global__ __launch_bounds__(512, 4) void rec_bwd_kernel(RecArgs a, Chain ch, in
         for (int i = 0; i < L; ++i) {
             if (i >= valid)
                 continue;
-            const bool s = start >> i & 1;
+            if (start >> i & 1) {
+                state_at<V>(a.h0, marks.starting(a, tile.b, first + i), a.D, c, U);
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    A[v] = 0.f;
+            }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                if (s) {
-                    A[v] = 0.f;
-                    U[v] = a.h0 ? a.h0[(size_t)marks.start[first + i] * a.D + c + v] : 0.f;
-                }
                 const float x = to_f32(rx[i].v[v]);
                 U[v] = fmaf(al[i][v], U[v], BLEND ? rest[i][v] * x : x);
                 A[v] *= al[i][v];
@@ -605,13 +641,14 @@ __global__ __launch_bounds__(512, 4) void rec_bwd_kernel(RecArgs a, Chain ch, in
         for (int i = L - 1; i >= 0; --i) {
             if (i >= valid)
                 continue;
-            const bool e = end >> i & 1;
+            if (end >> i & 1) {
+                state_at<V>(a.dh_T, marks.ending(a, tile.b, first + i), a.D, c, RU);
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    RA[v] = 0.f;
+            }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                if (e) {
-                    RA[v] = 0.f;
-                    RU[v] = a.dh_T ? a.dh_T[(size_t)marks.end[first + i] * a.D + c + v] : 0.f;
-                }
                 RU[v] = al[i][v] * (to_f32(rd[i].v[v]) + RU[v]);
                 RA[v] *= al[i][v];
             }
@@ -637,16 +674,26 @@ __global__ __launch_bounds__(512, 4) void rec_bwd_kernel(RecArgs a, Chain ch, in
 #pragma unroll
         for (int v = 0; v < V; ++v)
             h[v] = apply(spans[r][lane * V + v].x, spans[r][lane * V + v].y, h[v]);
-#pragma unroll
-    for (int i = 0; i < L; ++i)
+    auto forward = [&](int i) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            if (!plain && (start >> i & 1))
-                h[v] = a.h0 ? a.h0[(size_t)marks.start[first + i] * a.D + c + v] : 0.f;
             const float x = to_f32(rx[i].v[v]);
             part[i][v] = BLEND ? h[v] - x : h[v];
             h[v] = fmaf(al[i][v], h[v], BLEND ? rest[i][v] * x : x);
         }
+    };
+    if (plain) {
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+            forward(i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            if (start >> i & 1)
+                state_at<V>(a.h0, marks.starting(a, tile.b, first + i), a.D, c, h);
+            forward(i);
+        }
+    }
     __syncthreads();
     link.finish(ch, tile.k, tile.col);
 
@@ -657,17 +704,7 @@ __global__ __launch_bounds__(512, 4) void rec_bwd_kernel(RecArgs a, Chain ch, in
     char* pa = static_cast<char*>(a.da) + row0 * a.D * sizeof(GT);
     const uint32_t sx = (uint32_t)a.D * sizeof(IO), sa = (uint32_t)a.D * sizeof(GT);
     const uint32_t ox = first * sx + c * (uint32_t)sizeof(IO), oa = first * sa + c * (uint32_t)sizeof(GT);
-#pragma unroll
-    for (int i = L - 1; i >= 0; --i) {
-        if (!plain) {
-            if (i >= valid)
-                continue;
-            if (end >> i & 1) {
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    g[v] = a.dh_T ? a.dh_T[(size_t)marks.end[first + i] * a.D + c + v] : 0.f;
-            }
-        }
+    auto reverse = [&](int i) {
         float dx[V], da[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -679,10 +716,25 @@ __global__ __launch_bounds__(512, 4) void rec_bwd_kernel(RecArgs a, Chain ch, in
         }
         store_at<IO, V>(px + (size_t)i * sx, ox, dx);
         store_at<GT, V>(pa + (size_t)i * sa, oa, da);
-        if (!plain && (start >> i & 1) && a.dh0) {
+    };
+    if (plain) {
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                a.dh0[(size_t)marks.start[first + i] * a.D + c + v] = g[v];
+        for (int i = L - 1; i >= 0; --i)
+            reverse(i);
+    } else {
+#pragma unroll
+        for (int i = L - 1; i >= 0; --i) {
+            if (i >= valid)
+                continue;
+            if (end >> i & 1)
+                state_at<V>(a.dh_T, marks.ending(a, tile.b, first + i), a.D, c, g);
+            reverse(i);
+            if ((start >> i & 1) && a.dh0) {
+                float* p = a.dh0 + (size_t)marks.starting(a, tile.b, first + i) * a.D + c;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    p[v] = g[v];
+            }
         }
     }
 
@@ -714,12 +766,16 @@ __global__ __launch_bounds__(256) void rec_step_kernel(RecArgs a)
     static_cast<IO*>(a.h)[(size_t)b * a.D + c] = from_f32<IO>(h);
 }
 
-int tiles_of(int T) { return T > kTile ? (T + kTile - 1) / kTile : 1; }
+int tiles_of(int T, bool backward)
+{
+    const int t = backward ? kBwdL * kBwdRuns : kFwdL * kFwdRuns;
+    return T > t ? (int)(((long long)T + t - 1) / t) : 1;
+}
 
 template <typename IO, bool PRE, bool BLEND, int V>
 hipError_t launch(const RecArgs& a, bool backward, hipStream_t stream)
 {
-    const int ctiles = (a.D + 32 * V - 1) / (32 * V), tiles = tiles_of(a.T);
+    const int ctiles = (a.D + 32 * V - 1) / (32 * V), tiles = tiles_of(a.T, backward);
     const int columns = a.B * ctiles * 32 * V;
     // with fewer columns than XCDs some would have none of their own
     const Chain ch = chain_at(a.ws, tiles, columns, a.B * ctiles < kQueues ? 1 : kQueues);
@@ -729,9 +785,9 @@ hipError_t launch(const RecArgs& a, bool backward, hipStream_t stream)
     }
     const unsigned grid = (unsigned)((size_t)tiles * a.B * ctiles);
     if (backward)
-        rec_bwd_kernel<IO, PRE, BLEND, V><<<grid, 512, 0, stream>>>(a, ch, ctiles);
+        rec_bwd_kernel<IO, PRE, BLEND, V><<<grid, kBwdRuns * 32, 0, stream>>>(a, ch, ctiles);
     else
-        rec_fwd_kernel<IO, PRE, BLEND, V><<<grid, 256, 0, stream>>>(a, ch, ctiles);
+        rec_fwd_kernel<IO, PRE, BLEND, V><<<grid, kFwdRuns * 32, 0, stream>>>(a, ch, ctiles);
     return hipGetLastError();
 }
 
@@ -752,9 +808,9 @@ hipError_t launch_io(const RecArgs& a, bool backward, hipStream_t stream)
 
 }  // namespace
 
-size_t rec_workspace_bytes(int B, int T, int D)
+size_t rec_workspace_bytes(int B, int T, int D, bool backward)
 {
-    const int tiles = tiles_of(T), ct = D == 1 ? 32 : 64;
+    const int tiles = tiles_of(T, backward), ct = D == 1 ? 32 : 64;
     if (tiles == 1)
         return 0;
     return chain_units(tiles, B * ((D + ct - 1) / ct) * ct) * 16;
