@@ -78,6 +78,7 @@ struct RecArgs {
     void* ws;
 };
 size_t rec_workspace_bytes(int B, int T, int D, bool backward);
+unsigned long long rec_threads(int B, int T, int D, bool backward);  // of its largest launch
 hipError_t launch_rec_fwd(const RecArgs& a, bool bf, hipStream_t stream);
 hipError_t launch_rec_bwd(const RecArgs& a, bool bf, hipStream_t stream);
 hipError_t launch_rec_step(const RecArgs& a, bool bf, hipStream_t stream);

@@ -96,8 +96,11 @@ kdn_status check_sequence(int B, int T, int D, const int* cu, int& N)
     if (!cu)
         N = B;
     // 128-bit products: three factors below 2^31
-    if ((__int128)B * T * D >= kMaxElems || (__int128)N * D >= kMaxElems || (__int128)B * T >= kMaxElems)
+    if ((__int128)B * T * D >= kMaxElems || (__int128)N * D >= kMaxElems)
         return fail(KDN_ERR_UNSUPPORTED, "tensor sizes must stay below 2^31 elements");
+    // token numbers, and those a tile further, are ints; a row is a workgroup or more
+    if ((long long)B * T > 1ll << 30 || B >= 1 << 24)
+        return fail(KDN_ERR_UNSUPPORTED, "B T is at most 2^30 and B below 2^24 (got B=%d T=%d)", B, T);
     return KDN_OK;
 }
 
@@ -326,6 +329,14 @@ kdn_status kdn_conv_step(int B, int D, int W, int io_dtype, int activation, cons
                     "kdn_conv_step");
 }
 
+// a launch has fewer than 2^32 threads: only many rows of a few tokens come near
+static kdn_status check_rec_grid(int B, int T, int D, bool backward)
+{
+    if (kdn::rec_threads(B, T, D, backward) >> 32)
+        return fail(KDN_ERR_UNSUPPORTED, "too many short rows for one launch (B=%d T=%d D=%d)", B, T, D);
+    return KDN_OK;
+}
+
 static size_t rec_workspace_size(int B, int T, int D, bool backward)
 {
     if (B < 1 || T < 0 || D < 1 || D > kMaxD || (__int128)B * T * D >= kMaxElems)
@@ -346,6 +357,7 @@ kdn_status kdn_rec_fwd(int B, int T, int D, int io_dtype, int gate, int blend, c
     long long xspan, aspan;
     KDN_TRY(check_rows((long long)B * T, D, x_stride, "x", xspan));
     KDN_TRY(check_rows((long long)B * T, D, a_stride, "a", aspan));
+    KDN_TRY(check_rec_grid(B, T, D, false));
     const size_t need = kdn_rec_fwd_workspace_size(B, T, D);
     KDN_TRY(check_workspace(workspace, workspace_bytes, need));
     const int e = io_size(io_dtype), ea = gate == KDN_GATE_PREACT ? e : 4;
@@ -378,6 +390,7 @@ kdn_status kdn_rec_bwd(int B, int T, int D, int io_dtype, int gate, int blend, c
     long long xspan, aspan;
     KDN_TRY(check_rows((long long)B * T, D, x_stride, "x", xspan));
     KDN_TRY(check_rows((long long)B * T, D, a_stride, "a", aspan));
+    KDN_TRY(check_rec_grid(B, T, D, true));
     const size_t need = kdn_rec_bwd_workspace_size(B, T, D);
     KDN_TRY(check_workspace(workspace, workspace_bytes, need));
     const int e = io_size(io_dtype), ea = gate == KDN_GATE_PREACT ? e : 4;

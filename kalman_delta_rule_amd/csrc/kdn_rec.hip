@@ -7,7 +7,7 @@
 //
 // Both recurrences are affine in what they carry: over any span of tokens
 // carry -> A carry + U with A the product of the decays.  So a workgroup takes a
-// tile of 128 tokens and 64 channels, each half-wave of it a run of tokens (two
+// tile of 128 or 256 tokens and 64 channels, each half-wave of it a run of tokens (two
 // channels a lane): the run's (A, U) first, from registers; then one wave joins
 // the runs in order, gets what the tile starts from, and hands every run its own
 // start; then the runs are walked again, from the same registers, with their
@@ -412,20 +412,19 @@ __device__ __forceinline__ Tile take_tile(const RecArgs& a, const Chain& ch, int
 
 // ---- forward -------------------------------------------------------------------
 
-#ifndef FL
-#define FL 16
-#define FR 8
-#define FW 4
-#define BL 8
-#define BR 16
-#define BW 4
-#endif
-constexpr int kFwdL = FL, kFwdRuns = FR, kBwdL = BL, kBwdRuns = BR;
-template <typename IO, bool PRE, bool BLEND, int V>
-__global__ __launch_bounds__(kFwdRuns * 32, FW) void rec_fwd_kernel(RecArgs a, Chain ch, int ctiles)
+// Half-waves of 16 tokens: eight, or sixteen where the columns are few.  A longer tile
+// halves the chain, a shorter one leaves more workgroups out of step, one loading
+// while another waits (D 2048 bf16, eight and sixteen: B8 T4096 94 and 101 us, B32
+// T1024 99 and 110; B4 T4096 50 and 51; B2 T32768 177 and 164; B1 T65536 198 and 176;
+// D 64, B1 T65536 37 and 23).
+constexpr int kFwdRun = 16, kManyColumnTiles = 192;
+int fwd_runs(long long column_tiles) { return column_tiles >= kManyColumnTiles ? 8 : 16; }
+
+template <typename IO, bool PRE, bool BLEND, int V, int RUNS>
+__global__ __launch_bounds__(RUNS * 32, 4) void rec_fwd_kernel(RecArgs a, Chain ch, int ctiles)
 {
     typedef typename std::conditional<PRE, IO, float>::type GT;
-    constexpr int L = kFwdL, RUNS = kFwdRuns, TILE = L * RUNS, CT = 32 * V;
+    constexpr int L = kFwdRun, TILE = L * RUNS, CT = 32 * V;
     __shared__ Marks<TILE, L, RUNS * 32> marks;
     __shared__ Link<RUNS, CT, false> link;
 
@@ -556,15 +555,17 @@ __global__ __launch_bounds__(kFwdRuns * 32, FW) void rec_fwd_kernel(RecArgs a, C
 
 // ---- backward ------------------------------------------------------------------
 
-// 512 threads: sixteen half-waves of 8 tokens (the inputs, the decays and the
-// states of 16 tokens would not fit the registers of two workgroups a CU).  The
-// states before the runs come from the forward's checkpoints, so only the
-// adjoint is chained, in reverse.
+// Sixteen half-waves of 8 tokens: the inputs, the decays and the states of 16 would not
+// fit the registers of two workgroups a CU (with eight of them, B1 T65536 D2048
+// bf16 353 us against 312).  The states before the runs come from the forward's
+// checkpoints, so only the adjoint is chained, in reverse.
+constexpr int kBwdRun = 8, kBwdRuns = 16;
+
 template <typename IO, bool PRE, bool BLEND, int V>
-__global__ __launch_bounds__(kBwdRuns * 32, BW) void rec_bwd_kernel(RecArgs a, Chain ch, int ctiles)
+__global__ __launch_bounds__(kBwdRuns * 32, 4) void rec_bwd_kernel(RecArgs a, Chain ch, int ctiles)
 {
     typedef typename std::conditional<PRE, IO, float>::type GT;
-    constexpr int L = kBwdL, RUNS = kBwdRuns, TILE = L * RUNS, CT = 32 * V;
+    constexpr int L = kBwdRun, RUNS = kBwdRuns, TILE = L * RUNS, CT = 32 * V;
     constexpr int PER = kChk / L;  // runs of a checkpoint
     __shared__ Marks<TILE, L, RUNS * 32> marks;
     __shared__ float2 spans[RUNS][CT];
@@ -766,28 +767,39 @@ __global__ __launch_bounds__(256) void rec_step_kernel(RecArgs a)
     static_cast<IO*>(a.h)[(size_t)b * a.D + c] = from_f32<IO>(h);
 }
 
-int tiles_of(int T, bool backward)
+// The tiles of a call: of channels and of tokens.
+struct Tiling {
+    int ctiles, runs, tiles;  // runs: the forward's
+};
+Tiling tiling(int B, int T, int D, bool backward)
 {
-    const int t = backward ? kBwdL * kBwdRuns : kFwdL * kFwdRuns;
-    return T > t ? (int)(((long long)T + t - 1) / t) : 1;
+    const int ct = D == 1 ? 32 : 64;
+    Tiling t;
+    t.ctiles = (D + ct - 1) / ct;
+    t.runs = fwd_runs((long long)B * t.ctiles);
+    const int tokens = backward ? kBwdRun * kBwdRuns : kFwdRun * t.runs;
+    t.tiles = T > tokens ? (int)(((long long)T + tokens - 1) / tokens) : 1;
+    return t;
 }
 
 template <typename IO, bool PRE, bool BLEND, int V>
 hipError_t launch(const RecArgs& a, bool backward, hipStream_t stream)
 {
-    const int ctiles = (a.D + 32 * V - 1) / (32 * V), tiles = tiles_of(a.T, backward);
-    const int columns = a.B * ctiles * 32 * V;
+    const Tiling t = tiling(a.B, a.T, a.D, backward);
+    const int columns = a.B * t.ctiles * 32 * V;
     // with fewer columns than XCDs some would have none of their own
-    const Chain ch = chain_at(a.ws, tiles, columns, a.B * ctiles < kQueues ? 1 : kQueues);
-    if (tiles > 1) {
-        const size_t n = chain_units(tiles, columns);
+    const Chain ch = chain_at(a.ws, t.tiles, columns, a.B * t.ctiles < kQueues ? 1 : kQueues);
+    if (t.tiles > 1) {
+        const size_t n = chain_units(t.tiles, columns);
         rec_clear_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(static_cast<uint4*>(a.ws), n);
     }
-    const unsigned grid = (unsigned)((size_t)tiles * a.B * ctiles);
+    const unsigned grid = (unsigned)t.tiles * a.B * t.ctiles;
     if (backward)
-        rec_bwd_kernel<IO, PRE, BLEND, V><<<grid, kBwdRuns * 32, 0, stream>>>(a, ch, ctiles);
+        rec_bwd_kernel<IO, PRE, BLEND, V><<<grid, kBwdRuns * 32, 0, stream>>>(a, ch, t.ctiles);
+    else if (t.runs == 8)
+        rec_fwd_kernel<IO, PRE, BLEND, V, 8><<<grid, 8 * 32, 0, stream>>>(a, ch, t.ctiles);
     else
-        rec_fwd_kernel<IO, PRE, BLEND, V><<<grid, kFwdRuns * 32, 0, stream>>>(a, ch, ctiles);
+        rec_fwd_kernel<IO, PRE, BLEND, V, 16><<<grid, 16 * 32, 0, stream>>>(a, ch, t.ctiles);
     return hipGetLastError();
 }
 
@@ -810,10 +822,14 @@ hipError_t launch_io(const RecArgs& a, bool backward, hipStream_t stream)
 
 size_t rec_workspace_bytes(int B, int T, int D, bool backward)
 {
-    const int tiles = tiles_of(T, backward), ct = D == 1 ? 32 : 64;
-    if (tiles == 1)
-        return 0;
-    return chain_units(tiles, B * ((D + ct - 1) / ct) * ct) * 16;
+    const Tiling t = tiling(B, T, D, backward);
+    return t.tiles == 1 ? 0 : chain_units(t.tiles, B * t.ctiles * (D == 1 ? 32 : 64)) * 16;
+}
+
+unsigned long long rec_threads(int B, int T, int D, bool backward)
+{
+    const Tiling t = tiling(B, T, D, backward);
+    return (unsigned long long)t.tiles * B * t.ctiles * 32 * (backward ? kBwdRuns : t.runs);
 }
 
 hipError_t launch_rec_fwd(const RecArgs& a, bool bf, hipStream_t stream)

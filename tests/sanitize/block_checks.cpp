@@ -208,6 +208,9 @@ static void rec_checks()
     BAD(WITH(Rec, c.ws = 0).fwd(), KDN_ERR_WORKSPACE, "workspace");
     BAD(WITH(Rec, c.ws_bytes = 1).bwd(), KDN_ERR_WORKSPACE, "workspace");
     BAD(WITH(Rec, c.ws = c.chk).bwd(), KDN_ERR_INVALID_ARG, "overlap");
+    BAD(WITH(Rec, (c.B = 1 << 23, c.T = 2, c.D = 64)).bwd(), KDN_ERR_UNSUPPORTED, "too many short rows");
+    BAD(WITH(Rec, (c.B = 1 << 24, c.T = 1, c.D = 1, c.xs = c.as = 1)).step(), KDN_ERR_UNSUPPORTED, "2^24");
+    BAD(WITH(Rec, (c.B = 1, c.T = (1 << 30) + 1, c.D = 1, c.xs = c.as = 1)).fwd(), KDN_ERR_UNSUPPORTED, "2^30");
     BAD(WITH(Rec, (c.T = INT_MAX)).fwd(), KDN_ERR_UNSUPPORTED, "2^31");
     if (kdn_rec_fwd_workspace_size(1, 10, 0) || kdn_rec_bwd_workspace_size(INT_MAX, INT_MAX, 4))
         ++failures, std::printf("FAILED rec workspace size of a bad shape\n");

@@ -21,6 +21,10 @@ hipError_t launch_conv_fwd(const ConvArgs&, bool, hipStream_t) { return reached(
 hipError_t launch_conv_bwd(const ConvArgs&, bool, hipStream_t) { return reached(); }
 hipError_t launch_conv_step(const ConvArgs&, bool, hipStream_t) { return reached(); }
 size_t rec_workspace_bytes(int, int T, int, bool) { return T > 256 ? 4096 : 0; }
+unsigned long long rec_threads(int B, int T, int D, bool)
+{
+    return 256ull * B * (T / 128 + 1) * (D / 64 + 1);
+}
 hipError_t launch_rec_fwd(const RecArgs&, bool, hipStream_t) { return reached(); }
 hipError_t launch_rec_bwd(const RecArgs&, bool, hipStream_t) { return reached(); }
 hipError_t launch_rec_step(const RecArgs&, bool, hipStream_t) { return reached(); }
