@@ -25,8 +25,8 @@ namespace kdn {
 
 namespace {
 
-constexpr int kBatch = 4;  // rows loaded together (at least W - 1); a run is a multiple of twice that
-constexpr int kMostTokens = 32 * 16;  // of a workgroup's tile
+constexpr int kBatch = 4;  // rows loaded together (at least W - 1); a run is a multiple of it
+constexpr int kMostTokens = 1024, kMostRun = 128;  // of a workgroup's tile, of a run
 
 // VE adjacent values as they are in memory, at any alignment of an element
 template <typename E, int VE>
@@ -599,29 +599,31 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a)
 // ---- shapes ------------------------------------------------------------------------
 
 // Threads side by side on a row: as many as its vectors, 8 to 64.  Runs as long as
-// leave two workgroups for every compute unit, 8 or 16 tokens: a longer one reads
-// fewer rows twice and writes its sums once for more tokens, but then the chip
-// holds fewer of them (4 x 4096 x 2048 fp32 with 16 and 32 tokens: forward 52.5 and
-// 54.9 us, backward 99 and 113 us).
-Plan plan_of(int M, int D, int ve)
+// give each place for a workgroup on the chip three of them, 8 to 128 tokens.  A
+// longer run reads fewer of the rows before it twice and writes the backward's sums
+// once for more tokens, but the workgroups at work then reach over more memory at a
+// time (32768 x 2048 bf16, one, two and three a place: forward 58, 54 and 52 us,
+// backward 122, 107 and 101 us).
+Plan plan_of(int M, int D, int ve, bool backward)
 {
+    const int wanted = 3 * 256 * (backward ? 3 : 4);  // places a compute unit, by the registers
     Plan p;
     const int vecs = (D + ve - 1) / ve;
     p.lanes_log2 = vecs <= 8 ? 3 : vecs <= 16 ? 4 : vecs <= 32 ? 5 : 6;
     p.ctiles = (vecs + (1 << p.lanes_log2) - 1) >> p.lanes_log2;
-    const int runs = 256 >> p.lanes_log2;
-    p.batches = 16 / kBatch;
-    auto tiles = [&] { return (M + (long long)runs * p.batches * kBatch - 1) / (runs * p.batches * kBatch); };
-    while (p.batches > 2 && tiles() * p.ctiles < 512)
-        p.batches /= 2;
-    p.tiles = M ? (int)tiles() : 1;
+    const int runs = 256 >> p.lanes_log2, most = kMostTokens / runs < kMostRun ? kMostTokens / runs : kMostRun;
+    long long length = ((long long)M / runs * p.ctiles + wanted - 1) / wanted;
+    length = (length + kBatch - 1) / kBatch * kBatch;
+    p.batches = (int)(length < 8 ? 8 : length > most ? most : length) / kBatch;
+    const long long per = (long long)runs * p.batches * kBatch;
+    p.tiles = M ? (int)((M + per - 1) / per) : 1;
     return p;
 }
 
 template <typename IO, int VE, int W, bool SILU>
 void launch(const ConvArgs& a, bool backward, hipStream_t stream)
 {
-    const Plan p = plan_of(a.B * a.T, a.D, VE);
+    const Plan p = plan_of(a.B * a.T, a.D, VE, backward);
     const unsigned grid = (unsigned)p.tiles * p.ctiles;
     if (!backward) {
         conv_fwd_kernel<IO, VE, W, SILU><<<grid, 256, 0, stream>>>(a, p);
@@ -660,7 +662,7 @@ hipError_t launch_io(const ConvArgs& a, bool backward, hipStream_t stream)
 
 int conv_bwd_groups(int B, int T, int D)
 {
-    return T ? plan_of(B * T, D, vector_of(D)).tiles : 0;
+    return T ? plan_of(B * T, D, vector_of(D), true).tiles : 0;
 }
 
 hipError_t launch_conv_fwd(const ConvArgs& a, bool bf, hipStream_t stream)
