@@ -577,23 +577,51 @@ __global__ __launch_bounds__(1024) void conv_sum_kernel(ConvArgs a, int tiles)
 
 // ---- one token ---------------------------------------------------------------------
 
-template <typename IO>
+// Four channels a thread (at the end of a row as many as are left, one by one: the
+// state is moved on in place, so no two threads may have the same channel).  256 x
+// 6144 bf16, four taps: 25 MB.
+constexpr int kStepVec = 4;
+
+template <typename IO, int W>
 __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a)
 {
-    const int c = blockIdx.y * 256 + threadIdx.x, b = blockIdx.x, W = a.W;
-    if (c >= a.D)
-        return;
-    IO* st = static_cast<IO*>(a.state_T) + (size_t)b * (W - 1) * a.D + c;
-    float z = a.bias ? a.bias[c] : 0.f;
-    IO next = static_cast<const IO*>(a.x)[(size_t)b * a.xs + c];
-    z = fmaf(a.weight[(size_t)(W - 1) * a.D + c], to_f32(next), z);
-    for (int i = W - 2; i >= 0; --i) {
-        const IO old = st[(size_t)i * a.D];
-        z = fmaf(a.weight[(size_t)i * a.D + c], to_f32(old), z);
-        st[(size_t)i * a.D] = next;
-        next = old;
+    constexpr int VE = kStepVec;
+    const int c0 = (blockIdx.y * 256 + threadIdx.x) * VE, b = blockIdx.x;
+    auto step = [&](auto ve, int c) {
+        constexpr int N = decltype(ve)::value;
+        IO* st = static_cast<IO*>(a.state_T) + (size_t)b * (W - 1) * a.D + c;
+        Vec<IO, N> in[W];
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+            in[k] = load_vec<IO, N>(st + (size_t)k * a.D);
+        in[W - 1] = load_vec<IO, N>(static_cast<const IO*>(a.x) + (size_t)b * a.xs + c);
+        float z[N];
+        load_or_zero<float, N>(a.bias + c, a.bias, z);
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            float w[N], x[N];
+            load_or_zero<float, N>(a.weight + (size_t)k * a.D + c, true, w);
+            widen<IO, N>(in[k], x);
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                z[j] = fmaf(w[j], x[j], z[j]);
+        }
+        if (a.silu) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                z[j] = silu(z[j]);
+        }
+        store_vec<IO, N>(static_cast<IO*>(a.y) + (size_t)b * a.D + c, z);
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+            *reinterpret_cast<Vec<IO, N>*>(st + (size_t)k * a.D) = in[k + 1];
+    };
+    if (c0 + VE <= a.D) {
+        step(std::integral_constant<int, VE>{}, c0);
+    } else {
+        for (int c = c0; c < a.D; ++c)
+            step(std::integral_constant<int, 1>{}, c);
     }
-    static_cast<IO*>(a.y)[(size_t)b * a.D + c] = from_f32<IO>(a.silu ? silu(z) : z);
 }
 
 // ---- shapes ------------------------------------------------------------------------
@@ -675,14 +703,22 @@ hipError_t launch_conv_bwd(const ConvArgs& a, bool bf, hipStream_t stream)
     return bf ? launch_io<bf16>(a, true, stream) : launch_io<float>(a, true, stream);
 }
 
+template <typename IO>
+static hipError_t conv_step(const ConvArgs& a, hipStream_t stream)
+{
+    const dim3 grid(a.B, (a.D + 256 * kStepVec - 1) / (256 * kStepVec));
+    if (a.W == 2)
+        conv_step_kernel<IO, 2><<<grid, 256, 0, stream>>>(a);
+    else if (a.W == 3)
+        conv_step_kernel<IO, 3><<<grid, 256, 0, stream>>>(a);
+    else
+        conv_step_kernel<IO, 4><<<grid, 256, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
 hipError_t launch_conv_step(const ConvArgs& a, bool bf, hipStream_t stream)
 {
-    const dim3 grid(a.B, (a.D + 255) / 256);
-    if (bf)
-        conv_step_kernel<bf16><<<grid, 256, 0, stream>>>(a);
-    else
-        conv_step_kernel<float><<<grid, 256, 0, stream>>>(a);
-    return hipGetLastError();
+    return bf ? conv_step<bf16>(a, stream) : conv_step<float>(a, stream);
 }
 
 }  // namespace kdn

@@ -752,19 +752,39 @@ __global__ __launch_bounds__(kBwdRuns * 32, 4) void rec_bwd_kernel(RecArgs a, Ch
 
 // ---- one token ---------------------------------------------------------------------
 
+// Four channels a thread (at a row's end those left, one by one: the state is
+// updated in place, so no two threads may have the same channel).
+constexpr int kStepVec = 4;
+
 template <typename IO, bool PRE>
 __global__ __launch_bounds__(256) void rec_step_kernel(RecArgs a)
 {
     typedef typename std::conditional<PRE, IO, float>::type GT;
-    const int c = blockIdx.y * 256 + threadIdx.x, b = blockIdx.x;
-    if (c >= a.D)
-        return;
-    float alpha, rest;
-    gate_of<PRE>(to_f32(static_cast<const GT*>(a.a)[(size_t)b * a.as + c]), alpha, rest);
-    const float x = to_f32(static_cast<const IO*>(a.x)[(size_t)b * a.xs + c]);
-    const float h = fmaf(alpha, a.h_T[(size_t)b * a.D + c], a.blend ? rest * x : x);
-    a.h_T[(size_t)b * a.D + c] = h;
-    static_cast<IO*>(a.h)[(size_t)b * a.D + c] = from_f32<IO>(h);
+    constexpr int VE = kStepVec;
+    const int c0 = (blockIdx.y * 256 + threadIdx.x) * VE, b = blockIdx.x;
+    auto step = [&](auto ve, int c) {
+        constexpr int N = decltype(ve)::value;
+        float* st = a.h_T + (size_t)b * a.D + c;
+        const auto ra = load_at<GT, N>(reinterpret_cast<const char*>(static_cast<const GT*>(a.a) + (size_t)b * a.as + c), 0);
+        const auto rx = load_at<IO, N>(reinterpret_cast<const char*>(static_cast<const IO*>(a.x) + (size_t)b * a.xs + c), 0);
+        const auto rs = load_at<float, N>(reinterpret_cast<const char*>(st), 0);
+        float h[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            float alpha, rest;
+            gate_of<PRE>(to_f32(ra.v[j]), alpha, rest);
+            const float x = to_f32(rx.v[j]);
+            h[j] = fmaf(alpha, rs.v[j], a.blend ? rest * x : x);
+        }
+        store_at<float, N>(reinterpret_cast<char*>(st), 0, h);
+        store_at<IO, N>(reinterpret_cast<char*>(static_cast<IO*>(a.h) + (size_t)b * a.D + c), 0, h);
+    };
+    if (c0 + VE <= a.D) {
+        step(std::integral_constant<int, VE>{}, c0);
+    } else {
+        for (int c = c0; c < a.D; ++c)
+            step(std::integral_constant<int, 1>{}, c);
+    }
 }
 
 // The tiles of a call: of channels and of tokens.
@@ -844,7 +864,7 @@ hipError_t launch_rec_bwd(const RecArgs& a, bool bf, hipStream_t stream)
 
 hipError_t launch_rec_step(const RecArgs& a, bool bf, hipStream_t stream)
 {
-    const dim3 grid(a.B, (a.D + 255) / 256);
+    const dim3 grid(a.B, (a.D + 256 * kStepVec - 1) / (256 * kStepVec));
     if (bf)
         a.preact ? rec_step_kernel<bf16, true><<<grid, 256, 0, stream>>>(a)
                  : rec_step_kernel<bf16, false><<<grid, 256, 0, stream>>>(a);
