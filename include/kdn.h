@@ -421,7 +421,8 @@ kdn_status kdn_gain_scan_static(int variant, int B, int T, int H, int dk, int io
  *   - io dtype KDN_F32 or KDN_BF16 (no flags); parameters (weight, bias),
  *     statistics and recurrent states are fp32; all arithmetic is fp32 and a
  *     value is rounded once, when it is stored.
- *   - Any channel count D from 1 to 2^20, B below 2^24, B T up to 2^30.  Pointers need only their element's alignment
+ *   - Any channel count D from 1 to 2^20; rows, or B T, up to 2^30; B below
+ *     2^24.  Pointers need only their element's alignment
  *     (workspaces: 16 bytes); 16-byte alignment and D a multiple of 8 run
  *     fastest.
  *   - Inputs marked "rows of D, `stride` apart" may be slices of wider rows

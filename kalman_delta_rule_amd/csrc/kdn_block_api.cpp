@@ -17,7 +17,7 @@ using kdn::ok;
 
 constexpr long long kMaxElems = 1ll << 31;  // of every dense tensor
 constexpr long long kMaxStride = 1ll << 22;  // kernels step over a tile of rows with 32-bit byte offsets
-constexpr int kMaxD = 1 << 20;
+constexpr int kMaxD = 1 << 20, kMaxTokens = 1 << 30;
 
 // One buffer of a call: its bytes (0: not given) and what the call does to it.
 struct Buf {
@@ -99,7 +99,7 @@ kdn_status check_sequence(int B, int T, int D, const int* cu, int& N)
     if ((__int128)B * T * D >= kMaxElems || (__int128)N * D >= kMaxElems)
         return fail(KDN_ERR_UNSUPPORTED, "tensor sizes must stay below 2^31 elements");
     // token numbers, and those a tile further, are ints; a row is a workgroup or more
-    if ((long long)B * T > 1ll << 30 || B >= 1 << 24)
+    if ((long long)B * T > kMaxTokens || B >= 1 << 24)
         return fail(KDN_ERR_UNSUPPORTED, "B T is at most 2^30 and B below 2^24 (got B=%d T=%d)", B, T);
     return KDN_OK;
 }
@@ -137,6 +137,8 @@ kdn_status check_norm(int rows, int D, int io)
     KDN_TRY(check_width(D));
     if ((long long)rows * D >= kMaxElems)
         return fail(KDN_ERR_UNSUPPORTED, "tensor sizes must stay below 2^31 elements");
+    if (rows > kMaxTokens)  // row numbers, and those a stride further, are ints
+        return fail(KDN_ERR_UNSUPPORTED, "rows is at most 2^30, got %d", rows);
     return KDN_OK;
 }
 
@@ -191,7 +193,7 @@ kdn_status kdn_layer_norm_fwd(int rows, int D, int io_dtype, float eps, const vo
 
 size_t kdn_layer_norm_bwd_workspace_size(int rows, int D)
 {
-    if (rows < 0 || D < 1 || D > kMaxD || (long long)rows * D >= kMaxElems)
+    if (rows < 0 || rows > kMaxTokens || D < 1 || D > kMaxD || (long long)rows * D >= kMaxElems)
         return 0;
     return (size_t)kdn::norm_bwd_groups(rows, D) * 2 * D * sizeof(float);
 }
@@ -259,7 +261,8 @@ kdn_status kdn_conv_fwd(int B, int T, int D, int W, int io_dtype, int activation
 
 size_t kdn_conv_bwd_workspace_size(int B, int T, int D, int W)
 {
-    if (B < 1 || T < 0 || D < 1 || D > kMaxD || W < 2 || W > 4 || (__int128)B * T * D >= kMaxElems)
+    if (B < 1 || T < 0 || D < 1 || D > kMaxD || W < 2 || W > 4 ||
+        (__int128)B * T * D >= kMaxElems || (long long)B * T > kMaxTokens)
         return 0;
     return (size_t)kdn::conv_bwd_groups(B, T, D) * (W + 1) * D * sizeof(float);
 }
@@ -339,7 +342,8 @@ static kdn_status check_rec_grid(int B, int T, int D, bool backward)
 
 static size_t rec_workspace_size(int B, int T, int D, bool backward)
 {
-    if (B < 1 || T < 0 || D < 1 || D > kMaxD || (__int128)B * T * D >= kMaxElems)
+    if (B < 1 || T < 0 || D < 1 || D > kMaxD || (__int128)B * T * D >= kMaxElems ||
+        (long long)B * T > kMaxTokens)
         return 0;
     return kdn::rec_workspace_bytes(B, T, D, backward);
 }

@@ -19,7 +19,8 @@
 // A run without a sequence's border in reach goes the plain way, four tokens at a
 // time; the others look for a mark at every token: at a sequence's start the last inputs come
 // from its state, at its end they go there.
-#include "kdn_block_device.h"
+#include "kdn_block.h"
+#include "kdn_common.h"
 
 namespace kdn {
 

@@ -11,7 +11,8 @@
 // thread's columns) in registers all along.  The backward's sums are joined over
 // the workgroup at the end and written once a workgroup; a second launch adds
 // those, always in the same order.
-#include "kdn_block_device.h"
+#include "kdn_block.h"
+#include "kdn_common.h"
 
 namespace kdn {
 
@@ -495,13 +496,13 @@ hipError_t norm_fwd(const NormArgs& a, hipStream_t stream)
 }
 
 // workgroups of the backward (and partial sums): two a compute unit, or the one
-// that fits with several vectors a thread
+// that fits with several vectors a thread; for rows too wide for registers, so few
+// that the partial sums stay small beside the rows
 int bwd_groups(int rows, Shape s)
 {
-    const int per = s.tpr ? kBwdThreads / s.tpr : 1;
-    const long long groups = ((long long)rows + per - 1) / per;
-    const int most = s.nv == 1 ? 512 : 256;
-    return groups < most ? (int)groups : most;
+    const int per = s.tpr ? kBwdThreads / s.tpr : 16;
+    const int groups = (rows - 1) / per + 1, most = s.nv == 1 ? 512 : 256;  // (0 for no rows)
+    return rows < 1 ? 0 : groups < most ? groups : most;
 }
 
 template <typename IO>

@@ -27,7 +27,8 @@
 // a span with A = 0 gives U whatever it is handed: nothing, infinities and
 // NaN included, passes from one sequence to another.
 #include "kdn.h"
-#include "kdn_block_device.h"
+#include "kdn_block.h"
+#include "kdn_common.h"
 
 namespace kdn {
 

@@ -73,6 +73,7 @@ static void norm_checks()
     BAD(WITH(Norm, c.D = 0).fwd(), KDN_ERR_INVALID_ARG, "D >= 1");
     BAD(WITH(Norm, (c.D = 1 << 21, c.xs = 1 << 21)).fwd(), KDN_ERR_UNSUPPORTED, "2^20");
     BAD(WITH(Norm, (c.rows = INT_MAX)).bwd(), KDN_ERR_UNSUPPORTED, "2^31");
+    BAD(WITH(Norm, (c.rows = (1 << 30) + 1, c.D = 1, c.xs = 1)).fwd(), KDN_ERR_UNSUPPORTED, "2^30");
     BAD(WITH(Norm, c.eps = -1.f).fwd(), KDN_ERR_INVALID_ARG, "eps");
     BAD(WITH(Norm, c.eps = std::nanf("")).fwd(), KDN_ERR_INVALID_ARG, "eps");
     BAD(WITH(Norm, c.xs = 63).fwd(), KDN_ERR_INVALID_ARG, "x_stride");
