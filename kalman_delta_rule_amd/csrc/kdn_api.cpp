@@ -10,6 +10,7 @@
 #include <initializer_list>
 
 #include "kdn.h"
+#include "kdn_errors.h"
 #include "kdn_internal.h"
 #include "kdn_ops.h"
 

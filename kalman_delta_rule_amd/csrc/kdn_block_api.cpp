@@ -8,7 +8,7 @@
 
 #include "kdn.h"
 #include "kdn_block.h"
-#include "kdn_internal.h"
+#include "kdn_errors.h"
 
 namespace {
 

@@ -8,14 +8,7 @@
 #include <atomic>
 #include <stdint.h>
 
-#include "kdn.h"
-
 namespace kdn {
-
-// The calling thread's error message (kdn_last_error_message): fail() sets it
-// and returns the status, ok() clears it and returns KDN_OK.
-kdn_status fail(kdn_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-kdn_status ok();
 
 // Raise a kernel's dynamic-LDS limit to `bytes`, once per device and kernel
 // (the attribute holds for the process); later launches skip the call.
