@@ -229,14 +229,42 @@ struct Rows {
     }
 };
 
+// The rows before every run of a workgroup, which the run ahead of it ends with: read
+// once, by the run behind, and handed on through LDS (slot d - 1: d tokens before
+// the run, a thread its own channels).
+template <typename IO, int VE, int ROWS>
+struct Handed {
+    struct alignas(sizeof(IO) * VE) Row {
+        IO v[VE];
+    };
+    Row rows[ROWS][256];
+
+    __device__ __forceinline__ void put(int d, const Vec<IO, VE>& x)
+    {
+#pragma unroll
+        for (int j = 0; j < VE; ++j)
+            rows[d - 1][threadIdx.x].v[j] = x.v[j];
+    }
+    // of the run behind this thread's
+    __device__ __forceinline__ Vec<IO, VE> get(int d, int lanes) const
+    {
+        Vec<IO, VE> x;
+#pragma unroll
+        for (int j = 0; j < VE; ++j)
+            x.v[j] = rows[d - 1][threadIdx.x + lanes].v[j];
+        return x;
+    }
+};
+
 // ---- forward ------------------------------------------------------------------
 
 template <typename IO, int VE, int W, bool SILU>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, Plan plan)
 {
     __shared__ Marks marks;
+    __shared__ Handed<IO, VE, W - 1> handed;
     const Place<VE> at(plan, a.D);
-    const int M = a.B * a.T;
+    const int M = a.B * a.T, lanes = 1 << plan.lanes_log2;
     Filter<IO, VE, W> f;
     f.init(a, at.c);
 
@@ -250,11 +278,15 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, Plan plan)
         for (int i = 0; i < kBatch; ++i)
             next[i] = rows.near(at.m + i);
         mark_tokens(marks, a, at.m0 - (W - 1), at.runs * at.length + W - 1);
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+            handed.put(W - 1 - k, before[k]);
+        __syncthreads();
         const int base = at.run * at.length;  // mark of the first token before the run
         const int limit = token_limit(a);
         // (a run at the row's front has a mark, so a plain one has tokens all around it)
         const bool plain = !__any(at.m + at.length > limit ||
-                                  any_mark(marks, base, at.length + W - 1, at.lane, 1 << plan.lanes_log2));
+                                  any_mark(marks, base, at.length + W - 1, at.lane, lanes));
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
             float x[VE];
@@ -272,11 +304,10 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, Plan plan)
                 for (int i = 0; i < kBatch; ++i)
                     now[i] = next[i];
                 if (q + 1 < plan.batches) {
+                    const bool ends = q + 2 == plan.batches && at.run + 1 < at.runs;
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        next[i] = load_vec<IO, VE>(ahead);
-                        ahead += a.xs;
-                    }
+                    for (int i = 0; i < kBatch; ++i, ahead += a.xs)
+                        next[i] = ends && kBatch - i < W ? handed.get(kBatch - i, lanes) : load_vec<IO, VE>(ahead);
                 }
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i, y += a.D) {
@@ -342,6 +373,8 @@ template <typename IO, int VE, int W, bool SILU>
 __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs a, Plan plan)
 {
     __shared__ Marks marks;
+    __shared__ Handed<IO, VE, 2 * (W - 1)> handed_x;
+    __shared__ Handed<IO, VE, W - 1> handed_y;
     const Place<VE> at(plan, a.D);
     const int M = a.B * a.T;
     const int lanes = 1 << plan.lanes_log2;
@@ -371,6 +404,13 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs a, Plan plan)
             ny[i] = grads.near(at.m + i);
         }
         mark_tokens(marks, a, at.m0 - 2 * (W - 1), at.runs * at.length + 2 * (W - 1));
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) {
+            handed_x.put(2 * (W - 1) - k, before[k]);
+            handed_x.put(W - 1 - k, wx[k]);
+            handed_y.put(W - 1 - k, wy[k]);
+        }
+        __syncthreads();
         const int base = at.run * at.length;  // mark of the first token loaded
         const int limit = token_limit(a);
         const bool plain = !__any(at.m + at.length > limit ||
@@ -434,12 +474,12 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs a, Plan plan)
                 for (int i = 0; i < kBatch; ++i)
                     cx[i] = nx[i], cy[i] = ny[i];
                 if (q + 1 < plan.batches) {
+                    const bool ends = q + 2 == plan.batches && at.run + 1 < at.runs;
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        nx[i] = load_vec<IO, VE>(ax);
-                        ny[i] = load_vec<IO, VE>(ay);
-                        ax += a.xs;
-                        ay += a.D;
+                    for (int i = 0; i < kBatch; ++i, ax += a.xs, ay += a.D) {
+                        const int d = kBatch - i;
+                        nx[i] = ends && d <= 2 * (W - 1) ? handed_x.get(d <= 2 * (W - 1) ? d : 1, lanes) : load_vec<IO, VE>(ax);
+                        ny[i] = ends && d < W ? handed_y.get(d < W ? d : 1, lanes) : load_vec<IO, VE>(ay);
                     }
                 }
 #pragma unroll
