@@ -668,14 +668,14 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a)
 // ---- shapes ------------------------------------------------------------------------
 
 // Threads side by side on a row: as many as its vectors, 8 to 64.  Runs as long as
-// give each place for a workgroup on the chip three of them, 8 to 128 tokens.  A
-// longer run reads fewer of the rows before it twice and writes the backward's sums
-// once for more tokens, but the workgroups at work then reach over more memory at a
-// time (32768 x 2048 bf16, one, two and three a place: forward 58, 54 and 52 us,
-// backward 122, 107 and 101 us).
+// give each place for a workgroup on the chip four of them, 8 to 128 tokens.  A
+// longer run has fewer tokens before it to go through twice and writes the
+// backward's sums once for more tokens, but the workgroups at work then reach over
+// more memory at a time (one, three, four and eight a place: backward of 32768 x
+// 2048 bf16 122, 102, 101 and 112 us, of 4 x 4096 x 2048 fp32 122, 97, 88 and 90 us).
 Plan plan_of(int M, int D, int ve, bool backward)
 {
-    const int wanted = 3 * 256 * (backward ? 3 : 4);  // places a compute unit, by the registers
+    const int wanted = 4 * 256 * (backward ? 3 : 4);  // places a compute unit, by the registers
     Plan p;
     const int vecs = (D + ve - 1) / ve;
     p.lanes_log2 = vecs <= 8 ? 3 : vecs <= 16 ? 4 : vecs <= 32 ? 5 : 6;
