@@ -30,6 +30,10 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _need(t: torch.Tensor, name: str, shape, dtype, device) -> None:
+    # the usual case in one go: single-token calls are bound by these checks
+    if (type(t) is torch.Tensor and t.dtype == dtype and t.shape == shape
+            and t.is_contiguous() and t.device == device):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.device != device:
@@ -56,6 +60,7 @@ def _math_flag(math: Optional[str]) -> int:
 # torch's own accessor of a device's current stream handle: current_stream()
 # builds a Stream object around it, 1.9 us of a 10 us single-token call
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(device) -> int:
@@ -66,7 +71,7 @@ def _stream(device) -> int:
 
 def _launch(dev, fn, *args) -> None:
     """fn(*args, stream) on dev, whichever device is current."""
-    if torch.cuda.current_device() == dev.index:
+    if _current_device() == dev.index:
         st = fn(*args, _stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -559,6 +564,9 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
 
 def _need_rows(t, name, shape, dtype, device) -> int:
     """_need for a tensor that may be a slice of wider rows; the row stride."""
+    if (type(t) is torch.Tensor and t.dtype == dtype and t.shape == shape
+            and t.is_contiguous() and t.device == device):
+        return shape[-1]
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.device != device:
