@@ -13,15 +13,23 @@
 // start; then the runs are walked again, from the same registers, with their
 // outputs stored.  Inputs are read once and outputs written once.
 //
-// Tiles of the same channels are chained through the workspace (tile_carry):
-// each publishes its (A, U), the last of 8 that of the whole group, and the last
-// of 64 the value behind it.  A tile's start is that value of the 64 before, with
-// the (A, U) of the groups and tiles between applied in token order: always
-// the same operations, so results do not depend on timing, and few steps that
-// wait for one another (one in 64 tiles, about 2 us each, the time of a word
-// from one XCD to the next).  A word is 4 or 8 bytes, stored and loaded whole (relaxed, agent
-// scope: it may cross to another XCD's L2), and is its own flag: a launch before
-// sets them to all ones, which no published word is (a NaN is made canonical).
+// Tiles of the same channels are chained through the workspace (Link): each
+// publishes its (A, U), the last of 8 that of the whole group, and the last of 64
+// the value behind it.  A tile's start is that value of the 64 before, with the
+// (A, U) of the groups and tiles between applied in token order: always the same
+// operations, so results do not depend on timing, and few steps that wait for
+// one another (one in 64 tiles, about 2 us each, the time of a word from one XCD
+// to the next; chained by groups of 8 alone, B1 T65536 D64 took 117 us instead of
+// 37).  A word is 4 or 8 bytes, stored and loaded whole (relaxed, agent scope: it
+// may cross to another XCD's L2), and is its own flag: a launch before sets them
+// to all ones, which no published word is (a NaN is made canonical).
+//
+// Bound by HBM and by the time from load to store of the tiles that the registers
+// hold at a time.  Measured (kernel time; bytes of inputs and outputs): forward B8
+// T4096 D2048 bf16 90 us (4.5 TB/s), B1 T65536 180 us (4.5 TB/s); backward 153 us
+// (4.4 TB/s) and 311 us (4.3 TB/s).  Loading the next tile ahead in a workgroup that
+// stays (128 registers, or 8 tokens a run) was slower, 111 us and more; a scratch
+// access anywhere in the walks costs half the speed.
 //
 // Where a sequence starts (forward) or ends (backward) inside a span, A is 0, and
 // a span with A = 0 gives U whatever it is handed: nothing, infinities and
@@ -37,7 +45,7 @@ namespace {
 constexpr int kChk = KDN_REC_CHECKPOINT;
 constexpr int kGroup = 8;    // tiles of a group of the chain, groups of a block
 constexpr int kBlock = kGroup * kGroup;
-constexpr int kPolls = 1 << 21;
+constexpr int kPolls = 1 << 18;  // about 1 us each
 
 // ---- the chain through the workspace ----------------------------------------
 

@@ -136,6 +136,11 @@ SEQ_CASES = [(2, 0, 5, None), (3, 1, 4, None), (2, 2, 1, None), (1, 3, 3, None),
              (2, 16, 64, None), (1, 17, 130, None), (2, 64, 8, None), (3, 65, 33, None),
              (1, 200, 100, None), (2, 256, 66, None), (1, 257, 129, None), (2, 700, 72, None),
              (1, 1500, 31, None), (1, 0, 6, [0, 0, 0]), (1, 1, 6, [0, 0, 1])]
+# more sequences than a workgroup has threads; many rows (the recurrence's short tiles);
+# a single channel; several tiles of channels
+SEQ_CASES += [(1, 2000, 6, [0] + sorted(np.random.default_rng(8).integers(0, 1990, 1500).tolist()) + [1995]),
+              (200, 300, 5, None), (193, 1, 3, None), (1, 300, 1, None), (1, 300, 1, [0, 0, 7, 290]),
+              (1, 150, 12300, None), (1, 90, 520, [0, 33, 90])]
 SEQ_CASES += [(1, T, D, cu) for T, D in ((7, 9), (64, 16), (259, 40), (600, 70), (1301, 12)) for cu in layouts(T)]
 
 
@@ -190,6 +195,42 @@ def test_conv(case, W, silu, io):
     if b is not None:
         R.check(host(g["dbias"]), ref["dbias"], "f32", "dbias")
         R.check(host(g["dstate0"]), ref["dstate0"], io, "dstate0")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_conv_long_runs_are_the_short_ones(io):
+    """A call large enough for runs of many tokens against calls on pieces of it,
+    which have the shortest: the same operations for every y and dx, so the
+    same bits; the sums to their rounding."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    T, D, W = 40000, 2048, 4
+    x = torch.randn(1, T, D, generator=g, device="cuda").to(DT[io])
+    dy = torch.randn(1, T, D, generator=g, device="cuda").to(DT[io])
+    w, b = torch.randn(W, D, generator=g, device="cuda"), torch.randn(D, generator=g, device="cuda")
+    cut = 17001
+    cu = offsets([0, cut, T])
+    y, _ = kda.kdn_conv_fwd(x, w, bias=b, cu_seqlens=cu, activation="silu")
+    q = kda.kdn_conv_bwd(dy, x, w, bias=b, cu_seqlens=cu, activation="silu")
+    for p in (0, 5000, 16900, cut, 39000):
+        end = min(p + 1000, cut if p < cut else T)
+        reach = min(end + W - 1, cut if p < cut else T)  # dx takes what follows in the sequence
+        piece = x[:, p:reach].contiguous()
+        kw = dict(bias=b, activation="silu")
+        if p not in (0, cut):
+            kw["state0"] = x[:, p - W + 1:p].contiguous()
+        s, _ = kda.kdn_conv_fwd(piece, w, **kw)
+        assert same(y[:, p:end], s[:, :end - p]), p
+        d = kda.kdn_conv_bwd(dy[:, p:reach].contiguous(), piece, w, **kw)["dx"]
+        # (a piece's first tokens lack nothing: dx looks ahead only)
+        assert same(q["dx"][:, p:end], d[:, :end - p]), p
+    halves = [kda.kdn_conv_bwd(dy[:, p:e].contiguous(), x[:, p:e].contiguous(), w, bias=b, activation="silu")
+              for p, e in ((0, cut), (cut, T))]
+    for k in ("dweight", "dbias"):
+        # each side is off by at most its longest chain of additions times the sum of
+        # magnitudes; a chain has under 128 + 16 + 400 / 16 + 20 terms
+        size = (dy.float().abs() * 1.1).sum((0, 1)) * (x.float().abs().max() if k == "dweight" else 1)
+        off = (q[k].double() - halves[0][k].double() - halves[1][k].double()).abs()
+        assert (off <= 2 * 200 * R.U * size.double()).all(), k
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
@@ -257,10 +298,12 @@ def test_rec(case, gate, blend, io):
     R.check(host(g["dh0"]), ref["dh0"], "f32", "dh0")
 
 
-@pytest.mark.parametrize("T", [4096, 5000])
+@pytest.mark.parametrize("T", [4096, 5000, 20000])
 def test_rec_long(T):
-    # many tiles and joins of spans; decays close to one carry across all of them
-    for case, io in (((1, T, 64, None), "f32"), ((1, T, 10, [0, 3, 900, 900, 2500, T - 7]), "bf16")):
+    # many tiles, groups and (beyond 64 tiles) blocks of them; decays close to one
+    # carry across all of them
+    D = 64 if T < 10000 else 3
+    for case, io in (((1, T, D, None), "f32"), ((1, T, 10, [0, 3, 900, 900, 2500, T - 7]), "bf16")):
         (x, a, dh, h0, dT), (xr, ar, dhr, h0r, dTr) = rec_data(case, io, True, T)
         ref = R.rec(xr, ar, h0r, case[3], True, True, dhr, dTr)
         kw = dict(cu_seqlens=offsets(case[3]), blend=True)
