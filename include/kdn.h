@@ -427,7 +427,8 @@ kdn_status kdn_gain_scan_static(int variant, int B, int T, int H, int dk, int io
  *     fastest.
  *   - Inputs marked "rows of D, `stride` apart" may be slices of wider rows
  *     (one third of a fused projection, say): row i starts at element
- *     i * stride, D <= stride <= 2^22.  Everything else is dense.
+ *     i * stride, D <= stride <= 2^30 (2^22 in kdn_rec_fwd and kdn_rec_bwd).
+ *     Everything else is dense.
  *   - No output may overlap any other buffer, unless a call says so.
  *   - Packed sequences: with `cu_seqlens` (device, int32 [N+1], N >= 1) B must
  *     be 1, and sequence n is the tokens cu_seqlens[n] .. cu_seqlens[n+1] - 1

@@ -16,7 +16,9 @@ using kdn::fail;
 using kdn::ok;
 
 constexpr long long kMaxElems = 1ll << 31;  // of every dense tensor
-constexpr long long kMaxStride = 1ll << 22;  // kernels step over a tile of rows with 32-bit byte offsets
+constexpr long long kMaxStride = 1ll << 30;
+// the recurrence steps over a tile of rows with 32-bit byte offsets
+constexpr long long kMaxRecStride = 1ll << 22;
 constexpr int kMaxD = 1 << 20, kMaxTokens = 1 << 30;
 
 // One buffer of a call: its bytes (0: not given) and what the call does to it.
@@ -71,12 +73,13 @@ kdn_status check_width(int D)
 }
 
 // rows of D elements, stride apart: the elements from the first to the last
-kdn_status check_rows(long long rows, int D, long long stride, const char* name, long long& span)
+kdn_status check_rows(long long rows, int D, long long stride, const char* name, long long& span,
+                      long long most = kMaxStride)
 {
     if (stride < D)
         return fail(KDN_ERR_INVALID_ARG, "%s_stride must be at least D = %d, got %lld", name, D, stride);
-    if (stride > kMaxStride)
-        return fail(KDN_ERR_UNSUPPORTED, "%s_stride is at most 2^22, got %lld", name, stride);
+    if (stride > most)
+        return fail(KDN_ERR_UNSUPPORTED, "%s_stride is at most %lld, got %lld", name, most, stride);
     span = rows ? (rows - 1) * stride + D : 0;
     return KDN_OK;
 }
@@ -359,8 +362,8 @@ kdn_status kdn_rec_fwd(int B, int T, int D, int io_dtype, int gate, int blend, c
     KDN_TRY(check_rec(io_dtype, gate, blend));
     KDN_TRY(check_sequence(B, T, D, cu_seqlens, N));
     long long xspan, aspan;
-    KDN_TRY(check_rows((long long)B * T, D, x_stride, "x", xspan));
-    KDN_TRY(check_rows((long long)B * T, D, a_stride, "a", aspan));
+    KDN_TRY(check_rows((long long)B * T, D, x_stride, "x", xspan, kMaxRecStride));
+    KDN_TRY(check_rows((long long)B * T, D, a_stride, "a", aspan, kMaxRecStride));
     KDN_TRY(check_rec_grid(B, T, D, false));
     const size_t need = kdn_rec_fwd_workspace_size(B, T, D);
     KDN_TRY(check_workspace(workspace, workspace_bytes, need));
@@ -392,8 +395,8 @@ kdn_status kdn_rec_bwd(int B, int T, int D, int io_dtype, int gate, int blend, c
     KDN_TRY(check_rec(io_dtype, gate, blend));
     KDN_TRY(check_sequence(B, T, D, cu_seqlens, N));
     long long xspan, aspan;
-    KDN_TRY(check_rows((long long)B * T, D, x_stride, "x", xspan));
-    KDN_TRY(check_rows((long long)B * T, D, a_stride, "a", aspan));
+    KDN_TRY(check_rows((long long)B * T, D, x_stride, "x", xspan, kMaxRecStride));
+    KDN_TRY(check_rows((long long)B * T, D, a_stride, "a", aspan, kMaxRecStride));
     KDN_TRY(check_rec_grid(B, T, D, true));
     const size_t need = kdn_rec_bwd_workspace_size(B, T, D);
     KDN_TRY(check_workspace(workspace, workspace_bytes, need));

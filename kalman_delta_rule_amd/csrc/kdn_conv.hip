@@ -5,20 +5,26 @@
 //   g_t = dy_t act'(z_t),  dx_t = sum_k w_k g_{t+(W-1)-k},
 //   dw_k = sum_t g_t x_{t-(W-1)+k},  db = sum_t g_t
 //
-// Bound by HBM.  The rows [B,T] are taken as one row of B T tokens with a
-// sequence starting at every T-th (or where the offsets of packed sequences
-// say).  A thread walks a run of consecutive tokens for VE adjacent channels
-// with the last W - 1 inputs in registers, so that each input is read once (the
-// W - 1 tokens before a run again, from L2); the next rows' loads are issued
-// before the present ones are used.  The backward walks forward too: it keeps
-// the partial dx of the last W - 1 tokens and stores a token's when its last
-// term is added, W - 1 tokens later or at its sequence's end: a run stores what its
-// own tokens finish, after the W - 1 tokens before it have gone through to begin
-// those sums.
+// The rows [B,T] are taken as one row of B T tokens with a sequence starting at
+// every T-th (or where the offsets of packed sequences say).  A thread walks a run of
+// consecutive tokens for VE adjacent channels with the last W - 1 inputs in
+// registers, the next rows' loads issued before the present ones are used.  Each
+// input is read once: a run reads the W - 1 rows before it, and the run ahead of it in
+// the workgroup takes those, its own last ones, through LDS.  The backward walks
+// forward too: it keeps the partial dx of the last W - 1 tokens and stores a token's
+// when its last term is added, W - 1 tokens later or at its sequence's end; a run
+// stores what its own tokens finish, after the W - 1 tokens before it have gone
+// through to begin those sums.
 //
 // A run without a sequence's border in reach goes the plain way, four tokens at a
-// time; the others look for a mark at every token: at a sequence's start the last inputs come
-// from its state, at its end they go there.
+// time; the others look for a mark at every token: at a sequence's start the last
+// inputs come from its state, at its end they go there.
+//
+// The forward is bound by HBM: 32768 x 2048 bf16 49 us (5.5 TB/s of inputs and
+// outputs), 16384 x 2048 fp32 44 us (6.1 TB/s).  The backward, 96 to 101 and 88 us
+// (4.0 to 4.2 and 4.6 TB/s), is held back by its registers, 150 a thread with three
+// waves a SIMD: 33 vector instructions a value take 60% of the time, and neither two
+// nor four channels' fewer or more registers, nor fewer bytes (LDS), moved it.
 #include "kdn_block.h"
 #include "kdn_common.h"
 
@@ -413,7 +419,8 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs a, Plan plan)
         __syncthreads();
         const int base = at.run * at.length;  // mark of the first token loaded
         const int limit = token_limit(a);
-        const bool plain = !__any(at.m + at.length > limit ||
+        // (with bad offsets the row's front may have no mark: nothing lies before it)
+        const bool plain = !__any(at.m == 0 || at.m + at.length > limit ||
                                   any_mark(marks, base, at.length + 2 * (W - 1), at.lane, lanes));
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
@@ -498,7 +505,7 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs a, Plan plan)
                 if (m >= began) {
                     if (m >= 0)
                         store_vec<IO, VE>(dx + (size_t)m * a.D, v);
-                } else if (a.dstate0) {
+                } else if (seq >= 0 && a.dstate0) {
                     store_vec<IO, VE>(static_cast<IO*>(a.dstate0) +
                                           ((size_t)seq * (W - 1) + (m - began + W - 1)) * a.D + at.c, v);
                 }

@@ -78,7 +78,7 @@ static void norm_checks()
     BAD(WITH(Norm, c.eps = std::nanf("")).fwd(), KDN_ERR_INVALID_ARG, "eps");
     BAD(WITH(Norm, c.xs = 63).fwd(), KDN_ERR_INVALID_ARG, "x_stride");
     BAD(WITH(Norm, c.xs = -64).fwd(), KDN_ERR_INVALID_ARG, "x_stride");
-    BAD(WITH(Norm, c.xs = LLONG_MAX).fwd(), KDN_ERR_UNSUPPORTED, "2^22");
+    BAD(WITH(Norm, c.xs = LLONG_MAX).fwd(), KDN_ERR_UNSUPPORTED, "1073741824");
     BAD(WITH(Norm, c.x = 0).fwd(), KDN_ERR_INVALID_ARG, "x must not be NULL");
     BAD(WITH(Norm, c.y = 0).fwd(), KDN_ERR_INVALID_ARG, "y must not be NULL");
     BAD(WITH(Norm, c.mean = 0).bwd(), KDN_ERR_INVALID_ARG, "mean must not be NULL");
@@ -197,6 +197,9 @@ static void rec_checks()
     BAD(WITH(Rec, (c.B = 1, c.cu = 14 * G, c.N = -4)).fwd(), KDN_ERR_INVALID_ARG, "N >= 1");
     BAD(WITH(Rec, c.as = 1).fwd(), KDN_ERR_INVALID_ARG, "a_stride");
     BAD(WITH(Rec, c.xs = 1).step(), KDN_ERR_INVALID_ARG, "x_stride");
+    BAD(WITH(Rec, c.as = (1 << 22) + 1).bwd(), KDN_ERR_UNSUPPORTED, "a_stride is at most 4194304");
+    RUNS(WITH(Rec, (c.as = c.xs = (1 << 22) + 1)).step());
+    RUNS(WITH(Rec, (c.as = c.xs = 1 << 22)).fwd());
     BAD(WITH(Rec, (c.gate = KDN_GATE_ALPHA, c.a += 2)).fwd(), KDN_ERR_INVALID_ARG, "a must be 4-byte");
     RUNS(WITH(Rec, (c.a += 2)).fwd());
     BAD(WITH(Rec, c.chk = 0).bwd(), KDN_ERR_INVALID_ARG, "checkpoints must not be NULL");

@@ -331,6 +331,23 @@ def test_rec_steps_are_the_forward(B, D, gate, blend, io):
     R.check(host(state), ref["h_T"], "f32", "state")
 
 
+def test_steps_read_one_token_of_a_long_buffer():
+    # rows 6.3 million elements apart: beyond the recurrence's own limit for whole rows
+    B, T, D = 3, 3001, 2100
+    x = torch.randn(B, T, D, device="cuda")
+    t = 1234
+    cut, w = x[:, t].contiguous(), torch.randn(4, D, device="cuda")
+    s1, s2 = torch.zeros(B, 3, D, device="cuda"), torch.zeros(B, 3, D, device="cuda")
+    assert same(kda.kdn_conv_step(x[:, t], w, s1), kda.kdn_conv_step(cut, w, s2)) and same(s1, s2)
+    r1, r2 = torch.ones(B, D, device="cuda"), torch.ones(B, D, device="cuda")
+    assert same(kda.kdn_rec_step(x[:, t], x[:, t], r1), kda.kdn_rec_step(cut, cut, r2)) and same(r1, r2)
+    assert same(kda.kdn_layer_norm_fwd(x[:, t])[0], kda.kdn_layer_norm_fwd(cut)[0])
+    y, _ = kda.kdn_conv_fwd(x[:, t:t + 1], w)
+    assert same(y[:, 0], kda.kdn_conv_step(cut, w, torch.zeros(B, 3, D, device="cuda")))
+    with pytest.raises(kda.KdnError, match="x_stride is at most"):
+        kda.kdn_rec_fwd(x[:, t:t + 1], x[:, t:t + 1])
+
+
 # ---- values that must stay in their sequence -------------------------------------
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
