@@ -22,11 +22,12 @@
 //
 // The forward is bound by HBM: 32768 x 2048 bf16 49 us (5.5 TB/s of inputs and
 // outputs), 16384 x 2048 fp32 44 us (6.1 TB/s).  The backward, 96 to 101 and 88 us
-// (4.0 to 4.2 and 4.6 TB/s), is held back by its registers, 150 a thread with three
+// (4.0 to 4.2 and 4.6 TB/s; 65536 x 2048 bf16 89 us forward, 164 us backward), is held back by its registers, 150 a thread with three
 // waves a SIMD: 33 vector instructions a value take 60% of the time, and neither two
 // nor four channels' fewer or more registers, nor fewer bytes (LDS), moved it.
 #include "kdn_block.h"
 #include "kdn_common.h"
+#include "kdn_stream.h"
 
 namespace kdn {
 
@@ -35,34 +36,12 @@ namespace {
 constexpr int kBatch = 4;  // rows loaded together (at least W - 1); a run is a multiple of it
 constexpr int kMostTokens = 1024, kMostRun = 128;  // of a workgroup's tile, of a run
 
-// VE adjacent values as they are in memory, at any alignment of an element
 template <typename E, int VE>
-struct __attribute__((packed, aligned(sizeof(E)))) Vec {
-    E v[VE];
-};
-
-template <typename E, int VE>
-__device__ __forceinline__ Vec<E, VE> load_vec(const E* p)
-{
-    return *reinterpret_cast<const Vec<E, VE>*>(p);
-}
-
-template <typename E, int VE>
-__device__ __forceinline__ void store_vec(E* p, const float (&y)[VE])
-{
-    Vec<E, VE> o;
-#pragma unroll
-    for (int j = 0; j < VE; ++j)
-        o.v[j] = from_f32<E>(y[j]);
-    *reinterpret_cast<Vec<E, VE>*>(p) = o;
-}
-
-template <typename E, int VE>
-__device__ __forceinline__ void widen(const Vec<E, VE>& r, float (&x)[VE])
+__device__ __forceinline__ void widen(const Raw<E, VE>& r, float (&x)[VE])
 {
 #pragma unroll
     for (int j = 0; j < VE; ++j)
-        x[j] = to_f32(r.v[j]);
+        x[j] = r.get(j);
 }
 
 // fp32 values [VE] at p, or zeros
@@ -70,7 +49,7 @@ template <typename E, int VE>
 __device__ __forceinline__ void load_or_zero(const E* p, bool given, float (&x)[VE])
 {
     if (given) {
-        widen<E, VE>(load_vec<E, VE>(p), x);
+        widen<E, VE>(load_raw<false, E, VE>(p), x);
     } else {
 #pragma unroll
         for (int j = 0; j < VE; ++j)
@@ -217,7 +196,7 @@ struct Filter {
 };
 
 // Rows of VE channels of [tokens, `stride` apart].
-template <typename IO, int VE>
+template <typename IO, int VE, bool ONCE>
 struct Rows {
     const IO* base;
     size_t stride;
@@ -229,9 +208,9 @@ struct Rows {
     }
     __device__ __forceinline__ const IO* at(int m) const { return base + m * stride; }
     // tokens outside repeat the nearest
-    __device__ __forceinline__ Vec<IO, VE> near(int m) const
+    __device__ __forceinline__ Raw<IO, VE> near(int m) const
     {
-        return load_vec<IO, VE>(at(min(max(m, 0), last)));
+        return load_raw<ONCE, IO, VE>(at(min(max(m, 0), last)));
     }
 };
 
@@ -240,31 +219,31 @@ struct Rows {
 // the run, a thread its own channels).
 template <typename IO, int VE, int ROWS>
 struct Handed {
-    struct alignas(sizeof(IO) * VE) Row {
-        IO v[VE];
+    struct alignas(4 * Raw<IO, VE>::kWords) Row {
+        uint32_t w[Raw<IO, VE>::kWords];
     };
     Row rows[ROWS][256];
 
-    __device__ __forceinline__ void put(int d, const Vec<IO, VE>& x)
+    __device__ __forceinline__ void put(int d, const Raw<IO, VE>& x)
     {
 #pragma unroll
-        for (int j = 0; j < VE; ++j)
-            rows[d - 1][threadIdx.x].v[j] = x.v[j];
+        for (int j = 0; j < Raw<IO, VE>::kWords; ++j)
+            rows[d - 1][threadIdx.x].w[j] = x.w[j];
     }
     // of the run behind this thread's
-    __device__ __forceinline__ Vec<IO, VE> get(int d, int lanes) const
+    __device__ __forceinline__ Raw<IO, VE> get(int d, int lanes) const
     {
-        Vec<IO, VE> x;
+        Raw<IO, VE> x;
 #pragma unroll
-        for (int j = 0; j < VE; ++j)
-            x.v[j] = rows[d - 1][threadIdx.x + lanes].v[j];
+        for (int j = 0; j < Raw<IO, VE>::kWords; ++j)
+            x.w[j] = rows[d - 1][threadIdx.x + lanes].w[j];
         return x;
     }
 };
 
 // ---- forward ------------------------------------------------------------------
 
-template <typename IO, int VE, int W, bool SILU>
+template <typename IO, int VE, int W, bool SILU, bool ONCE>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, Plan plan)
 {
     __shared__ Marks marks;
@@ -275,8 +254,8 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, Plan plan)
     f.init(a, at.c);
 
     if (M) {
-        const Rows<IO, VE> rows(a.x, a.xs, M, at.c);
-        Vec<IO, VE> before[W - 1], next[kBatch];
+        const Rows<IO, VE, ONCE> rows(a.x, a.xs, M, at.c);
+        Raw<IO, VE> before[W - 1], next[kBatch];
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
             before[k] = rows.near(at.m - (W - 1) + k);
@@ -305,7 +284,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, Plan plan)
             const IO* ahead = rows.at(at.m + kBatch);
             IO* y = static_cast<IO*>(a.y) + (size_t)at.m * a.D + at.c;
             for (int q = 0; q < plan.batches; ++q) {
-                Vec<IO, VE> now[kBatch];
+                Raw<IO, VE> now[kBatch];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i)
                     now[i] = next[i];
@@ -313,7 +292,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, Plan plan)
                     const bool ends = q + 2 == plan.batches && at.run + 1 < at.runs;
 #pragma unroll
                     for (int i = 0; i < kBatch; ++i, ahead += a.xs)
-                        next[i] = ends && kBatch - i < W ? handed.get(kBatch - i, lanes) : load_vec<IO, VE>(ahead);
+                        next[i] = ends && kBatch - i < W ? handed.get(kBatch - i, lanes) : load_raw<ONCE, IO, VE>(ahead);
                 }
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i, y += a.D) {
@@ -325,7 +304,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, Plan plan)
                         for (int j = 0; j < VE; ++j)
                             z[j] = silu(z[j]);
                     }
-                    store_vec<IO, VE>(y, z);
+                    store_raw<IO, VE>(y, z);
                     f.push(x);
                 }
             }
@@ -347,13 +326,13 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, Plan plan)
                     for (int j = 0; j < VE; ++j)
                         z[j] = silu(z[j]);
                 }
-                store_vec<IO, VE>(static_cast<IO*>(a.y) + (size_t)(at.m + i) * a.D + at.c, z);
+                store_raw<IO, VE>(static_cast<IO*>(a.y) + (size_t)(at.m + i) * a.D + at.c, z);
                 f.push(x);
                 if (marks.end[k] >= 0 && a.state_T) {
                     IO* s = static_cast<IO*>(a.state_T) + (size_t)marks.end[k] * (W - 1) * a.D + at.c;
 #pragma unroll
                     for (int r = 0; r < W - 1; ++r)
-                        store_vec<IO, VE>(s + (size_t)r * a.D, f.win[r]);
+                        store_raw<IO, VE>(s + (size_t)r * a.D, f.win[r]);
                 }
             }
         }
@@ -368,14 +347,14 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, Plan plan)
             IO* s = static_cast<IO*>(a.state_T) + (size_t)n * (W - 1) * a.D + at.c;
 #pragma unroll
             for (int r = 0; r < W - 1; ++r)
-                store_vec<IO, VE>(s + (size_t)r * a.D, f.win[r]);
+                store_raw<IO, VE>(s + (size_t)r * a.D, f.win[r]);
         }
     }
 }
 
 // ---- backward -----------------------------------------------------------------
 
-template <typename IO, int VE, int W, bool SILU>
+template <typename IO, int VE, int W, bool SILU, bool ONCE>
 __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs a, Plan plan)
 {
     __shared__ Marks marks;
@@ -396,8 +375,8 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs a, Plan plan)
     }
 
     if (M) {
-        const Rows<IO, VE> rows(a.x, a.xs, M, at.c), grads(a.dy, a.D, M, at.c);
-        Vec<IO, VE> before[W - 1], wx[W - 1], wy[W - 1], nx[kBatch], ny[kBatch];
+        const Rows<IO, VE, ONCE> rows(a.x, a.xs, M, at.c), grads(a.dy, a.D, M, at.c);
+        Raw<IO, VE> before[W - 1], wx[W - 1], wy[W - 1], nx[kBatch], ny[kBatch];
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
             before[k] = rows.near(at.m - 2 * (W - 1) + k);
@@ -432,7 +411,7 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs a, Plan plan)
         }
         // adds a token, of input x and output gradient dy, to the partial gradients;
         // `own`: to the sums too
-        auto add = [&](const Vec<IO, VE>& rx, const Vec<IO, VE>& ry, bool own) {
+        auto add = [&](const Raw<IO, VE>& rx, const Raw<IO, VE>& ry, bool own) {
             float x[VE], g[VE];
             widen<IO, VE>(rx, x);
             widen<IO, VE>(ry, g);
@@ -476,7 +455,7 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs a, Plan plan)
             const IO *ax = rows.at(at.m + kBatch), *ay = grads.at(at.m + kBatch);
             IO* out = dx + (size_t)(at.m - (W - 1)) * a.D;
             for (int q = 0; q < plan.batches; ++q) {
-                Vec<IO, VE> cx[kBatch], cy[kBatch];
+                Raw<IO, VE> cx[kBatch], cy[kBatch];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i)
                     cx[i] = nx[i], cy[i] = ny[i];
@@ -485,14 +464,14 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs a, Plan plan)
 #pragma unroll
                     for (int i = 0; i < kBatch; ++i, ax += a.xs, ay += a.D) {
                         const int d = kBatch - i;
-                        nx[i] = ends && d <= 2 * (W - 1) ? handed_x.get(d <= 2 * (W - 1) ? d : 1, lanes) : load_vec<IO, VE>(ax);
-                        ny[i] = ends && d < W ? handed_y.get(d < W ? d : 1, lanes) : load_vec<IO, VE>(ay);
+                        nx[i] = ends && d <= 2 * (W - 1) ? handed_x.get(d <= 2 * (W - 1) ? d : 1, lanes) : load_raw<ONCE, IO, VE>(ax);
+                        ny[i] = ends && d < W ? handed_y.get(d < W ? d : 1, lanes) : load_raw<ONCE, IO, VE>(ay);
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
                     add(cx[i], cy[i], true);
-                    store_vec<IO, VE>(out, part[0]);
+                    store_raw<IO, VE>(out, part[0]);
                     out += a.D;
                     shift();
                 }
@@ -504,18 +483,18 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs a, Plan plan)
             auto finish = [&](int m, const float (&v)[VE]) {
                 if (m >= began) {
                     if (m >= 0)
-                        store_vec<IO, VE>(dx + (size_t)m * a.D, v);
+                        store_raw<IO, VE>(dx + (size_t)m * a.D, v);
                 } else if (seq >= 0 && a.dstate0) {
-                    store_vec<IO, VE>(static_cast<IO*>(a.dstate0) +
+                    store_raw<IO, VE>(static_cast<IO*>(a.dstate0) +
                                           ((size_t)seq * (W - 1) + (m - began + W - 1)) * a.D + at.c, v);
                 }
             };
             // (one row ahead: more would hold the registers of a wave's worth)
-            Vec<IO, VE> x1 = wx[0], y1 = wy[0];
+            Raw<IO, VE> x1 = wx[0], y1 = wy[0];
             const int stop = min(at.length, limit - at.m);
             for (int i = -(W - 1); i < stop; ++i) {
                 const int m = at.m + i, k = base + 2 * (W - 1) + i;
-                const Vec<IO, VE> cx = x1, cy = y1;
+                const Raw<IO, VE> cx = x1, cy = y1;
                 x1 = rows.near(m + 1);
                 y1 = grads.near(m + 1);
                 if (m < 0)
@@ -560,7 +539,7 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs a, Plan plan)
             for (int r = 0; r < W - 1; ++r) {
                 float d[VE];
                 load_or_zero<IO, VE>(static_cast<const IO*>(a.dstate_T) + o + (size_t)r * a.D, a.dstate_T, d);
-                store_vec<IO, VE>(static_cast<IO*>(a.dstate0) + o + (size_t)r * a.D, d);
+                store_raw<IO, VE>(static_cast<IO*>(a.dstate0) + o + (size_t)r * a.D, d);
             }
         }
     }
@@ -591,7 +570,7 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs a, Plan plan)
 #pragma unroll
             for (int j = 0; j < VE; ++j)
                 s[j] = (sums[0][l * VE + j] + sums[1][l * VE + j]) + (sums[2][l * VE + j] + sums[3][l * VE + j]);
-            store_vec<float, VE>(out + (size_t)k * a.D + at.c, s);
+            store_raw<float, VE>(out + (size_t)k * a.D + at.c, s);
         }
     }
 }
@@ -638,11 +617,11 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a)
     auto step = [&](auto ve, int c) {
         constexpr int N = decltype(ve)::value;
         IO* st = static_cast<IO*>(a.state_T) + (size_t)b * (W - 1) * a.D + c;
-        Vec<IO, N> in[W];
+        Raw<IO, N> in[W];
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
-            in[k] = load_vec<IO, N>(st + (size_t)k * a.D);
-        in[W - 1] = load_vec<IO, N>(static_cast<const IO*>(a.x) + (size_t)b * a.xs + c);
+            in[k] = load_raw<false, IO, N>(st + (size_t)k * a.D);
+        in[W - 1] = load_raw<false, IO, N>(static_cast<const IO*>(a.x) + (size_t)b * a.xs + c);
         float z[N];
         load_or_zero<float, N>(a.bias + c, a.bias, z);
 #pragma unroll
@@ -659,10 +638,10 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a)
             for (int j = 0; j < N; ++j)
                 z[j] = silu(z[j]);
         }
-        store_vec<IO, N>(static_cast<IO*>(a.y) + (size_t)b * a.D + c, z);
+        store_raw<IO, N>(static_cast<IO*>(a.y) + (size_t)b * a.D + c, z);
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
-            *reinterpret_cast<Vec<IO, N>*>(st + (size_t)k * a.D) = in[k + 1];
+            store_same<IO, N>(st + (size_t)k * a.D, in[k + 1]);
     };
     if (c0 + VE <= a.D) {
         step(std::integral_constant<int, VE>{}, c0);
@@ -701,12 +680,19 @@ void launch(const ConvArgs& a, bool backward, hipStream_t stream)
 {
     const Plan p = plan_of(a.B * a.T, a.D, VE, backward);
     const unsigned grid = (unsigned)p.tiles * p.ctiles;
-    if (!backward) {
-        conv_fwd_kernel<IO, VE, W, SILU><<<grid, 256, 0, stream>>>(a, p);
-        return;
-    }
-    conv_bwd_kernel<IO, VE, W, SILU><<<grid, 256, 0, stream>>>(a, p);
-    conv_sum_kernel<<<((a.W + 1) * a.D + 63) / 64, 1024, 0, stream>>>(a, a.T ? p.tiles : 0);
+    auto run = [&](auto once) {
+        constexpr bool ONCE = decltype(once)::value;
+        if (backward)
+            conv_bwd_kernel<IO, VE, W, SILU, ONCE><<<grid, 256, 0, stream>>>(a, p);
+        else
+            conv_fwd_kernel<IO, VE, W, SILU, ONCE><<<grid, 256, 0, stream>>>(a, p);
+    };
+    if (VE > 1 && (long long)a.B * a.T * a.D * (long long)sizeof(IO) >= kLastLevelCache)
+        run(std::integral_constant<bool, (VE > 1)>{});
+    else
+        run(std::false_type{});
+    if (backward)
+        conv_sum_kernel<<<((a.W + 1) * a.D + 63) / 64, 1024, 0, stream>>>(a, a.T ? p.tiles : 0);
 }
 
 template <typename IO, int VE, int W>

@@ -26,8 +26,9 @@
 //
 // Bound by HBM and by the time from load to store of the tiles that the registers
 // hold at a time.  Measured (kernel time; bytes of inputs and outputs): forward B8
-// T4096 D2048 bf16 90 us (4.5 TB/s), B1 T65536 180 us (4.5 TB/s); backward 153 us
-// (4.4 TB/s) and 311 us (4.3 TB/s).  Loading the next tile ahead in a workgroup that
+// T4096 D2048 bf16 78 us (5.2 TB/s), B1 T65536 170 us (4.7 TB/s); backward 134 us
+// (5.0 TB/s) and 303 us (4.4 TB/s); with loads that are not marked as non-temporal 88,
+// 184, 148 and 319 us.  Loading the next tile ahead in a workgroup that
 // stays (128 registers, or 8 tokens a run) was slower, 111 us and more; a scratch
 // access anywhere in the walks costs half the speed.
 //
@@ -37,6 +38,7 @@
 #include "kdn.h"
 #include "kdn_block.h"
 #include "kdn_common.h"
+#include "kdn_stream.h"
 
 namespace kdn {
 
@@ -245,44 +247,22 @@ struct Link {
 
 // ---- values ------------------------------------------------------------------
 
-// V adjacent values as they are in memory (any alignment of their elements)
-template <typename E, int V>
-struct __attribute__((packed, aligned(sizeof(E)))) Pack {
-    E v[V];
-};
-
-template <typename E, int V>
-__device__ __forceinline__ Pack<E, V> load_at(const char* base, uint32_t off)
-{
-    return *reinterpret_cast<const Pack<E, V>*>(base + off);
-}
-
-template <typename E, int V>
-__device__ __forceinline__ void store_at(char* base, uint32_t off, const float (&v)[V])
-{
-    Pack<E, V> p;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        p.v[i] = from_f32<E>(v[i]);
-    *reinterpret_cast<Pack<E, V>*>(base + off) = p;
-}
-
 // V values of each of a run's L tokens: rows `stride` bytes apart from `base`, the
 // run's first at row `first`, the lane's values at byte `col` of a row.  Where the
 // tile reaches behind the row's end (`rows` < TILE), the last row is repeated.
-template <int TILE, typename E, int V, int L>
-__device__ __forceinline__ void load_run(Pack<E, V> (&r)[L], const char* base, uint32_t stride,
+template <bool ONCE, int TILE, typename E, int V, int L>
+__device__ __forceinline__ void load_run(Raw<E, V> (&r)[L], const char* base, uint32_t stride,
                                          int first, uint32_t col, int rows)
 {
     if (rows >= TILE) {
         const uint32_t off = first * stride + col;
 #pragma unroll
         for (int i = 0; i < L; ++i)
-            r[i] = load_at<E, V>(base + (size_t)i * stride, off);
+            r[i] = load_raw<ONCE, E, V>(reinterpret_cast<const E*>(base + (size_t)i * stride + off));
     } else if (rows > 0) {
 #pragma unroll
         for (int i = 0; i < L; ++i)
-            r[i] = load_at<E, V>(base, min(first + i, rows - 1) * stride + col);
+            r[i] = load_raw<ONCE, E, V>(reinterpret_cast<const E*>(base + min(first + i, rows - 1) * stride + col));
     }
 }
 
@@ -423,13 +403,13 @@ __device__ __forceinline__ Tile take_tile(const RecArgs& a, const Chain& ch, int
 
 // Half-waves of 16 tokens: eight, or sixteen where the columns are few.  A longer tile
 // halves the chain, a shorter one leaves more workgroups out of step, one loading
-// while another waits (D 2048 bf16, eight and sixteen: B8 T4096 94 and 101 us, B32
+// while another waits (D 2048 bf16, loads not marked, eight and sixteen: B8 T4096 94 and 101 us, B32
 // T1024 99 and 110; B4 T4096 50 and 51; B2 T32768 177 and 164; B1 T65536 198 and 176;
 // D 64, B1 T65536 37 and 23).
 constexpr int kFwdRun = 16, kManyColumnTiles = 192;
 int fwd_runs(long long column_tiles) { return column_tiles >= kManyColumnTiles ? 8 : 16; }
 
-template <typename IO, bool PRE, bool BLEND, int V, int RUNS>
+template <typename IO, bool PRE, bool BLEND, int V, int RUNS, bool ONCE>
 __global__ __launch_bounds__(RUNS * 32, 4) void rec_fwd_kernel(RecArgs a, Chain ch, int ctiles)
 {
     typedef typename std::conditional<PRE, IO, float>::type GT;
@@ -444,12 +424,12 @@ __global__ __launch_bounds__(RUNS * 32, 4) void rec_fwd_kernel(RecArgs a, Chain 
     const int first = run * L;  // of the run, in the tile
     const size_t row0 = (size_t)tile.b * a.T + tile.t0;
 
-    Pack<GT, V> ra[L];
-    Pack<IO, V> rx[L];
+    Raw<GT, V> ra[L];
+    Raw<IO, V> rx[L];
     const int rows = a.T - tile.t0;
-    load_run<TILE, GT, V, L>(ra, static_cast<const char*>(a.a) + row0 * a.as * sizeof(GT),
+    load_run<ONCE, TILE, GT, V, L>(ra, static_cast<const char*>(a.a) + row0 * a.as * sizeof(GT),
                        (uint32_t)a.as * sizeof(GT), first, c * sizeof(GT), rows);
-    load_run<TILE, IO, V, L>(rx, static_cast<const char*>(a.x) + row0 * a.xs * sizeof(IO),
+    load_run<ONCE, TILE, IO, V, L>(rx, static_cast<const char*>(a.x) + row0 * a.xs * sizeof(IO),
                        (uint32_t)a.xs * sizeof(IO), first, c * sizeof(IO), rows);
 
     marks.fill(a, tile.t0);
@@ -463,8 +443,8 @@ __global__ __launch_bounds__(RUNS * 32, 4) void rec_fwd_kernel(RecArgs a, Chain 
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             float rest;
-            gate_of<PRE>(to_f32(ra[i].v[v]), al[i][v], rest);
-            const float x = to_f32(rx[i].v[v]);
+            gate_of<PRE>(ra[i].get(v), al[i][v], rest);
+            const float x = rx[i].get(v);
             u[i][v] = BLEND ? rest * x : x;
         }
 
@@ -528,7 +508,7 @@ __global__ __launch_bounds__(RUNS * 32, 4) void rec_fwd_kernel(RecArgs a, Chain 
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 h[v] = fmaf(al[i][v], h[v], u[i][v]);
-            store_at<IO, V>(ph + (size_t)i * sh, oh, h);
+            store_raw<IO, V>(reinterpret_cast<IO*>(ph + (size_t)i * sh + oh), h);
         }
     } else {
 #pragma unroll
@@ -546,7 +526,7 @@ __global__ __launch_bounds__(RUNS * 32, 4) void rec_fwd_kernel(RecArgs a, Chain 
                 for (int v = 0; v < V; ++v)
                     p[v] = h[v];
             }
-            store_at<IO, V>(ph + (size_t)i * sh, oh, h);
+            store_raw<IO, V>(reinterpret_cast<IO*>(ph + (size_t)i * sh + oh), h);
         }
     }
 
@@ -570,7 +550,7 @@ __global__ __launch_bounds__(RUNS * 32, 4) void rec_fwd_kernel(RecArgs a, Chain 
 // checkpoints, so only the adjoint is chained, in reverse.
 constexpr int kBwdRun = 8, kBwdRuns = 16;
 
-template <typename IO, bool PRE, bool BLEND, int V>
+template <typename IO, bool PRE, bool BLEND, int V, bool ONCE>
 __global__ __launch_bounds__(kBwdRuns * 32, 4) void rec_bwd_kernel(RecArgs a, Chain ch, int ctiles)
 {
     typedef typename std::conditional<PRE, IO, float>::type GT;
@@ -586,14 +566,14 @@ __global__ __launch_bounds__(kBwdRuns * 32, 4) void rec_bwd_kernel(RecArgs a, Ch
     const int first = run * L;
     const size_t row0 = (size_t)tile.b * a.T + tile.t0;
 
-    Pack<GT, V> ra[L];
-    Pack<IO, V> rx[L], rd[L];
+    Raw<GT, V> ra[L];
+    Raw<IO, V> rx[L], rd[L];
     const int rows = a.T - tile.t0;
-    load_run<TILE, GT, V, L>(ra, static_cast<const char*>(a.a) + row0 * a.as * sizeof(GT),
+    load_run<ONCE, TILE, GT, V, L>(ra, static_cast<const char*>(a.a) + row0 * a.as * sizeof(GT),
                        (uint32_t)a.as * sizeof(GT), first, c * sizeof(GT), rows);
-    load_run<TILE, IO, V, L>(rx, static_cast<const char*>(a.x) + row0 * a.xs * sizeof(IO),
+    load_run<ONCE, TILE, IO, V, L>(rx, static_cast<const char*>(a.x) + row0 * a.xs * sizeof(IO),
                        (uint32_t)a.xs * sizeof(IO), first, c * sizeof(IO), rows);
-    load_run<TILE, IO, V, L>(rd, static_cast<const char*>(a.dh) + row0 * a.D * sizeof(IO),
+    load_run<ONCE, TILE, IO, V, L>(rd, static_cast<const char*>(a.dh) + row0 * a.D * sizeof(IO),
                        (uint32_t)a.D * sizeof(IO), first, c * sizeof(IO), rows);
 
     marks.fill(a, tile.t0);
@@ -606,7 +586,7 @@ __global__ __launch_bounds__(kBwdRuns * 32, 4) void rec_bwd_kernel(RecArgs a, Ch
     for (int i = 0; i < L; ++i)
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            gate_of<PRE>(to_f32(ra[i].v[v]), al[i][v], rest[i][v]);
+            gate_of<PRE>(ra[i].get(v), al[i][v], rest[i][v]);
 
     float A[V], U[V], RA[V], RU[V];
 #pragma unroll
@@ -617,7 +597,7 @@ __global__ __launch_bounds__(kBwdRuns * 32, 4) void rec_bwd_kernel(RecArgs a, Ch
         for (int i = 0; i < L; ++i)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float x = to_f32(rx[i].v[v]);
+                const float x = rx[i].get(v);
                 U[v] = fmaf(al[i][v], U[v], BLEND ? rest[i][v] * x : x);
                 A[v] *= al[i][v];
             }
@@ -625,7 +605,7 @@ __global__ __launch_bounds__(kBwdRuns * 32, 4) void rec_bwd_kernel(RecArgs a, Ch
         for (int i = L - 1; i >= 0; --i)
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                RU[v] = al[i][v] * (to_f32(rd[i].v[v]) + RU[v]);
+                RU[v] = al[i][v] * (rd[i].get(v) + RU[v]);
 #pragma unroll
         for (int v = 0; v < V; ++v)
             RA[v] = A[v];
@@ -642,7 +622,7 @@ __global__ __launch_bounds__(kBwdRuns * 32, 4) void rec_bwd_kernel(RecArgs a, Ch
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float x = to_f32(rx[i].v[v]);
+                const float x = rx[i].get(v);
                 U[v] = fmaf(al[i][v], U[v], BLEND ? rest[i][v] * x : x);
                 A[v] *= al[i][v];
             }
@@ -659,7 +639,7 @@ __global__ __launch_bounds__(kBwdRuns * 32, 4) void rec_bwd_kernel(RecArgs a, Ch
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                RU[v] = al[i][v] * (to_f32(rd[i].v[v]) + RU[v]);
+                RU[v] = al[i][v] * (rd[i].get(v) + RU[v]);
                 RA[v] *= al[i][v];
             }
         }
@@ -687,7 +667,7 @@ __global__ __launch_bounds__(kBwdRuns * 32, 4) void rec_bwd_kernel(RecArgs a, Ch
     auto forward = [&](int i) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float x = to_f32(rx[i].v[v]);
+            const float x = rx[i].get(v);
             part[i][v] = BLEND ? h[v] - x : h[v];
             h[v] = fmaf(al[i][v], h[v], BLEND ? rest[i][v] * x : x);
         }
@@ -718,14 +698,14 @@ __global__ __launch_bounds__(kBwdRuns * 32, 4) void rec_bwd_kernel(RecArgs a, Ch
         float dx[V], da[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float lam = to_f32(rd[i].v[v]) + g[v];
+            const float lam = rd[i].get(v) + g[v];
             dx[v] = BLEND ? lam * rest[i][v] : lam;
             g[v] = al[i][v] * lam;
             // dalpha times alpha (1 - alpha), of the factors at hand
             da[v] = PRE ? g[v] * rest[i][v] * part[i][v] : lam * part[i][v];
         }
-        store_at<IO, V>(px + (size_t)i * sx, ox, dx);
-        store_at<GT, V>(pa + (size_t)i * sa, oa, da);
+        store_raw<IO, V>(reinterpret_cast<IO*>(px + (size_t)i * sx + ox), dx);
+        store_raw<GT, V>(reinterpret_cast<GT*>(pa + (size_t)i * sa + oa), da);
     };
     if (plain) {
 #pragma unroll
@@ -774,19 +754,19 @@ __global__ __launch_bounds__(256) void rec_step_kernel(RecArgs a)
     auto step = [&](auto ve, int c) {
         constexpr int N = decltype(ve)::value;
         float* st = a.h_T + (size_t)b * a.D + c;
-        const auto ra = load_at<GT, N>(reinterpret_cast<const char*>(static_cast<const GT*>(a.a) + (size_t)b * a.as + c), 0);
-        const auto rx = load_at<IO, N>(reinterpret_cast<const char*>(static_cast<const IO*>(a.x) + (size_t)b * a.xs + c), 0);
-        const auto rs = load_at<float, N>(reinterpret_cast<const char*>(st), 0);
+        const auto ra = load_raw<false, GT, N>(static_cast<const GT*>(a.a) + (size_t)b * a.as + c);
+        const auto rx = load_raw<false, IO, N>(static_cast<const IO*>(a.x) + (size_t)b * a.xs + c);
+        const auto rs = load_raw<false, float, N>(st);
         float h[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             float alpha, rest;
-            gate_of<PRE>(to_f32(ra.v[j]), alpha, rest);
-            const float x = to_f32(rx.v[j]);
-            h[j] = fmaf(alpha, rs.v[j], a.blend ? rest * x : x);
+            gate_of<PRE>(ra.get(j), alpha, rest);
+            const float x = rx.get(j);
+            h[j] = fmaf(alpha, rs.get(j), a.blend ? rest * x : x);
         }
-        store_at<float, N>(reinterpret_cast<char*>(st), 0, h);
-        store_at<IO, N>(reinterpret_cast<char*>(static_cast<IO*>(a.h) + (size_t)b * a.D + c), 0, h);
+        store_raw<float, N>(st, h);
+        store_raw<IO, N>(static_cast<IO*>(a.h) + (size_t)b * a.D + c, h);
     };
     if (c0 + VE <= a.D) {
         step(std::integral_constant<int, VE>{}, c0);
@@ -823,12 +803,20 @@ hipError_t launch(const RecArgs& a, bool backward, hipStream_t stream)
         rec_clear_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(static_cast<uint4*>(a.ws), n);
     }
     const unsigned grid = (unsigned)t.tiles * a.B * t.ctiles;
-    if (backward)
-        rec_bwd_kernel<IO, PRE, BLEND, V><<<grid, kBwdRuns * 32, 0, stream>>>(a, ch, t.ctiles);
-    else if (t.runs == 8)
-        rec_fwd_kernel<IO, PRE, BLEND, V, 8><<<grid, 8 * 32, 0, stream>>>(a, ch, t.ctiles);
+    auto run = [&](auto once) {
+        constexpr bool ONCE = decltype(once)::value;
+        if (backward)
+            rec_bwd_kernel<IO, PRE, BLEND, V, ONCE><<<grid, kBwdRuns * 32, 0, stream>>>(a, ch, t.ctiles);
+        else if (t.runs == 8)
+            rec_fwd_kernel<IO, PRE, BLEND, V, 8, ONCE><<<grid, 8 * 32, 0, stream>>>(a, ch, t.ctiles);
+        else
+            rec_fwd_kernel<IO, PRE, BLEND, V, 16, ONCE><<<grid, 16 * 32, 0, stream>>>(a, ch, t.ctiles);
+    };
+    const long long io = sizeof(IO), gate = PRE ? io : 4, values = (long long)a.B * a.T * a.D;
+    if (V > 1 && values * (backward ? 3 * io + 2 * gate : 2 * io + gate) > kLastLevelCache)
+        run(std::integral_constant<bool, (V > 1)>{});
     else
-        rec_fwd_kernel<IO, PRE, BLEND, V, 16><<<grid, 16 * 32, 0, stream>>>(a, ch, t.ctiles);
+        run(std::false_type{});
     return hipGetLastError();
 }
 

@@ -617,3 +617,67 @@ def test_offsets_beyond_32_bits():
     gn = kda.kdn_layer_norm_bwd(n, x, m, r)
     qn = kda.kdn_layer_norm_bwd(last, x[:, -3:].contiguous(), m[:, -3:].contiguous(), r[:, -3:].contiguous())
     assert torch.equal(gn["dx"][:, -3:], qn["dx"])
+
+
+def in_thirds(B, calls):
+    """The whole call gives what a third of the rows gives: the same bits, since the
+    thirds are cut into the same tiles."""
+    whole = calls(slice(0, B))
+    for k in range(0, B, B // 3):
+        p = slice(k, k + B // 3)
+        for i, (v, t) in enumerate(zip(whole, calls(p))):
+            assert torch.equal(v[p], t), (i, k)
+
+
+@pytest.mark.parametrize("io,gate,T", [("bf16", "preact", 1900), ("bf16", "alpha", 1500), ("f32", "preact", 950),
+                                       ("f32", "alpha", 950)])
+def test_rec_larger_than_the_last_level_cache(io, gate, T):
+    B, D = 18, 2050
+    dt = torch.bfloat16 if io == "bf16" else torch.float32
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x, dy = (torch.empty(B, T, D, device="cuda").normal_(generator=g).to(dt) for _ in range(2))
+    a = torch.empty(B, T, D, device="cuda").normal_(generator=g).add_(2)
+    a = torch.sigmoid(a) if gate == "alpha" else a.to(dt)
+    h0, dh_T = (torch.empty(B, D, device="cuda").normal_(generator=g) for _ in range(2))
+    assert x.numel() * (2 * x.element_size() + a.element_size()) > 256 << 20
+
+    def calls(p):
+        h, h_T, chk = kda.kdn_rec_fwd(x[p], a[p], h0=h0[p], gate=gate, blend=True, want_checkpoints=True)
+        r = kda.kdn_rec_bwd(dy[p], x[p], a[p], chk, h0=h0[p], dh_T=dh_T[p], gate=gate, blend=True)
+        return [h, h_T, chk, r["dx"], r["da"], r["dh0"]]
+    in_thirds(B, calls)
+
+
+@pytest.mark.parametrize("W", [2, 3, 4])
+@pytest.mark.parametrize("io,T", [("bf16", 3650), ("f32", 1825)])
+def test_conv_larger_than_the_last_level_cache(io, T, W):
+    B, D = 18, 2050
+    dt = torch.bfloat16 if io == "bf16" else torch.float32
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x, dy = (torch.empty(B, T, D, device="cuda").normal_(generator=g).to(dt) for _ in range(2))
+    w, b = torch.randn(W, D, device="cuda"), torch.randn(D, device="cuda")
+    s0 = torch.randn(B, W - 1, D, device="cuda").to(dt)
+    assert x.numel() * x.element_size() > 256 << 20
+
+    def calls(p):
+        kw = dict(bias=b, state0=s0[p], activation="silu")
+        y, s_T = kda.kdn_conv_fwd(x[p], w, want_state=True, **kw)
+        c = kda.kdn_conv_bwd(dy[p], x[p], w, **kw)
+        return [y, s_T, c["dx"], c["dstate0"]]
+    in_thirds(B, calls)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [60, 128, 250, 500, 1000, 2050, 6144, 8200, 16384])
+def test_layer_norm_larger_than_the_last_level_cache(D, io):
+    dt = torch.bfloat16 if io == "bf16" else torch.float32
+    rows = ((256 << 20) // (D * dt.itemsize) // 3 + 1) * 3
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x, dy = (torch.empty(rows, D, device="cuda").normal_(generator=g).to(dt) for _ in range(2))
+    w, b = torch.randn(D, device="cuda"), torch.randn(D, device="cuda")
+    assert x.numel() * x.element_size() >= 256 << 20
+
+    def calls(p):
+        y, m, r = kda.kdn_layer_norm_fwd(x[p], w, b, want_stats=True)
+        return [y, m, r, kda.kdn_layer_norm_bwd(dy[p], x[p], m, r, w)["dx"]]
+    in_thirds(rows, calls)
