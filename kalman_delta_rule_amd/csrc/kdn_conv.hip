@@ -21,10 +21,11 @@
 // inputs come from its state, at its end they go there.
 //
 // The forward is bound by HBM: 32768 x 2048 bf16 49 us (5.5 TB/s of inputs and
-// outputs), 16384 x 2048 fp32 44 us (6.1 TB/s).  The backward, 96 to 101 and 88 us
-// (4.0 to 4.2 and 4.6 TB/s; 65536 x 2048 bf16 89 us forward, 164 us backward), is held back by its registers, 150 a thread with three
-// waves a SIMD: 33 vector instructions a value take 60% of the time, and neither two
-// nor four channels' fewer or more registers, nor fewer bytes (LDS), moved it.
+// outputs), 65536 x 2048 89 us (6.0 TB/s), 16384 x 2048 fp32 44 us (6.1 TB/s).  The
+// backward, 96 to 101, 164 and 88 us (4.0 to 4.9 TB/s), is held back by its registers,
+// 150 a thread with three waves a SIMD: 33 vector instructions a value take 60% of the
+// time, and neither two nor four channels' fewer or more registers, nor fewer bytes
+// (LDS), moved it.
 #include "kdn_block.h"
 #include "kdn_common.h"
 #include "kdn_stream.h"
