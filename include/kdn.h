@@ -438,7 +438,8 @@ kdn_status kdn_gain_scan_static(int variant, int B, int T, int H, int dk, int io
  *     gradient.  Without cu_seqlens (NULL, N ignored) each of the B rows is one
  *     sequence and N below means B.  Offsets are not checked; bad ones give
  *     unspecified values, but no access outside the tensors.
- *   - Infinities and NaN of one sequence never reach another one.
+ *   - Infinities and NaN of one sequence never reach another one; in the
+ *     recurrence's states and adjoints they go on to the end of their own.
  *   - Deterministic, capturable into a HIP graph; two calls that may run at
  *     the same time need a workspace each.
  */

@@ -32,9 +32,11 @@
 // stays (128 registers, or 8 tokens a run) was slower, 111 us and more; a scratch
 // access anywhere in the walks costs half the speed.
 //
-// Where a sequence starts (forward) or ends (backward) inside a span, A is 0, and
-// a span with A = 0 gives U whatever it is handed: nothing, infinities and
-// NaN included, passes from one sequence to another.
+// Where a sequence starts (forward) or ends (backward) inside a span, A is kCut, and
+// such a span gives U whatever it is handed: nothing, infinities and NaN included,
+// passes from one sequence to another.  Within a sequence they stay to its end, as by
+// the definition: a product of decays that underflows is kept above zero, where an
+// infinity stays one, and a decay of zero (kZero) makes it NaN.
 #include "kdn.h"
 #include "kdn_block.h"
 #include "kdn_common.h"
@@ -127,9 +129,14 @@ __device__ __forceinline__ Word await(const Word* p, Word v)
     return v;
 }
 
+// A of a span: the product of its decays, at least kLeast; kZero if one of them is
+// zero; kCut with a sequence's border in it (or with a decay that is NaN: U is then NaN
+// too).
+constexpr float kLeast = 0x1p-149f, kZero = -0.f, kCut = __builtin_nanf("");
+
 __device__ __forceinline__ float apply(float A, float U, float carry)
 {
-    return A == 0.f ? U : fmaf(A, carry, U);
+    return A != A ? U : fmaf(A, carry, U);
 }
 
 // The spans [kGroup - 1][columns] at p up to the n-th, as they are now.
@@ -149,7 +156,10 @@ __device__ __forceinline__ float2 span_of(unsigned long long w)
 // span a, then span b
 __device__ __forceinline__ float2 join(float2 a, float2 b)
 {
-    return float2{b.x == 0.f ? 0.f : a.x * b.x, apply(b.x, b.y, a.y)};
+    // kCut and kZero on either side stay; of unsigned numbers +0 alone, a product that
+    // underflowed, is less than kLeast
+    const uint32_t A = __float_as_uint(a.x * fabsf(b.x)) | (__float_as_uint(b.x) & 0x80000000u);
+    return float2{__uint_as_float(max(A, __float_as_uint(kLeast))), apply(b.x, b.y, a.y)};
 }
 
 // For column `col` of this lane and tile `k` in chain order, whose span is
@@ -349,6 +359,30 @@ __device__ __forceinline__ int token_limit(const RecArgs& a)
     return a.cu ? min(max(a.cu[a.N], 0), a.T) : a.T;
 }
 
+// The A of a run from the product of the decays of its tokens (those before `valid`)
+template <int L, int V>
+__device__ __forceinline__ void close_run(float (&A)[V], const float (&al)[L][V], int valid, bool cut)
+{
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if (A[v] == 0.f) {
+            bool zero = false;
+#pragma unroll
+            for (int i = 0; i < L; ++i)
+                zero |= i < valid && al[i][v] == 0.f;
+            A[v] = zero ? kZero : kLeast;
+        }
+        if (cut)
+            A[v] = kCut;
+    }
+}
+
+// whether a mark is set at one of a run's tokens before `valid`
+__device__ __forceinline__ bool any_before(uint32_t marks, int valid)
+{
+    return valid > 0 && (valid < 32 ? marks & ((1u << valid) - 1) : marks);
+}
+
 struct Tile {
     int k;   // in chain order
     int b, t0, c0;  // row, first token, first channel
@@ -465,12 +499,8 @@ __global__ __launch_bounds__(RUNS * 32, 4) void rec_fwd_kernel(RecArgs a, Chain 
         for (int i = 0; i < L; ++i) {
             if (i >= valid)
                 continue;
-            if (start >> i & 1) {
+            if (start >> i & 1)
                 state_at<V>(a.h0, marks.starting(a, tile.b, first + i), a.D, c, U);
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    A[v] = 0.f;
-            }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 U[v] = fmaf(al[i][v], U[v], u[i][v]);
@@ -478,6 +508,7 @@ __global__ __launch_bounds__(RUNS * 32, 4) void rec_fwd_kernel(RecArgs a, Chain 
             }
         }
     }
+    close_run<L, V>(A, al, valid, any_before(start, valid));
 #pragma unroll
     for (int v = 0; v < V; ++v)
         link.runs[run][lane * V + v] = float2{A[v], U[v]};
@@ -588,10 +619,10 @@ __global__ __launch_bounds__(kBwdRuns * 32, 4) void rec_bwd_kernel(RecArgs a, Ch
         for (int v = 0; v < V; ++v)
             gate_of<PRE>(ra[i].get(v), al[i][v], rest[i][v]);
 
-    float A[V], U[V], RA[V], RU[V];
+    float A[V], U[V], RU[V];
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        A[v] = RA[v] = 1.f, U[v] = RU[v] = 0.f;
+        A[v] = 1.f, U[v] = RU[v] = 0.f;
     if (plain) {
 #pragma unroll
         for (int i = 0; i < L; ++i)
@@ -606,20 +637,13 @@ __global__ __launch_bounds__(kBwdRuns * 32, 4) void rec_bwd_kernel(RecArgs a, Ch
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 RU[v] = al[i][v] * (rd[i].get(v) + RU[v]);
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            RA[v] = A[v];
     } else {
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             if (i >= valid)
                 continue;
-            if (start >> i & 1) {
+            if (start >> i & 1)
                 state_at<V>(a.h0, marks.starting(a, tile.b, first + i), a.D, c, U);
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    A[v] = 0.f;
-            }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float x = rx[i].get(v);
@@ -631,23 +655,19 @@ __global__ __launch_bounds__(kBwdRuns * 32, 4) void rec_bwd_kernel(RecArgs a, Ch
         for (int i = L - 1; i >= 0; --i) {
             if (i >= valid)
                 continue;
-            if (end >> i & 1) {
+            if (end >> i & 1)
                 state_at<V>(a.dh_T, marks.ending(a, tile.b, first + i), a.D, c, RU);
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    RA[v] = 0.f;
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
+            for (int v = 0; v < V; ++v)
                 RU[v] = al[i][v] * (rd[i].get(v) + RU[v]);
-                RA[v] *= al[i][v];
-            }
         }
     }
+    close_run<L, V>(A, al, valid, false);
+    const bool starts = any_before(start, valid), ends = any_before(end, valid);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        spans[run][lane * V + v] = float2{A[v], U[v]};
-        link.runs[run][lane * V + v] = float2{RA[v], RU[v]};
+        spans[run][lane * V + v] = float2{starts ? kCut : A[v], U[v]};
+        link.runs[run][lane * V + v] = float2{ends ? kCut : A[v], RU[v]};
     }
     __syncthreads();
 
