@@ -418,9 +418,9 @@ kdn_status kdn_gain_scan_static(int variant, int B, int T, int H, int dk, int io
  * convolution that feeds q, k and v, and a gated recurrence per channel (the
  * memory recurrence S <- D S + ... without keys).  Conventions as above, with
  * these differences:
- *   - io dtype KDN_F32 or KDN_BF16 (no flags); parameters (weight, bias),
- *     statistics and recurrent states are fp32; all arithmetic is fp32 and a
- *     value is rounded once, when it is stored.
+ *   - io dtype KDN_F32 or KDN_BF16 (no flags but KDN_CLEAR_TAIL, below);
+ *     parameters (weight, bias), statistics and recurrent states are fp32; all
+ *     arithmetic is fp32 and a value is rounded once, when it is stored.
  *   - Any channel count D from 1 to 2^20; rows, or B T, up to 2^30; B below
  *     2^24.  Pointers need only their element's alignment
  *     (workspaces: 16 bytes); 16-byte alignment and D a multiple of 8 run
@@ -434,8 +434,8 @@ kdn_status kdn_gain_scan_static(int variant, int B, int T, int H, int dk, int io
  *     be 1, and sequence n is the tokens cu_seqlens[n] .. cu_seqlens[n+1] - 1
  *     of the row.  Offsets start at 0, never decrease and end at or before T;
  *     a sequence may be empty.  Tokens from cu_seqlens[N] on belong to no
- *     sequence: nothing of an output is written there, and they add to no
- *     gradient.  Without cu_seqlens (NULL, N ignored) each of the B rows is one
+ *     sequence: nothing of an output is written there (zeros with
+ *     KDN_CLEAR_TAIL), and they add to no gradient.  Without cu_seqlens (NULL, N ignored) each of the B rows is one
  *     sequence and N below means B.  Offsets are not checked; bad ones give
  *     unspecified values, but no access outside the tensors.
  *   - Infinities and NaN of one sequence never reach another one; in the
@@ -443,6 +443,13 @@ kdn_status kdn_gain_scan_static(int variant, int B, int T, int H, int dk, int io
  *   - Deterministic, capturable into a HIP graph; two calls that may run at
  *     the same time need a workspace each.
  */
+
+/*
+ * OR-ed into the io_dtype of kdn_conv_fwd, kdn_conv_bwd, kdn_rec_fwd and
+ * kdn_rec_bwd: the rows of y, of h and checkpoints, of dx and da behind the last
+ * packed sequence are set to zero instead of left as they were.
+ */
+enum { KDN_CLEAR_TAIL = 0x400 };
 
 /*
  * Layer norm over the last axis: rows of D,

@@ -7,6 +7,7 @@ does, and fails loudly if it has not been built.
 """
 from .api import (  # noqa: F401
     KDN_BF16,
+    KDN_CLEAR_TAIL,
     KDN_DIAG,
     KDN_F32,
     KDN_ISO,

@@ -16,6 +16,7 @@ KDN_F32, KDN_BF16 = 0, 1
 KDN_DIAG, KDN_ISO = 0, 1
 KDN_MATH_BF16 = 0x100  # OR-ed into io_dtype: single bf16 products in the Diagonal bf16 forward
 KDN_OUT_F32 = 0x200    # OR-ed into io_dtype: fp32 o from bf16 q, k, v (Diagonal, split products)
+KDN_CLEAR_TAIL = 0x400  # OR-ed into io_dtype: zeros behind the last packed sequence
 KDN_ACT_NONE, KDN_ACT_SILU = 0, 1
 KDN_GATE_ALPHA, KDN_GATE_PREACT = 0, 1
 KDN_REC_CHECKPOINT = 64  # tokens between the states the recurrence's forward keeps

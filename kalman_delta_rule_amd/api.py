@@ -13,8 +13,8 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib
-from ._lib import (KDN_BF16, KDN_DIAG, KDN_F32, KDN_ISO, KDN_MATH_BF16, KDN_OUT_F32,  # noqa: F401
-                   KdnError)
+from ._lib import (KDN_BF16, KDN_CLEAR_TAIL, KDN_DIAG, KDN_F32, KDN_ISO, KDN_MATH_BF16,  # noqa: F401
+                   KDN_OUT_F32, KdnError)
 
 
 def _io_code(t: torch.Tensor) -> int:
@@ -621,6 +621,20 @@ def _sequences(cu_seqlens, B, dev) -> int:
     return cu_seqlens.numel() - 1
 
 
+def _tail(cu_seqlens, *given) -> int:
+    """KDN_CLEAR_TAIL where rows of packed sequences get no output of the
+    caller's: nothing that this layer allocates is left unwritten.  A caller's
+    output keeps what it holds behind the last sequence."""
+    return KDN_CLEAR_TAIL if cu_seqlens is not None and all(t is None for t in given) else 0
+
+
+def _beside(shape, dtype, dev, cu_seqlens, tail):
+    """A new output of a call whose tail is cleared, or (beside one of the
+    caller's) cleared here."""
+    new = torch.zeros if cu_seqlens is not None and not tail else torch.empty
+    return new(shape, dtype=dtype, device=dev)
+
+
 def _workspace(workspace, need: int, dev):
     if workspace is not None:
         if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
@@ -700,7 +714,8 @@ def kdn_conv_fwd(x, weight, bias=None, state0=None, cu_seqlens=None, activation=
     state0 [N,W-1,D] (x's dtype) holds the inputs before each sequence, zeros
     without; cu_seqlens (int32 [N+1]) packs N sequences into one row.  Returns
     (y, state_T): state_T [N,W-1,D], the last inputs of each sequence, if
-    given or with ``want_state`` (None otherwise)."""
+    given or with ``want_state`` (None otherwise).  Behind the last sequence a
+    new y holds zeros, and a caller's keeps what it held."""
     L = _lib.lib()
     dev, io = _first(x, "x", 3)
     B, T, D = x.shape
@@ -711,12 +726,13 @@ def kdn_conv_fwd(x, weight, bias=None, state0=None, cu_seqlens=None, activation=
     _need(weight, "weight", (W, D), f32, dev)
     _optional(dev, (bias, "bias", (D,), f32), (state0, "state0", (N, W - 1, D), x.dtype))
     act = _activation(activation)
+    tail = _tail(cu_seqlens, y)
     y = _given(y, "y", x)
     if state_T is not None:
         _need(state_T, "state_T", (N, W - 1, D), x.dtype, dev)
     elif want_state:
         state_T = torch.empty((N, max(W - 1, 0), D), dtype=x.dtype, device=dev)
-    _launch(dev, L.kdn_conv_fwd, B, T, D, W, io, act, x.data_ptr(), stride, weight.data_ptr(),
+    _launch(dev, L.kdn_conv_fwd, B, T, D, W, io | tail, act, x.data_ptr(), stride, weight.data_ptr(),
             _ptr(bias), _ptr(state0), _ptr(cu_seqlens), N, y.data_ptr(), _ptr(state_T))
     return y, state_T
 
@@ -726,7 +742,8 @@ def kdn_conv_bwd(dy, x, weight, bias=None, state0=None, cu_seqlens=None, activat
     """Backward of kdn_conv_fwd given by the same arguments, for dL/dy = dy and
     dL/dstate_T = dstate_T (optional).  Returns a dict with dx (x's dtype),
     dweight [W,D] (fp32), dbias [D] (fp32) where bias is given and dstate0
-    (x's dtype) where state0 is given."""
+    (x's dtype) where state0 is given.  Behind the last sequence a new dx holds
+    zeros, and a caller's keeps what it held."""
     L = _lib.lib()
     dev, io = _first(x, "x", 3)
     B, T, D = x.shape
@@ -739,13 +756,14 @@ def kdn_conv_bwd(dy, x, weight, bias=None, state0=None, cu_seqlens=None, activat
     _optional(dev, (bias, "bias", (D,), f32), (state0, "state0", (N, W - 1, D), x.dtype),
               (dstate_T, "dstate_T", (N, W - 1, D), x.dtype))
     act = _activation(activation)
+    tail = _tail(cu_seqlens, dx)
     g = {"dx": _given(dx, "dx", x), "dweight": torch.empty((W, D), dtype=f32, device=dev)}
     if bias is not None:
         g["dbias"] = torch.empty(D, dtype=f32, device=dev)
     if state0 is not None:
         g["dstate0"] = torch.empty_like(state0)
     ws, ws_bytes = _workspace(workspace, L.kdn_conv_bwd_workspace_size(B, T, D, W), dev)
-    _launch(dev, L.kdn_conv_bwd, B, T, D, W, io, act, dy.data_ptr(), x.data_ptr(), stride,
+    _launch(dev, L.kdn_conv_bwd, B, T, D, W, io | tail, act, dy.data_ptr(), x.data_ptr(), stride,
             weight.data_ptr(), _ptr(bias), _ptr(state0), _ptr(cu_seqlens), N, _ptr(dstate_T),
             g["dx"].data_ptr(), g["dweight"].data_ptr(), _ptr(g.get("dbias")),
             _ptr(g.get("dstate0")), _ptr(ws), ws_bytes)
@@ -787,7 +805,8 @@ def kdn_rec_fwd(x, a, h0=None, cu_seqlens=None, gate: str = "preact", blend: boo
     (int32 [N+1]) packs N sequences into one row.  Returns (h, h_T,
     checkpoints): h in x's dtype, h_T [N,D] fp32 and, with
     ``want_checkpoints``, the states that kdn_rec_bwd starts from (None
-    otherwise)."""
+    otherwise).  Behind the last sequence a new h holds zeros, and a caller's
+    keeps what it held."""
     L = _lib.lib()
     dev, io = _first(x, "x", 3)
     B, T, D = x.shape
@@ -797,6 +816,7 @@ def kdn_rec_fwd(x, a, h0=None, cu_seqlens=None, gate: str = "preact", blend: boo
     N = _sequences(cu_seqlens, B, dev)
     f32 = torch.float32
     _optional(dev, (h0, "h0", (N, D), f32))
+    tail = _tail(cu_seqlens, h)
     h = _given(h, "h", x)
     if h_T is not None:
         _need(h_T, "h_T", (N, D), f32, dev)
@@ -804,20 +824,21 @@ def kdn_rec_fwd(x, a, h0=None, cu_seqlens=None, gate: str = "preact", blend: boo
         h_T = torch.empty((N, D), dtype=f32, device=dev)
     chk = None
     if want_checkpoints:
-        chk = torch.empty((B, -(-T // _lib.KDN_REC_CHECKPOINT), D), dtype=f32, device=dev)
+        chk = _beside((B, -(-T // _lib.KDN_REC_CHECKPOINT), D), f32, dev, cu_seqlens, tail)
     ws, ws_bytes = _workspace(workspace, L.kdn_rec_fwd_workspace_size(B, T, D), dev)
-    _launch(dev, L.kdn_rec_fwd, B, T, D, io, code, int(bool(blend)), x.data_ptr(), stride,
+    _launch(dev, L.kdn_rec_fwd, B, T, D, io | tail, code, int(bool(blend)), x.data_ptr(), stride,
             a.data_ptr(), a_stride, _ptr(h0), _ptr(cu_seqlens), N, h.data_ptr(), h_T.data_ptr(),
             _ptr(chk), _ptr(ws), ws_bytes)
     return h, h_T, chk
 
 
 def kdn_rec_bwd(dh, x, a, checkpoints, h0=None, dh_T=None, cu_seqlens=None, gate: str = "preact",
-                blend: bool = False, dx=None, workspace=None) -> dict:
+                blend: bool = False, dx=None, workspace=None, da=None) -> dict:
     """Backward of kdn_rec_fwd given by the same arguments and its checkpoints,
     for dL/dh = dh and dL/dh_T = dh_T (optional).  Returns a dict with dx (x's
     dtype), da (a's dtype: the gradient by alpha or by its pre-activation)
-    and dh0 [N,D] fp32."""
+    and dh0 [N,D] fp32.  Behind the last sequence new dx and da hold zeros, and
+    the caller's keep what they held."""
     L = _lib.lib()
     dev, io = _first(x, "x", 3)
     B, T, D = x.shape
@@ -828,12 +849,14 @@ def kdn_rec_bwd(dh, x, a, checkpoints, h0=None, dh_T=None, cu_seqlens=None, gate
     f32 = torch.float32
     _need(dh, "dh", x.shape, x.dtype, dev)
     _need(checkpoints, "checkpoints", (B, -(-T // _lib.KDN_REC_CHECKPOINT), D), f32, dev)
-    _optional(dev, (h0, "h0", (N, D), f32), (dh_T, "dh_T", (N, D), f32))
-    g = {"dx": _given(dx, "dx", x),
-         "da": torch.empty(x.shape, dtype=adt, device=dev),
+    _optional(dev, (h0, "h0", (N, D), f32), (dh_T, "dh_T", (N, D), f32),
+              (dx, "dx", x.shape, x.dtype), (da, "da", x.shape, adt))
+    tail = _tail(cu_seqlens, dx, da)
+    new = lambda t, dtype: _beside(x.shape, dtype, dev, cu_seqlens, tail) if t is None else t
+    g = {"dx": new(dx, x.dtype), "da": new(da, adt),
          "dh0": torch.empty((N, D), dtype=f32, device=dev)}
     ws, ws_bytes = _workspace(workspace, L.kdn_rec_bwd_workspace_size(B, T, D), dev)
-    _launch(dev, L.kdn_rec_bwd, B, T, D, io, code, int(bool(blend)), dh.data_ptr(), x.data_ptr(),
+    _launch(dev, L.kdn_rec_bwd, B, T, D, io | tail, code, int(bool(blend)), dh.data_ptr(), x.data_ptr(),
             stride, a.data_ptr(), a_stride, checkpoints.data_ptr(), _ptr(h0), _ptr(cu_seqlens), N,
             _ptr(dh_T), g["dx"].data_ptr(), g["da"].data_ptr(), g["dh0"].data_ptr(), _ptr(ws),
             ws_bytes)

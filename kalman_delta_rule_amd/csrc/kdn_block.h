@@ -40,6 +40,7 @@ struct ConvArgs {
     const void* state0;   // nullable [N,W-1,D]
     const int* cu;        // nullable [N+1]
     int N;
+    bool clear;  // zeros behind the last sequence, in y or dx
     void* y;
     void* state_T;  // nullable
     // backward
@@ -66,6 +67,7 @@ struct RecArgs {
     const float* h0;  // nullable [N,D]
     const int* cu;    // nullable [N+1]
     int N;
+    bool clear;  // zeros behind the last sequence, in h and ckpt or dx and da
     void* h;
     float* h_T;   // nullable [N,D]; step: the state, in place
     float* ckpt;  // [B, ceil(T / 64), D]; forward: nullable, written; backward: read

@@ -63,6 +63,17 @@ kdn_status check_io(int io)
     return KDN_OK;
 }
 
+// an io_dtype that may hold KDN_CLEAR_TAIL, which is taken out of it
+kdn_status check_packed_io(int& io, bool& clear)
+{
+    clear = io & KDN_CLEAR_TAIL;
+    io &= ~KDN_CLEAR_TAIL;
+    if (io != KDN_F32 && io != KDN_BF16)
+        return fail(KDN_ERR_INVALID_ARG, "io_dtype must be KDN_F32 (0) or KDN_BF16 (1), with KDN_CLEAR_TAIL (0x400) "
+                    "if wanted, got %d", clear ? io | KDN_CLEAR_TAIL : io);
+    return KDN_OK;
+}
+
 kdn_status check_width(int D)
 {
     if (D < 1)
@@ -238,6 +249,8 @@ kdn_status kdn_conv_fwd(int B, int T, int D, int W, int io_dtype, int activation
                         const void* state0, const int* cu_seqlens, int N, void* y, void* state_T,
                         void* stream)
 {
+    bool clear;
+    KDN_TRY(check_packed_io(io_dtype, clear));
     KDN_TRY(check_conv(W, io_dtype, activation));
     KDN_TRY(check_sequence(B, T, D, cu_seqlens, N));
     if ((__int128)N * (W - 1) * D >= kMaxElems)
@@ -255,7 +268,7 @@ kdn_status kdn_conv_fwd(int B, int T, int D, int W, int io_dtype, int activation
                         {state_T, ns, e, "state_T", true, false}};
     KDN_TRY(check_buffers(bufs));
     kdn::ConvArgs a{};
-    a.B = B, a.T = T, a.D = D, a.W = W, a.silu = activation == KDN_ACT_SILU;
+    a.B = B, a.T = T, a.D = D, a.W = W, a.silu = activation == KDN_ACT_SILU, a.clear = clear;
     a.x = x, a.xs = x_stride, a.weight = weight, a.bias = bias;
     a.state0 = state0, a.cu = cu_seqlens, a.N = N, a.y = y, a.state_T = state_T;
     return launched(kdn::launch_conv_fwd(a, io_dtype == KDN_BF16, (hipStream_t)stream),
@@ -276,6 +289,8 @@ kdn_status kdn_conv_bwd(int B, int T, int D, int W, int io_dtype, int activation
                         void* dx, float* dweight, float* dbias, void* dstate0, void* workspace,
                         size_t workspace_bytes, void* stream)
 {
+    bool clear;
+    KDN_TRY(check_packed_io(io_dtype, clear));
     KDN_TRY(check_conv(W, io_dtype, activation));
     KDN_TRY(check_sequence(B, T, D, cu_seqlens, N));
     if ((__int128)N * (W - 1) * D >= kMaxElems)
@@ -300,7 +315,7 @@ kdn_status kdn_conv_bwd(int B, int T, int D, int W, int io_dtype, int activation
                         {need ? workspace : nullptr, (long long)need, 1, "workspace", true, false}};
     KDN_TRY(check_buffers(bufs));
     kdn::ConvArgs a{};
-    a.B = B, a.T = T, a.D = D, a.W = W, a.silu = activation == KDN_ACT_SILU;
+    a.B = B, a.T = T, a.D = D, a.W = W, a.silu = activation == KDN_ACT_SILU, a.clear = clear;
     a.x = x, a.xs = x_stride, a.weight = weight, a.bias = bias;
     a.state0 = state0, a.cu = cu_seqlens, a.N = N;
     a.dy = dy, a.dstate_T = dstate_T, a.dx = dx, a.dweight = dweight, a.dbias = dbias;
@@ -359,6 +374,8 @@ kdn_status kdn_rec_fwd(int B, int T, int D, int io_dtype, int gate, int blend, c
                        const int* cu_seqlens, int N, void* h, float* h_T, float* checkpoints,
                        void* workspace, size_t workspace_bytes, void* stream)
 {
+    bool clear;
+    KDN_TRY(check_packed_io(io_dtype, clear));
     KDN_TRY(check_rec(io_dtype, gate, blend));
     KDN_TRY(check_sequence(B, T, D, cu_seqlens, N));
     long long xspan, aspan;
@@ -380,7 +397,7 @@ kdn_status kdn_rec_fwd(int B, int T, int D, int io_dtype, int gate, int blend, c
                         {need ? workspace : nullptr, (long long)need, 1, "workspace", true, false}};
     KDN_TRY(check_buffers(bufs));
     kdn::RecArgs r{};
-    r.B = B, r.T = T, r.D = D, r.preact = gate == KDN_GATE_PREACT, r.blend = blend == 1;
+    r.B = B, r.T = T, r.D = D, r.preact = gate == KDN_GATE_PREACT, r.blend = blend == 1, r.clear = clear;
     r.x = x, r.xs = x_stride, r.a = a, r.as = a_stride, r.h0 = h0, r.cu = cu_seqlens, r.N = N;
     r.h = h, r.h_T = h_T, r.ckpt = checkpoints, r.ws = workspace;
     return launched(kdn::launch_rec_fwd(r, io_dtype == KDN_BF16, (hipStream_t)stream), "kdn_rec_fwd");
@@ -392,6 +409,8 @@ kdn_status kdn_rec_bwd(int B, int T, int D, int io_dtype, int gate, int blend, c
                        const float* dh_T, void* dx, void* da, float* dh0, void* workspace,
                        size_t workspace_bytes, void* stream)
 {
+    bool clear;
+    KDN_TRY(check_packed_io(io_dtype, clear));
     KDN_TRY(check_rec(io_dtype, gate, blend));
     KDN_TRY(check_sequence(B, T, D, cu_seqlens, N));
     long long xspan, aspan;
@@ -416,7 +435,7 @@ kdn_status kdn_rec_bwd(int B, int T, int D, int io_dtype, int gate, int blend, c
                         {need ? workspace : nullptr, (long long)need, 1, "workspace", true, false}};
     KDN_TRY(check_buffers(bufs));
     kdn::RecArgs r{};
-    r.B = B, r.T = T, r.D = D, r.preact = gate == KDN_GATE_PREACT, r.blend = blend == 1;
+    r.B = B, r.T = T, r.D = D, r.preact = gate == KDN_GATE_PREACT, r.blend = blend == 1, r.clear = clear;
     r.x = x, r.xs = x_stride, r.a = a, r.as = a_stride, r.h0 = h0, r.cu = cu_seqlens, r.N = N;
     r.ckpt = const_cast<float*>(checkpoints), r.dh = dh, r.dh_T = dh_T;
     r.dx = dx, r.da = da, r.dh0 = dh0, r.ws = workspace;

@@ -128,6 +128,19 @@ __device__ __forceinline__ int token_limit(const ConvArgs& a)
     return a.cu ? min(max(a.cu[a.N], 0), a.T) : a.B * a.T;
 }
 
+// zeros in the rows of `out` for a run's tokens from the i-th on, where the call asks
+// for them: those behind the last sequence
+template <typename IO, int VE>
+__device__ __forceinline__ void clear_rows(const ConvArgs& a, const Place<VE>& at, int i, IO* out)
+{
+    if (!a.clear)
+        return;
+    constexpr float zeros[VE] = {};
+    const int stop = min(at.length, a.B * a.T - at.m);
+    for (i = max(i, 0); i < stop; ++i)
+        store_raw<IO, VE>(out + (size_t)(at.m + i) * a.D, zeros);
+}
+
 // whether any of marks [i, i + count) is set, for this thread's run (`lanes`
 // threads side by side look)
 __device__ __forceinline__ bool any_mark(const Marks& k, int i, int count, int lane, int lanes)
@@ -336,6 +349,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, Plan plan)
                         store_raw<IO, VE>(s + (size_t)r * a.D, f.win[r]);
                 }
             }
+            clear_rows<IO, VE>(a, at, stop, static_cast<IO*>(a.y) + at.c);
         }
     }
 
@@ -527,6 +541,7 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs a, Plan plan)
                     }
                 }
             }
+            clear_rows<IO, VE>(a, at, stop, dx);
         }
     }
 

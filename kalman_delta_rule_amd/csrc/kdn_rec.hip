@@ -521,18 +521,19 @@ __global__ __launch_bounds__(RUNS * 32, 4) void rec_fwd_kernel(RecArgs a, Chain 
 #pragma unroll
     for (int v = 0; v < V; ++v)
         h[v] = link.start(run, lane * V + v);
-    if (a.ckpt && (tile.t0 + first) % kChk == 0 && valid > 0) {
+    if (a.ckpt && (tile.t0 + first) % kChk == 0 && (valid > 0 || (a.clear && first < rows))) {
         const int blocks = (a.T + kChk - 1) / kChk;
         float* p = a.ckpt + ((size_t)tile.b * blocks + (tile.t0 + first) / kChk) * a.D + c;
         if (start & 1)
             state_at<V>(a.h0, marks.starting(a, tile.b, first), a.D, c, h);
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            p[v] = h[v];
+            p[v] = valid > 0 ? h[v] : 0.f;
     }
     char* ph = static_cast<char*>(a.h) + row0 * a.D * sizeof(IO);
     const uint32_t sh = (uint32_t)a.D * sizeof(IO);
     const uint32_t oh = first * sh + c * (uint32_t)sizeof(IO);
+    constexpr float zeros[V] = {};
     if (plain) {
 #pragma unroll
         for (int i = 0; i < L; ++i) {
@@ -544,8 +545,12 @@ __global__ __launch_bounds__(RUNS * 32, 4) void rec_fwd_kernel(RecArgs a, Chain 
     } else {
 #pragma unroll
         for (int i = 0; i < L; ++i) {
-            if (i >= valid)
+            IO* out = reinterpret_cast<IO*>(ph + (size_t)i * sh + oh);
+            if (i >= valid) {
+                if (a.clear && first + i < rows)
+                    store_raw<IO, V>(out, zeros);
                 continue;
+            }
             if (start >> i & 1)
                 state_at<V>(a.h0, marks.starting(a, tile.b, first + i), a.D, c, h);
 #pragma unroll
@@ -557,7 +562,7 @@ __global__ __launch_bounds__(RUNS * 32, 4) void rec_fwd_kernel(RecArgs a, Chain 
                 for (int v = 0; v < V; ++v)
                     p[v] = h[v];
             }
-            store_raw<IO, V>(reinterpret_cast<IO*>(ph + (size_t)i * sh + oh), h);
+            store_raw<IO, V>(out, h);
         }
     }
 
@@ -714,6 +719,10 @@ __global__ __launch_bounds__(kBwdRuns * 32, 4) void rec_bwd_kernel(RecArgs a, Ch
     char* pa = static_cast<char*>(a.da) + row0 * a.D * sizeof(GT);
     const uint32_t sx = (uint32_t)a.D * sizeof(IO), sa = (uint32_t)a.D * sizeof(GT);
     const uint32_t ox = first * sx + c * (uint32_t)sizeof(IO), oa = first * sa + c * (uint32_t)sizeof(GT);
+    auto store = [&](int i, const float(&dx)[V], const float(&da)[V]) {
+        store_raw<IO, V>(reinterpret_cast<IO*>(px + (size_t)i * sx + ox), dx);
+        store_raw<GT, V>(reinterpret_cast<GT*>(pa + (size_t)i * sa + oa), da);
+    };
     auto reverse = [&](int i) {
         float dx[V], da[V];
 #pragma unroll
@@ -724,9 +733,9 @@ __global__ __launch_bounds__(kBwdRuns * 32, 4) void rec_bwd_kernel(RecArgs a, Ch
             // dalpha times alpha (1 - alpha), of the factors at hand
             da[v] = PRE ? g[v] * rest[i][v] * part[i][v] : lam * part[i][v];
         }
-        store_raw<IO, V>(reinterpret_cast<IO*>(px + (size_t)i * sx + ox), dx);
-        store_raw<GT, V>(reinterpret_cast<GT*>(pa + (size_t)i * sa + oa), da);
+        store(i, dx, da);
     };
+    constexpr float zeros[V] = {};
     if (plain) {
 #pragma unroll
         for (int i = L - 1; i >= 0; --i)
@@ -734,8 +743,11 @@ __global__ __launch_bounds__(kBwdRuns * 32, 4) void rec_bwd_kernel(RecArgs a, Ch
     } else {
 #pragma unroll
         for (int i = L - 1; i >= 0; --i) {
-            if (i >= valid)
+            if (i >= valid) {
+                if (a.clear && first + i < rows)
+                    store(i, zeros, zeros);
                 continue;
+            }
             if (end >> i & 1)
                 state_at<V>(a.dh_T, marks.ending(a, tile.b, first + i), a.D, c, g);
             reverse(i);
