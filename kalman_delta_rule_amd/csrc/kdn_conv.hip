@@ -28,6 +28,7 @@
 // (LDS), moved it.
 #include "kdn_block.h"
 #include "kdn_common.h"
+#include "kdn_sequences.h"
 #include "kdn_stream.h"
 
 namespace kdn {
@@ -101,7 +102,8 @@ __device__ __forceinline__ void mark_tokens(Marks& k, const ConvArgs& a, int fir
         for (int i = threadIdx.x; i < count; i += 256)
             k.start[i] = k.end[i] = -1;
         __syncthreads();
-        for (int n = threadIdx.x; n < a.N; n += 256) {
+        const SequenceRange near = sequences_at<256>(a.cu, a.N, first, count);
+        for (int n = near.first + threadIdx.x; n < near.end; n += 256) {
             const int p = a.cu[n], q = a.cu[n + 1];
             if (p < 0 || p >= q)
                 continue;

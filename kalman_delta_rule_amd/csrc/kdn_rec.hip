@@ -40,6 +40,7 @@
 #include "kdn.h"
 #include "kdn_block.h"
 #include "kdn_common.h"
+#include "kdn_sequences.h"
 #include "kdn_stream.h"
 
 namespace kdn {
@@ -309,7 +310,8 @@ struct Marks {
         for (int i = threadIdx.x; i < TILE; i += THREADS)
             start[i] = end[i] = -1;
         __syncthreads();
-        for (int n = threadIdx.x; n < a.N; n += THREADS) {
+        const SequenceRange near = sequences_at<THREADS>(a.cu, a.N, t0, TILE);
+        for (int n = near.first + threadIdx.x; n < near.end; n += THREADS) {
             const int p = a.cu[n], q = a.cu[n + 1];
             if (p < 0 || p >= q)
                 continue;
