@@ -356,7 +356,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, Plan plan)
     }
 
     // the state of an empty sequence stays what it was
-    if (at.m0 == 0 && a.state_T && (a.cu || !M)) {
+    if (at.m0 == 0 && a.state_T && (a.cu || !M) && a.N <= kStatesOfRun * at.runs) {
         for (int n = at.run; n < a.N; n += at.runs) {
             if (a.cu && a.cu[n] < a.cu[n + 1])
                 continue;
@@ -548,7 +548,7 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs a, Plan plan)
     }
 
     // the gradient by the state of an empty sequence
-    if (at.m0 == 0 && a.dstate0 && (a.cu || !M)) {
+    if (at.m0 == 0 && a.dstate0 && (a.cu || !M) && a.N <= kStatesOfRun * at.runs) {
         for (int n = at.run; n < a.N; n += at.runs) {
             if (a.cu && a.cu[n] < a.cu[n + 1])
                 continue;
@@ -709,6 +709,9 @@ void launch(const ConvArgs& a, bool backward, hipStream_t stream)
         run(std::integral_constant<bool, (VE > 1)>{});
     else
         run(std::false_type{});
+    void* states = backward ? a.dstate0 : a.state_T;
+    if (states && (a.cu || !a.T) && a.N > kStatesOfRun * (256 >> p.lanes_log2))
+        launch_empty_states<IO>(a.cu, a.N, (W - 1) * a.D, backward ? a.dstate_T : a.state0, states, stream);
     if (backward)
         conv_sum_kernel<<<((a.W + 1) * a.D + 63) / 64, 1024, 0, stream>>>(a, a.T ? p.tiles : 0);
 }

@@ -569,7 +569,7 @@ __global__ __launch_bounds__(RUNS * 32, 4) void rec_fwd_kernel(RecArgs a, Chain 
     }
 
     // empty sequences keep their state
-    if (tile.k == 0 && a.h_T) {
+    if (tile.k == 0 && a.h_T && (!a.cu || a.N <= kStatesOfRun * RUNS)) {
         for (int n = a.cu ? run : tile.b; n < (a.cu ? a.N : tile.b + 1); n += RUNS) {
             if (a.cu ? a.cu[n] < a.cu[n + 1] : a.T > 0 || run > 0)
                 continue;
@@ -762,7 +762,7 @@ __global__ __launch_bounds__(kBwdRuns * 32, 4) void rec_bwd_kernel(RecArgs a, Ch
         }
     }
 
-    if (tile.k == 0 && a.dh0) {
+    if (tile.k == 0 && a.dh0 && (!a.cu || a.N <= kStatesOfRun * RUNS)) {
         for (int n = a.cu ? run : tile.b; n < (a.cu ? a.N : tile.b + 1); n += RUNS) {
             if (a.cu ? a.cu[n] < a.cu[n + 1] : a.T > 0 || run > 0)
                 continue;
@@ -851,6 +851,9 @@ hipError_t launch(const RecArgs& a, bool backward, hipStream_t stream)
         run(std::integral_constant<bool, (V > 1)>{});
     else
         run(std::false_type{});
+    float* states = backward ? a.dh0 : a.h_T;
+    if (states && a.cu && a.N > kStatesOfRun * (backward ? kBwdRuns : t.runs))
+        launch_empty_states<float>(a.cu, a.N, a.D, backward ? a.dh_T : a.h0, states, stream);
     return hipGetLastError();
 }
 

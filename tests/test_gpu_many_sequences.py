@@ -39,9 +39,9 @@ def crowd(T, N, at):
     return [0] + [at] * (N - 1) + [T]
 
 
-# (around 16 a run: 4 to 32 runs of the convolution, 8 and 16 of the recurrence)
-CASES = [(1000, 6, cuts(1000, n, n)) for n in (64, 65, 128, 129, 256, 257, 512, 513)]
-CASES += [(1500, 300, cuts(1500, 65, 3)), (1500, 300, cuts(1500, 257, 4)),
+# (around 20 a run: 4 to 32 runs of the convolution, 8 and 16 of the recurrence)
+CASES = [(1000, 6, cuts(1000, n, n)) for n in (80, 81, 160, 161, 320, 321, 640, 641)]
+CASES += [(1500, 300, cuts(1500, 81, 3)), (1500, 300, cuts(1500, 321, 4)),
           (5000, 6, cuts(5000, 4500, 5)), (5000, 6, cuts(5000, 9000, 6, 4990)), (300, 3, cuts(300, 20000, 7)),
           (700, 5, crowd(700, 5000, 300)), (700, 5, crowd(700, 5000, 0)), (700, 5, crowd(700, 5000, 700)),
           (1, 2, cuts(1, 3000, 8)), (0, 4, [0] * 3001), (40, 4, [0] * 5001), (2600, 1, cuts(2600, 2500, 9))]
@@ -134,6 +134,17 @@ def test_borders_of_many_sequences_take_little_time():
     at every offset, 230 times)."""
     many, one = calls(65536, 512, 1 << 20, False), calls(65536, 512, 2, False)
     for k in ("conv forward", "conv backward"):
+        t, t1 = timed(many[k]), timed(one[k])
+        print("%s: %.3f ms, with two sequences %.3f ms" % (k, t, t1))
+        assert t < 20 * t1, (k, t, t1)
+
+
+def test_states_of_many_sequences_take_little_time():
+    """65536 sequences in as many tokens, 512 channels: their states are as many bytes as x
+    four times over, and no run of the first tile may go through them one by one (100 times
+    the time of the call with one sequence, and more).  Measured 2 to 7 times."""
+    many, one = calls(65536, 512, 65536, True), calls(65536, 512, 2, True)
+    for k in many:
         t, t1 = timed(many[k]), timed(one[k])
         print("%s: %.3f ms, with two sequences %.3f ms" % (k, t, t1))
         assert t < 20 * t1, (k, t, t1)
