@@ -17,7 +17,6 @@
 // 32768 x 2048 bf16 77 us (5.2 TB/s) and 5 us for the sums, 4099 x 1537 fp32 16 and 4 us.
 #include "kdn_block.h"
 #include "kdn_common.h"
-#include "kdn_stream.h"
 
 namespace kdn {
 
@@ -94,18 +93,13 @@ struct Part {
         }
     }
 
-    template <bool ONCE, typename E>
+    template <typename E>
     __device__ __forceinline__ void load(const E* row, Vec<E, VE> (&x)[NV]) const
     {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             if (n[v] == VE) {
-                if constexpr (ONCE)
-                    x[v] = __builtin_bit_cast(
-                        Vec<E, VE>, __builtin_nontemporal_load(reinterpret_cast<const Words<E, sizeof(x[v]) / 4>*>(
-                                        row + col[v])));
-                else
-                    x[v] = *reinterpret_cast<const Vec<E, VE>*>(row + col[v]);
+                x[v] = *reinterpret_cast<const Vec<E, VE>*>(row + col[v]);
             } else {
 #pragma unroll
                 for (int j = 0; j < VE; ++j)
@@ -142,7 +136,7 @@ struct Part {
         if (!p)
             return;
         Vec<float, VE> x[NV];
-        load<false>(p, x);
+        load(p, x);
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -160,7 +154,7 @@ __device__ __forceinline__ int row_of_thread()
     return TPR >= 64 ? __builtin_amdgcn_readfirstlane(r) : r;
 }
 
-template <typename IO, int TPR, int NV, bool ONCE>
+template <typename IO, int TPR, int NV>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArgs a)
 {
     typedef Part<IO, TPR, NV> P;
@@ -176,7 +170,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArg
     const IO* x = static_cast<const IO*>(a.x);
     int row = blockIdx.x * per + row_of_thread<TPR>();
     Vec<IO, VE> raw[NV];
-    part.template load<ONCE>(x + (size_t)min(row, a.rows - 1) * a.xs, raw);
+    part.load(x + (size_t)min(row, a.rows - 1) * a.xs, raw);
     // every thread walks the same number of rows: rows behind the last repeat it
     for (int r0 = blockIdx.x * per; r0 < a.rows; r0 += step, row += step) {
         float d[NV][VE];
@@ -189,7 +183,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArg
                 s += d[v][j];
             }
         if (r0 + step < a.rows)
-            part.template load<ONCE>(x + (size_t)min(row + step, a.rows - 1) * a.xs, raw);
+            part.load(x + (size_t)min(row + step, a.rows - 1) * a.xs, raw);
         const float mean = row_sum<TPR>(s, 0.f, red).x / n;
         s = 0.f;
 #pragma unroll
@@ -228,7 +222,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArg
 // threads a workgroup 91 us, with four times the sums to write).
 constexpr int kBwdThreads = 1024;
 
-template <typename IO, int TPR, int NV, bool ONCE>
+template <typename IO, int TPR, int NV>
 __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs a)
 {
     typedef Part<IO, TPR, NV> P;
@@ -251,8 +245,8 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs a)
     for (int r0 = blockIdx.x * per; r0 < a.rows; r0 += step, row += step) {
         const int at = min(row, a.rows - 1);
         Vec<IO, VE> rx[NV], ry[NV];
-        part.template load<ONCE>(x + (size_t)at * a.xs, rx);
-        part.template load<ONCE>(dy + (size_t)at * a.D, ry);
+        part.load(x + (size_t)at * a.xs, rx);
+        part.load(dy + (size_t)at * a.D, ry);
         const float mean = a.mean[at], rstd = a.rstd[at];
         const bool mine = row < a.rows;
         float s1 = 0.f, s2 = 0.f;
@@ -498,11 +492,8 @@ hipError_t norm_fwd(const NormArgs& a, hipStream_t stream)
     // unasked for (524288 x 128 bf16 1024, 2048, 4096: 64, 51, 53 us; 32768 x 2048 49,
     // 48, 46 us)
     const int grid = groups < 2048 ? groups : 2048;
-    const bool once = (long long)a.rows * a.D * (long long)sizeof(IO) >= kLastLevelCache;
     auto run = [&](auto t, auto n) {
-        constexpr int T = decltype(t)::value, N = decltype(n)::value;
-        once ? norm_fwd_kernel<IO, T, N, true><<<grid, threads, 0, stream>>>(a)
-             : norm_fwd_kernel<IO, T, N, false><<<grid, threads, 0, stream>>>(a);
+        norm_fwd_kernel<IO, decltype(t)::value, decltype(n)::value><<<grid, threads, 0, stream>>>(a);
     };
     with_shape<8, 1>(s, run) || with_shape<16, 1>(s, run) || with_shape<32, 1>(s, run) ||
         with_shape<64, 1>(s, run) || with_shape<64, 2>(s, run) || with_shape<64, 4>(s, run) ||
@@ -536,11 +527,8 @@ hipError_t norm_bwd(const NormArgs& args, hipStream_t stream)
         if (sums)
             norm_bwd_wide_sums_kernel<IO><<<dim3(groups, (a.D + 255) / 256), 256, 0, stream>>>(a);
     } else if (a.rows) {
-        const bool once = (long long)a.rows * a.D * (long long)sizeof(IO) >= kLastLevelCache;
         auto run = [&](auto t, auto n) {
-            constexpr int T = decltype(t)::value, N = decltype(n)::value;
-            once ? norm_bwd_kernel<IO, T, N, true><<<groups, kBwdThreads, 0, stream>>>(a)
-                 : norm_bwd_kernel<IO, T, N, false><<<groups, kBwdThreads, 0, stream>>>(a);
+            norm_bwd_kernel<IO, decltype(t)::value, decltype(n)::value><<<groups, kBwdThreads, 0, stream>>>(a);
         };
         with_shape<8, 1>(s, run) || with_shape<16, 1>(s, run) || with_shape<32, 1>(s, run) ||
             with_shape<64, 1>(s, run) || with_shape<128, 1>(s, run) || with_shape<256, 1>(s, run) ||

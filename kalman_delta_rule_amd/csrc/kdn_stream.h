@@ -82,16 +82,18 @@ __device__ __forceinline__ void store_raw(E* p, const float (&v)[N])
 
 // Bytes of the last-level cache.  A call too large for it loads its rows as ONCE: they
 // then take no place in it from the rows being written, which leave it for HBM at their
-// own pace.  What is too large is measured (without and with, us): the recurrence gains
-// where all that it reads and writes is more than the cache (forward 403 MB 92 and 80,
-// 805 MB 175 and 161, backward 335 MB 85 and 74, 1.3 GB 311 and 291; fp32 40 MB read
-// again 29.9 and 32.3); the convolution and the layer norm, whose next call may still
-// find a smaller x there, where x alone fills it (convolution forward 537 MB 112 and
-// 89, backward 805 MB 179 and 164; layer norm forward 537 MB 101 and 90, fp32 102 and
-// 83, backward 805 MB 152 and 136; forward and backward on one x of 134 MB, marked
-// from half the size on, layer norm 129 and 140, packed convolution 157 and 164).
-// Stores marked the same way gave less, and cost up to 12% where a row is not whole
-// cache lines.
+// own pace.  What is too large is measured (bf16, without and with, us): the recurrence
+// gains where all that it reads and writes is more than the cache (forward 403 MB 92
+// and 82, 805 MB 154 and 140, backward 1.3 GB 271 and 270; forward and backward on one x
+// of 134, 268, 537 MB 232 and 219, 419 and 403, 818 and 796; fp32 40 MB read again 29.9
+// and 32.3).  The convolution, whose next call may still find a smaller x there, gains
+// from the size on where x alone fills it (forward 268 MB 112 and 89, 336 MB 140 and 141,
+// 537 MB 224 and 224; forward and backward on one x of 268, 336, 537 MB 290 and 250, 363
+// and 362, 581 and 586).  The layer norm does not: marked, its forward takes 100 and 88
+// at 268 MB and its backward 151 and 136, but the forward 124 and 127 at 336 MB, and both
+// on one x 252 and 254, 311 and 325, 490 and 513 (268, 336, 537 MB of 2048 channels), 509
+// and 578 (537 MB of 128).  Stores marked the same way gave less, and cost up to 12% where a row is not
+// whole cache lines.
 constexpr long long kLastLevelCache = 256ll << 20;
 
 }  // namespace kdn
