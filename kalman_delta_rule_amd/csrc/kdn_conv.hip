@@ -705,7 +705,9 @@ void launch(const ConvArgs& a, bool backward, hipStream_t stream)
         else
             conv_fwd_kernel<IO, VE, W, SILU, ONCE><<<grid, 256, 0, stream>>>(a, p);
     };
-    if (VE > 1 && (long long)a.B * a.T * a.D * (long long)sizeof(IO) >= kLastLevelCache)
+    const size_t e = sizeof(IO), row = a.D * e, x_row = a.xs * e;
+    const bool lines = (row | x_row | reinterpret_cast<uintptr_t>(a.x)) % kCacheLine == 0;
+    if (VE > 1 && lines && (long long)a.B * a.T * (long long)row >= kLastLevelCache)
         run(std::integral_constant<bool, (VE > 1)>{});
     else
         run(std::false_type{});

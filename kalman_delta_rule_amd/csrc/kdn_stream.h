@@ -89,11 +89,14 @@ __device__ __forceinline__ void store_raw(E* p, const float (&v)[N])
 // and 32.3).  The convolution, whose next call may still find a smaller x there, gains
 // from the size on where x alone fills it (forward 268 MB 112 and 89, 336 MB 140 and 141,
 // 537 MB 224 and 224; forward and backward on one x of 268, 336, 537 MB 290 and 250, 363
-// and 362, 581 and 586).  The layer norm does not: marked, its forward takes 100 and 88
+// and 362, 581 and 586), if rows are whole cache lines: others are read in pieces, a line
+// twice, and lose (280 MB of 2040 channels, forward and backward 367 and 434, of 2045 366 and
+// 446; the forward alone 144 and 119).  The layer norm does not: marked, its forward takes 100 and 88
 // at 268 MB and its backward 151 and 136, but the forward 124 and 127 at 336 MB, and both
 // on one x 252 and 254, 311 and 325, 490 and 513 (268, 336, 537 MB of 2048 channels), 509
 // and 578 (537 MB of 128).  Stores marked the same way gave less, and cost up to 12% where a row is not
 // whole cache lines.
 constexpr long long kLastLevelCache = 256ll << 20;
+constexpr size_t kCacheLine = 128;
 
 }  // namespace kdn
