@@ -847,7 +847,9 @@ hipError_t launch(const RecArgs& a, bool backward, hipStream_t stream)
             rec_fwd_kernel<IO, PRE, BLEND, V, 16, ONCE><<<grid, 16 * 32, 0, stream>>>(a, ch, t.ctiles);
     };
     const long long io = sizeof(IO), gate = PRE ? io : 4, values = (long long)a.B * a.T * a.D;
-    if (V > 1 && values * (backward ? 3 * io + 2 * gate : 2 * io + gate) > kLastLevelCache)
+    const bool lines = (a.D * io | a.xs * io | a.as * gate) % kCacheLine == 0;
+    if (V > 1 && values * (backward ? 3 * io + 2 * gate : 2 * io + gate) > kLastLevelCache &&
+        (lines || values * io < kLastLevelCache))
         run(std::integral_constant<bool, (V > 1)>{});
     else
         run(std::false_type{});

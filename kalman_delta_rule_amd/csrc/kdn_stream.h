@@ -82,20 +82,22 @@ __device__ __forceinline__ void store_raw(E* p, const float (&v)[N])
 
 // Bytes of the last-level cache.  A call too large for it loads its rows as ONCE: they
 // then take no place in it from the rows being written, which leave it for HBM at their
-// own pace.  What is too large is measured (bf16, without and with, us): the recurrence
-// gains where all that it reads and writes is more than the cache (forward 403 MB 92
-// and 82, 805 MB 154 and 140, backward 1.3 GB 271 and 270; forward and backward on one x
-// of 134, 268, 537 MB 232 and 219, 419 and 403, 818 and 796; fp32 40 MB read again 29.9
-// and 32.3).  The convolution, whose next call may still find a smaller x there, gains
-// from the size on where x alone fills it (forward 268 MB 112 and 89, 336 MB 140 and 141,
-// 537 MB 224 and 224; forward and backward on one x of 268, 336, 537 MB 290 and 250, 363
-// and 362, 581 and 586), if rows are whole cache lines: others are read in pieces, a line
-// twice, and lose (280 MB of 2040 channels, forward and backward 367 and 434, of 2045 366 and
-// 446; the forward alone 144 and 119).  The layer norm does not: marked, its forward takes 100 and 88
-// at 268 MB and its backward 151 and 136, but the forward 124 and 127 at 336 MB, and both
-// on one x 252 and 254, 311 and 325, 490 and 513 (268, 336, 537 MB of 2048 channels), 509
-// and 578 (537 MB of 128).  Stores marked the same way gave less, and cost up to 12% where a row is not
-// whole cache lines.
+// own pace.  What is too large is measured (us, without and with; sizes are x's, bf16):
+// - The recurrence gains where all that it reads and writes is more than the cache:
+//   forward 134 MB 92 and 82, 268 MB 154 and 140; forward and backward on one x of 134,
+//   268, 537 MB 232 and 219, 419 and 403, 818 and 796 (fp32 of 40 MB in all 29.9 and 32.3).
+//   Where rows are not whole cache lines a line is read in pieces by two workgroups, and x
+//   alone has to be less than the cache (fp32 1023 channels, 134 MB, forward 95 and 86; 2047
+//   channels, 537 MB, 342 and 390).
+// - The convolution, whose next call may still find a smaller x there, gains where x alone
+//   fills it and rows are whole cache lines: forward 268, 336, 537 MB 112 and 89, 140 and 141,
+//   224 and 224; forward and backward on one x 290 and 250, 363 and 362, 581 and 586.  2040
+//   channels, 286 MB: forward 144 and 119, but with the backward 367 and 434.
+// - The layer norm does not: its forward takes 100 and 88 for 268 MB and its backward 151 and
+//   136, but the forward 124 and 127 for 336 MB, and both on one x of 268, 336, 537 MB 252
+//   and 254, 311 and 325, 490 and 513 (537 MB in rows of 128 509 and 578).
+// Stores marked the same way gave less, and cost up to 12% where a row is not whole cache
+// lines.
 constexpr long long kLastLevelCache = 256ll << 20;
 constexpr size_t kCacheLine = 128;
 
