@@ -22,10 +22,12 @@
 //
 // The forward is bound by HBM: 32768 x 2048 bf16 49 us (5.5 TB/s of inputs and
 // outputs), 65536 x 2048 89 us (6.0 TB/s), 16384 x 2048 fp32 44 us (6.1 TB/s).  The
-// backward, 96 to 101, 164 and 88 us (4.0 to 4.9 TB/s), is held back by its registers,
-// 150 a thread with three waves a SIMD: 33 vector instructions a value take 60% of the
-// time, and neither two nor four channels' fewer or more registers, nor fewer bytes
-// (LDS), moved it.
+// backward, 95 to 103, 164 and 88 us (3.9 to 4.9 TB/s), is bound by neither HBM nor the
+// vector units alone: 31 instructions a value keep those busy 69% of the time (counted),
+// with three waves a SIMD to cover loads (four taps and SiLU: 152 registers a thread in
+// bf16; in fp32 168, and 20 more spilled).  3 x 1021 x 333 fp32, three taps: 6 us forward,
+// 9 and 4 us backward, 192 workgroups whose runs of 8 tokens are walked one token after
+// another.
 #include "kdn_block.h"
 #include "kdn_common.h"
 #include "kdn_sequences.h"

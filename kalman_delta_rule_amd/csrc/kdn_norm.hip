@@ -14,7 +14,9 @@
 //
 // Measured (kernel time; bytes of inputs and outputs): forward 524288 x 128 bf16 49 us
 // (5.5 TB/s), 32768 x 2048 46 us (5.8 TB/s), 4099 x 1537 fp32 11 us (4.6 TB/s); backward
-// 32768 x 2048 bf16 77 us (5.2 TB/s) and 5 us for the sums, 4099 x 1537 fp32 16 and 4 us.
+// 32768 x 2048 bf16 79 us (5.1 TB/s) and 5 us for the sums, 4099 x 1537 fp32 16 and 4 us.
+// Few wide rows are further off: backward 1024 x 16384 bf16 30 and 6 us (2.8 TB/s), 256 x
+// 16384 18 and 6 us, where the partial sums of up to 256 workgroups outweigh the rows.
 #include "kdn_block.h"
 #include "kdn_common.h"
 
@@ -355,6 +357,8 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(NormArgs a, int groups)
 }
 
 // ---- rows too wide for registers: walked three times, from L2 --------------------
+// A value a load: 512 x 32768 bf16 forward 32 us (2.1 TB/s of inputs and outputs), backward
+// 32 us and 17 + 5 us for the sums; fp32 51 us (2.6 TB/s), 60 and 21 + 5 us.
 
 __device__ __forceinline__ float wide_sum(float v, float2* red) { return row_sum<1024>(v, 0.f, red).x; }
 

@@ -26,9 +26,10 @@
 //
 // Bound by HBM and by the time from load to store of the tiles that the registers
 // hold at a time.  Measured (kernel time; bytes of inputs and outputs): forward B8
-// T4096 D2048 bf16 78 us (5.2 TB/s), B1 T65536 170 us (4.7 TB/s); backward 134 us
-// (5.0 TB/s) and 303 us (4.4 TB/s); with loads that are not marked as non-temporal 88,
-// 184, 148 and 319 us.  Loading the next tile ahead in a workgroup that
+// T4096 D2048 bf16 77 us (5.2 TB/s), B1 T65536 172 us (4.7 TB/s); backward 134 us
+// (5.0 TB/s) and 305 us (4.4 TB/s); with loads that are not marked as non-temporal 88,
+// 184, 148 and 319 us.  fp32, alpha given, B4 T4096 D2048: 73 us (5.5 TB/s) and 118 us (5.7
+// TB/s, part of it from the last-level cache).  Loading the next tile ahead in a workgroup that
 // stays (128 registers, or 8 tokens a run) was slower, 111 us and more; a scratch
 // access anywhere in the walks costs half the speed.
 //
