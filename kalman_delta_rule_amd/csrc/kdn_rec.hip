@@ -37,7 +37,7 @@
 // such a span gives U whatever it is handed: nothing, infinities and NaN included,
 // passes from one sequence to another.  Within a sequence they stay to its end, as by
 // the definition: a product of decays that underflows is kept above zero, where an
-// infinity stays one, and a decay of zero (kZero) makes it NaN.
+// infinity stays one, and a decay of zero makes it NaN.
 #include "kdn.h"
 #include "kdn_block.h"
 #include "kdn_common.h"
@@ -131,10 +131,9 @@ __device__ __forceinline__ Word await(const Word* p, Word v)
     return v;
 }
 
-// A of a span: the product of its decays, at least kLeast; kZero if one of them is
-// zero; kCut with a sequence's border in it (or with a decay that is NaN: U is then NaN
-// too).
-constexpr float kLeast = 0x1p-149f, kZero = -0.f, kCut = __builtin_nanf("");
+// A of a span: the product of its decays, at least kLeast unless one of them is zero;
+// kCut with a sequence's border in it (or with a decay that is NaN: U is then NaN too).
+constexpr float kLeast = 0x1p-149f, kCut = __builtin_nanf("");
 
 __device__ __forceinline__ float apply(float A, float U, float carry)
 {
@@ -158,10 +157,8 @@ __device__ __forceinline__ float2 span_of(unsigned long long w)
 // span a, then span b
 __device__ __forceinline__ float2 join(float2 a, float2 b)
 {
-    // kCut and kZero on either side stay; of unsigned numbers +0 alone, a product that
-    // underflowed, is less than kLeast
-    const uint32_t A = __float_as_uint(a.x * fabsf(b.x)) | (__float_as_uint(b.x) & 0x80000000u);
-    return float2{__uint_as_float(max(A, __float_as_uint(kLeast))), apply(b.x, b.y, a.y)};
+    const float A = a.x * b.x, least = fminf(fminf(fabsf(a.x), fabsf(b.x)), kLeast);
+    return float2{A == 0.f ? least : A, apply(b.x, b.y, a.y)};
 }
 
 // For column `col` of this lane and tile `k` in chain order, whose span is
@@ -373,7 +370,7 @@ __device__ __forceinline__ void close_run(float (&A)[V], const float (&al)[L][V]
 #pragma unroll
             for (int i = 0; i < L; ++i)
                 zero |= i < valid && al[i][v] == 0.f;
-            A[v] = zero ? kZero : kLeast;
+            A[v] = zero ? 0.f : kLeast;
         }
         if (cut)
             A[v] = kCut;

@@ -97,3 +97,18 @@ def test_bad_values_stay_to_the_end(case, bad, gate, blend, io):
         fine = np.isfinite(ref["da"][0][:, :end])
         got = host(g["da"])[:, :end]
         assert np.isfinite(got[fine]).all() and not np.isfinite(got[~fine]).any()
+
+
+@pytest.mark.parametrize("T,D", [(2000, 70), (300, 1)])
+def test_negative_decays_keep_their_sign(T, D):
+    """A decay given below zero is outside what the call promises, and is computed all the
+    same; its errors are at most those of its magnitude."""
+    rng = np.random.default_rng(7)
+    (x, xr), (dh, dhr) = (dev(rng.standard_normal((1, T, D))) for _ in range(2))
+    a, ar = dev(rng.uniform(-1, 1, (1, T, D)))
+    ref = R.rec(xr, ar, None, None, False, False, dhr)
+    size = R.rec(np.abs(xr), np.abs(ar), None, None, False, False, np.abs(dhr))
+    h, h_T, chk = kda.kdn_rec_fwd(x, a, gate="alpha", want_checkpoints=True)
+    g = kda.kdn_rec_bwd(dh, x, a, chk, gate="alpha")
+    for got, k in ((h, "h"), (h_T, "h_T"), (g["dx"], "dx"), (g["da"], "da"), (g["dh0"], "dh0")):
+        check(host(got), (ref[k][0], size[k][1]), "f32", k)
