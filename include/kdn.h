@@ -445,9 +445,10 @@ kdn_status kdn_gain_scan_static(int variant, int B, int T, int H, int dk, int io
  */
 
 /*
- * OR-ed into the io_dtype of kdn_conv_fwd, kdn_conv_bwd, kdn_rec_fwd and
- * kdn_rec_bwd: the rows of y, of h and checkpoints, of dx and da behind the last
- * packed sequence are set to zero instead of left as they were.
+ * OR-ed into the io_dtype of the forward and backward calls that take packed
+ * sequences (kdn_conv, kdn_rec, kdn_linattn): the rows of y, of h and
+ * checkpoints, of o and of the gradients by token behind the last packed sequence are set to
+ * zero instead of left as they were.
  */
 enum { KDN_CLEAR_TAIL = 0x400 };
 
@@ -573,6 +574,72 @@ kdn_status kdn_rec_bwd(int B, int T, int D, int io_dtype, int gate, int blend, c
 kdn_status kdn_rec_step(int B, int D, int io_dtype, int gate, int blend, const void* x,
                         long long x_stride, const void* a, long long a_stride, float* state,
                         void* h, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the memory recurrence without
+ * a gain and without the delta rule.  Conventions as for the operators above.
+ * Per token and head h, with g = decay[h] and the q and k of head h / (H / Hk):
+ *   S_t = g S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+ *   q, k  [B,T,Hk,dk], v [B,T,H,dv] io dtype; H a multiple of Hk (a group of
+ *         adjacent heads shares one q and k); dk, dv from 1 to 256.  Token t of
+ *         a row's head starts `stride` elements behind token t - 1 (rows follow
+ *         one another T tokens apart) and `head_stride` behind the head before:
+ *         dim <= head_stride, (heads - 1) head_stride + dim <= stride <= 2^22
+ *   decay [H] fp32, 0 <= g <= 1 (constants: they have no gradient here)
+ *   scale finite
+ *   S0    [N,H,dk,dv] fp32 state before each sequence, nullable (zeros)
+ *   o     [B,T,H,dv] io dtype;  S_T [N,H,dk,dv] fp32, nullable: the state after
+ *         each sequence (S0 for an empty one)
+ *   workspace  kdn_linattn_fwd_workspace_size bytes (0 unless few heads have
+ *         many tokens: the states handed between pieces of a sequence)
+ * bf16: products of bf16 operands, summed in fp32; the products' own operands
+ * that are not inputs (the decayed q k^T, and the state where o is formed from
+ * it) are rounded to bf16, those that states are summed from to 16 bits.  fp32:
+ * products of fp32 operands.
+ * What is not finite stays in its sequence and head and reaches no earlier
+ * token; an infinity may become a NaN later in the sequence.
+ */
+size_t kdn_linattn_fwd_workspace_size(int B, int T, int H, int dk, int dv);
+kdn_status kdn_linattn_fwd(int B, int T, int H, int Hk, int dk, int dv, int io_dtype, float scale,
+                           const void* q, long long q_stride, long long q_head_stride,
+                           const void* k, long long k_stride, long long k_head_stride,
+                           const void* v, long long v_stride, long long v_head_stride,
+                           const float* decay, const float* S0, const int* cu_seqlens, int N,
+                           void* o, float* S_T, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * Backward of kdn_linattn_fwd, for d_o [B,T,H,dv] (io dtype) = dL/do and dS_T
+ * [N,H,dk,dv] (fp32, nullable: zeros) = dL/dS_T.  With
+ * R_t = scale q_t d_o_t^T + g R_{t+1} (dS_T in place of the second term at a
+ * sequence's end):
+ *   dq_t = scale S_t d_o_t, dk_t = R_t v_t, summed over a group's heads
+ *                                                   [B,T,Hk,dk] io dtype
+ *   dv_t = R_t^T k_t                                [B,T,H,dv]  io dtype
+ *   dS0  = g R_1 (dS_T for an empty sequence)       [N,H,dk,dv] fp32, nullable
+ * S_t is formed again from S0, k and v.
+ */
+size_t kdn_linattn_bwd_workspace_size(int B, int T, int H, int Hk, int dk, int dv);
+kdn_status kdn_linattn_bwd(int B, int T, int H, int Hk, int dk, int dv, int io_dtype, float scale,
+                           const void* d_o, const void* q, long long q_stride,
+                           long long q_head_stride, const void* k, long long k_stride,
+                           long long k_head_stride, const void* v, long long v_stride,
+                           long long v_head_stride, const float* decay, const float* S0,
+                           const int* cu_seqlens, int N, const float* dS_T, void* dq, void* dk_out,
+                           void* dv_out, float* dS0, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * One token of kdn_linattn_fwd for each of B sequences: q, k (rows of [Hk,dk]),
+ * v (rows of [H,dv]), strides as above; o [B,H,dv]; state [B,H,dk,dv] fp32 is
+ * updated in place.
+ */
+kdn_status kdn_linattn_step(int B, int H, int Hk, int dk, int dv, int io_dtype, float scale,
+                            const void* q, long long q_stride, long long q_head_stride,
+                            const void* k, long long k_stride, long long k_head_stride,
+                            const void* v, long long v_stride, long long v_head_stride,
+                            const float* decay, float* state, void* o, void* stream);
 
 const char* kdn_status_string(int status);
 const char* kdn_last_error_message(void);

@@ -116,6 +116,18 @@ def lib():
                               + [fp, vp, sz, vp])
     L.kdn_rec_step.restype = i
     L.kdn_rec_step.argtypes = [i] * 5 + [vp, ll] * 2 + [fp, vp, vp]
+    rows = [vp, ll, ll]  # a tensor of heads: its pointer, and the strides of tokens and heads
+    L.kdn_linattn_fwd_workspace_size.restype = sz
+    L.kdn_linattn_fwd_workspace_size.argtypes = [i] * 5
+    L.kdn_linattn_fwd.restype = i
+    L.kdn_linattn_fwd.argtypes = [i] * 7 + [f] + rows * 3 + [fp] * 2 + [vp, i, vp, fp, vp, sz, vp]
+    L.kdn_linattn_bwd_workspace_size.restype = sz
+    L.kdn_linattn_bwd_workspace_size.argtypes = [i] * 6
+    L.kdn_linattn_bwd.restype = i
+    L.kdn_linattn_bwd.argtypes = ([i] * 7 + [f, vp] + rows * 3 + [fp] * 2 + [vp, i, fp] + [vp] * 3
+                                  + [fp, vp, sz, vp])
+    L.kdn_linattn_step.restype = i
+    L.kdn_linattn_step.argtypes = [i] * 6 + [f] + rows * 3 + [fp] * 2 + [vp, vp]
     L.kdn_status_string.restype = ctypes.c_char_p
     L.kdn_status_string.argtypes = [i]
     L.kdn_last_error_message.restype = ctypes.c_char_p
@@ -134,7 +146,9 @@ EXPORTED = ("kdn_fwd_workspace_size", "kdn_diag_fwd", "kdn_iso_fwd", "kdn_step",
             "kdn_gain_scan_static", "kdn_layer_norm_fwd", "kdn_layer_norm_bwd_workspace_size",
             "kdn_layer_norm_bwd", "kdn_conv_fwd", "kdn_conv_bwd_workspace_size", "kdn_conv_bwd",
             "kdn_conv_step", "kdn_rec_fwd_workspace_size", "kdn_rec_fwd",
-            "kdn_rec_bwd_workspace_size", "kdn_rec_bwd", "kdn_rec_step", "kdn_status_string",
+            "kdn_rec_bwd_workspace_size", "kdn_rec_bwd", "kdn_rec_step",
+            "kdn_linattn_fwd_workspace_size", "kdn_linattn_fwd", "kdn_linattn_bwd_workspace_size",
+            "kdn_linattn_bwd", "kdn_linattn_step", "kdn_status_string",
             "kdn_last_error_message", "kdn_version")
 
 

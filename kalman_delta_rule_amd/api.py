@@ -877,3 +877,141 @@ def kdn_rec_step(x, a, state, gate: str = "preact", blend: bool = False, h=None)
     _launch(dev, L.kdn_rec_step, B, D, io, code, int(bool(blend)), x.data_ptr(), stride,
             a.data_ptr(), a_stride, state.data_ptr(), h.data_ptr())
     return h
+
+
+def _heads(t, name, shape, dtype, device):
+    """_need for heads [..., heads, dim] that may lie in wider rows (q, k and v
+    of a fused projection, say): (pointer, stride of a token, of a head).  The
+    axes in front are tokens, evenly spaced."""
+    heads, dim = shape[-2:]
+    if (type(t) is torch.Tensor and t.dtype == dtype and t.shape == shape
+            and t.is_contiguous() and t.device == device):
+        return t.data_ptr(), heads * dim, dim
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.numel() == 0:
+        return t.data_ptr(), heads * dim, dim
+    if dim > 1 and t.stride(-1) != 1:
+        raise ValueError("%s must have its channels side by side (stride 1)" % name)
+    hs = t.stride(-2) if heads > 1 else dim
+    row = (heads - 1) * hs + dim
+    if hs < dim:
+        raise ValueError("%s has heads that overlap" % name)
+    step, rows = row, 0
+    for size, stride in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        if size == 1:
+            continue
+        if rows == 0:
+            step, rows = stride, size
+        elif stride == step * rows:
+            rows *= size
+        else:
+            raise ValueError("%s must have its tokens evenly spaced" % name)
+    if step < row:
+        raise ValueError("%s must have a token's heads side by side, and no tokens that overlap" % name)
+    return t.data_ptr(), step, hs
+
+
+def _linattn_sizes(q, v, axes):
+    """The checks that a call's first tensors get: device, io code, Hk, H, dk, dv."""
+    dev, io = _first(q, "q", axes)
+    if not isinstance(v, torch.Tensor) or v.dim() != axes:
+        raise ValueError("v must be a tensor with %d axes" % axes)
+    Hk, dk = q.shape[-2:]
+    H, dv = v.shape[-2:]
+    if Hk < 1 or H < 1 or H % Hk:
+        raise ValueError("v's heads (%d) must be a multiple of q's (%d)" % (H, Hk))
+    return dev, io, Hk, H, dk, dv
+
+
+def _scale(scale, dk) -> float:
+    return max(dk, 1) ** -0.5 if scale is None else float(scale)
+
+
+def kdn_linattn_fwd(q, k, v, decay, scale=None, S0=None, cu_seqlens=None, want_state: bool = False,
+                    o=None, S_T=None, workspace=None):
+    """Linear attention with a decay for each head: S_t = g S_{t-1} + k_t v_t^T,
+    o_t = scale S_t^T q_t, over q, k [B,T,Hk,dk] and v [B,T,H,dv] (bf16 or fp32;
+    slices of wider rows are fine; H a multiple of Hk: adjacent heads share a q
+    and k) with decay g [H] fp32.  ``scale`` is dk^-0.5 without.  S0 [N,H,dk,dv]
+    fp32 is the state before each sequence (zeros without); cu_seqlens (int32
+    [N+1]) packs N sequences into one row.  Returns (o [B,T,H,dv], S_T): S_T
+    [N,H,dk,dv] fp32, the state after each sequence, if given or with
+    ``want_state`` (None otherwise).  Behind the last sequence a new o holds
+    zeros, and a caller's keeps what it held."""
+    L = _lib.lib()
+    dev, io, Hk, H, dk, dv = _linattn_sizes(q, v, 4)
+    B, T = q.shape[:2]
+    N = _sequences(cu_seqlens, B, dev)
+    f32 = torch.float32
+    qh = _heads(q, "q", q.shape, q.dtype, dev)
+    kh = _heads(k, "k", q.shape, q.dtype, dev)
+    vh = _heads(v, "v", (B, T, H, dv), q.dtype, dev)
+    _need(decay, "decay", (H,), f32, dev)
+    _optional(dev, (S0, "S0", (N, H, dk, dv), f32), (S_T, "S_T", (N, H, dk, dv), f32))
+    tail = _tail(cu_seqlens, o)
+    o = _given(o, "o", v)
+    if S_T is None and want_state:
+        S_T = torch.empty((N, H, dk, dv), dtype=f32, device=dev)
+    ws, ws_bytes = _workspace(workspace, L.kdn_linattn_fwd_workspace_size(B, T, H, dk, dv), dev)
+    _launch(dev, L.kdn_linattn_fwd, B, T, H, Hk, dk, dv, io | tail, _scale(scale, dk), *qh, *kh, *vh,
+            decay.data_ptr(), _ptr(S0), _ptr(cu_seqlens), N, o.data_ptr(), _ptr(S_T), _ptr(ws),
+            ws_bytes)
+    return o, S_T
+
+
+def kdn_linattn_bwd(d_o, q, k, v, decay, scale=None, S0=None, dS_T=None, cu_seqlens=None, dq=None,
+                    dk=None, dv=None, workspace=None) -> dict:
+    """Backward of kdn_linattn_fwd given by the same arguments, for dL/do = d_o
+    [B,T,H,dv] and dL/dS_T = dS_T (optional).  Returns a dict with dq, dk
+    [B,T,Hk,dk] (summed over the heads that share them), dv [B,T,H,dv] (q's
+    dtype) and, where S0 is given, dS0 (fp32).  The decays have no gradient.
+    Behind the last sequence new dq, dk and dv hold zeros, and the caller's keep
+    what they held."""
+    L = _lib.lib()
+    dev, io, Hk, H, d_k, d_v = _linattn_sizes(q, v, 4)
+    B, T = q.shape[:2]
+    N = _sequences(cu_seqlens, B, dev)
+    f32 = torch.float32
+    qh = _heads(q, "q", q.shape, q.dtype, dev)
+    kh = _heads(k, "k", q.shape, q.dtype, dev)
+    vh = _heads(v, "v", (B, T, H, d_v), q.dtype, dev)
+    _need(d_o, "d_o", (B, T, H, d_v), q.dtype, dev)
+    _need(decay, "decay", (H,), f32, dev)
+    _optional(dev, (S0, "S0", (N, H, d_k, d_v), f32), (dS_T, "dS_T", (N, H, d_k, d_v), f32),
+              (dq, "dq", q.shape, q.dtype), (dk, "dk", q.shape, q.dtype),
+              (dv, "dv", (B, T, H, d_v), q.dtype))
+    tail = _tail(cu_seqlens, dq, dk, dv)
+    new = lambda t, shape: _beside(shape, q.dtype, dev, cu_seqlens, tail) if t is None else t
+    g = {"dq": new(dq, q.shape), "dk": new(dk, q.shape), "dv": new(dv, (B, T, H, d_v))}
+    if S0 is not None:
+        g["dS0"] = torch.empty_like(S0)
+    ws, ws_bytes = _workspace(workspace, L.kdn_linattn_bwd_workspace_size(B, T, H, Hk, d_k, d_v), dev)
+    _launch(dev, L.kdn_linattn_bwd, B, T, H, Hk, d_k, d_v, io | tail, _scale(scale, d_k),
+            d_o.data_ptr(), *qh, *kh, *vh, decay.data_ptr(), _ptr(S0), _ptr(cu_seqlens), N, _ptr(dS_T),
+            g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(), _ptr(g.get("dS0")), _ptr(ws),
+            ws_bytes)
+    return g
+
+
+def kdn_linattn_step(q, k, v, decay, state, scale=None, o=None) -> torch.Tensor:
+    """One token of kdn_linattn_fwd: q, k [B,Hk,dk], v [B,H,dv]; state
+    [B,H,dk,dv] fp32 is updated in place.  Returns o [B,H,dv]."""
+    L = _lib.lib()
+    dev, io, Hk, H, dk, dv = _linattn_sizes(q, v, 3)
+    B = q.shape[0]
+    qh = _heads(q, "q", q.shape, q.dtype, dev)
+    kh = _heads(k, "k", q.shape, q.dtype, dev)
+    vh = _heads(v, "v", (B, H, dv), q.dtype, dev)
+    _need(decay, "decay", (H,), torch.float32, dev)
+    _need(state, "state", (B, H, dk, dv), torch.float32, dev)
+    o = _given(o, "o", v)
+    _launch(dev, L.kdn_linattn_step, B, H, Hk, dk, dv, io, _scale(scale, dk), *qh, *kh, *vh,
+            decay.data_ptr(), state.data_ptr(), o.data_ptr())
+    return o

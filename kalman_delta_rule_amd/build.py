@@ -17,9 +17,10 @@ LIB = os.path.join(HERE, "libkdn.so")
 SOURCES = ["kdn_api.cpp", "kdn_walk.hip", "kdn_chunk.hip", "kdn_step.hip", "kdn_gain.hip",
            "kdn_dense.hip", "kdn_bwd.hip", "kdn_bwd_chunk.hip",
            "kdn_prologue.hip", "kdn_seqpar.hip", "kdn_plan.cpp",
-           "kdn_block_api.cpp", "kdn_norm.hip", "kdn_conv.hip", "kdn_rec.hip"]
+           "kdn_block_api.cpp", "kdn_norm.hip", "kdn_conv.hip", "kdn_rec.hip",
+           "kdn_linattn_api.cpp", "kdn_linattn.hip"]
 # sources whose kernels use the matrix cores (checked by isa_check)
-MFMA_SOURCES = ["kdn_walk.hip", "kdn_chunk.hip", "kdn_bwd_chunk.hip"]
+MFMA_SOURCES = ["kdn_walk.hip", "kdn_chunk.hip", "kdn_bwd_chunk.hip", "kdn_linattn.hip"]
 ARCH = os.environ.get("KDN_OFFLOAD_ARCH", "gfx950")
 
 HIPCC_FLAGS = [

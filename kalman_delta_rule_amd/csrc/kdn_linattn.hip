@@ -1,0 +1,853 @@
+// kdn_linattn.hip -- linear attention with a decay for each head, gfx950.
+//
+//   S_t = g S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+//
+// Every pass over a sequence is one walk with a state X [kd x vd] and inputs
+// q, k [kd], v [vd] a token, in the order of the walk:
+//
+//   y_i = of_x g^(i + 1 - late) X^T q_i + of_p sum_{j <= i} g^(i - j) (q_i k_j) v_j
+//   X  <- g^C X + of_u sum_j g^(C - 1 - j + late) k_j v_j^T          (chunks of C tokens)
+//
+//   forward   y = o:  q, k, v; state S
+//   backward  y = dq: do, v, k forwards, state S^T
+//             y = dv: k, q, do backwards, state dL/dS, with late = 1: a state behind a
+//                     token has decayed once more before it meets that token's k
+//             y = dk: v, do, q backwards, state (dL/dS)^T, late = 1
+//
+// A workgroup of four waves has one head and 64 columns of v and X.  A wave keeps X of
+// its 16 columns in matrix accumulators for the whole walk: they are at once the operand
+// of q X (the lanes of an accumulator hold four adjacent rows, which is a piece of the
+// operand if q's pieces are taken in the same order).  q k^T is formed transposed, so that
+// a lane's four values are adjacent in a row of the decayed product, which goes through
+// LDS to all waves.  The token's decay is put on v, in registers, not on k.
+//
+// bf16: the products' operands are bf16, sums and states fp32.  q, k, v are exact.  What
+// is rounded to an operand once: the decayed q k (2^-8 of each term of a y that is
+// itself rounded to 2^-8) and X where y is formed from it (the same).  X itself is summed
+// from v's decayed values as two bf16 parts (2^-16 of each term), since states are fp32
+// outputs.  fp32: matrix instructions with fp32 operands throughout.
+#include "kdn_common.h"
+#include "kdn_linattn.h"
+#include "kdn_sequences.h"
+#include "kdn_stream.h"
+
+#include <type_traits>
+
+namespace kdn {
+
+namespace {
+
+constexpr int kThreads = 256, kCols = 64;  // columns of v a workgroup
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// Operands of one step of a 16 x 16 product, and how they are read.  A lane (g, c) =
+// (lane / 16, lane % 16) holds for row c of an operand those k of the step that lie in
+// the rows of accumulators which it holds: 4 g .. 4 g + 3 of every 16.
+template <typename IO>
+struct Op;
+
+template <>
+struct Op<bf16> {
+    typedef bf16x8 frag;
+    static constexpr int K = 32;   // of a step
+    static constexpr int VE = 8;   // elements of 16 bytes
+    static constexpr int PAD = 8;  // of a row in LDS
+    // a row of `m` holds the k: [row][k]
+    static __device__ __forceinline__ frag rows(const bf16* m, int ld, int row, int k, int lane)
+    {
+        const bf16* p = m + (row + (lane & 15)) * ld + k + 4 * (lane >> 4);
+        const bf16x4 a = *reinterpret_cast<const bf16x4*>(p), b = *reinterpret_cast<const bf16x4*>(p + 16);
+        return frag{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    }
+    // a column of `m` does: [k][row].  The transposing read gives lane j of 16 element
+    // j % 4 of the 8-byte pieces that lanes 4 e + j / 4 address, e = 0 .. 3.
+    static __device__ __forceinline__ frag cols(const bf16* m, int ld, int k, int row, int lane)
+    {
+        const bf16* p = m + (k + 4 * (lane >> 4) + ((lane >> 2) & 3)) * ld + row + 4 * (lane & 3);
+        const bf16x4 a = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
+        const bf16x4 b = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * ld)));
+        return frag{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    }
+    static __device__ __forceinline__ void mma(f32x4& acc, const frag& a, const frag& b)
+    {
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
+    }
+};
+
+template <>
+struct Op<float> {
+    typedef f32x4 frag;
+    static constexpr int K = 16, VE = 4, PAD = 4;
+    static __device__ __forceinline__ frag rows(const float* m, int ld, int row, int k, int lane)
+    {
+        return *reinterpret_cast<const f32x4*>(m + (row + (lane & 15)) * ld + k + 4 * (lane >> 4));
+    }
+    static __device__ __forceinline__ frag cols(const float* m, int ld, int k, int row, int lane)
+    {
+        const float* p = m + (k + 4 * (lane >> 4)) * ld + row + (lane & 15);
+        return frag{p[0], p[ld], p[2 * ld], p[3 * ld]};
+    }
+    static __device__ __forceinline__ void mma(f32x4& acc, const frag& a, const frag& b)
+    {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], acc, 0, 0, 0);
+    }
+};
+
+// g^n, n >= 0.  The exponent's product is formed in 64 bits: its rounding would show
+// in powers of a decay near one.
+struct Decay {
+    double log;
+    __device__ __forceinline__ float power(int n) const { return n > 0 ? expf((float)(n * log)) : 1.f; }
+};
+
+// Elements of 16 bytes as in memory, at any alignment of an element, or fewer at a row's end.
+template <typename IO>
+struct Piece {
+    static constexpr int VE = Op<IO>::VE;
+    uint32_t w[4];
+    __device__ __forceinline__ void load(const IO* p, int n)
+    {
+        if (n >= VE) {
+            const Raw<IO, VE> r = load_raw<false, IO, VE>(p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = r.w[i];
+            return;
+        }
+        IO e[VE];
+#pragma unroll
+        for (int j = 0; j < VE; ++j)
+            e[j] = j < n ? p[j] : IO(0.f);
+        __builtin_memcpy(w, e, 16);
+    }
+    __device__ __forceinline__ void store(IO* p, int n) const
+    {
+        if (n >= VE) {
+            typedef Words<IO, 4> W;
+            W x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[i] = w[i];
+            *reinterpret_cast<W*>(p) = x;
+            return;
+        }
+        IO e[VE];
+        __builtin_memcpy(e, w, 16);
+#pragma unroll
+        for (int j = 0; j < VE; ++j)
+            if (j < n)
+                p[j] = e[j];
+    }
+    __device__ __forceinline__ void to_lds(IO* p) const { __builtin_memcpy(__builtin_assume_aligned(p, 16), w, 16); }
+    __device__ __forceinline__ void from_lds(const IO* p) { __builtin_memcpy(w, __builtin_assume_aligned(p, 16), 16); }
+};
+
+// A tile of C tokens by W columns: which 16 bytes a thread moves between memory and LDS
+template <typename IO, int C, int W>
+struct Tile {
+    static constexpr int VE = Op<IO>::VE, LD = W + Op<IO>::PAD, PER = W / VE, NP = C * PER / kThreads;
+    static_assert(C * PER % kThreads == 0, "whole pieces");
+    static __device__ __forceinline__ int row(int i) { return (i * kThreads + (int)threadIdx.x) / PER; }
+    static __device__ __forceinline__ int col(int i) { return (i * kThreads + (int)threadIdx.x) % PER * VE; }
+    // tokens p, p + ts, .. (backwards: ts < 0), `len` of them, `width` columns; zeros elsewhere
+    static __device__ __forceinline__ void load(Piece<IO> (&x)[NP], const IO* p, int ts, int len, int width)
+    {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int n = row(i) < len ? width - col(i) : 0;
+            if (n > 0)
+                x[i].load(p + (ptrdiff_t)row(i) * ts + col(i), n);
+            else
+                x[i].w[0] = x[i].w[1] = x[i].w[2] = x[i].w[3] = 0;
+        }
+    }
+    static __device__ __forceinline__ void put(const Piece<IO> (&x)[NP], IO* lds)
+    {
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+            x[i].to_lds(lds + row(i) * LD + col(i));
+    }
+};
+
+// Tokens [from, to) of sequence n, and whether they hold its first and last token in
+// the order of the walk
+struct Span {
+    int n, from, to;
+    bool first, last;
+};
+
+// The spans of one segment [t0, t1) of a row, in the order of the walk.  Offsets may hold
+// anything: spans lie in the segment and follow one another.
+struct Spans {
+    const int* cu;
+    int N, t0, t1, rev, at, n;
+
+    // (all threads) cu[n] <= token, the last such n
+    __device__ __forceinline__ int holding(int token) const { return count_at_most<kThreads>(cu, N, token) - 1; }
+
+    __device__ __forceinline__ void start(const LinArgs& a, int b, int begin, int end, int backwards)
+    {
+        cu = a.cu, N = a.N, t0 = begin, t1 = end, rev = backwards;
+        at = rev ? t1 : t0;
+        n = -1;
+        if (!cu)
+            n = b;
+    }
+    __device__ __forceinline__ bool next(Span& s, int T)
+    {
+        if (rev ? at <= t0 : at >= t1)
+            return false;
+        if (!cu) {
+            s = Span{n, t0, t1, rev ? t1 == T : t0 == 0, rev ? t0 == 0 : t1 == T};
+            at = rev ? t0 : t1;
+            return true;
+        }
+        // the sequence of the next token: mostly the neighbour of the last one
+        const int token = rev ? at - 1 : at;
+        int m = rev ? n - 1 : n + 1;
+        if (n < 0 || m < 0 || m >= N || cu[m] > token || cu[m + 1] <= token)
+            m = holding(token);
+        if (m < 0 || cu[m + 1] <= token) {
+            // behind the last sequence; backwards there may be sequences before
+            if (!rev || m < 0)
+                return false;
+            const int e = min(cu[m + 1], token);
+            if (e <= t0)
+                return false;
+            at = e;
+            n = -1;
+            return next_of(s, holding(e - 1));
+        }
+        return next_of(s, m);
+    }
+    __device__ __forceinline__ bool next_of(Span& s, int m)
+    {
+        if (m < 0)
+            return false;
+        const int p = cu[m], e = cu[m + 1];
+        s.n = m;
+        if (rev) {
+            s.to = at, s.from = max(p, t0);
+            if (s.from >= s.to || e < at)
+                return false;
+            s.first = e == s.to, s.last = p == s.from;
+            at = s.from;
+        } else {
+            s.from = at, s.to = min(e, t1);
+            if (s.to <= s.from || p > at)
+                return false;
+            s.first = p == s.from, s.last = e == s.to;
+            at = s.to;
+        }
+        n = m;
+        return true;
+    }
+};
+
+// Which tokens of the segment before (in the order of the walk) the state handed on to
+// segment s comes from: false where s begins with a sequence of its own.
+__device__ __forceinline__ bool handed_on(const LinArgs& a, int b, int s, int rev, Span& x)
+{
+    // the border between segment s and the next one in the order of the walk
+    const int border = rev ? s * a.L : (s + 1) * a.L;
+    const int t0 = s * a.L, t1 = min(a.T, t0 + a.L);
+    x.n = b;
+    int p = 0, e = a.T;
+    if (a.cu) {
+        x.n = count_at_most<kThreads>(a.cu, a.N, border - 1) - 1;
+        if (x.n < 0)
+            return false;
+        p = a.cu[x.n], e = a.cu[x.n + 1];
+    }
+    if (p >= border || e <= border)
+        return false;
+    x.from = rev ? border : max(p, t0);
+    x.to = rev ? min(e, t1) : border;
+    x.first = rev ? e <= t1 : p >= t0;
+    x.last = false;
+    return true;
+}
+
+template <typename IO, int KD, int C>
+struct Walk {
+    typedef Op<IO> O;
+    typedef typename O::frag frag;
+    typedef Tile<IO, C, KD> TK;
+    typedef Tile<IO, C, kCols> TV;
+    static constexpr int NT = C / 16, ST = KD / 16, KS = KD / O::K, CS = C / O::K, FE = O::K / 4;
+    static constexpr int LDP = C + O::PAD;
+    static constexpr bool BF = sizeof(IO) == 2;
+    static constexpr int kTileK = C * TK::LD, kTileV = C * TV::LD, kTileP = C * LDP;
+    static constexpr size_t kLds = sizeof(IO) * (2 * kTileK + kTileV + kTileP);
+};
+
+// STATE: the states that segments hand on, nothing else
+template <typename IO, int KD, int C, bool STATE>
+__global__ __launch_bounds__(kThreads) void linattn_kernel(LinArgs a)
+{
+    typedef Walk<IO, KD, C> W;
+    typedef typename W::O O;
+    typedef typename W::frag frag;
+    typedef typename W::TK TK;
+    typedef typename W::TV TV;
+    constexpr int NT = W::NT, ST = W::ST, KS = W::KS, CS = W::CS, FE = W::FE, LDP = W::LDP;
+    constexpr bool BF = W::BF;
+    __shared__ __attribute__((aligned(16))) IO lds[W::kLds / sizeof(IO)];
+    IO* const Qs = lds;
+    IO* const Ks = Qs + W::kTileK;
+    IO* const Vs = Ks + W::kTileK;
+    IO* const Ps = Vs + W::kTileV;
+
+    const LinRole& r = a.role[blockIdx.y];
+    // slices of one head follow one another on one XCD (workgroups go round the eight)
+    const int slices = (r.vd + kCols - 1) / kCols;
+    const int index = blockIdx.x / 8, unit = index / slices * 8 + (int)(blockIdx.x & 7), slice = index % slices;
+    if (unit >= a.B * a.H * a.S)
+        return;
+    const int h = unit % a.H, s = unit / a.H % a.S, b = unit / a.H / a.S;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 4, c = lane & 15;
+    const int col0 = slice * kCols, width = min(r.vd - col0, kCols);  // of v
+    const int mycol = col0 + 16 * wave + c;
+    const int rev = r.rev, dir = rev ? -1 : 1;
+
+    const long long row0 = (long long)b * a.T;
+    const IO* q = static_cast<const IO*>(r.q.p) + (long long)(h / r.q.div) * r.q.hs;
+    const IO* k = static_cast<const IO*>(r.k.p) + (long long)(h / r.k.div) * r.k.hs;
+    const IO* v = static_cast<const IO*>(r.v.p) + (long long)(h / r.v.div) * r.v.hs + col0;
+
+    const Decay decay{log((double)a.decay[h])};
+    // decays of q k^T: lane (g, c) holds rows j = 4 g + e of column i = c of a 16 x 16
+    // block; those below the diagonal block are 16 further each
+    float on[4], below[4], front[4], weight[CS][FE];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        on[e] = c >= 4 * g + e ? r.of_p * decay.power(c - 4 * g - e) : 0.f;
+        below[e] = r.of_p * decay.power(16 + c - 4 * g - e);
+        front[e] = r.of_x * decay.power(4 * g + e + 1 - rev);
+    }
+    const float g16 = decay.power(16);
+    int held = -1;  // tokens of the chunk that `weight` is for
+    float whole = 0.f;
+
+    f32x4 X[ST];
+    const size_t dense = (size_t)r.kd * r.vd;
+    auto state_in = [&](const float* p, int rs, int cs) {
+#pragma unroll
+        for (int t = 0; t < ST; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 16 * t + 4 * g + e;
+                X[t][e] = p && i < r.kd && mycol < r.vd ? p[(size_t)i * rs + (size_t)mycol * cs] : 0.f;
+            }
+    };
+    auto state_out = [&](float* p, int rs, int cs) {
+        if (mycol >= r.vd)
+            return;
+#pragma unroll
+        for (int t = 0; t < ST; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 16 * t + 4 * g + e;
+                if (i < r.kd)
+                    p[(size_t)i * rs + (size_t)mycol * cs] = X[t][e];
+            }
+    };
+    auto handed = [&](int seg) { return r.seg + (((size_t)b * a.S + seg) * a.H + h) * dense; };
+
+    // blocks of the decayed product above the diagonal that a step of K tokens covers
+    if constexpr (!STATE) {
+        for (int i = threadIdx.x; i < W::kTileP; i += kThreads)
+            Ps[i] = IO(0.f);
+    }
+
+    Piece<IO> nq[STATE ? 1 : TK::NP], nk[TK::NP], nv[TV::NP];
+    // the chunk of `len` tokens whose first (in the order of the walk) is `token`
+    auto fetch = [&](int token, int len) {
+        const long long at = row0 + token;
+        if constexpr (!STATE)
+            TK::load(nq, q + at * r.q.ts, dir * (int)r.q.ts, len, r.kd);
+        TK::load(nk, k + at * r.k.ts, dir * (int)r.k.ts, len, r.kd);
+        TV::load(nv, v + at * r.v.ts, dir * (int)r.v.ts, len, width);
+    };
+
+    auto walk = [&](const Span& span) {
+        int token = rev ? span.to - 1 : span.from, left = span.to - span.from;
+        fetch(token, min(left, C));
+        while (left > 0) {
+            const int len = min(left, C);
+            __syncthreads();  // the last chunk's reads are done
+            if constexpr (!STATE)
+                TK::put(nq, Qs);
+            TK::put(nk, Ks);
+            TV::put(nv, Vs);
+            __syncthreads();
+            if (left > C)
+                fetch(token + dir * C, min(left - C, C));
+            if (len != held) {
+                held = len;
+                whole = decay.power(len);
+#pragma unroll
+                for (int s = 0; s < CS; ++s)
+#pragma unroll
+                    for (int e = 0; e < FE; ++e) {
+                        const int j = s * O::K + 16 * (e / 4) + 4 * g + e % 4;
+                        weight[s][e] = r.of_u * decay.power(len - 1 - j + rev);
+                    }
+            }
+            frag fv[CS];
+#pragma unroll
+            for (int s = 0; s < CS; ++s)
+                fv[s] = O::cols(Vs, TV::LD, s * O::K, 16 * wave, lane);
+            f32x4 acc[NT];
+            if constexpr (!STATE) {
+                frag fx[KS];
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    if constexpr (BF) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            fx[s][e] = static_cast<bf16>(X[2 * s + e / 4][e % 4]);
+                    } else {
+                        fx[s] = X[s];
+                    }
+                }
+                // C = 64: a wave has 16 tokens' k for every block of q; C = 32: one block
+                const int jt = NT == 4 ? wave : wave & 1;
+                frag fk[KS];
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+                    fk[s] = O::rows(Ks, TK::LD, 16 * jt, s * O::K, lane);
+                float far = 1.f;
+#pragma unroll
+                for (int it = 0; it < NT; ++it) {
+                    frag fq[KS];
+#pragma unroll
+                    for (int s = 0; s < KS; ++s)
+                        fq[s] = O::rows(Qs, TK::LD, 16 * it, s * O::K, lane);
+                    acc[it] = zero4();
+#pragma unroll
+                    for (int s = 0; s < KS; ++s)
+                        O::mma(acc[it], fq[s], fx[s]);
+                    if (it >= jt && (NT == 4 || it == wave >> 1)) {
+                        f32x4 p = zero4();
+#pragma unroll
+                        for (int s = 0; s < KS; ++s)
+                            O::mma(p, fk[s], fq[s]);
+                        typedef IO Four __attribute__((ext_vector_type(4)));
+                        Four out;
+                        if (it == jt) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)  // a choice, not a product: k may be infinite
+                                out[e] = from_f32<IO>(c >= 4 * g + e ? p[e] * on[e] : 0.f);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                out[e] = from_f32<IO>(p[e] * (below[e] * far));
+                            far *= g16;
+                        }
+                        *reinterpret_cast<Four*>(Ps + (16 * it + c) * LDP + 16 * jt + 4 * g) = out;
+                    }
+                }
+                float tile = 1.f;
+#pragma unroll
+                for (int it = 0; it < NT; ++it) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[it][e] *= front[e] * tile;
+                    tile *= g16;
+                }
+            }
+            // v's decayed values, in two parts where they are rounded; any that is not finite
+            frag hi[CS], lo[BF ? CS : 1];
+            float wrong = 0.f;
+#pragma unroll
+            for (int s = 0; s < CS; ++s)
+#pragma unroll
+                for (int e = 0; e < FE; ++e) {
+                    const float x = to_f32(fv[s][e]), y = x * weight[s][e];
+                    wrong = fmaf(x, 0.f, wrong);
+                    hi[s][e] = from_f32<IO>(y);
+                    if constexpr (BF) {
+                        const float rest = y - to_f32(hi[s][e]);
+                        lo[s][e] = static_cast<bf16>(rest == rest ? rest : 0.f);  // of an infinity: none
+                    }
+                }
+            if constexpr (!STATE) {
+                __syncthreads();  // Ps is whole
+                const bool bad = __ballot(wrong != 0.f);
+                if (bad) {
+                    // zeros of Ps times what is not finite: those are left out of the products,
+                    // and added where they belong
+#pragma unroll
+                    for (int s = 0; s < CS; ++s)
+#pragma unroll
+                        for (int e = 0; e < FE; ++e) {
+                            const float x = to_f32(fv[s][e]);
+                            fv[s][e] = from_f32<IO>(x - x == 0.f ? x : 0.f);
+                        }
+                }
+#pragma unroll
+                for (int it = 0; it < NT; ++it)
+#pragma unroll
+                    for (int s = 0; s < CS; ++s)
+                        if (s * O::K < 16 * (it + 1))
+                            O::mma(acc[it], O::rows(Ps, LDP, 16 * it, s * O::K, lane), fv[s]);
+                if (bad) {
+                    for (int j = 0; j < len; ++j) {
+                        const float x = to_f32(Vs[j * TV::LD + 16 * wave + c]);
+                        if (x - x == 0.f)
+                            continue;
+#pragma unroll
+                        for (int it = 0; it < NT; ++it)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int i = 16 * it + 4 * g + e;
+                                if (i >= j)
+                                    acc[it][e] = fmaf(to_f32(Ps[i * LDP + j]), x, acc[it][e]);
+                            }
+                    }
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < ST; ++t) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    X[t][e] *= whole;
+#pragma unroll
+                for (int s = 0; s < CS; ++s) {
+                    const frag fk = O::cols(Ks, TK::LD, s * O::K, 16 * t, lane);
+                    O::mma(X[t], fk, hi[s]);
+                    if constexpr (BF)
+                        O::mma(X[t], fk, lo[s]);
+                }
+            }
+            if constexpr (!STATE) {
+                if (r.out_f32) {
+                    float* y = static_cast<float*>(r.out);
+#pragma unroll
+                    for (int it = 0; it < NT; ++it)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int i = 16 * it + 4 * g + e;
+                            if (i < len && mycol < r.vd)
+                                y[((row0 + token + dir * i) * a.H + h) * r.vd + mycol] = acc[it][e];
+                        }
+                } else {
+                    // this wave's columns of Vs are its own: y takes v's place, and whole rows
+                    // are stored from there
+#pragma unroll
+                    for (int it = 0; it < NT; ++it)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            Vs[(16 * it + 4 * g + e) * TV::LD + 16 * wave + c] = from_f32<IO>(acc[it][e]);
+                    __syncthreads();
+                    IO* y = static_cast<IO*>(r.out);
+#pragma unroll
+                    for (int i = 0; i < TV::NP; ++i) {
+                        const int row = TV::row(i), n = row < len ? width - TV::col(i) : 0;
+                        if (n > 0) {
+                            Piece<IO> x;
+                            x.from_lds(Vs + row * TV::LD + TV::col(i));
+                            x.store(y + ((row0 + token + dir * row) * a.H + h) * r.vd + col0 + TV::col(i), n);
+                        }
+                    }
+                }
+            }
+            token += dir * C;
+            left -= len;
+        }
+    };
+
+    if constexpr (STATE) {
+        Span span;
+        if (handed_on(a, b, s, rev, span)) {
+            state_in(nullptr, 0, 0);
+            walk(span);
+            state_out(handed(s), r.vd, 1);
+        }
+    } else {
+        const int t0 = s * a.L, t1 = min(a.T, t0 + a.L);
+        Spans spans;
+        Span span;
+        spans.start(a, b, t0, t1, rev);
+        while (spans.next(span, a.T)) {
+            const size_t n = ((size_t)span.n * a.H + h) * dense;
+            // (offsets that begin below zero claim a segment before the first one)
+            if (span.first || (rev ? s + 1 >= a.S : s == 0))
+                state_in(r.X0 ? r.X0 + n : nullptr, r.rs, r.cs);
+            else
+                state_in(handed(rev ? s + 1 : s - 1), r.vd, 1);
+            walk(span);
+            if (span.last && r.XT)
+                state_out(r.XT + n, r.rs, r.cs);
+        }
+        if (a.cu && a.clear && !r.out_f32) {
+            IO* y = static_cast<IO*>(r.out);
+            for (int t = max(t0, max(a.cu[a.N], 0)); t < t1; ++t)
+                if ((int)threadIdx.x < width)
+                    y[((row0 + t) * a.H + h) * r.vd + col0 + threadIdx.x] = IO(0.f);
+        }
+    }
+}
+
+// The states handed on, one segment after another: what a segment adds, and what it got,
+// decayed over its tokens.  A thread has one element of one head's state.
+__global__ __launch_bounds__(kThreads) void linattn_join_kernel(LinArgs a)
+{
+    const LinRole& r = a.role[blockIdx.z];
+    const int h = blockIdx.y % a.H, b = blockIdx.y / a.H;
+    const size_t dense = (size_t)r.kd * r.vd, i = (size_t)blockIdx.x * kThreads + threadIdx.x;
+    const Decay decay{log((double)a.decay[h])};
+    float x = 0.f;
+    for (int m = 0; m + 1 < a.S; ++m) {
+        const int s = r.rev ? a.S - 1 - m : m;
+        Span span;
+        if (!handed_on(a, b, s, r.rev, span) || i >= dense)
+            continue;
+        if (span.first)
+            x = r.X0 ? r.X0[((size_t)span.n * a.H + h) * dense + (i / r.vd) * r.rs + (i % r.vd) * r.cs] : 0.f;
+        float* p = r.seg + (((size_t)b * a.S + s) * a.H + h) * dense + i;
+        x = fmaf(decay.power(span.to - span.from), x, *p);
+        *p = x;
+    }
+}
+
+// y [tokens, Hk, d] = the sum over each group's heads of x [tokens, H, d] (fp32)
+template <typename IO>
+__global__ __launch_bounds__(256) void linattn_group_kernel(LinArgs a, const float* x, IO* y, int G, int d)
+{
+    const int Hk = a.H / G;
+    const long long n = (long long)a.B * a.T * Hk * d;
+    const int end = a.cu ? a.cu[a.N] : 0;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+        const long long token = i / (Hk * d);
+        const int at = (int)(i % (Hk * d)), hk = at / d, j = at % d;
+        if (a.cu && token >= end) {
+            if (a.clear)
+                y[i] = IO(0.f);
+            continue;
+        }
+        float s = 0.f;
+        for (int m = 0; m < G; ++m)
+            s += x[(token * a.H + hk * G + m) * d + j];
+        y[i] = from_f32<IO>(s);
+    }
+}
+
+// ---- single tokens -------------------------------------------------------------------
+
+// One token: a workgroup has one head and 64 columns of the state, a thread four columns
+// of every 16th row; rows are joined through LDS.
+template <typename IO>
+__global__ __launch_bounds__(256) void linattn_step_kernel(LinStepArgs a)
+{
+    __shared__ float part[16][kCols];
+    const int slices = (a.dv + kCols - 1) / kCols;
+    const int slice = blockIdx.x % slices, unit = blockIdx.x / slices, h = unit % a.H, b = unit / a.H;
+    const int rg = threadIdx.x >> 4, c = 4 * (threadIdx.x & 15), col = slice * kCols + c, n = min(a.dv - col, 4);
+    const IO* q = static_cast<const IO*>(a.q) + (long long)b * a.qs + (long long)(h / a.G) * a.qh;
+    const IO* k = static_cast<const IO*>(a.k) + (long long)b * a.ks + (long long)(h / a.G) * a.kh;
+    const IO* v = static_cast<const IO*>(a.v) + (long long)b * a.vs + (long long)h * a.vh;
+    float* S = a.S + (size_t)unit * a.dk * a.dv;
+    const float g = a.decay[h];
+    float vv[4], o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        vv[e] = e < n ? to_f32(v[col + e]) : 0.f;
+    if (n > 0) {
+        for (int i = rg; i < a.dk; i += 16) {
+            const float kk = to_f32(k[i]), qq = to_f32(q[i]);
+            float* p = S + (size_t)i * a.dv + col;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < n) {
+                    const float x = fmaf(g, p[e], kk * vv[e]);
+                    p[e] = x;
+                    o[e] = fmaf(qq, x, o[e]);
+                }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        part[rg][c + e] = o[e];
+    __syncthreads();
+    const int out = slice * kCols + threadIdx.x;
+    if (threadIdx.x < kCols && out < a.dv) {
+        float s = 0.f;
+#pragma unroll
+        for (int m = 0; m < 16; ++m)
+            s += part[m][threadIdx.x];
+        static_cast<IO*>(a.o)[(size_t)unit * a.dv + out] = from_f32<IO>(s * a.scale);
+    }
+}
+
+// ---- host ------------------------------------------------------------------------------
+
+int padded(int kd) { return kd <= 32 ? 32 : kd <= 64 ? 64 : kd <= 128 ? 128 : 256; }
+
+template <typename IO, int KD, bool STATE>
+void launch_walk(const LinArgs& a, int roles, hipStream_t stream)
+{
+    constexpr int C = sizeof(IO) == 2 && KD <= 128 ? 64 : 32;
+    const int slices = (a.role[0].vd + kCols - 1) / kCols;
+    const unsigned units = ((unsigned)a.B * a.H * a.S + 7) / 8 * 8;
+    linattn_kernel<IO, KD, C, STATE><<<dim3(units * slices, roles), kThreads, 0, stream>>>(a);
+}
+
+template <typename IO>
+void launch_walks(const LinArgs& a, int roles, hipStream_t stream)
+{
+    const int kd = padded(a.role[0].kd);
+    auto run = [&](auto state) {
+        constexpr bool S = decltype(state)::value;
+        if (kd == 32)
+            launch_walk<IO, 32, S>(a, roles, stream);
+        else if (kd == 64)
+            launch_walk<IO, 64, S>(a, roles, stream);
+        else if (kd == 128)
+            launch_walk<IO, 128, S>(a, roles, stream);
+        else
+            launch_walk<IO, 256, S>(a, roles, stream);
+    };
+    if (a.S > 1) {
+        run(std::true_type{});
+        const size_t dense = (size_t)a.role[0].kd * a.role[0].vd;
+        linattn_join_kernel<<<dim3((unsigned)((dense + kThreads - 1) / kThreads), a.B * a.H, roles), kThreads, 0,
+                              stream>>>(a);
+    }
+    run(std::false_type{});
+}
+
+// Tokens of a segment: a multiple of 64
+int segments(int B, int T, int H, int slices, int& L)
+{
+    const long long groups = (long long)B * H * slices;
+    const long long want = (512 + groups - 1) / groups, most = T / 512;
+    const long long S = want < most ? want : most;
+    L = S <= 1 ? (T > 0 ? T : 1) : (int)(((T + S - 1) / S + 63) / 64 * 64);
+    return T > 0 ? (T + L - 1) / L : 1;
+}
+
+int slices_of(int vd) { return (vd + kCols - 1) / kCols; }
+
+size_t aligned16(size_t n) { return (n + 15) / 16 * 16; }
+
+template <typename IO>
+hipError_t linattn_fwd(const LinArgs& a, hipStream_t stream)
+{
+    if (a.T > 0)
+        launch_walks<IO>(a, 1, stream);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t linattn_fwd_workspace_bytes(int B, int T, int H, int dk, int dv)
+{
+    int L;
+    const int S = segments(B, T, H, slices_of(dv), L);
+    return S > 1 ? sizeof(float) * B * S * H * dk * dv : 0;
+}
+
+static size_t bwd_segments_bytes(int B, int T, int H, int dk, int dv, int& S, int& L)
+{
+    S = segments(B, T, H, slices_of(dk) * 2 + slices_of(dv), L);
+    return S > 1 ? sizeof(float) * B * S * H * dk * dv : 0;
+}
+
+size_t linattn_bwd_workspace_bytes(int B, int T, int H, int Hk, int dk, int dv)
+{
+    int S, L;
+    const size_t seg = bwd_segments_bytes(B, T, H, dk, dv, S, L);
+    return 3 * seg + (Hk != H ? 2 * aligned16(sizeof(float) * B * T * H * dk) : 0);
+}
+
+// the states of sequences without tokens
+static void empty_states(const LinArgs& a, const float* from, float* to, hipStream_t stream)
+{
+    if (to && (a.cu || a.T == 0))
+        launch_empty_states<float>(a.cu, a.N, a.H * a.role[0].kd * a.role[0].vd, from, to, stream);
+}
+
+hipError_t launch_linattn_fwd(const LinCall& c, bool bf, hipStream_t stream)
+{
+    LinArgs a{};
+    a.B = c.B, a.T = c.T, a.H = c.H, a.N = c.N, a.cu = c.cu, a.decay = c.decay, a.clear = c.clear;
+    a.S = segments(c.B, c.T, c.H, slices_of(c.dv), a.L);
+    LinRole& r = a.role[0];
+    r.q = c.q, r.k = c.k, r.v = c.v;
+    r.out = c.o, r.X0 = c.S0, r.XT = c.S_T, r.seg = static_cast<float*>(c.ws);
+    r.kd = c.dk, r.vd = c.dv, r.rs = c.dv, r.cs = 1;
+    r.of_p = r.of_x = c.scale, r.of_u = 1.f;
+    empty_states(a, c.S0, c.S_T, stream);
+    return bf ? linattn_fwd<bf16>(a, stream) : linattn_fwd<float>(a, stream);
+}
+
+template <typename IO>
+static hipError_t linattn_bwd(const LinCall& c, hipStream_t stream)
+{
+    LinArgs a{};
+    a.B = c.B, a.T = c.T, a.H = c.H, a.N = c.N, a.cu = c.cu, a.decay = c.decay, a.clear = c.clear;
+    const int G = c.H / c.Hk;
+    const size_t seg = bwd_segments_bytes(c.B, c.T, c.H, c.dk, c.dv, a.S, a.L) / sizeof(float);
+    float* ws = static_cast<float*>(c.ws);
+    const size_t whole = aligned16(sizeof(float) * c.B * c.T * c.H * c.dk) / sizeof(float);
+    float* gq = ws + 3 * seg;
+    float* gk = gq + whole;
+
+    LinRole dq{}, dk{}, dv{};
+    dq.q = c.d_o, dq.k = c.v, dq.v = c.k;
+    dq.out = G > 1 ? gq : c.dq, dq.out_f32 = G > 1;
+    dq.X0 = c.S0, dq.kd = c.dv, dq.vd = c.dk, dq.rs = 1, dq.cs = c.dv;
+    dq.of_p = dq.of_x = c.scale, dq.of_u = 1.f, dq.seg = ws;
+    dk.q = c.v, dk.k = c.d_o, dk.v = c.q;
+    dk.out = G > 1 ? gk : c.dk_out, dk.out_f32 = G > 1;
+    dk.X0 = c.dS_T, dk.kd = c.dv, dk.vd = c.dk, dk.rs = 1, dk.cs = c.dv;
+    dk.of_p = dk.of_u = c.scale, dk.of_x = 1.f, dk.rev = 1, dk.seg = ws + seg;
+    dv.q = c.k, dv.k = c.q, dv.v = c.d_o;
+    dv.out = c.dv_out, dv.X0 = c.dS_T, dv.XT = c.dS0;
+    dv.kd = c.dk, dv.vd = c.dv, dv.rs = c.dv, dv.cs = 1;
+    dv.of_p = dv.of_u = c.scale, dv.of_x = 1.f, dv.rev = 1, dv.seg = ws + 2 * seg;
+
+    a.role[0] = dv;
+    empty_states(a, c.dS_T, c.dS0, stream);
+    if (c.T == 0)
+        return hipGetLastError();
+    if (c.dk == c.dv) {
+        a.role[1] = dq, a.role[2] = dk;
+        launch_walks<IO>(a, 3, stream);
+    } else {
+        launch_walks<IO>(a, 1, stream);
+        a.role[0] = dq, a.role[1] = dk;
+        launch_walks<IO>(a, 2, stream);
+    }
+    if (G > 1) {
+        const long long n = (long long)c.B * c.T * c.Hk * c.dk;
+        const unsigned groups = (unsigned)((n + 255) / 256 < 8192 ? (n + 255) / 256 : 8192);
+        linattn_group_kernel<IO><<<groups, 256, 0, stream>>>(a, gq, static_cast<IO*>(c.dq), G, c.dk);
+        linattn_group_kernel<IO><<<groups, 256, 0, stream>>>(a, gk, static_cast<IO*>(c.dk_out), G, c.dk);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_linattn_bwd(const LinCall& c, bool bf, hipStream_t stream)
+{
+    return bf ? linattn_bwd<bf16>(c, stream) : linattn_bwd<float>(c, stream);
+}
+
+hipError_t launch_linattn_step(const LinStepArgs& a, bool bf, hipStream_t stream)
+{
+    const unsigned groups = (unsigned)a.B * a.H * slices_of(a.dv);
+    if (bf)
+        linattn_step_kernel<bf16><<<groups, 256, 0, stream>>>(a);
+    else
+        linattn_step_kernel<float><<<groups, 256, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace kdn
