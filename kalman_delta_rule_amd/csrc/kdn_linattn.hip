@@ -104,35 +104,17 @@ struct Decay {
     __device__ __forceinline__ float power(int n) const { return n > 0 ? expf((float)(n * log)) : 1.f; }
 };
 
-// Elements of 16 bytes as in memory, at any alignment of an element, or fewer at a row's end.
+// Elements of 16 bytes, as in memory.
 template <typename IO>
 struct Piece {
     static constexpr int VE = Op<IO>::VE;
     uint32_t w[4];
-    __device__ __forceinline__ void load(const IO* p, int n)
-    {
-        if (n >= VE) {
-            const Raw<IO, VE> r = load_raw<false, IO, VE>(p);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = r.w[i];
-            return;
-        }
-        IO e[VE];
-#pragma unroll
-        for (int j = 0; j < VE; ++j)
-            e[j] = j < n ? p[j] : IO(0.f);
-        __builtin_memcpy(w, e, 16);
-    }
+    // its first n elements, at any alignment of an element
     __device__ __forceinline__ void store(IO* p, int n) const
     {
         if (n >= VE) {
             typedef Words<IO, 4> W;
-            W x;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[i] = w[i];
-            *reinterpret_cast<W*>(p) = x;
+            *reinterpret_cast<W*>(p) = W{w[0], w[1], w[2], w[3]};
             return;
         }
         IO e[VE];
@@ -146,30 +128,65 @@ struct Piece {
     __device__ __forceinline__ void from_lds(const IO* p) { __builtin_memcpy(w, __builtin_assume_aligned(p, 16), 16); }
 };
 
-// A tile of C tokens by W columns: which 16 bytes a thread moves between memory and LDS
+// A tile of C tokens by W columns, of which `width` are there: 16 bytes a thread and turn,
+// always of the same columns.  Loads go through a buffer descriptor that ends behind the
+// tile's last element: rows and columns that are not there read as zero without a branch.
 template <typename IO, int C, int W>
 struct Tile {
-    static constexpr int VE = Op<IO>::VE, LD = W + Op<IO>::PAD, PER = W / VE, NP = C * PER / kThreads;
-    static_assert(C * PER % kThreads == 0, "whole pieces");
-    static __device__ __forceinline__ int row(int i) { return (i * kThreads + (int)threadIdx.x) / PER; }
-    static __device__ __forceinline__ int col(int i) { return (i * kThreads + (int)threadIdx.x) % PER * VE; }
-    // tokens p, p + ts, .. (backwards: ts < 0), `len` of them, `width` columns; zeros elsewhere
-    static __device__ __forceinline__ void load(Piece<IO> (&x)[NP], const IO* p, int ts, int len, int width)
+    static constexpr int VE = Op<IO>::VE, LD = W + Op<IO>::PAD, PER = W / VE, ROWS = kThreads / PER, NP = C / ROWS;
+    static_assert(kThreads % PER == 0 && C % ROWS == 0, "whole turns of the threads");
+    static __device__ __forceinline__ int row(int i) { return i * ROWS + (int)threadIdx.x / PER; }
+    static __device__ __forceinline__ int col() { return (int)threadIdx.x % PER * VE; }
+    // rows p, p + ts, .. or, backwards, from the last to p
+    static __device__ __forceinline__ void load(Piece<IO> (&x)[NP], const IO* p, int ts, int len, int width, bool back)
     {
+        constexpr int E = sizeof(IO);
+        const int end = ((len - 1) * ts + width) * E;
+        const bool odd = E == 2 && ((reinterpret_cast<uintptr_t>(p) & 3) || (ts & 1));
+        // a word that ends half a word behind the last element is read whole where words are
+        // aligned (it lies in one page); elsewhere it is out of range
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<IO*>(p), (short)0, odd ? end : (end + 3) & ~3, 0x00020000);
+        int at = ((back ? len - 1 - row(0) : row(0)) * ts + col()) * E;
+        const int step = (back ? -ROWS : ROWS) * ts * E;
+        if (col() >= width)
+            at = (int)0x80000000u;  // out of range, and so are steps of it: a tile spans less than 2^30 bytes
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            const int n = row(i) < len ? width - col(i) : 0;
-            if (n > 0)
-                x[i].load(p + (ptrdiff_t)row(i) * ts + col(i), n);
-            else
-                x[i].w[0] = x[i].w[1] = x[i].w[2] = x[i].w[3] = 0;
+            typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+            const u32x4 r = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (uint32_t)at + (uint32_t)(i * step), 0u, 0));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                x[i].w[j] = r[j];
+        }
+        if (odd && ((width - 1) % VE) % 2 == 0) {
+            const int last = back ? 0 : len - 1;
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+                if (row(i) == last && col() == (width - 1) / VE * VE) {
+                    const uint32_t e = *reinterpret_cast<const uint16_t*>(p + (ptrdiff_t)(len - 1) * ts + width - 1);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        x[i].w[j] = j == (width - 1) % VE / 2 ? e : x[i].w[j];
+                }
         }
     }
-    static __device__ __forceinline__ void put(const Piece<IO> (&x)[NP], IO* lds)
+    static __device__ __forceinline__ void put(Piece<IO> (&x)[NP], IO* lds, int width)
     {
+        // elements of a piece behind the row's end: the next head's, or the next token's
+        if (width % VE) {
+            constexpr int EW = VE / 4;  // elements of a word
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int n = width - col() - j * EW;
+                const uint32_t mask = n >= EW ? ~0u : n <= 0 ? 0u : 0xFFFFu;
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+                    x[i].w[j] &= mask;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < NP; ++i)
-            x[i].to_lds(lds + row(i) * LD + col(i));
+            x[i].to_lds(lds + row(i) * LD + col());
     }
 };
 
@@ -287,7 +304,7 @@ struct Walk {
 
 // STATE: the states that segments hand on, nothing else
 template <typename IO, int KD, int C, bool STATE>
-__global__ __launch_bounds__(kThreads) void linattn_kernel(LinArgs a)
+__global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
 {
     typedef Walk<IO, KD, C> W;
     typedef typename W::O O;
@@ -368,23 +385,41 @@ __global__ __launch_bounds__(kThreads) void linattn_kernel(LinArgs a)
     Piece<IO> nq[STATE ? 1 : TK::NP], nk[TK::NP], nv[TV::NP];
     // the chunk of `len` tokens whose first (in the order of the walk) is `token`
     auto fetch = [&](int token, int len) {
-        const long long at = row0 + token;
+        const long long at = row0 + (rev ? token - len + 1 : token);
         if constexpr (!STATE)
-            TK::load(nq, q + at * r.q.ts, dir * (int)r.q.ts, len, r.kd);
-        TK::load(nk, k + at * r.k.ts, dir * (int)r.k.ts, len, r.kd);
-        TV::load(nv, v + at * r.v.ts, dir * (int)r.v.ts, len, width);
+            TK::load(nq, q + at * r.q.ts, (int)r.q.ts, len, r.kd, rev);
+        TK::load(nk, k + at * r.k.ts, (int)r.k.ts, len, r.kd, rev);
+        TV::load(nv, v + at * r.v.ts, (int)r.v.ts, len, width, rev);
+    };
+    // y of a chunk, which stands in Vs: each thread stores the pieces whose places it fills
+    // with v next
+    auto store = [&](int token, int len) {
+        IO* y = static_cast<IO*>(r.out);
+        const int n = width - TV::col();
+#pragma unroll
+        for (int i = 0; i < TV::NP; ++i) {
+            const int row = TV::row(i);
+            if (row < len && n > 0) {
+                Piece<IO> x;
+                x.from_lds(Vs + row * TV::LD + TV::col());
+                x.store(y + ((row0 + token + dir * row) * a.H + h) * r.vd + col0 + TV::col(), n);
+            }
+        }
     };
 
     auto walk = [&](const Span& span) {
         int token = rev ? span.to - 1 : span.from, left = span.to - span.from;
         fetch(token, min(left, C));
-        while (left > 0) {
+        for (bool first = true; left > 0; first = false) {
             const int len = min(left, C);
-            __syncthreads();  // the last chunk's reads are done
-            if constexpr (!STATE)
-                TK::put(nq, Qs);
-            TK::put(nk, Ks);
-            TV::put(nv, Vs);
+            __syncthreads();  // the last chunk's reads are done, its y is whole
+            if constexpr (!STATE) {
+                if (!first && !r.out_f32)
+                    store(token - dir * C, C);
+                TK::put(nq, Qs, r.kd);
+            }
+            TK::put(nk, Ks, r.kd);
+            TV::put(nv, Vs, width);
             __syncthreads();
             if (left > C)
                 fetch(token + dir * C, min(left - C, C));
@@ -538,25 +573,17 @@ __global__ __launch_bounds__(kThreads) void linattn_kernel(LinArgs a)
                                 y[((row0 + token + dir * i) * a.H + h) * r.vd + mycol] = acc[it][e];
                         }
                 } else {
-                    // this wave's columns of Vs are its own: y takes v's place, and whole rows
-                    // are stored from there
+                    // this wave's columns of Vs are its own: y takes v's place
 #pragma unroll
                     for (int it = 0; it < NT; ++it)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             Vs[(16 * it + 4 * g + e) * TV::LD + 16 * wave + c] = from_f32<IO>(acc[it][e]);
-                    __syncthreads();
-                    IO* y = static_cast<IO*>(r.out);
-#pragma unroll
-                    for (int i = 0; i < TV::NP; ++i) {
-                        const int row = TV::row(i), n = row < len ? width - TV::col(i) : 0;
-                        if (n > 0) {
-                            Piece<IO> x;
-                            x.from_lds(Vs + row * TV::LD + TV::col(i));
-                            x.store(y + ((row0 + token + dir * row) * a.H + h) * r.vd + col0 + TV::col(i), n);
-                        }
-                    }
                 }
+            }
+            if (!STATE && left <= C && !r.out_f32) {
+                __syncthreads();
+                store(token, len);
             }
             token += dir * C;
             left -= len;
