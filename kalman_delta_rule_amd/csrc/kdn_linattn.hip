@@ -16,8 +16,7 @@
 //
 // A workgroup of four waves has one head and 64 columns of v and X.  A wave keeps X of
 // its 16 columns in matrix accumulators for the whole walk: they are at once the operand
-// of q X (the lanes of an accumulator hold four adjacent rows, which is a piece of the
-// operand if q's pieces are taken in the same order).  q k^T is formed transposed, so that
+// of q X.  q k^T is formed transposed, so that
 // a lane's four values are adjacent in a row of the decayed product, which goes through
 // LDS to all waves.  The token's decay is put on v, in registers, not on k.
 //
@@ -33,6 +32,9 @@
 
 #include <type_traits>
 
+// the steps of a walk are lambdas; called out of line they would put the state into memory
+#define KDN_INLINE __attribute__((always_inline))
+
 namespace kdn {
 
 namespace {
@@ -42,34 +44,89 @@ constexpr int kThreads = 256, kCols = 64;  // columns of v a workgroup
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
+// A matrix in LDS, rows of W elements without a gap.  Its 16-byte blocks are exchanged
+// within a row by a number that goes by the row, so that all banks are busy in each of
+// the ways it is read: one block of 16 rows, and
+// - bf16, read transposed: pieces of 4 to 16 bytes of 4 adjacent rows;
+// - fp32, read by columns: 4 blocks of rows that lie 4 apart.
+// (256 bytes are all banks: of rows of 128 or 64 bytes, two or four lie side by side.)
+// The number's bits are bits of the row, so a place ROW rows and BLOCK blocks further, in
+// bits that the place itself has not set, is an exclusive or and an offset away.
+template <typename IO, int W>
+struct Lds {
+    static constexpr int VE = 16 / sizeof(IO), BLOCKS = W / VE, BYTES = W * sizeof(IO);
+    static_assert(BLOCKS == 4 || BLOCKS == 8 || BLOCKS % 16 == 0, "rows of 64, 128 or whole 256 bytes");
+    static __device__ __forceinline__ constexpr int turn(int row)
+    {
+        if constexpr (sizeof(IO) == 4)
+            return BLOCKS == 8 ? (row >> 1 & 1) | (row >> 1 & 6) : (row >> 2 & 3) << 2 | (row & 3);
+        else
+            return BLOCKS == 4   ? row >> 2 & 3
+                   : BLOCKS == 8 ? (row >> 1 & 1) << 2 | (row >> 2 & 3)
+                                 : (row & 3) << 2 | (row >> 2 & 3);
+    }
+    // bytes from the matrix's front, which is a multiple of 256
+    static __device__ __forceinline__ uint32_t at(int row, int block)
+    {
+        return row * BYTES + ((block ^ turn(row)) << 4);
+    }
+    static __device__ __forceinline__ uint32_t further(uint32_t place, int row, int block)
+    {
+        return (place ^ (uint32_t)((turn(row) ^ (block & 15)) << 4)) + row * BYTES + (block >> 4) * 256;
+    }
+};
+
+template <typename V>
+__device__ __forceinline__ V lds_read(uint32_t at)
+{
+    return *(const __attribute__((address_space(3))) V*)(size_t)at;
+}
+template <typename V>
+__device__ __forceinline__ void lds_write(uint32_t at, const V& v)
+{
+    *(__attribute__((address_space(3))) V*)(size_t)at = v;
+}
+
 // Operands of one step of a 16 x 16 product, and how they are read.  A lane (g, c) =
-// (lane / 16, lane % 16) holds for row c of an operand those k of the step that lie in
-// the rows of accumulators which it holds: 4 g .. 4 g + 3 of every 16.
+// (lane / 16, lane % 16) holds VE adjacent k for row c of an operand, VE g the first.  The
+// state's accumulators are such an operand: of the two tiles of 16 rows that a step of 32
+// takes in bf16, the first stands for rows 8 g .. 8 g + 3 of the step, the second for
+// 8 g + 4 .. 8 g + 7 (an accumulator's lane holds rows 4 g .. 4 g + 3 of its tile).
 template <typename IO>
 struct Op;
 
 template <>
 struct Op<bf16> {
     typedef bf16x8 frag;
-    static constexpr int K = 32;   // of a step
-    static constexpr int VE = 8;   // elements of 16 bytes
-    static constexpr int PAD = 8;  // of a row in LDS
-    // a row of `m` holds the k: [row][k]
-    static __device__ __forceinline__ frag rows(const bf16* m, int ld, int row, int k, int lane)
+    static constexpr int K = 32;  // of a step
+    static constexpr int VE = 8;  // elements of 16 bytes
+    // row of the state that tile t's row 4 g + e stands for
+    static __device__ __forceinline__ int state_row(int t, int g, int e) { return 32 * (t / 2) + 8 * g + 4 * (t % 2) + e; }
+    // From a matrix whose columns hold the k, [k][row]: the transposing read gives lane j of
+    // 16 element j % 4 of the 8 bytes that lanes 4 e + j / 4 address, e = 0 .. 3.  Place of the
+    // first piece; the operand's rows are four pieces of 4 columns, `apart` elements apart.
+    template <int W>
+    static __device__ __forceinline__ uint32_t cols_at(int col, int apart, int lane)
     {
-        const bf16* p = m + (row + (lane & 15)) * ld + k + 4 * (lane >> 4);
-        const bf16x4 a = *reinterpret_cast<const bf16x4*>(p), b = *reinterpret_cast<const bf16x4*>(p + 16);
+        const int at = col + apart * (lane & 3);
+        return Lds<bf16, W>::at(8 * (lane >> 4) + ((lane >> 2) & 3), at / 8) + at % 8 * 2;
+    }
+    template <int W>
+    static __device__ __forceinline__ frag cols(uint32_t place, int step, int block)
+    {
+        const auto a = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4*)(size_t)Lds<bf16, W>::further(place, 32 * step, block)));
+        const auto b = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4*)(size_t)Lds<bf16, W>::further(place, 32 * step + 4, block)));
         return frag{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
     }
-    // a column of `m` does: [k][row].  The transposing read gives lane j of 16 element
-    // j % 4 of the 8-byte pieces that lanes 4 e + j / 4 address, e = 0 .. 3.
-    static __device__ __forceinline__ frag cols(const bf16* m, int ld, int k, int row, int lane)
+    // rows of the state's tile t, from [k][row]
+    template <int W>
+    static __device__ __forceinline__ frag state_cols(uint32_t place, int step, int t)
     {
-        const bf16* p = m + (k + 4 * (lane >> 4) + ((lane >> 2) & 3)) * ld + row + 4 * (lane & 3);
-        const bf16x4 a = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
-        const bf16x4 b = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * ld)));
-        return frag{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+        return cols<W>(place + 8 * (t % 2), step, 4 * (t / 2));
     }
+    static constexpr int kApart = 8;  // of cols_at for them
     static __device__ __forceinline__ void mma(f32x4& acc, const frag& a, const frag& b)
     {
         acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
@@ -79,15 +136,27 @@ struct Op<bf16> {
 template <>
 struct Op<float> {
     typedef f32x4 frag;
-    static constexpr int K = 16, VE = 4, PAD = 4;
-    static __device__ __forceinline__ frag rows(const float* m, int ld, int row, int k, int lane)
+    static constexpr int K = 16, VE = 4, kApart = 4;
+    static __device__ __forceinline__ int state_row(int t, int g, int e) { return 16 * t + 4 * g + e; }
+    template <int W>
+    static __device__ __forceinline__ uint32_t cols_at(int col, int, int lane)
     {
-        return *reinterpret_cast<const f32x4*>(m + (row + (lane & 15)) * ld + k + 4 * (lane >> 4));
+        const int at = col + (lane & 15);
+        return Lds<float, W>::at(4 * (lane >> 4), at / 4) + at % 4 * 4;
     }
-    static __device__ __forceinline__ frag cols(const float* m, int ld, int k, int row, int lane)
+    template <int W>
+    static __device__ __forceinline__ frag cols(uint32_t place, int step, int block)
     {
-        const float* p = m + (k + 4 * (lane >> 4)) * ld + row + (lane & 15);
-        return frag{p[0], p[ld], p[2 * ld], p[3 * ld]};
+        frag x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            x[e] = lds_read<float>(Lds<float, W>::further(place, 16 * step + e, block));
+        return x;
+    }
+    template <int W>
+    static __device__ __forceinline__ frag state_cols(uint32_t place, int step, int t)
+    {
+        return cols<W>(place, step, 4 * t);
     }
     static __device__ __forceinline__ void mma(f32x4& acc, const frag& a, const frag& b)
     {
@@ -96,6 +165,19 @@ struct Op<float> {
             acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], acc, 0, 0, 0);
     }
 };
+
+// From a matrix whose rows hold the k, [row][k]: place of row c's first piece, and the
+// operand of 16 rows from `row` on.
+template <typename IO, int W>
+__device__ __forceinline__ uint32_t rows_at(int lane)
+{
+    return Lds<IO, W>::at(lane & 15, lane >> 4);
+}
+template <typename IO, int W>
+__device__ __forceinline__ typename Op<IO>::frag rows(uint32_t place, int row, int step)
+{
+    return lds_read<typename Op<IO>::frag>(Lds<IO, W>::further(place, row, 4 * step));
+}
 
 // g^n, n >= 0.  The exponent's product is formed in 64 bits: its rounding would show
 // in powers of a decay near one.
@@ -108,24 +190,23 @@ struct Decay {
 template <typename IO>
 struct Piece {
     static constexpr int VE = Op<IO>::VE;
-    uint32_t w[4];
+    typedef uint32_t four __attribute__((ext_vector_type(4)));
+    four w;
     // its first n elements, at any alignment of an element
     __device__ __forceinline__ void store(IO* p, int n) const
     {
         if (n >= VE) {
             typedef Words<IO, 4> W;
-            *reinterpret_cast<W*>(p) = W{w[0], w[1], w[2], w[3]};
+            *reinterpret_cast<W*>(p) = w;
             return;
         }
         IO e[VE];
-        __builtin_memcpy(e, w, 16);
+        __builtin_memcpy(e, &w, 16);
 #pragma unroll
         for (int j = 0; j < VE; ++j)
             if (j < n)
                 p[j] = e[j];
     }
-    __device__ __forceinline__ void to_lds(IO* p) const { __builtin_memcpy(__builtin_assume_aligned(p, 16), w, 16); }
-    __device__ __forceinline__ void from_lds(const IO* p) { __builtin_memcpy(w, __builtin_assume_aligned(p, 16), 16); }
 };
 
 // A tile of C tokens by W columns, of which `width` are there: 16 bytes a thread and turn,
@@ -133,7 +214,7 @@ struct Piece {
 // tile's last element: rows and columns that are not there read as zero without a branch.
 template <typename IO, int C, int W>
 struct Tile {
-    static constexpr int VE = Op<IO>::VE, LD = W + Op<IO>::PAD, PER = W / VE, ROWS = kThreads / PER, NP = C / ROWS;
+    static constexpr int VE = Op<IO>::VE, PER = W / VE, ROWS = kThreads / PER, NP = C / ROWS;
     static_assert(kThreads % PER == 0 && C % ROWS == 0, "whole turns of the threads");
     static __device__ __forceinline__ int row(int i) { return i * ROWS + (int)threadIdx.x / PER; }
     static __device__ __forceinline__ int col() { return (int)threadIdx.x % PER * VE; }
@@ -152,11 +233,8 @@ struct Tile {
             at = (int)0x80000000u;  // out of range, and so are steps of it: a tile spans less than 2^30 bytes
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-            const u32x4 r = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (uint32_t)at + (uint32_t)(i * step), 0u, 0));
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                x[i].w[j] = r[j];
+            x[i].w = __builtin_bit_cast(typename Piece<IO>::four, __builtin_amdgcn_raw_buffer_load_b128(
+                rsrc, (uint32_t)at + (uint32_t)(i * step), 0u, 0));
         }
         if (odd && ((width - 1) % VE) % 2 == 0) {
             const int last = back ? 0 : len - 1;
@@ -170,7 +248,10 @@ struct Tile {
                 }
         }
     }
-    static __device__ __forceinline__ void put(Piece<IO> (&x)[NP], IO* lds, int width)
+    // place of this thread's first piece
+    static __device__ __forceinline__ uint32_t place() { return Lds<IO, W>::at(row(0), col() / VE); }
+    static __device__ __forceinline__ uint32_t place(uint32_t first, int i) { return Lds<IO, W>::further(first, i * ROWS, 0); }
+    static __device__ __forceinline__ void put(Piece<IO> (&x)[NP], uint32_t first, int width)
     {
         // elements of a piece behind the row's end: the next head's, or the next token's
         if (width % VE) {
@@ -186,7 +267,7 @@ struct Tile {
         }
 #pragma unroll
         for (int i = 0; i < NP; ++i)
-            x[i].to_lds(lds + row(i) * LD + col());
+            lds_write(place(first, i), x[i].w);
     }
 };
 
@@ -296,10 +377,9 @@ struct Walk {
     typedef Tile<IO, C, KD> TK;
     typedef Tile<IO, C, kCols> TV;
     static constexpr int NT = C / 16, ST = KD / 16, KS = KD / O::K, CS = C / O::K, FE = O::K / 4;
-    static constexpr int LDP = C + O::PAD;
     static constexpr bool BF = sizeof(IO) == 2;
-    static constexpr int kTileK = C * TK::LD, kTileV = C * TV::LD, kTileP = C * LDP;
-    static constexpr size_t kLds = sizeof(IO) * (2 * kTileK + kTileV + kTileP);
+    static constexpr int E = sizeof(IO), kTileK = C * KD * E, kTileV = C * kCols * E, kTileP = C * C * E;  // bytes
+    static constexpr int kLds = 2 * kTileK + kTileV + kTileP + C * 4;
 };
 
 // STATE: the states that segments hand on, nothing else
@@ -311,13 +391,15 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
     typedef typename W::frag frag;
     typedef typename W::TK TK;
     typedef typename W::TV TV;
-    constexpr int NT = W::NT, ST = W::ST, KS = W::KS, CS = W::CS, FE = W::FE, LDP = W::LDP;
+    typedef Lds<IO, kCols> LV;
+    typedef Lds<IO, C> LP;
+    typedef Lds<IO, KD> LK;
+    constexpr int NT = W::NT, ST = W::ST, KS = W::KS, CS = W::CS, FE = W::FE;
     constexpr bool BF = W::BF;
-    __shared__ __attribute__((aligned(16))) IO lds[W::kLds / sizeof(IO)];
-    IO* const Qs = lds;
-    IO* const Ks = Qs + W::kTileK;
-    IO* const Vs = Ks + W::kTileK;
-    IO* const Ps = Vs + W::kTileV;
+    __shared__ __attribute__((aligned(256))) char lds[W::kLds];
+    const uint32_t Qs = (uint32_t)(size_t)(__attribute__((address_space(3))) char*)lds;
+    const uint32_t Ks = Qs + W::kTileK, Vs = Ks + W::kTileK, Ps = Vs + W::kTileV,
+                   Ws = Ps + W::kTileP;  // of_u g^(len - 1 - j + rev), of each token of a chunk of `len`
 
     const LinRole& r = a.role[blockIdx.y];
     // slices of one head follow one another on one XCD (workgroups go round the eight)
@@ -329,7 +411,7 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, c = lane & 15;
     const int col0 = slice * kCols, width = min(r.vd - col0, kCols);  // of v
-    const int mycol = col0 + 16 * wave + c;
+    const int mine = 16 * wave + c, mycol = col0 + mine;
     const int rev = r.rev, dir = rev ? -1 : 1;
 
     const long long row0 = (long long)b * a.T;
@@ -340,7 +422,7 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
     const Decay decay{log((double)a.decay[h])};
     // decays of q k^T: lane (g, c) holds rows j = 4 g + e of column i = c of a 16 x 16
     // block; those below the diagonal block are 16 further each
-    float on[4], below[4], front[4], weight[CS][FE];
+    float on[4], below[4], front[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         on[e] = c >= 4 * g + e ? r.of_p * decay.power(c - 4 * g - e) : 0.f;
@@ -348,43 +430,61 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
         front[e] = r.of_x * decay.power(4 * g + e + 1 - rev);
     }
     const float g16 = decay.power(16);
-    int held = -1;  // tokens of the chunk that `weight` is for
+    int held = -1;  // tokens of the chunk that Ws is for
     float whole = 0.f;
 
     f32x4 X[ST];
     const size_t dense = (size_t)r.kd * r.vd;
-    auto state_in = [&](const float* p, int rs, int cs) {
+    // elements that are not there are out of the descriptor's range: read as zero, not written
+    auto state = [&](const float* p, int rs, int cs, auto each) KDN_INLINE {
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p), (short)0, (int)dense * 4, 0x00020000);
+        int at = mycol < r.vd ? mycol * cs * 4 : 1 << 30;
+        asm volatile("" : "+v"(at));  // formed here, not held over the walk
 #pragma unroll
         for (int t = 0; t < ST; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int i = 16 * t + 4 * g + e;
-                X[t][e] = p && i < r.kd && mycol < r.vd ? p[(size_t)i * rs + (size_t)mycol * cs] : 0.f;
+                const int i = O::state_row(t, g, e);
+                each(rsrc, i < r.kd ? at + i * rs * 4 : 1 << 30, t, e);
             }
     };
-    auto state_out = [&](float* p, int rs, int cs) {
-        if (mycol >= r.vd)
+    auto state_in = [&](const float* p, int rs, int cs) KDN_INLINE {
+        if (!p) {
+#pragma unroll
+            for (int t = 0; t < ST; ++t)
+                X[t] = zero4();
             return;
-#pragma unroll
-        for (int t = 0; t < ST; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = 16 * t + 4 * g + e;
-                if (i < r.kd)
-                    p[(size_t)i * rs + (size_t)mycol * cs] = X[t][e];
-            }
+        }
+        state(p, rs, cs, [&](auto rsrc, int at, int t, int e) KDN_INLINE {
+            X[t][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsrc, at, 0, 0));
+        });
     };
-    auto handed = [&](int seg) { return r.seg + (((size_t)b * a.S + seg) * a.H + h) * dense; };
+    auto state_out = [&](float* p, int rs, int cs) KDN_INLINE {
+        state(p, rs, cs, [&](auto rsrc, int at, int t, int e) KDN_INLINE {
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(X[t][e]), rsrc, at, 0, 0);
+        });
+    };
+    auto handed = [&](int seg) KDN_INLINE { return r.seg + (((size_t)b * a.S + seg) * a.H + h) * dense; };
 
     // blocks of the decayed product above the diagonal that a step of K tokens covers
     if constexpr (!STATE) {
-        for (int i = threadIdx.x; i < W::kTileP; i += kThreads)
-            Ps[i] = IO(0.f);
+        for (int i = threadIdx.x * 4; i < W::kTileP; i += kThreads * 4)
+            lds_write(Ps + i, 0);
     }
+
+    // places in LDS, of a lane or a thread, in the first row or tile that it touches
+    uint32_t kput = Ks + TK::place(), vput = Vs + TV::place();
+    uint32_t qrow = Qs + rows_at<IO, KD>(lane), kcol = Ks + O::template cols_at<KD>(0, O::kApart, lane);
+    uint32_t vcol = Vs + O::template cols_at<kCols>(16 * wave, 4, lane);
+    uint32_t prow = Ps + rows_at<IO, C>(lane);
+    // C = 64: a wave forms q k^T for 16 tokens' k and every q behind; C = 32: for one block of q
+    const int jt = NT == 4 ? wave : wave & 1;
+    uint32_t pput = Ps + LP::at(c, (16 * jt + 4 * g) / O::VE) + 4 * g % O::VE * W::E;
+    uint32_t yput = Vs + LV::at(4 * g, mine / O::VE) + mine % O::VE * W::E;
 
     Piece<IO> nq[STATE ? 1 : TK::NP], nk[TK::NP], nv[TV::NP];
     // the chunk of `len` tokens whose first (in the order of the walk) is `token`
-    auto fetch = [&](int token, int len) {
+    auto fetch = [&](int token, int len) KDN_INLINE {
         const long long at = row0 + (rev ? token - len + 1 : token);
         if constexpr (!STATE)
             TK::load(nq, q + at * r.q.ts, (int)r.q.ts, len, r.kd, rev);
@@ -393,51 +493,52 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
     };
     // y of a chunk, which stands in Vs: each thread stores the pieces whose places it fills
     // with v next
-    auto store = [&](int token, int len) {
-        IO* y = static_cast<IO*>(r.out);
+    const int apart = a.H * r.vd;  // elements from a token's y to the next one's
+    auto lowest = [&](int token, int len) { return ((row0 + (rev ? token - len + 1 : token)) * a.H + h) * r.vd + col0; };
+    auto store = [&](int token, int len) KDN_INLINE {
+        IO* y = static_cast<IO*>(r.out) + lowest(token, len);
         const int n = width - TV::col();
 #pragma unroll
         for (int i = 0; i < TV::NP; ++i) {
             const int row = TV::row(i);
             if (row < len && n > 0) {
                 Piece<IO> x;
-                x.from_lds(Vs + row * TV::LD + TV::col());
-                x.store(y + ((row0 + token + dir * row) * a.H + h) * r.vd + col0 + TV::col(), n);
+                x.w = lds_read<typename Piece<IO>::four>(TV::place(vput, i));
+                x.store(y + (rev ? len - 1 - row : row) * apart + TV::col(), n);
             }
         }
     };
 
-    auto walk = [&](const Span& span) {
+    auto walk = [&](const Span& span) KDN_INLINE {
         int token = rev ? span.to - 1 : span.from, left = span.to - span.from;
         fetch(token, min(left, C));
         for (bool first = true; left > 0; first = false) {
             const int len = min(left, C);
+            // places a few bits away are formed again in every chunk: held over the walk, they
+            // would take the registers of the products
+            for (uint32_t* p : {&kput, &vput, &qrow, &kcol, &vcol, &prow, &pput, &yput})
+                asm volatile("" : "+v"(*p));
             __syncthreads();  // the last chunk's reads are done, its y is whole
             if constexpr (!STATE) {
                 if (!first && !r.out_f32)
                     store(token - dir * C, C);
-                TK::put(nq, Qs, r.kd);
+                TK::put(nq, kput - W::kTileK, r.kd);
             }
-            TK::put(nk, Ks, r.kd);
-            TV::put(nv, Vs, width);
-            __syncthreads();
-            if (left > C)
-                fetch(token + dir * C, min(left - C, C));
+            TK::put(nk, kput, r.kd);
+            TV::put(nv, vput, width);
             if (len != held) {
                 held = len;
                 whole = decay.power(len);
-#pragma unroll
-                for (int s = 0; s < CS; ++s)
-#pragma unroll
-                    for (int e = 0; e < FE; ++e) {
-                        const int j = s * O::K + 16 * (e / 4) + 4 * g + e % 4;
-                        weight[s][e] = r.of_u * decay.power(len - 1 - j + rev);
-                    }
+                if (threadIdx.x < C)
+                    lds_write(Ws + 4 * threadIdx.x, r.of_u * decay.power(len - 1 - (int)threadIdx.x + rev));
             }
+            __syncthreads();
+            if (left > C)
+                fetch(token + dir * C, min(left - C, C));
             frag fv[CS];
 #pragma unroll
             for (int s = 0; s < CS; ++s)
-                fv[s] = O::cols(Vs, TV::LD, s * O::K, 16 * wave, lane);
+                fv[s] = O::template cols<kCols>(vcol, s, 0);
             f32x4 acc[NT];
             if constexpr (!STATE) {
                 frag fx[KS];
@@ -451,28 +552,42 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
                         fx[s] = X[s];
                     }
                 }
-                // C = 64: a wave has 16 tokens' k for every block of q; C = 32: one block
-                const int jt = NT == 4 ? wave : wave & 1;
-                frag fk[KS];
+                const uint32_t krow = qrow + W::kTileK + 16 * jt * LK::BYTES;
+                frag fk[BF ? KS : 1];
+                if constexpr (BF) {
 #pragma unroll
-                for (int s = 0; s < KS; ++s)
-                    fk[s] = O::rows(Ks, TK::LD, 16 * jt, s * O::K, lane);
+                    for (int s = 0; s < KS; ++s)
+                        fk[s] = rows<IO, KD>(krow, 0, s);
+                }
                 float far = 1.f;
 #pragma unroll
                 for (int it = 0; it < NT; ++it) {
-                    frag fq[KS];
-#pragma unroll
-                    for (int s = 0; s < KS; ++s)
-                        fq[s] = O::rows(Qs, TK::LD, 16 * it, s * O::K, lane);
+                    const bool mixed = it >= jt && (NT == 4 || it == wave >> 1);
+                    f32x4 p = zero4();
                     acc[it] = zero4();
-#pragma unroll
-                    for (int s = 0; s < KS; ++s)
-                        O::mma(acc[it], fq[s], fx[s]);
-                    if (it >= jt && (NT == 4 || it == wave >> 1)) {
-                        f32x4 p = zero4();
+                    if constexpr (BF) {
+                        frag fq[KS];
 #pragma unroll
                         for (int s = 0; s < KS; ++s)
-                            O::mma(p, fk[s], fq[s]);
+                            fq[s] = rows<IO, KD>(qrow, 16 * it, s);
+#pragma unroll
+                        for (int s = 0; s < KS; ++s)
+                            O::mma(acc[it], fq[s], fx[s]);
+                        if (mixed) {
+#pragma unroll
+                            for (int s = 0; s < KS; ++s)
+                                O::mma(p, fk[s], fq[s]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int s = 0; s < KS; ++s) {
+                            const frag fq = rows<IO, KD>(qrow, 16 * it, s);
+                            O::mma(acc[it], fq, fx[s]);
+                            if (mixed)
+                                O::mma(p, rows<IO, KD>(krow, 0, s), fq);
+                        }
+                    }
+                    if (mixed) {
                         typedef IO Four __attribute__((ext_vector_type(4)));
                         Four out;
                         if (it == jt) {
@@ -485,7 +600,7 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
                                 out[e] = from_f32<IO>(p[e] * (below[e] * far));
                             far *= g16;
                         }
-                        *reinterpret_cast<Four*>(Ps + (16 * it + c) * LDP + 16 * jt + 4 * g) = out;
+                        lds_write(LP::further(pput, 16 * it, 0), out);
                     }
                 }
                 float tile = 1.f;
@@ -501,20 +616,34 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
             frag hi[CS], lo[BF ? CS : 1];
             float wrong = 0.f;
 #pragma unroll
-            for (int s = 0; s < CS; ++s)
+            for (int s = 0; s < CS; ++s) {
+                f32x4 weight[FE / 4];
+#pragma unroll
+                for (int e = 0; e < FE / 4; ++e)
+                    weight[e] = lds_read<f32x4>(Ws + 4 * (s * O::K + FE * g + 4 * e));
 #pragma unroll
                 for (int e = 0; e < FE; ++e) {
-                    const float x = to_f32(fv[s][e]), y = x * weight[s][e];
+                    const float x = to_f32(fv[s][e]), y = x * weight[e / 4][e % 4];
                     wrong = fmaf(x, 0.f, wrong);
                     hi[s][e] = from_f32<IO>(y);
                     if constexpr (BF) {
-                        const float rest = y - to_f32(hi[s][e]);
-                        lo[s][e] = static_cast<bf16>(rest == rest ? rest : 0.f);  // of an infinity: none
+                        lo[s][e] = static_cast<bf16>(y - to_f32(hi[s][e]));
                     }
                 }
+            }
+            const bool bad = __ballot(wrong != 0.f);
+            if constexpr (BF) {
+                if (bad) {  // the second part of an infinity is none, not a NaN
+#pragma unroll
+                    for (int s = 0; s < CS; ++s)
+#pragma unroll
+                        for (int e = 0; e < FE; ++e)
+                            if (lo[s][e] != lo[s][e])
+                                lo[s][e] = bf16(0.f);
+                }
+            }
             if constexpr (!STATE) {
                 __syncthreads();  // Ps is whole
-                const bool bad = __ballot(wrong != 0.f);
                 if (bad) {
                     // zeros of Ps times what is not finite: those are left out of the products,
                     // and added where they belong
@@ -531,10 +660,10 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
 #pragma unroll
                     for (int s = 0; s < CS; ++s)
                         if (s * O::K < 16 * (it + 1))
-                            O::mma(acc[it], O::rows(Ps, LDP, 16 * it, s * O::K, lane), fv[s]);
+                            O::mma(acc[it], rows<IO, C>(prow, 16 * it, s), fv[s]);
                 if (bad) {
                     for (int j = 0; j < len; ++j) {
-                        const float x = to_f32(Vs[j * TV::LD + 16 * wave + c]);
+                        const float x = to_f32(lds_read<IO>(Vs + LV::at(j, mine / O::VE) + mine % O::VE * W::E));
                         if (x - x == 0.f)
                             continue;
 #pragma unroll
@@ -543,7 +672,9 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
                             for (int e = 0; e < 4; ++e) {
                                 const int i = 16 * it + 4 * g + e;
                                 if (i >= j)
-                                    acc[it][e] = fmaf(to_f32(Ps[i * LDP + j]), x, acc[it][e]);
+                                    acc[it][e] = fmaf(
+                                        to_f32(lds_read<IO>(Ps + LP::at(i, j / O::VE) + j % O::VE * W::E)), x,
+                                        acc[it][e]);
                             }
                     }
                 }
@@ -555,7 +686,7 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
                     X[t][e] *= whole;
 #pragma unroll
                 for (int s = 0; s < CS; ++s) {
-                    const frag fk = O::cols(Ks, TK::LD, s * O::K, 16 * t, lane);
+                    const frag fk = O::template state_cols<KD>(kcol, s, t);
                     O::mma(X[t], fk, hi[s]);
                     if constexpr (BF)
                         O::mma(X[t], fk, lo[s]);
@@ -563,22 +694,23 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
             }
             if constexpr (!STATE) {
                 if (r.out_f32) {
-                    float* y = static_cast<float*>(r.out);
+                    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+                        static_cast<float*>(r.out) + lowest(token, len), (short)0, ((len - 1) * apart + width) * 4, 0x00020000);
+                    int at = mine < width ? ((rev ? len - 1 - 4 * g : 4 * g) * apart + mine) * 4 : (int)0x80000000u;
+                    asm volatile("" : "+v"(at));
 #pragma unroll
                     for (int it = 0; it < NT; ++it)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int i = 16 * it + 4 * g + e;
-                            if (i < len && mycol < r.vd)
-                                y[((row0 + token + dir * i) * a.H + h) * r.vd + mycol] = acc[it][e];
-                        }
+                        for (int e = 0; e < 4; ++e)  // tokens that are not there: out of range
+                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[it][e]), rsrc,
+                                                                  (uint32_t)at + (uint32_t)(dir * (16 * it + e) * apart * 4), 0, 0);
                 } else {
                     // this wave's columns of Vs are its own: y takes v's place
 #pragma unroll
                     for (int it = 0; it < NT; ++it)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            Vs[(16 * it + 4 * g + e) * TV::LD + 16 * wave + c] = from_f32<IO>(acc[it][e]);
+                            lds_write(LV::further(yput, 16 * it + e, 0), from_f32<IO>(acc[it][e]));
                 }
             }
             if (!STATE && left <= C && !r.out_f32) {
