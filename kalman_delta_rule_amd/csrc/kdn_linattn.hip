@@ -186,88 +186,77 @@ struct Decay {
     __device__ __forceinline__ float power(int n) const { return n > 0 ? expf((float)(n * log)) : 1.f; }
 };
 
-// Elements of 16 bytes, as in memory.
-template <typename IO>
-struct Piece {
-    static constexpr int VE = Op<IO>::VE;
-    typedef uint32_t four __attribute__((ext_vector_type(4)));
-    four w;
-    // its first n elements, at any alignment of an element
-    __device__ __forceinline__ void store(IO* p, int n) const
-    {
-        if (n >= VE) {
-            typedef Words<IO, 4> W;
-            *reinterpret_cast<W*>(p) = w;
-            return;
-        }
-        IO e[VE];
-        __builtin_memcpy(e, &w, 16);
-#pragma unroll
-        for (int j = 0; j < VE; ++j)
-            if (j < n)
-                p[j] = e[j];
-    }
-};
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// What this wave copies into LDS, loads and stores has arrived.  (The compiler has to know:
+// it would otherwise wait for loads of before the walk inside it, and so for the copies.)
+__device__ __forceinline__ void copies_done()
+{
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    asm volatile("" ::: "memory");
+}
 
-// A tile of C tokens by W columns, of which `width` are there: 16 bytes a thread and turn,
-// always of the same columns.  Loads go through a buffer descriptor that ends behind the
-// tile's last element: rows and columns that are not there read as zero without a branch.
+// A tile of C tokens by W columns of which `width` are there, 16 bytes a thread and turn.
+// It is copied from memory straight into LDS, through a buffer descriptor that ends behind
+// the tile's last element: what is not there arrives as zeros.  A wave's 1024 bytes follow
+// one another in LDS, so blocks change places in the addresses that are read.
 template <typename IO, int C, int W>
 struct Tile {
-    static constexpr int VE = Op<IO>::VE, PER = W / VE, ROWS = kThreads / PER, NP = C / ROWS;
+    typedef Lds<IO, W> L;
+    static constexpr int VE = Op<IO>::VE, E = sizeof(IO), PER = W / VE, ROWS = kThreads / PER, NP = C / ROWS;
     static_assert(kThreads % PER == 0 && C % ROWS == 0, "whole turns of the threads");
     static __device__ __forceinline__ int row(int i) { return i * ROWS + (int)threadIdx.x / PER; }
-    static __device__ __forceinline__ int col() { return (int)threadIdx.x % PER * VE; }
-    // rows p, p + ts, .. or, backwards, from the last to p
-    static __device__ __forceinline__ void load(Piece<IO> (&x)[NP], const IO* p, int ts, int len, int width, bool back)
+    static __device__ __forceinline__ int block(int i) { return (int)threadIdx.x % PER ^ L::turn(row(0)) ^ L::turn(i * ROWS); }
+    // Bytes of a thread's pieces from the first row's front, turns that differ in the blocks'
+    // exchange apart; out of any range for columns that are not there (a tile spans less
+    // than 2^30 bytes, so what is added to them leaves them out of range)
+    static constexpr int KINDS = ROWS < 16 ? 16 / ROWS : 1;
+    struct Places {
+        uint32_t at[KINDS];
+        __device__ __forceinline__ Places(int ts, int width, int dir)
+        {
+#pragma unroll
+            for (int i = 0; i < KINDS; ++i)
+                at[i] = block(i) * VE < width ? (uint32_t)(dir * row(0) * ts * E + block(i) * 16) : 0x80000000u;
+        }
+    };
+    // to LDS from rows p, p + ts, .. or (dir < 0) from the last of them to p
+    static __device__ __forceinline__ void copy(uint32_t lds, const Places& from, const IO* p, int ts, int len, int width, int dir)
     {
-        constexpr int E = sizeof(IO);
-        const int end = ((len - 1) * ts + width) * E;
-        const bool odd = E == 2 && ((reinterpret_cast<uintptr_t>(p) & 3) || (ts & 1));
-        // a word that ends half a word behind the last element is read whole where words are
-        // aligned (it lies in one page); elsewhere it is out of range
-        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<IO*>(p), (short)0, odd ? end : (end + 3) & ~3, 0x00020000);
-        int at = ((back ? len - 1 - row(0) : row(0)) * ts + col()) * E;
-        const int step = (back ? -ROWS : ROWS) * ts * E;
-        if (col() >= width)
-            at = (int)0x80000000u;  // out of range, and so are steps of it: a tile spans less than 2^30 bytes
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            x[i].w = __builtin_bit_cast(typename Piece<IO>::four, __builtin_amdgcn_raw_buffer_load_b128(
-                rsrc, (uint32_t)at + (uint32_t)(i * step), 0u, 0));
-        }
-        if (odd && ((width - 1) % VE) % 2 == 0) {
-            const int last = back ? 0 : len - 1;
-#pragma unroll
-            for (int i = 0; i < NP; ++i)
-                if (row(i) == last && col() == (width - 1) / VE * VE) {
-                    const uint32_t e = *reinterpret_cast<const uint16_t*>(p + (ptrdiff_t)(len - 1) * ts + width - 1);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        x[i].w[j] = j == (width - 1) % VE / 2 ? e : x[i].w[j];
-                }
-        }
-    }
-    // place of this thread's first piece
-    static __device__ __forceinline__ uint32_t place() { return Lds<IO, W>::at(row(0), col() / VE); }
-    static __device__ __forceinline__ uint32_t place(uint32_t first, int i) { return Lds<IO, W>::further(first, i * ROWS, 0); }
-    static __device__ __forceinline__ void put(Piece<IO> (&x)[NP], uint32_t first, int width)
-    {
-        // elements of a piece behind the row's end: the next head's, or the next token's
-        if (width % VE) {
-            constexpr int EW = VE / 4;  // elements of a word
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = width - col() - j * EW;
-                const uint32_t mask = n >= EW ? ~0u : n <= 0 ? 0u : 0xFFFFu;
-#pragma unroll
-                for (int i = 0; i < NP; ++i)
-                    x[i].w[j] &= mask;
-            }
-        }
+        typedef uint32_t four __attribute__((ext_vector_type(4)));
+        const uint64_t at = reinterpret_cast<uint64_t>(p);
+        const uint32_t last = (uint32_t)(len - 1) * ts * E, step = (uint32_t)(dir * ROWS * ts * E);
+        // a word that ends behind the last element is read whole (it lies in one page)
+        const four rsrc = {(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, (last + width * E + 3) & ~3u, 0x00020000u};
+        const uint32_t first = dir < 0 ? last : 0;
 #pragma unroll
         for (int i = 0; i < NP; ++i)
-            lds_write(place(first, i), x[i].w);
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                         ::"s"(lds + i * (kThreads * 16)), "v"(from.at[i % KINDS] + (first + i * step)), "s"(rsrc)
+                         : "memory");
+    }
+    // the same where rows begin in the middle of a word: an element at a time
+    static __device__ __forceinline__ void copy_odd(uint32_t lds, const IO* p, int ts, int len, int width, int dir)
+    {
+        for (int x = threadIdx.x; x < C * W; x += kThreads) {
+            const int i = x / W, j = x % W;
+            IO v = IO(0.f);
+            if (i < len && j < width)
+                v = p[(ptrdiff_t)(dir < 0 ? len - 1 - i : i) * ts + j];
+            lds_write(lds + L::at(i, j / VE) + j % VE * E, v);
+        }
+    }
+    // row i's piece that the row ends in: what follows is the next head's, or the next token's
+    static __device__ __forceinline__ void end_row(uint32_t lds, int i, int width)
+    {
+        typedef uint32_t four __attribute__((ext_vector_type(4)));
+        const uint32_t at = lds + L::at(i, width / VE);
+        four w = lds_read<four>(at);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int n = width % VE - j * (VE / 4);
+            w[j] &= n >= VE / 4 ? ~0u : n <= 0 ? 0u : 0xFFFFu;
+        }
+        lds_write(at, w);
     }
 };
 
@@ -379,12 +368,14 @@ struct Walk {
     static constexpr int NT = C / 16, ST = KD / 16, KS = KD / O::K, CS = C / O::K, FE = O::K / 4;
     static constexpr bool BF = sizeof(IO) == 2;
     static constexpr int E = sizeof(IO), kTileK = C * KD * E, kTileV = C * kCols * E, kTileP = C * C * E;  // bytes
-    static constexpr int kLds = 2 * kTileK + kTileV + kTileP + C * 4;
+    // q once, k and v twice, the decayed product, the tokens' decays
+    static constexpr int lds(bool state) { return (state ? 2 : 3) * kTileK + 2 * kTileV + (state ? 0 : kTileP) + C * 4; }
 };
 
 // STATE: the states that segments hand on, nothing else
-template <typename IO, int KD, int C, bool STATE>
-__global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
+// ODD: some rows begin in the middle of a word (bf16)
+template <typename IO, int KD, int C, bool STATE, bool ODD>
+__global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linattn_kernel(LinArgs a)
 {
     typedef Walk<IO, KD, C> W;
     typedef typename W::O O;
@@ -396,10 +387,10 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
     typedef Lds<IO, KD> LK;
     constexpr int NT = W::NT, ST = W::ST, KS = W::KS, CS = W::CS, FE = W::FE;
     constexpr bool BF = W::BF;
-    __shared__ __attribute__((aligned(256))) char lds[W::kLds];
+    __shared__ __attribute__((aligned(256))) char lds[W::lds(STATE)];
     const uint32_t Qs = (uint32_t)(size_t)(__attribute__((address_space(3))) char*)lds;
-    const uint32_t Ks = Qs + W::kTileK, Vs = Ks + W::kTileK, Ps = Vs + W::kTileV,
-                   Ws = Ps + W::kTileP;  // of_u g^(len - 1 - j + rev), of each token of a chunk of `len`
+    const uint32_t Ks = Qs + (STATE ? 0 : W::kTileK), Vs = Ks + 2 * W::kTileK, Ps = Vs + 2 * W::kTileV,
+                   Ws = Ps + (STATE ? 0 : W::kTileP);  // of_u g^(len - 1 - j + rev) of each token of a chunk
 
     const LinRole& r = a.role[blockIdx.y];
     // slices of one head follow one another on one XCD (workgroups go round the eight)
@@ -422,13 +413,13 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
     const Decay decay{log((double)a.decay[h])};
     // decays of q k^T: lane (g, c) holds rows j = 4 g + e of column i = c of a 16 x 16
     // block; those below the diagonal block are 16 further each
-    float on[4], below[4], front[4];
+    float on[4], below[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         on[e] = c >= 4 * g + e ? r.of_p * decay.power(c - 4 * g - e) : 0.f;
         below[e] = r.of_p * decay.power(16 + c - 4 * g - e);
-        front[e] = r.of_x * decay.power(4 * g + e + 1 - rev);
     }
+    const float front = r.of_x * decay.power(c + 1 - rev);
     const float g16 = decay.power(16);
     int held = -1;  // tokens of the chunk that Ws is for
     float whole = 0.f;
@@ -472,73 +463,109 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
             lds_write(Ps + i, 0);
     }
 
-    // places in LDS, of a lane or a thread, in the first row or tile that it touches
-    uint32_t kput = Ks + TK::place(), vput = Vs + TV::place();
-    uint32_t qrow = Qs + rows_at<IO, KD>(lane), kcol = Ks + O::template cols_at<KD>(0, O::kApart, lane);
-    uint32_t vcol = Vs + O::template cols_at<kCols>(16 * wave, 4, lane);
-    uint32_t prow = Ps + rows_at<IO, C>(lane);
+    // places in LDS of a lane, in the first row or tile that it touches
+    uint32_t qrow = Qs + rows_at<IO, KD>(lane), prow = Ps + rows_at<IO, C>(lane);
+    const uint32_t kcol = Ks + O::template cols_at<KD>(0, O::kApart, lane);
+    const uint32_t vcol = Vs + O::template cols_at<kCols>(16 * wave, 4, lane);
     // C = 64: a wave forms q k^T for 16 tokens' k and every q behind; C = 32: for one block of q
     const int jt = NT == 4 ? wave : wave & 1;
     uint32_t pput = Ps + LP::at(c, (16 * jt + 4 * g) / O::VE) + 4 * g % O::VE * W::E;
-    uint32_t yput = Vs + LV::at(4 * g, mine / O::VE) + mine % O::VE * W::E;
 
-    Piece<IO> nq[STATE ? 1 : TK::NP], nk[TK::NP], nv[TV::NP];
+    const LinTensor tq = r.q, tk = r.k, tv = r.v;
+    const int kd = r.kd;
+    const typename TK::Places qfrom((int)tq.ts, kd, dir), kfrom((int)tk.ts, kd, dir);
+    const typename TV::Places vfrom((int)tv.ts, width, dir);
+    const uint32_t part = 1024 * wave;  // of a turn's copies, this wave's
+    const bool ragged = kd % O::VE || width % O::VE;
     // the chunk of `len` tokens whose first (in the order of the walk) is `token`
-    auto fetch = [&](int token, int len) KDN_INLINE {
-        const long long at = row0 + (rev ? token - len + 1 : token);
-        if constexpr (!STATE)
-            TK::load(nq, q + at * r.q.ts, (int)r.q.ts, len, r.kd, rev);
-        TK::load(nk, k + at * r.k.ts, (int)r.k.ts, len, r.kd, rev);
-        TV::load(nv, v + at * r.v.ts, (int)r.v.ts, len, width, rev);
+    auto lowest = [&](int token, int len) { return row0 + (rev ? token - len + 1 : token); };
+    auto copy = [&](auto tile, uint32_t to, const auto& from, const IO* p, long long ts, int wide, int token, int len) KDN_INLINE {
+        typedef decltype(tile) Kind;
+        if constexpr (ODD)
+            Kind::copy_odd(to, p + lowest(token, len) * ts, (int)ts, len, wide, dir);
+        else
+            Kind::copy(to + part, from, p + lowest(token, len) * ts, (int)ts, len, wide, dir);
     };
-    // y of a chunk, which stands in Vs: each thread stores the pieces whose places it fills
-    // with v next
+    // y: a lane has four adjacent columns of a token
     const int apart = a.H * r.vd;  // elements from a token's y to the next one's
-    auto lowest = [&](int token, int len) { return ((row0 + (rev ? token - len + 1 : token)) * a.H + h) * r.vd + col0; };
-    auto store = [&](int token, int len) KDN_INLINE {
-        IO* y = static_cast<IO*>(r.out) + lowest(token, len);
-        const int n = width - TV::col();
+    const int left_cols = width - (16 * wave + 4 * g);
+    const bool whole_words = width % 4 == 0 && (reinterpret_cast<uintptr_t>(r.out) & 3) == 0;
+    auto store = [&](const f32x4 (&y)[NT], int token, int len, auto type) KDN_INLINE {
+        typedef decltype(type) T;
+        constexpr int E = sizeof(T);
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+            static_cast<T*>(r.out) + (lowest(token, len) * a.H + h) * r.vd + col0, (short)0, ((len - 1) * apart + width) * E, 0x00020000);
+        int at = left_cols > 0 ? ((rev ? len - 1 - c : c) * apart + 16 * wave + 4 * g) * E : (int)0x80000000u;
+        asm volatile("" : "+v"(at));  // formed here, not held over the walk
 #pragma unroll
-        for (int i = 0; i < TV::NP; ++i) {
-            const int row = TV::row(i);
-            if (row < len && n > 0) {
-                Piece<IO> x;
-                x.w = lds_read<typename Piece<IO>::four>(TV::place(vput, i));
-                x.store(y + (rev ? len - 1 - row : row) * apart + TV::col(), n);
+        for (int it = 0; it < NT; ++it) {  // tokens that are not there are out of range
+            const uint32_t to = (uint32_t)at + (uint32_t)(dir * 16 * it * apart * E);
+            if (whole_words) {
+                if constexpr (E == 4) {
+                    typedef uint32_t four __attribute__((ext_vector_type(4)));
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(four, y[it]), rsrc, to, 0, 0);
+                } else {
+                    typedef uint32_t two __attribute__((ext_vector_type(2)));
+                    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(two, __builtin_convertvector(y[it], bf16x4)), rsrc, to, 0, 0);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t one = e < left_cols ? to + e * E : 0x80000000u;
+                    if constexpr (E == 4)
+                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y[it][e]), rsrc, one, 0, 0);
+                    else
+                        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, static_cast<bf16>(y[it][e])), rsrc, one, 0, 0);
+                }
             }
         }
     };
 
     auto walk = [&](const Span& span) KDN_INLINE {
-        int token = rev ? span.to - 1 : span.from, left = span.to - span.from;
-        fetch(token, min(left, C));
-        for (bool first = true; left > 0; first = false) {
-            const int len = min(left, C);
+        // (the same in all lanes; said so, addresses and counts are scalars)
+        const int from = __builtin_amdgcn_readfirstlane(span.from), to = __builtin_amdgcn_readfirstlane(span.to);
+        int token = rev ? to - 1 : from, left = to - from, turn = 0;
+        lds_barrier();  // the last span's reads are done
+        if constexpr (!STATE)
+            copy(TK{}, Qs, qfrom, q, tq.ts, kd, token, min(left, C));
+        copy(TK{}, Ks, kfrom, k, tk.ts, kd, token, min(left, C));
+        copy(TV{}, Vs, vfrom, v, tv.ts, width, token, min(left, C));
+        for (; left > 0; turn ^= 1) {
+            const int len = min(left, C), next = token + dir * C, more = min(left - C, C);
+            const uint32_t K = Ks + turn * W::kTileK, V = Vs + turn * W::kTileV;
+            // the other buffers of k and v
+            const uint32_t K2 = Ks + (turn ^ 1) * W::kTileK, V2 = Vs + (turn ^ 1) * W::kTileV;
             // places a few bits away are formed again in every chunk: held over the walk, they
             // would take the registers of the products
-            for (uint32_t* p : {&kput, &vput, &qrow, &kcol, &vcol, &prow, &pput, &yput})
+            for (uint32_t* p : {&qrow, &prow, &pput})
                 asm volatile("" : "+v"(*p));
-            __syncthreads();  // the last chunk's reads are done, its y is whole
-            if constexpr (!STATE) {
-                if (!first && !r.out_f32)
-                    store(token - dir * C, C);
-                TK::put(nq, kput - W::kTileK, r.kd);
-            }
-            TK::put(nk, kput, r.kd);
-            TV::put(nv, vput, width);
-            if (len != held) {
+            copies_done();
+            lds_barrier();  // so are all waves'; the last chunk's reads are done
+            if (ragged || len != held) {
+                const int x = threadIdx.x;
+                if (x < C) {
+                    if (kd % O::VE)
+                        TK::end_row(K, x, kd);
+                    if (!STATE && kd % O::VE)
+                        TK::end_row(Qs, x, kd);
+                    if (width % O::VE)
+                        TV::end_row(V, x, width);
+                    if (len != held)
+                        lds_write(Ws + 4 * x, r.of_u * decay.power(len - 1 - x + rev));
+                }
+                if (len != held)
+                    whole = decay.power(len);
                 held = len;
-                whole = decay.power(len);
-                if (threadIdx.x < C)
-                    lds_write(Ws + 4 * threadIdx.x, r.of_u * decay.power(len - 1 - (int)threadIdx.x + rev));
+                lds_barrier();
             }
-            __syncthreads();
-            if (left > C)
-                fetch(token + dir * C, min(left - C, C));
+            if (more > 0) {
+                copy(TK{}, K2, kfrom, k, tk.ts, kd, next, more);
+                copy(TV{}, V2, vfrom, v, tv.ts, width, next, more);
+            }
             frag fv[CS];
 #pragma unroll
             for (int s = 0; s < CS; ++s)
-                fv[s] = O::template cols<kCols>(vcol, s, 0);
+                fv[s] = O::template cols<kCols>(vcol + turn * W::kTileV, s, 0);
             f32x4 acc[NT];
             if constexpr (!STATE) {
                 frag fx[KS];
@@ -552,42 +579,44 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
                         fx[s] = X[s];
                     }
                 }
-                const uint32_t krow = qrow + W::kTileK + 16 * jt * LK::BYTES;
-                frag fk[BF ? KS : 1];
-                if constexpr (BF) {
+                const uint32_t krow = K + (qrow - Qs) + 16 * jt * LK::BYTES;
+                // q's operands are read a group ahead of their products
+                constexpr int GS = KS < 4 ? KS : 4, NG = KS / GS;
+                frag fk[NT == 4 ? KS : 1], fq[2][GS];
+                if constexpr (NT == 4) {
 #pragma unroll
                     for (int s = 0; s < KS; ++s)
                         fk[s] = rows<IO, KD>(krow, 0, s);
                 }
+                auto read = [&](int u) KDN_INLINE {
+#pragma unroll
+                    for (int s = 0; s < GS; ++s)
+                        fq[u % 2][s] = rows<IO, KD>(qrow, 16 * (u / NG), u % NG * GS + s);
+                };
+                read(0);
                 float far = 1.f;
+                f32x4 p;
 #pragma unroll
-                for (int it = 0; it < NT; ++it) {
+                for (int u = 0; u < NT * NG; ++u) {
+                    const int it = u / NG, s0 = u % NG * GS;
                     const bool mixed = it >= jt && (NT == 4 || it == wave >> 1);
-                    f32x4 p = zero4();
-                    acc[it] = zero4();
-                    if constexpr (BF) {
-                        frag fq[KS];
+                    if (u + 1 < NT * NG)
+                        read(u + 1);
+                    if (s0 == 0)
+                        acc[it] = p = zero4();
 #pragma unroll
-                        for (int s = 0; s < KS; ++s)
-                            fq[s] = rows<IO, KD>(qrow, 16 * it, s);
+                    for (int s = 0; s < GS; ++s)
+                        O::mma(acc[it], fx[s0 + s], fq[u % 2][s]);
+                    if (mixed) {
 #pragma unroll
-                        for (int s = 0; s < KS; ++s)
-                            O::mma(acc[it], fq[s], fx[s]);
-                        if (mixed) {
-#pragma unroll
-                            for (int s = 0; s < KS; ++s)
-                                O::mma(p, fk[s], fq[s]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int s = 0; s < KS; ++s) {
-                            const frag fq = rows<IO, KD>(qrow, 16 * it, s);
-                            O::mma(acc[it], fq, fx[s]);
-                            if (mixed)
-                                O::mma(p, rows<IO, KD>(krow, 0, s), fq);
+                        for (int s = 0; s < GS; ++s) {
+                            if constexpr (NT == 4)
+                                O::mma(p, fk[s0 + s], fq[u % 2][s]);
+                            else
+                                O::mma(p, rows<IO, KD>(krow, 0, s0 + s), fq[u % 2][s]);
                         }
                     }
-                    if (mixed) {
+                    if (mixed && s0 + GS == KS) {
                         typedef IO Four __attribute__((ext_vector_type(4)));
                         Four out;
                         if (it == jt) {
@@ -603,35 +632,32 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
                         lds_write(LP::further(pput, 16 * it, 0), out);
                     }
                 }
-                float tile = 1.f;
+                float decayed = front;
 #pragma unroll
                 for (int it = 0; it < NT; ++it) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[it][e] *= front[e] * tile;
-                    tile *= g16;
+                    acc[it] *= decayed;
+                    decayed *= g16;
                 }
             }
-            // v's decayed values, in two parts where they are rounded; any that is not finite
+            // v's decayed values, in two parts where they are rounded
             frag hi[CS], lo[BF ? CS : 1];
-            float wrong = 0.f;
+            f32x4 none = zero4();  // zero times v: what is not finite shows
 #pragma unroll
             for (int s = 0; s < CS; ++s) {
                 f32x4 weight[FE / 4];
 #pragma unroll
                 for (int e = 0; e < FE / 4; ++e)
                     weight[e] = lds_read<f32x4>(Ws + 4 * (s * O::K + FE * g + 4 * e));
+                O::mma(none, frag{}, fv[s]);
 #pragma unroll
                 for (int e = 0; e < FE; ++e) {
-                    const float x = to_f32(fv[s][e]), y = x * weight[e / 4][e % 4];
-                    wrong = fmaf(x, 0.f, wrong);
+                    const float y = to_f32(fv[s][e]) * weight[e / 4][e % 4];
                     hi[s][e] = from_f32<IO>(y);
-                    if constexpr (BF) {
+                    if constexpr (BF)
                         lo[s][e] = static_cast<bf16>(y - to_f32(hi[s][e]));
-                    }
                 }
             }
-            const bool bad = __ballot(wrong != 0.f);
+            const bool bad = __ballot(none[0] != 0.f);
             if constexpr (BF) {
                 if (bad) {  // the second part of an infinity is none, not a NaN
 #pragma unroll
@@ -643,7 +669,9 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
                 }
             }
             if constexpr (!STATE) {
-                __syncthreads();  // Ps is whole
+                lds_barrier();  // Ps is whole, q is read
+                if (more > 0)
+                    copy(TK{}, Qs, qfrom, q, tq.ts, kd, next, more);
                 if (bad) {
                     // zeros of Ps times what is not finite: those are left out of the products,
                     // and added where they belong
@@ -660,62 +688,54 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
 #pragma unroll
                     for (int s = 0; s < CS; ++s)
                         if (s * O::K < 16 * (it + 1))
-                            O::mma(acc[it], rows<IO, C>(prow, 16 * it, s), fv[s]);
+                            O::mma(acc[it], fv[s], rows<IO, C>(prow, 16 * it, s));
                 if (bad) {
+                    typedef IO Four __attribute__((ext_vector_type(4)));
+                    int i = c, four = 16 * wave + 4 * g;  // of v's columns, this lane's
+                    asm volatile("" : "+v"(i), "+v"(four));
+#pragma unroll 1
                     for (int j = 0; j < len; ++j) {
-                        const float x = to_f32(lds_read<IO>(Vs + LV::at(j, mine / O::VE) + mine % O::VE * W::E));
-                        if (x - x == 0.f)
-                            continue;
+                        const Four vj = lds_read<Four>(V + LV::at(j, four / O::VE) + four % O::VE * W::E);
+                        f32x4 x;
 #pragma unroll
-                        for (int it = 0; it < NT; ++it)
+                        for (int e = 0; e < 4; ++e)
+                            x[e] = to_f32(vj[e]);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int i = 16 * it + 4 * g + e;
-                                if (i >= j)
-                                    acc[it][e] = fmaf(
-                                        to_f32(lds_read<IO>(Ps + LP::at(i, j / O::VE) + j % O::VE * W::E)), x,
-                                        acc[it][e]);
-                            }
+                        for (int it = 0; it < NT; ++it) {
+                            const float pj = to_f32(lds_read<IO>(Ps + LP::at(16 * it + i, j / O::VE) + j % O::VE * W::E));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (16 * it + i >= j && x[e] - x[e] != 0.f)
+                                    acc[it][e] = fmaf(pj, x[e], acc[it][e]);
+                        }
                     }
                 }
+                if (!BF || r.out_f32)
+                    store(acc, token, len, 0.f);
+                else
+                    store(acc, token, len, IO{});
             }
+            const uint32_t kc = kcol + turn * W::kTileK;
+            frag fk[2][CS];
+            auto read = [&](int t) KDN_INLINE {
+#pragma unroll
+                for (int s = 0; s < CS; ++s)
+                    fk[t % 2][s] = O::template state_cols<KD>(kc, s, t);
+            };
+            read(0);
 #pragma unroll
             for (int t = 0; t < ST; ++t) {
+                if (t + 1 < ST)
+                    read(t + 1);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     X[t][e] *= whole;
 #pragma unroll
                 for (int s = 0; s < CS; ++s) {
-                    const frag fk = O::template state_cols<KD>(kcol, s, t);
-                    O::mma(X[t], fk, hi[s]);
+                    O::mma(X[t], fk[t % 2][s], hi[s]);
                     if constexpr (BF)
-                        O::mma(X[t], fk, lo[s]);
+                        O::mma(X[t], fk[t % 2][s], lo[s]);
                 }
-            }
-            if constexpr (!STATE) {
-                if (r.out_f32) {
-                    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
-                        static_cast<float*>(r.out) + lowest(token, len), (short)0, ((len - 1) * apart + width) * 4, 0x00020000);
-                    int at = mine < width ? ((rev ? len - 1 - 4 * g : 4 * g) * apart + mine) * 4 : (int)0x80000000u;
-                    asm volatile("" : "+v"(at));
-#pragma unroll
-                    for (int it = 0; it < NT; ++it)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)  // tokens that are not there: out of range
-                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[it][e]), rsrc,
-                                                                  (uint32_t)at + (uint32_t)(dir * (16 * it + e) * apart * 4), 0, 0);
-                } else {
-                    // this wave's columns of Vs are its own: y takes v's place
-#pragma unroll
-                    for (int it = 0; it < NT; ++it)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            lds_write(LV::further(yput, 16 * it + e, 0), from_f32<IO>(acc[it][e]));
-                }
-            }
-            if (!STATE && left <= C && !r.out_f32) {
-                __syncthreads();
-                store(token, len);
             }
             token += dir * C;
             left -= len;
@@ -735,7 +755,7 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_kernel(LinArgs a)
         Span span;
         spans.start(a, b, t0, t1, rev);
         while (spans.next(span, a.T)) {
-            const size_t n = ((size_t)span.n * a.H + h) * dense;
+            const size_t n = ((size_t)__builtin_amdgcn_readfirstlane(span.n) * a.H + h) * dense;
             // (offsets that begin below zero claim a segment before the first one)
             if (span.first || (rev ? s + 1 >= a.S : s == 0))
                 state_in(r.X0 ? r.X0 + n : nullptr, r.rs, r.cs);
@@ -849,13 +869,29 @@ __global__ __launch_bounds__(256) void linattn_step_kernel(LinStepArgs a)
 
 int padded(int kd) { return kd <= 32 ? 32 : kd <= 64 ? 64 : kd <= 128 ? 128 : 256; }
 
+// whether copies of words reach a tensor's rows
+bool in_words(const LinTensor& t)
+{
+    return !((reinterpret_cast<uintptr_t>(t.p) & 3) || (t.ts & 1) || (t.hs & 1));
+}
+
 template <typename IO, int KD, bool STATE>
 void launch_walk(const LinArgs& a, int roles, hipStream_t stream)
 {
     constexpr int C = sizeof(IO) == 2 && KD <= 128 ? 64 : 32;
     const int slices = (a.role[0].vd + kCols - 1) / kCols;
     const unsigned units = ((unsigned)a.B * a.H * a.S + 7) / 8 * 8;
-    linattn_kernel<IO, KD, C, STATE><<<dim3(units * slices, roles), kThreads, 0, stream>>>(a);
+    const dim3 grid(units * slices, roles);
+    if constexpr (sizeof(IO) == 2) {
+        bool odd = false;
+        for (int i = 0; i < roles; ++i)
+            odd = odd || !in_words(a.role[i].q) || !in_words(a.role[i].k) || !in_words(a.role[i].v);
+        if (odd) {
+            linattn_kernel<IO, KD, C, STATE, true><<<grid, kThreads, 0, stream>>>(a);
+            return;
+        }
+    }
+    linattn_kernel<IO, KD, C, STATE, false><<<grid, kThreads, 0, stream>>>(a);
 }
 
 template <typename IO>
@@ -886,7 +922,7 @@ void launch_walks(const LinArgs& a, int roles, hipStream_t stream)
 int segments(int B, int T, int H, int slices, int& L)
 {
     const long long groups = (long long)B * H * slices;
-    const long long want = (512 + groups - 1) / groups, most = T / 512;
+    const long long want = (256 + groups - 1) / groups, most = T / 512;
     const long long S = want < most ? want : most;
     L = S <= 1 ? (T > 0 ? T : 1) : (int)(((T + S - 1) / S + 63) / 64 * 64);
     return T > 0 ? (T + L - 1) / L : 1;
