@@ -219,21 +219,35 @@ struct Tile {
                 at[i] = block(i) * VE < width ? (uint32_t)(dir * row(0) * ts * E + block(i) * 16) : 0x80000000u;
         }
     };
-    // to LDS from rows p, p + ts, .. or (dir < 0) from the last of them to p
-    static __device__ __forceinline__ void copy(uint32_t lds, const Places& from, const IO* p, int ts, int len, int width, int dir)
-    {
+    // Copies to LDS from rows p, p + ts, .. or (dir < 0) from the last of them to p, turn by
+    // turn: a wave that asks for many at once waits for the last.
+    struct Copy {
         typedef uint32_t four __attribute__((ext_vector_type(4)));
-        const uint64_t at = reinterpret_cast<uint64_t>(p);
-        const uint32_t last = (uint32_t)(len - 1) * ts * E, step = (uint32_t)(dir * ROWS * ts * E);
-        // a word that ends behind the last element is read whole (it lies in one page)
-        const four rsrc = {(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, (last + width * E + 3) & ~3u, 0x00020000u};
-        const uint32_t first = dir < 0 ? last : 0;
-#pragma unroll
-        for (int i = 0; i < NP; ++i)
+        four rsrc;
+        uint32_t lds, first, step;
+        __device__ __forceinline__ Copy(uint32_t to, const IO* p, int ts, int len, int width, int dir)
+        {
+            const uint64_t at = reinterpret_cast<uint64_t>(p);
+            const uint32_t last = (uint32_t)(len - 1) * ts * E;
+            // a word that ends behind the last element is read whole (it lies in one page)
+            rsrc = four{(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, (last + width * E + 3) & ~3u, 0x00020000u};
+            lds = to, first = dir < 0 ? last : 0, step = (uint32_t)(dir * ROWS * ts * E);
+        }
+        __device__ __forceinline__ void turn(const Places& from, int i) const
+        {
             asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                          ::"s"(lds + i * (kThreads * 16)), "v"(from.at[i % KINDS] + (first + i * step)), "s"(rsrc)
                          : "memory");
-    }
+        }
+        // its share of `of` parts, the whole of them being all turns
+        __device__ __forceinline__ void share(const Places& from, int part, int of) const
+        {
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+                if (i * of / NP == part)
+                    turn(from, i);
+        }
+    };
     // the same where rows begin in the middle of a word: an element at a time
     static __device__ __forceinline__ void copy_odd(uint32_t lds, const IO* p, int ts, int len, int width, int dir)
     {
@@ -479,12 +493,12 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
     const bool ragged = kd % O::VE || width % O::VE;
     // the chunk of `len` tokens whose first (in the order of the walk) is `token`
     auto lowest = [&](int token, int len) { return row0 + (rev ? token - len + 1 : token); };
-    auto copy = [&](auto tile, uint32_t to, const auto& from, const IO* p, long long ts, int wide, int token, int len) KDN_INLINE {
-        typedef decltype(tile) Kind;
-        if constexpr (ODD)
-            Kind::copy_odd(to, p + lowest(token, len) * ts, (int)ts, len, wide, dir);
-        else
-            Kind::copy(to + part, from, p + lowest(token, len) * ts, (int)ts, len, wide, dir);
+    auto copies = [&](auto tile, uint32_t to, const IO* p, long long ts, int wide, int token, int len) KDN_INLINE {
+        return typename decltype(tile)::Copy(to + part, p + lowest(token, len) * ts, (int)ts, len, wide, dir);
+    };
+    // (the walks of odd rows copy a chunk's tiles one element after another)
+    auto copy_odd = [&](auto tile, uint32_t to, const IO* p, long long ts, int wide, int token, int len) KDN_INLINE {
+        decltype(tile)::copy_odd(to, p + lowest(token, len) * ts, (int)ts, len, wide, dir);
     };
     // y: a lane has four adjacent columns of a token
     const int apart = a.H * r.vd;  // elements from a token's y to the next one's
@@ -526,10 +540,18 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
         const int from = __builtin_amdgcn_readfirstlane(span.from), to = __builtin_amdgcn_readfirstlane(span.to);
         int token = rev ? to - 1 : from, left = to - from, turn = 0;
         lds_barrier();  // the last span's reads are done
-        if constexpr (!STATE)
-            copy(TK{}, Qs, qfrom, q, tq.ts, kd, token, min(left, C));
-        copy(TK{}, Ks, kfrom, k, tk.ts, kd, token, min(left, C));
-        copy(TV{}, Vs, vfrom, v, tv.ts, width, token, min(left, C));
+        // the first chunk
+        if constexpr (ODD) {
+            if constexpr (!STATE)
+                copy_odd(TK{}, Qs, q, tq.ts, kd, token, min(left, C));
+            copy_odd(TK{}, Ks, k, tk.ts, kd, token, min(left, C));
+            copy_odd(TV{}, Vs, v, tv.ts, width, token, min(left, C));
+        } else {
+            if constexpr (!STATE)
+                copies(TK{}, Qs, q, tq.ts, kd, token, min(left, C)).share(qfrom, 0, 1);
+            copies(TK{}, Ks, k, tk.ts, kd, token, min(left, C)).share(kfrom, 0, 1);
+            copies(TV{}, Vs, v, tv.ts, width, token, min(left, C)).share(vfrom, 0, 1);
+        }
         for (; left > 0; turn ^= 1) {
             const int len = min(left, C), next = token + dir * C, more = min(left - C, C);
             const uint32_t K = Ks + turn * W::kTileK, V = Vs + turn * W::kTileV;
@@ -558,10 +580,23 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                 held = len;
                 lds_barrier();
             }
-            if (more > 0) {
-                copy(TK{}, K2, kfrom, k, tk.ts, kd, next, more);
-                copy(TV{}, V2, vfrom, v, tv.ts, width, next, more);
+            // the next chunk's copies, asked for between the products (none: of no tokens)
+            const auto k2 = copies(TK{}, K2, k, tk.ts, kd, next, more);
+            const auto v2 = copies(TV{}, V2, v, tv.ts, width, next, more);
+            if constexpr (ODD) {
+                if (more > 0) {
+                    copy_odd(TK{}, K2, k, tk.ts, kd, next, more);
+                    copy_odd(TV{}, V2, v, tv.ts, width, next, more);
+                }
             }
+            auto ahead = [&](int part, int of) KDN_INLINE {
+                if (!ODD && more > 0) {
+                    k2.share(kfrom, part, of);
+                    v2.share(vfrom, part, of);
+                }
+            };
+            if constexpr (STATE)
+                ahead(0, 1);
             frag fv[CS];
 #pragma unroll
             for (int s = 0; s < CS; ++s)
@@ -602,6 +637,7 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                     const bool mixed = it >= jt && (NT == 4 || it == wave >> 1);
                     if (u + 1 < NT * NG)
                         read(u + 1);
+                    ahead(u, NT * NG);
                     if (s0 == 0)
                         acc[it] = p = zero4();
 #pragma unroll
@@ -639,6 +675,14 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                     decayed *= g16;
                 }
             }
+            if constexpr (!STATE) {
+                lds_barrier();  // Ps is whole, q is read
+                if constexpr (ODD) {
+                    if (more > 0)
+                        copy_odd(TK{}, Qs, q, tq.ts, kd, next, more);
+                }
+            }
+            const auto q2 = copies(TK{}, Qs, q, tq.ts, kd, next, more);
             // v's decayed values, in two parts where they are rounded
             frag hi[CS], lo[BF ? CS : 1];
             f32x4 none = zero4();  // zero times v: what is not finite shows
@@ -649,6 +693,8 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                 for (int e = 0; e < FE / 4; ++e)
                     weight[e] = lds_read<f32x4>(Ws + 4 * (s * O::K + FE * g + 4 * e));
                 O::mma(none, frag{}, fv[s]);
+                if (!STATE && !ODD && more > 0)
+                    q2.share(qfrom, s, CS);
 #pragma unroll
                 for (int e = 0; e < FE; ++e) {
                     const float y = to_f32(fv[s][e]) * weight[e / 4][e % 4];
@@ -669,9 +715,6 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                 }
             }
             if constexpr (!STATE) {
-                lds_barrier();  // Ps is whole, q is read
-                if (more > 0)
-                    copy(TK{}, Qs, qfrom, q, tq.ts, kd, next, more);
                 if (bad) {
                     // zeros of Ps times what is not finite: those are left out of the products,
                     // and added where they belong
