@@ -55,6 +55,7 @@ struct LinArgs {
     const float* decay;
     bool clear;
     int S, L;  // segments of each row, and their tokens
+    bool odd;  // rows of some input begin in the middle of a word
     LinRole role[3];
 };
 

@@ -187,11 +187,13 @@ struct Decay {
 };
 
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-// What this wave copies into LDS, loads and stores has arrived.  (The compiler has to know:
-// it would otherwise wait for loads of before the walk inside it, and so for the copies.)
-__device__ __forceinline__ void copies_done()
+// What this wave copies into LDS, loads and stores has arrived, but for the last N asked
+// for.  (The compiler has to know: it would otherwise wait for loads of before the walk
+// inside it, and so for the copies.)
+template <int N>
+__device__ __forceinline__ void arrived()
 {
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    __builtin_amdgcn_s_waitcnt(0x0F70 | N);  // vmcnt
     asm volatile("" ::: "memory");
 }
 
@@ -387,8 +389,8 @@ struct Walk {
 };
 
 // STATE: the states that segments hand on, nothing else
-// ODD: some rows begin in the middle of a word (bf16)
-template <typename IO, int KD, int C, bool STATE, bool ODD>
+// EDGE: rows that are not whole pieces of 16 bytes, or y's not whole words
+template <typename IO, int KD, int C, bool STATE, bool EDGE>
 __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linattn_kernel(LinArgs a)
 {
     typedef Walk<IO, KD, C> W;
@@ -425,14 +427,15 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
     const IO* v = static_cast<const IO*>(r.v.p) + (long long)(h / r.v.div) * r.v.hs + col0;
 
     const Decay decay{log((double)a.decay[h])};
-    // decays of q k^T: lane (g, c) holds rows j = 4 g + e of column i = c of a 16 x 16
-    // block; those below the diagonal block are 16 further each
-    float on[4], below[4];
+    // C = 64: a wave forms q k^T for 16 tokens' k (block jt) and every q; C = 32: for one block
+    // of q.  Lane (g, c) holds q k^T of k's tokens j = 4 g + e of a block and q's token i = c.
+    const int jt = NT == 4 ? wave : wave & 1;
+    f32x4 pdecay[NT == 4 ? 4 : 1];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        on[e] = c >= 4 * g + e ? r.of_p * decay.power(c - 4 * g - e) : 0.f;
-        below[e] = r.of_p * decay.power(16 + c - 4 * g - e);
-    }
+    for (int i = 0; i < (NT == 4 ? 4 : 1); ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            pdecay[i][e] = r.of_p * decay.power(16 * ((NT == 4 ? i : wave >> 1) - jt) + c - 4 * g - e);
     const float front = r.of_x * decay.power(c + 1 - rev);
     const float g16 = decay.power(16);
     int held = -1;  // tokens of the chunk that Ws is for
@@ -481,8 +484,6 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
     uint32_t qrow = Qs + rows_at<IO, KD>(lane), prow = Ps + rows_at<IO, C>(lane);
     const uint32_t kcol = Ks + O::template cols_at<KD>(0, O::kApart, lane);
     const uint32_t vcol = Vs + O::template cols_at<kCols>(16 * wave, 4, lane);
-    // C = 64: a wave forms q k^T for 16 tokens' k and every q behind; C = 32: for one block of q
-    const int jt = NT == 4 ? wave : wave & 1;
     uint32_t pput = Ps + LP::at(c, (16 * jt + 4 * g) / O::VE) + 4 * g % O::VE * W::E;
 
     const LinTensor tq = r.q, tk = r.k, tv = r.v;
@@ -490,70 +491,73 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
     const typename TK::Places qfrom((int)tq.ts, kd, dir), kfrom((int)tk.ts, kd, dir);
     const typename TV::Places vfrom((int)tv.ts, width, dir);
     const uint32_t part = 1024 * wave;  // of a turn's copies, this wave's
-    const bool ragged = kd % O::VE || width % O::VE;
-    // the chunk of `len` tokens whose first (in the order of the walk) is `token`
-    auto lowest = [&](int token, int len) { return row0 + (rev ? token - len + 1 : token); };
-    auto copies = [&](auto tile, uint32_t to, const IO* p, long long ts, int wide, int token, int len) KDN_INLINE {
-        return typename decltype(tile)::Copy(to + part, p + lowest(token, len) * ts, (int)ts, len, wide, dir);
+    const bool ragged = EDGE && (kd % O::VE || width % O::VE);
+    const bool odd = EDGE && a.odd;  // some rows begin in the middle of a word
+    auto copies = [&](auto tile, uint32_t to, const IO* p, int ts, int wide, int len) KDN_INLINE {
+        return typename decltype(tile)::Copy(to + part, p, ts, len, wide, dir);
     };
-    // (the walks of odd rows copy a chunk's tiles one element after another)
-    auto copy_odd = [&](auto tile, uint32_t to, const IO* p, long long ts, int wide, int token, int len) KDN_INLINE {
-        decltype(tile)::copy_odd(to, p + lowest(token, len) * ts, (int)ts, len, wide, dir);
-    };
-    // y: a lane has four adjacent columns of a token
-    const int apart = a.H * r.vd;  // elements from a token's y to the next one's
+    // y: a lane has four adjacent columns of a token in each 16 of them
+    const bool out_f32 = r.out_f32;
+    const int eo = BF && !out_f32 ? 2 : 4, apart = a.H * r.vd * eo;  // bytes of an element, to the next token
     const int left_cols = width - (16 * wave + 4 * g);
-    const bool whole_words = width % 4 == 0 && (reinterpret_cast<uintptr_t>(r.out) & 3) == 0;
-    auto store = [&](const f32x4 (&y)[NT], int token, int len, auto type) KDN_INLINE {
-        typedef decltype(type) T;
-        constexpr int E = sizeof(T);
-        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
-            static_cast<T*>(r.out) + (lowest(token, len) * a.H + h) * r.vd + col0, (short)0, ((len - 1) * apart + width) * E, 0x00020000);
-        int at = left_cols > 0 ? ((rev ? len - 1 - c : c) * apart + 16 * wave + 4 * g) * E : (int)0x80000000u;
-        asm volatile("" : "+v"(at));  // formed here, not held over the walk
+    const uint32_t yfrom = left_cols > 0 ? (uint32_t)(dir * c * apart + (16 * wave + 4 * g) * eo) : 0x80000000u;
+    auto store = [&](const f32x4 (&y)[NT], char* to, int len) KDN_INLINE {
+        const int last = (len - 1) * apart;
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(to, (short)0, last + width * eo, 0x00020000);
+        // tokens that are not there are out of range
+        const uint32_t first = yfrom + (rev ? last : 0), step = dir * 16 * apart;
+        typedef uint32_t two __attribute__((ext_vector_type(2)));
+        typedef uint32_t four __attribute__((ext_vector_type(4)));
+        if (EDGE && (width % 4 || (reinterpret_cast<uintptr_t>(r.out) & 3))) {
 #pragma unroll
-        for (int it = 0; it < NT; ++it) {  // tokens that are not there are out of range
-            const uint32_t to = (uint32_t)at + (uint32_t)(dir * 16 * it * apart * E);
-            if (whole_words) {
-                if constexpr (E == 4) {
-                    typedef uint32_t four __attribute__((ext_vector_type(4)));
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(four, y[it]), rsrc, to, 0, 0);
-                } else {
-                    typedef uint32_t two __attribute__((ext_vector_type(2)));
-                    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(two, __builtin_convertvector(y[it], bf16x4)), rsrc, to, 0, 0);
-                }
-            } else {
+            for (int it = 0; it < NT; ++it)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const uint32_t one = e < left_cols ? to + e * E : 0x80000000u;
-                    if constexpr (E == 4)
-                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y[it][e]), rsrc, one, 0, 0);
+                    const uint32_t at = e < left_cols ? first + it * step + e * eo : 0x80000000u;
+                    if (!BF || out_f32)
+                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y[it][e]), rsrc, at, 0, 0);
                     else
-                        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, static_cast<bf16>(y[it][e])), rsrc, one, 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b16(
+                            __builtin_bit_cast(unsigned short, static_cast<bf16>(y[it][e])), rsrc, at, 0, 0);
                 }
-            }
+        } else if (!BF || out_f32) {
+#pragma unroll
+            for (int it = 0; it < NT; ++it)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(four, y[it]), rsrc, first + it * step, 0, 0);
+        } else {
+#pragma unroll
+            for (int it = 0; it < NT; ++it)
+                __builtin_amdgcn_raw_buffer_store_b64(
+                    __builtin_bit_cast(two, __builtin_convertvector(y[it], bf16x4)), rsrc, first + it * step, 0, 0);
         }
     };
 
     auto walk = [&](const Span& span) KDN_INLINE {
         // (the same in all lanes; said so, addresses and counts are scalars)
         const int from = __builtin_amdgcn_readfirstlane(span.from), to = __builtin_amdgcn_readfirstlane(span.to);
-        int token = rev ? to - 1 : from, left = to - from, turn = 0;
+        int left = to - from, turn = 0;
         lds_barrier();  // the last span's reads are done
+        // lowest addresses of the next chunk to copy, and of the one whose y is next
+        const int qts = (int)tq.ts, kts = (int)tk.ts, vts = (int)tv.ts;
+        const long long low = row0 + (rev ? to - min(left, C) : from);
+        const IO *qp = q + low * qts, *kp = k + low * kts, *vp = v + low * vts;
+        char* yp = static_cast<char*>(r.out) + low * apart + (h * r.vd + col0) * eo;
         // the first chunk
-        if constexpr (ODD) {
+        const int some = min(left, C);
+        if (odd) {
             if constexpr (!STATE)
-                copy_odd(TK{}, Qs, q, tq.ts, kd, token, min(left, C));
-            copy_odd(TK{}, Ks, k, tk.ts, kd, token, min(left, C));
-            copy_odd(TV{}, Vs, v, tv.ts, width, token, min(left, C));
+                TK::copy_odd(Qs, qp, qts, some, kd, dir);
+            TK::copy_odd(Ks, kp, kts, some, kd, dir);
+            TV::copy_odd(Vs, vp, vts, some, width, dir);
         } else {
             if constexpr (!STATE)
-                copies(TK{}, Qs, q, tq.ts, kd, token, min(left, C)).share(qfrom, 0, 1);
-            copies(TK{}, Ks, k, tk.ts, kd, token, min(left, C)).share(kfrom, 0, 1);
-            copies(TV{}, Vs, v, tv.ts, width, token, min(left, C)).share(vfrom, 0, 1);
+                copies(TK{}, Qs, qp, qts, kd, some).share(qfrom, 0, 1);
+            copies(TK{}, Ks, kp, kts, kd, some).share(kfrom, 0, 1);
+            copies(TV{}, Vs, vp, vts, width, some).share(vfrom, 0, 1);
         }
+        arrived<0>();
         for (; left > 0; turn ^= 1) {
-            const int len = min(left, C), next = token + dir * C, more = min(left - C, C);
+            const int len = min(left, C), more = min(left - C, C);
             const uint32_t K = Ks + turn * W::kTileK, V = Vs + turn * W::kTileV;
             // the other buffers of k and v
             const uint32_t K2 = Ks + (turn ^ 1) * W::kTileK, V2 = Vs + (turn ^ 1) * W::kTileV;
@@ -561,8 +565,7 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
             // would take the registers of the products
             for (uint32_t* p : {&qrow, &prow, &pput})
                 asm volatile("" : "+v"(*p));
-            copies_done();
-            lds_barrier();  // so are all waves'; the last chunk's reads are done
+            lds_barrier();  // all waves' copies have arrived, and the last chunk's reads are done
             if (ragged || len != held) {
                 const int x = threadIdx.x;
                 if (x < C) {
@@ -581,16 +584,16 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                 lds_barrier();
             }
             // the next chunk's copies, asked for between the products (none: of no tokens)
-            const auto k2 = copies(TK{}, K2, k, tk.ts, kd, next, more);
-            const auto v2 = copies(TV{}, V2, v, tv.ts, width, next, more);
-            if constexpr (ODD) {
-                if (more > 0) {
-                    copy_odd(TK{}, K2, k, tk.ts, kd, next, more);
-                    copy_odd(TV{}, V2, v, tv.ts, width, next, more);
-                }
+            const int on = rev ? -more : C;  // tokens to its lowest
+            qp += on * qts, kp += on * kts, vp += on * vts;
+            const auto k2 = copies(TK{}, K2, kp, kts, kd, more);
+            const auto v2 = copies(TV{}, V2, vp, vts, width, more);
+            if (odd && more > 0) {
+                TK::copy_odd(K2, kp, kts, more, kd, dir);
+                TV::copy_odd(V2, vp, vts, more, width, dir);
             }
             auto ahead = [&](int part, int of) KDN_INLINE {
-                if (!ODD && more > 0) {
+                if (!odd && more > 0) {
                     k2.share(kfrom, part, of);
                     v2.share(vfrom, part, of);
                 }
@@ -629,12 +632,12 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                         fq[u % 2][s] = rows<IO, KD>(qrow, 16 * (u / NG), u % NG * GS + s);
                 };
                 read(0);
-                float far = 1.f;
                 f32x4 p;
 #pragma unroll
                 for (int u = 0; u < NT * NG; ++u) {
                     const int it = u / NG, s0 = u % NG * GS;
-                    const bool mixed = it >= jt && (NT == 4 || it == wave >> 1);
+                    // (C = 32: two waves form a block each)
+                    const bool mixed = NT == 4 || it == wave >> 1;
                     if (u + 1 < NT * NG)
                         read(u + 1);
                     ahead(u, NT * NG);
@@ -655,15 +658,10 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                     if (mixed && s0 + GS == KS) {
                         typedef IO Four __attribute__((ext_vector_type(4)));
                         Four out;
-                        if (it == jt) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)  // a choice, not a product: k may be infinite
-                                out[e] = from_f32<IO>(c >= 4 * g + e ? p[e] * on[e] : 0.f);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                out[e] = from_f32<IO>(p[e] * (below[e] * far));
-                            far *= g16;
+                        for (int e = 0; e < 4; ++e) {  // a choice, not a product with zero: k may be infinite
+                            const bool before = it > jt || (it == jt && c >= 4 * g + e);
+                            out[e] = from_f32<IO>(before ? p[e] * pdecay[NT == 4 ? it : 0][e] : 0.f);
                         }
                         lds_write(LP::further(pput, 16 * it, 0), out);
                     }
@@ -677,12 +675,10 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
             }
             if constexpr (!STATE) {
                 lds_barrier();  // Ps is whole, q is read
-                if constexpr (ODD) {
-                    if (more > 0)
-                        copy_odd(TK{}, Qs, q, tq.ts, kd, next, more);
-                }
+                if (odd && more > 0)
+                    TK::copy_odd(Qs, qp, qts, more, kd, dir);
             }
-            const auto q2 = copies(TK{}, Qs, q, tq.ts, kd, next, more);
+            const auto q2 = copies(TK{}, Qs, qp, qts, kd, more);
             // v's decayed values, in two parts where they are rounded
             frag hi[CS], lo[BF ? CS : 1];
             f32x4 none = zero4();  // zero times v: what is not finite shows
@@ -693,7 +689,7 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                 for (int e = 0; e < FE / 4; ++e)
                     weight[e] = lds_read<f32x4>(Ws + 4 * (s * O::K + FE * g + 4 * e));
                 O::mma(none, frag{}, fv[s]);
-                if (!STATE && !ODD && more > 0)
+                if (!STATE && !odd && more > 0)
                     q2.share(qfrom, s, CS);
 #pragma unroll
                 for (int e = 0; e < FE; ++e) {
@@ -753,10 +749,6 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                         }
                     }
                 }
-                if (!BF || r.out_f32)
-                    store(acc, token, len, 0.f);
-                else
-                    store(acc, token, len, IO{});
             }
             const uint32_t kc = kcol + turn * W::kTileK;
             frag fk[2][CS];
@@ -780,7 +772,13 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                         O::mma(X[t], fk[t % 2][s], lo[s]);
                 }
             }
-            token += dir * C;
+            if constexpr (!STATE) {
+                store(acc, yp, len);
+                yp += (rev ? -more : C) * apart;
+                arrived<NT>();  // all but the stores, which follow the copies
+            } else {
+                arrived<0>();
+            }
             left -= len;
         }
     };
@@ -925,16 +923,19 @@ void launch_walk(const LinArgs& a, int roles, hipStream_t stream)
     const int slices = (a.role[0].vd + kCols - 1) / kCols;
     const unsigned units = ((unsigned)a.B * a.H * a.S + 7) / 8 * 8;
     const dim3 grid(units * slices, roles);
-    if constexpr (sizeof(IO) == 2) {
-        bool odd = false;
-        for (int i = 0; i < roles; ++i)
-            odd = odd || !in_words(a.role[i].q) || !in_words(a.role[i].k) || !in_words(a.role[i].v);
-        if (odd) {
-            linattn_kernel<IO, KD, C, STATE, true><<<grid, kThreads, 0, stream>>>(a);
-            return;
-        }
+    constexpr int VE = 16 / sizeof(IO);
+    LinArgs b = a;
+    bool edge = a.role[0].kd % VE || a.role[0].vd % VE;
+    for (int i = 0; i < roles; ++i) {
+        if (sizeof(IO) == 2 && !(in_words(a.role[i].q) && in_words(a.role[i].k) && in_words(a.role[i].v)))
+            b.odd = true;
+        if (reinterpret_cast<uintptr_t>(a.role[i].out) & 3)
+            edge = true;
     }
-    linattn_kernel<IO, KD, C, STATE, false><<<grid, kThreads, 0, stream>>>(a);
+    if (edge || b.odd)
+        linattn_kernel<IO, KD, C, STATE, true><<<grid, kThreads, 0, stream>>>(b);
+    else
+        linattn_kernel<IO, KD, C, STATE, false><<<grid, kThreads, 0, stream>>>(b);
 }
 
 template <typename IO>
