@@ -45,7 +45,8 @@ struct LinRole {
     bool out_f32;
     const float* X0;  // nullable; element (i, j) of a state at i rs + j cs
     float* XT;        // nullable
-    float* seg;       // [B,S,H,kd,vd] states handed from segment to segment
+    float* seg;       // [B,S,H] states handed from segment to segment
+    int srs, scs;     // strides of an element in seg
     int kd, vd, rs, cs, rev;
     float of_p, of_x, of_u;
 };
@@ -57,6 +58,12 @@ struct LinArgs {
     int S, L;  // segments of each row, and their tokens
     bool odd;  // rows of some input begin in the middle of a word
     LinRole role[3];
+};
+
+// sums over the heads of a group
+struct LinSums {
+    const float* x[2];
+    void* y[2];
 };
 
 struct LinStepArgs {

@@ -801,7 +801,7 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
             if (span.first || (rev ? s + 1 >= a.S : s == 0))
                 state_in(r.X0 ? r.X0 + n : nullptr, r.rs, r.cs);
             else
-                state_in(handed(rev ? s + 1 : s - 1), r.vd, 1);
+                state_in(handed(rev ? s + 1 : s - 1), r.srs, r.scs);
             walk(span);
             if (span.last && r.XT)
                 state_out(r.XT + n, r.rs, r.cs);
@@ -837,25 +837,33 @@ __global__ __launch_bounds__(kThreads) void linattn_join_kernel(LinArgs a)
     }
 }
 
-// y [tokens, Hk, d] = the sum over each group's heads of x [tokens, H, d] (fp32)
-template <typename IO>
-__global__ __launch_bounds__(256) void linattn_group_kernel(LinArgs a, const float* x, IO* y, int G, int d)
+// y [tokens, Hk, d] = the sum over each group's heads of x [tokens, H, d] (fp32), of both
+// tensors; VE values a thread.  Bound by HBM, which x's fp32 keeps busy.
+template <typename IO, int VE>
+__global__ __launch_bounds__(256) void linattn_group_kernel(LinArgs a, LinSums sums, int G, int d)
 {
-    const int Hk = a.H / G;
-    const long long n = (long long)a.B * a.T * Hk * d;
+    const float* x = sums.x[blockIdx.y];
+    IO* y = static_cast<IO*>(sums.y[blockIdx.y]);
+    const int Hk = a.H / G, row = Hk * d;
+    const long long n = (long long)a.B * a.T * row / VE;
     const int end = a.cu ? a.cu[a.N] : 0;
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-        const long long token = i / (Hk * d);
-        const int at = (int)(i % (Hk * d)), hk = at / d, j = at % d;
+        const long long token = i * VE / row;
+        const int at = (int)(i * VE - token * row), hk = at / d, j = at % d;
+        float s[VE] = {};
         if (a.cu && token >= end) {
-            if (a.clear)
-                y[i] = IO(0.f);
-            continue;
+            if (!a.clear)
+                continue;
+        } else {
+            const float* p = x + (token * a.H + hk * G) * d + j;
+            for (int m = 0; m < G; ++m, p += d) {
+                const Raw<float, VE> r = load_raw<false, float, VE>(p);
+#pragma unroll
+                for (int e = 0; e < VE; ++e)
+                    s[e] += r.get(e);
+            }
         }
-        float s = 0.f;
-        for (int m = 0; m < G; ++m)
-            s += x[(token * a.H + hk * G + m) * d + j];
-        y[i] = from_f32<IO>(s);
+        store_raw<IO, VE>(y + i * VE, s);
     }
 }
 
@@ -908,6 +916,8 @@ __global__ __launch_bounds__(256) void linattn_step_kernel(LinStepArgs a)
 
 // ---- host ------------------------------------------------------------------------------
 
+int slices_of(int vd) { return (vd + kCols - 1) / kCols; }
+
 int padded(int kd) { return kd <= 32 ? 32 : kd <= 64 ? 64 : kd <= 128 ? 128 : 256; }
 
 // whether copies of words reach a tensor's rows
@@ -920,13 +930,16 @@ template <typename IO, int KD, bool STATE>
 void launch_walk(const LinArgs& a, int roles, hipStream_t stream)
 {
     constexpr int C = sizeof(IO) == 2 && KD <= 128 ? 64 : 32;
-    const int slices = (a.role[0].vd + kCols - 1) / kCols;
+    int slices = 0;
+    for (int i = 0; i < roles; ++i)
+        slices = slices > slices_of(a.role[i].vd) ? slices : slices_of(a.role[i].vd);
     const unsigned units = ((unsigned)a.B * a.H * a.S + 7) / 8 * 8;
     const dim3 grid(units * slices, roles);
     constexpr int VE = 16 / sizeof(IO);
     LinArgs b = a;
-    bool edge = a.role[0].kd % VE || a.role[0].vd % VE;
+    bool edge = false;
     for (int i = 0; i < roles; ++i) {
+        edge = edge || a.role[i].kd % VE || a.role[i].vd % VE;
         if (sizeof(IO) == 2 && !(in_words(a.role[i].q) && in_words(a.role[i].k) && in_words(a.role[i].v)))
             b.odd = true;
         if (reinterpret_cast<uintptr_t>(a.role[i].out) & 3)
@@ -938,49 +951,50 @@ void launch_walk(const LinArgs& a, int roles, hipStream_t stream)
         linattn_kernel<IO, KD, C, STATE, false><<<grid, kThreads, 0, stream>>>(b);
 }
 
-template <typename IO>
-void launch_walks(const LinArgs& a, int roles, hipStream_t stream)
+template <typename IO, bool STATE>
+void launch_roles(const LinArgs& a, int roles, hipStream_t stream)
 {
     const int kd = padded(a.role[0].kd);
-    auto run = [&](auto state) {
-        constexpr bool S = decltype(state)::value;
-        if (kd == 32)
-            launch_walk<IO, 32, S>(a, roles, stream);
-        else if (kd == 64)
-            launch_walk<IO, 64, S>(a, roles, stream);
-        else if (kd == 128)
-            launch_walk<IO, 128, S>(a, roles, stream);
-        else
-            launch_walk<IO, 256, S>(a, roles, stream);
-    };
-    if (a.S > 1) {
-        run(std::true_type{});
-        const size_t dense = (size_t)a.role[0].kd * a.role[0].vd;
-        linattn_join_kernel<<<dim3((unsigned)((dense + kThreads - 1) / kThreads), a.B * a.H, roles), kThreads, 0,
-                              stream>>>(a);
-    }
-    run(std::false_type{});
+    if (kd == 32)
+        launch_walk<IO, 32, STATE>(a, roles, stream);
+    else if (kd == 64)
+        launch_walk<IO, 64, STATE>(a, roles, stream);
+    else if (kd == 128)
+        launch_walk<IO, 128, STATE>(a, roles, stream);
+    else
+        launch_walk<IO, 256, STATE>(a, roles, stream);
 }
 
-// Tokens of a segment: a multiple of 64
+// the states that segments hand on
+template <typename IO>
+void launch_states(const LinArgs& a, int roles, hipStream_t stream)
+{
+    launch_roles<IO, true>(a, roles, stream);
+    const size_t dense = (size_t)a.role[0].kd * a.role[0].vd;
+    linattn_join_kernel<<<dim3((unsigned)((dense + kThreads - 1) / kThreads), a.B * a.H, roles), kThreads, 0, stream>>>(a);
+}
+
+// Segments of a row and the tokens of one, a multiple of 64: one where the walks fill the
+// chip, else two workgroups a compute unit.
 int segments(int B, int T, int H, int slices, int& L)
 {
     const long long groups = (long long)B * H * slices;
-    const long long want = (256 + groups - 1) / groups, most = T / 512;
+    const long long want = groups >= 256 ? 1 : (512 + groups - 1) / groups, most = T / 512;
     const long long S = want < most ? want : most;
     L = S <= 1 ? (T > 0 ? T : 1) : (int)(((T + S - 1) / S + 63) / 64 * 64);
     return T > 0 ? (T + L - 1) / L : 1;
 }
-
-int slices_of(int vd) { return (vd + kCols - 1) / kCols; }
 
 size_t aligned16(size_t n) { return (n + 15) / 16 * 16; }
 
 template <typename IO>
 hipError_t linattn_fwd(const LinArgs& a, hipStream_t stream)
 {
-    if (a.T > 0)
-        launch_walks<IO>(a, 1, stream);
+    if (a.T > 0) {
+        if (a.S > 1)
+            launch_states<IO>(a, 1, stream);
+        launch_roles<IO, false>(a, 1, stream);
+    }
     return hipGetLastError();
 }
 
@@ -1003,7 +1017,7 @@ size_t linattn_bwd_workspace_bytes(int B, int T, int H, int Hk, int dk, int dv)
 {
     int S, L;
     const size_t seg = bwd_segments_bytes(B, T, H, dk, dv, S, L);
-    return 3 * seg + (Hk != H ? 2 * aligned16(sizeof(float) * B * T * H * dk) : 0);
+    return 2 * seg + (Hk != H ? 2 * aligned16(sizeof(float) * B * T * H * dk) : 0);
 }
 
 // the states of sequences without tokens
@@ -1021,7 +1035,7 @@ hipError_t launch_linattn_fwd(const LinCall& c, bool bf, hipStream_t stream)
     LinRole& r = a.role[0];
     r.q = c.q, r.k = c.k, r.v = c.v;
     r.out = c.o, r.X0 = c.S0, r.XT = c.S_T, r.seg = static_cast<float*>(c.ws);
-    r.kd = c.dk, r.vd = c.dv, r.rs = c.dv, r.cs = 1;
+    r.kd = c.dk, r.vd = c.dv, r.rs = r.srs = c.dv, r.cs = r.scs = 1;
     r.of_p = r.of_x = c.scale, r.of_u = 1.f;
     empty_states(a, c.S0, c.S_T, stream);
     return bf ? linattn_fwd<bf16>(a, stream) : linattn_fwd<float>(a, stream);
@@ -1036,40 +1050,52 @@ static hipError_t linattn_bwd(const LinCall& c, hipStream_t stream)
     const size_t seg = bwd_segments_bytes(c.B, c.T, c.H, c.dk, c.dv, a.S, a.L) / sizeof(float);
     float* ws = static_cast<float*>(c.ws);
     const size_t whole = aligned16(sizeof(float) * c.B * c.T * c.H * c.dk) / sizeof(float);
-    float* gq = ws + 3 * seg;
+    float* gq = ws + 2 * seg;
     float* gk = gq + whole;
 
     LinRole dq{}, dk{}, dv{};
     dq.q = c.d_o, dq.k = c.v, dq.v = c.k;
     dq.out = G > 1 ? gq : c.dq, dq.out_f32 = G > 1;
-    dq.X0 = c.S0, dq.kd = c.dv, dq.vd = c.dk, dq.rs = 1, dq.cs = c.dv;
+    dq.X0 = c.S0, dq.kd = c.dv, dq.vd = c.dk, dq.rs = dq.srs = 1, dq.cs = dq.scs = c.dv;
     dq.of_p = dq.of_x = c.scale, dq.of_u = 1.f, dq.seg = ws;
     dk.q = c.v, dk.k = c.d_o, dk.v = c.q;
     dk.out = G > 1 ? gk : c.dk_out, dk.out_f32 = G > 1;
-    dk.X0 = c.dS_T, dk.kd = c.dv, dk.vd = c.dk, dk.rs = 1, dk.cs = c.dv;
+    dk.X0 = c.dS_T, dk.kd = c.dv, dk.vd = c.dk, dk.rs = dk.srs = 1, dk.cs = dk.scs = c.dv;
     dk.of_p = dk.of_u = c.scale, dk.of_x = 1.f, dk.rev = 1, dk.seg = ws + seg;
     dv.q = c.k, dv.k = c.q, dv.v = c.d_o;
     dv.out = c.dv_out, dv.X0 = c.dS_T, dv.XT = c.dS0;
-    dv.kd = c.dk, dv.vd = c.dv, dv.rs = c.dv, dv.cs = 1;
-    dv.of_p = dv.of_u = c.scale, dv.of_x = 1.f, dv.rev = 1, dv.seg = ws + 2 * seg;
+    dv.kd = c.dk, dv.vd = c.dv, dv.rs = dv.srs = c.dv, dv.cs = dv.scs = 1;
+    dv.of_p = dv.of_u = c.scale, dv.of_x = 1.f, dv.rev = 1, dv.seg = ws + seg;
 
     a.role[0] = dv;
     empty_states(a, c.dS_T, c.dS0, stream);
     if (c.T == 0)
         return hipGetLastError();
-    if (c.dk == c.dv) {
+    if (a.S > 1) {
+        // the forward's states, and those that dv and (turned) dk start from
+        LinRole& fwd = a.role[1];
+        fwd = dv;
+        fwd.q = c.q, fwd.k = c.k, fwd.v = c.v;
+        fwd.X0 = c.S0, fwd.of_u = 1.f, fwd.rev = 0, fwd.seg = ws;
+        launch_states<IO>(a, 2, stream);
+    }
+    if (padded(c.dk) == padded(c.dv)) {
         a.role[1] = dq, a.role[2] = dk;
-        launch_walks<IO>(a, 3, stream);
+        launch_roles<IO, false>(a, 3, stream);
     } else {
-        launch_walks<IO>(a, 1, stream);
+        launch_roles<IO, false>(a, 1, stream);
         a.role[0] = dq, a.role[1] = dk;
-        launch_walks<IO>(a, 2, stream);
+        launch_roles<IO, false>(a, 2, stream);
     }
     if (G > 1) {
-        const long long n = (long long)c.B * c.T * c.Hk * c.dk;
-        const unsigned groups = (unsigned)((n + 255) / 256 < 8192 ? (n + 255) / 256 : 8192);
-        linattn_group_kernel<IO><<<groups, 256, 0, stream>>>(a, gq, static_cast<IO*>(c.dq), G, c.dk);
-        linattn_group_kernel<IO><<<groups, 256, 0, stream>>>(a, gk, static_cast<IO*>(c.dk_out), G, c.dk);
+        const LinSums sums{{gq, gk}, {c.dq, c.dk_out}};
+        const bool four = c.dk % 4 == 0;
+        const long long n = (long long)c.B * c.T * c.Hk * c.dk / (four ? 4 : 1), groups = (n + 255) / 256;
+        const dim3 grid((unsigned)(groups < 4096 ? groups : 4096), 2);
+        if (four)
+            linattn_group_kernel<IO, 4><<<grid, 256, 0, stream>>>(a, sums, G, c.dk);
+        else
+            linattn_group_kernel<IO, 1><<<grid, 256, 0, stream>>>(a, sums, G, c.dk);
     }
     return hipGetLastError();
 }
