@@ -46,6 +46,7 @@ struct LinRole {
     const float* X0;  // nullable; element (i, j) of a state at i rs + j cs
     float* XT;        // nullable
     float* seg;       // [B,S,H] states handed from segment to segment
+    int4* spans;      // [B,S] the tokens they are of, and the sequence if it begins there (or -1)
     int srs, scs;     // strides of an element in seg
     int kd, vd, rs, cs, rev;
     float of_p, of_x, of_u;
@@ -56,6 +57,7 @@ struct LinArgs {
     const float* decay;
     bool clear;
     int S, L;  // segments of each row, and their tokens
+    int roles, slices;  // walks of a launch, and the most slices that one has
     bool odd;  // rows of some input begin in the middle of a word
     LinRole role[3];
 };

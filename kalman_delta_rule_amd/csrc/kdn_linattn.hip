@@ -408,11 +408,12 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
     const uint32_t Ks = Qs + (STATE ? 0 : W::kTileK), Vs = Ks + 2 * W::kTileK, Ps = Vs + 2 * W::kTileV,
                    Ws = Ps + (STATE ? 0 : W::kTileP);  // of_u g^(len - 1 - j + rev) of each token of a chunk
 
-    const LinRole& r = a.role[blockIdx.y];
-    // slices of one head follow one another on one XCD (workgroups go round the eight)
-    const int slices = (r.vd + kCols - 1) / kCols;
-    const int index = blockIdx.x / 8, unit = index / slices * 8 + (int)(blockIdx.x & 7), slice = index % slices;
-    if (unit >= a.B * a.H * a.S)
+    // the walks over one head's tokens, and their slices, follow one another on one XCD
+    // (workgroups go round the eight) and find each other's inputs in its cache
+    const int index = blockIdx.x / 8, each = a.slices * a.roles, unit = index / each * 8 + (int)(blockIdx.x & 7);
+    const LinRole& r = a.role[index % each / a.slices];
+    const int slice = index % a.slices;
+    if (unit >= a.B * a.H * a.S || slice * kCols >= r.vd)
         return;
     const int h = unit % a.H, s = unit / a.H % a.S, b = unit / a.H / a.S;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -785,7 +786,10 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
 
     if constexpr (STATE) {
         Span span;
-        if (handed_on(a, b, s, rev, span)) {
+        const bool some = handed_on(a, b, s, rev, span);
+        if (h == 0 && slice == 0 && threadIdx.x == 0)
+            r.spans[b * a.S + s] = int4{some ? span.to - span.from : 0, span.first ? span.n : -1, 0, 0};
+        if (some) {
             state_in(nullptr, 0, 0);
             walk(span);
             state_out(handed(s), r.vd, 1);
@@ -816,24 +820,42 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
 }
 
 // The states handed on, one segment after another: what a segment adds, and what it got,
-// decayed over its tokens.  A thread has one element of one head's state.
+// decayed over its tokens.  A thread has one element of one head's state; what the next
+// segments add is loaded ahead.
 __global__ __launch_bounds__(kThreads) void linattn_join_kernel(LinArgs a)
 {
     const LinRole& r = a.role[blockIdx.z];
     const int h = blockIdx.y % a.H, b = blockIdx.y / a.H;
     const size_t dense = (size_t)r.kd * r.vd, i = (size_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= dense)
+        return;
     const Decay decay{log((double)a.decay[h])};
-    float x = 0.f;
-    for (int m = 0; m + 1 < a.S; ++m) {
-        const int s = r.rev ? a.S - 1 - m : m;
-        Span span;
-        if (!handed_on(a, b, s, r.rev, span) || i >= dense)
-            continue;
-        if (span.first)
-            x = r.X0 ? r.X0[((size_t)span.n * a.H + h) * dense + (i / r.vd) * r.rs + (i % r.vd) * r.cs] : 0.f;
-        float* p = r.seg + (((size_t)b * a.S + s) * a.H + h) * dense + i;
-        x = fmaf(decay.power(span.to - span.from), x, *p);
-        *p = x;
+    const size_t far = (size_t)a.H * dense;  // to the next segment's state
+    float* seg = r.seg + ((size_t)b * a.S * a.H + h) * dense + i;
+    const int n = a.S - 1;  // segments that hand on
+    auto at = [&](int m) { return r.rev ? a.S - 1 - m : m; };
+    constexpr int AHEAD = 8;
+    float next[AHEAD], x = 0.f;
+#pragma unroll
+    for (int m = 0; m < AHEAD; ++m)
+        next[m] = m < n ? seg[at(m) * far] : 0.f;
+    for (int m0 = 0; m0 < n; m0 += AHEAD) {
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const int m = m0 + k;
+            const float added = next[k];
+            if (m + AHEAD < n)
+                next[k] = seg[at(m + AHEAD) * far];
+            if (m >= n)
+                break;
+            const int4 span = r.spans[b * a.S + at(m)];  // tokens (0: nothing is handed on), sequence that begins
+            if (span.x == 0)
+                continue;
+            if (span.y >= 0)
+                x = r.X0 ? r.X0[((size_t)span.y * a.H + h) * dense + (i / r.vd) * r.rs + (i % r.vd) * r.cs] : 0.f;
+            x = fmaf(decay.power(span.x), x, added);
+            seg[at(m) * far] = x;
+        }
     }
 }
 
@@ -869,52 +891,70 @@ __global__ __launch_bounds__(256) void linattn_group_kernel(LinArgs a, LinSums s
 
 // ---- single tokens -------------------------------------------------------------------
 
-// One token: a workgroup has one head and 64 columns of the state, a thread four columns
-// of every 16th row; rows are joined through LDS.
-template <typename IO>
+// One token.  A workgroup has a head's state rows by 64 columns, a thread VE adjacent
+// columns of every 16th (64th) row: bound by HBM, the state being read and written once.
+// Rows are taken ROWS at a time, so that many loads are on their way; the rows' shares of o
+// are joined through LDS.
+template <typename IO, int VE, int ROWS>
 __global__ __launch_bounds__(256) void linattn_step_kernel(LinStepArgs a)
 {
-    __shared__ float part[16][kCols];
+    constexpr int LANES = kCols / VE, STEP = 256 / LANES;
+    __shared__ float part[STEP][kCols];
     const int slices = (a.dv + kCols - 1) / kCols;
     const int slice = blockIdx.x % slices, unit = blockIdx.x / slices, h = unit % a.H, b = unit / a.H;
-    const int rg = threadIdx.x >> 4, c = 4 * (threadIdx.x & 15), col = slice * kCols + c, n = min(a.dv - col, 4);
+    const int rg = threadIdx.x / LANES, c = VE * (threadIdx.x % LANES), col = slice * kCols + c;
     const IO* q = static_cast<const IO*>(a.q) + (long long)b * a.qs + (long long)(h / a.G) * a.qh;
     const IO* k = static_cast<const IO*>(a.k) + (long long)b * a.ks + (long long)(h / a.G) * a.kh;
     const IO* v = static_cast<const IO*>(a.v) + (long long)b * a.vs + (long long)h * a.vh;
-    float* S = a.S + (size_t)unit * a.dk * a.dv;
+    float* S = a.S + (size_t)unit * a.dk * a.dv + col;
     const float g = a.decay[h];
-    float vv[4], o[4] = {0.f, 0.f, 0.f, 0.f};
+    float vv[VE], o[VE] = {};
+    if (col < a.dv) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        vv[e] = e < n ? to_f32(v[col + e]) : 0.f;
-    if (n > 0) {
-        for (int i = rg; i < a.dk; i += 16) {
-            const float kk = to_f32(k[i]), qq = to_f32(q[i]);
-            float* p = S + (size_t)i * a.dv + col;
+        for (int e = 0; e < VE; ++e)
+            vv[e] = to_f32(v[col + e]);
+        for (int i0 = rg; i0 < a.dk; i0 += STEP * ROWS) {
+            Raw<float, VE> x[ROWS];
+            float kk[ROWS], qq[ROWS];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e < n) {
-                    const float x = fmaf(g, p[e], kk * vv[e]);
-                    p[e] = x;
-                    o[e] = fmaf(qq, x, o[e]);
+            for (int m = 0; m < ROWS; ++m) {
+                const int i = min(i0 + m * STEP, a.dk - 1);
+                x[m] = load_raw<false, float, VE>(S + (size_t)i * a.dv);
+                kk[m] = to_f32(k[i]);
+                qq[m] = to_f32(q[i]);
+            }
+#pragma unroll
+            for (int m = 0; m < ROWS; ++m) {
+                const int i = i0 + m * STEP;
+                if (i >= a.dk)
+                    break;
+                float y[VE];
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    y[e] = fmaf(g, x[m].get(e), kk[m] * vv[e]);
+                    o[e] = fmaf(qq[m], y[e], o[e]);
                 }
+                store_raw<float, VE>(S + (size_t)i * a.dv, y);
+            }
         }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < VE; ++e)
         part[rg][c + e] = o[e];
     __syncthreads();
     const int out = slice * kCols + threadIdx.x;
     if (threadIdx.x < kCols && out < a.dv) {
         float s = 0.f;
 #pragma unroll
-        for (int m = 0; m < 16; ++m)
+        for (int m = 0; m < STEP; ++m)
             s += part[m][threadIdx.x];
         static_cast<IO*>(a.o)[(size_t)unit * a.dv + out] = from_f32<IO>(s * a.scale);
     }
 }
 
 // ---- host ------------------------------------------------------------------------------
+
+size_t aligned16(size_t n) { return (n + 15) / 16 * 16; }
 
 int slices_of(int vd) { return (vd + kCols - 1) / kCols; }
 
@@ -930,21 +970,19 @@ template <typename IO, int KD, bool STATE>
 void launch_walk(const LinArgs& a, int roles, hipStream_t stream)
 {
     constexpr int C = sizeof(IO) == 2 && KD <= 128 ? 64 : 32;
-    int slices = 0;
-    for (int i = 0; i < roles; ++i)
-        slices = slices > slices_of(a.role[i].vd) ? slices : slices_of(a.role[i].vd);
-    const unsigned units = ((unsigned)a.B * a.H * a.S + 7) / 8 * 8;
-    const dim3 grid(units * slices, roles);
     constexpr int VE = 16 / sizeof(IO);
     LinArgs b = a;
+    b.roles = roles;
     bool edge = false;
     for (int i = 0; i < roles; ++i) {
+        b.slices = b.slices > slices_of(a.role[i].vd) ? b.slices : slices_of(a.role[i].vd);
         edge = edge || a.role[i].kd % VE || a.role[i].vd % VE;
         if (sizeof(IO) == 2 && !(in_words(a.role[i].q) && in_words(a.role[i].k) && in_words(a.role[i].v)))
             b.odd = true;
         if (reinterpret_cast<uintptr_t>(a.role[i].out) & 3)
             edge = true;
     }
+    const unsigned grid = ((unsigned)a.B * a.H * a.S + 7) / 8 * 8 * b.slices * roles;
     if (edge || b.odd)
         linattn_kernel<IO, KD, C, STATE, true><<<grid, kThreads, 0, stream>>>(b);
     else
@@ -975,17 +1013,27 @@ void launch_states(const LinArgs& a, int roles, hipStream_t stream)
 }
 
 // Segments of a row and the tokens of one, a multiple of 64: one where the walks fill the
-// chip, else two workgroups a compute unit.
+// chip, else as many as let two workgroups stay on a compute unit, of 128 tokens at least.
 int segments(int B, int T, int H, int slices, int& L)
 {
     const long long groups = (long long)B * H * slices;
-    const long long want = groups >= 256 ? 1 : (512 + groups - 1) / groups, most = T / 512;
+    const long long want = groups >= 256 ? 1 : 512 / groups, most = T < 512 ? 1 : T / 128;
     const long long S = want < most ? want : most;
     L = S <= 1 ? (T > 0 ? T : 1) : (int)(((T + S - 1) / S + 63) / 64 * 64);
     return T > 0 ? (T + L - 1) / L : 1;
 }
 
-size_t aligned16(size_t n) { return (n + 15) / 16 * 16; }
+// workspace of a walk's handed states: they, and which tokens they are of
+size_t handed_bytes(int B, int S, int H, int dk, int dv)
+{
+    return S > 1 ? aligned16(sizeof(float) * B * S * H * dk * dv) + sizeof(int4) * B * S : 0;
+}
+
+void set_handed(LinRole& r, void* ws, int B, int S, int H)
+{
+    r.seg = static_cast<float*>(ws);
+    r.spans = reinterpret_cast<int4*>(static_cast<char*>(ws) + aligned16(sizeof(float) * B * S * H * r.kd * r.vd));
+}
 
 template <typename IO>
 hipError_t linattn_fwd(const LinArgs& a, hipStream_t stream)
@@ -1004,13 +1052,13 @@ size_t linattn_fwd_workspace_bytes(int B, int T, int H, int dk, int dv)
 {
     int L;
     const int S = segments(B, T, H, slices_of(dv), L);
-    return S > 1 ? sizeof(float) * B * S * H * dk * dv : 0;
+    return handed_bytes(B, S, H, dk, dv);
 }
 
 static size_t bwd_segments_bytes(int B, int T, int H, int dk, int dv, int& S, int& L)
 {
     S = segments(B, T, H, slices_of(dk) * 2 + slices_of(dv), L);
-    return S > 1 ? sizeof(float) * B * S * H * dk * dv : 0;
+    return handed_bytes(B, S, H, dk, dv);
 }
 
 size_t linattn_bwd_workspace_bytes(int B, int T, int H, int Hk, int dk, int dv)
@@ -1034,9 +1082,10 @@ hipError_t launch_linattn_fwd(const LinCall& c, bool bf, hipStream_t stream)
     a.S = segments(c.B, c.T, c.H, slices_of(c.dv), a.L);
     LinRole& r = a.role[0];
     r.q = c.q, r.k = c.k, r.v = c.v;
-    r.out = c.o, r.X0 = c.S0, r.XT = c.S_T, r.seg = static_cast<float*>(c.ws);
+    r.out = c.o, r.X0 = c.S0, r.XT = c.S_T;
     r.kd = c.dk, r.vd = c.dv, r.rs = r.srs = c.dv, r.cs = r.scs = 1;
     r.of_p = r.of_x = c.scale, r.of_u = 1.f;
+    set_handed(r, c.ws, a.B, a.S, a.H);
     empty_states(a, c.S0, c.S_T, stream);
     return bf ? linattn_fwd<bf16>(a, stream) : linattn_fwd<float>(a, stream);
 }
@@ -1047,25 +1096,28 @@ static hipError_t linattn_bwd(const LinCall& c, hipStream_t stream)
     LinArgs a{};
     a.B = c.B, a.T = c.T, a.H = c.H, a.N = c.N, a.cu = c.cu, a.decay = c.decay, a.clear = c.clear;
     const int G = c.H / c.Hk;
-    const size_t seg = bwd_segments_bytes(c.B, c.T, c.H, c.dk, c.dv, a.S, a.L) / sizeof(float);
-    float* ws = static_cast<float*>(c.ws);
+    const size_t seg = bwd_segments_bytes(c.B, c.T, c.H, c.dk, c.dv, a.S, a.L);
+    char* ws = static_cast<char*>(c.ws);
     const size_t whole = aligned16(sizeof(float) * c.B * c.T * c.H * c.dk) / sizeof(float);
-    float* gq = ws + 2 * seg;
+    float* gq = reinterpret_cast<float*>(ws + 2 * seg);
     float* gk = gq + whole;
 
     LinRole dq{}, dk{}, dv{};
     dq.q = c.d_o, dq.k = c.v, dq.v = c.k;
     dq.out = G > 1 ? gq : c.dq, dq.out_f32 = G > 1;
     dq.X0 = c.S0, dq.kd = c.dv, dq.vd = c.dk, dq.rs = dq.srs = 1, dq.cs = dq.scs = c.dv;
-    dq.of_p = dq.of_x = c.scale, dq.of_u = 1.f, dq.seg = ws;
+    dq.of_p = dq.of_x = c.scale, dq.of_u = 1.f;
+    set_handed(dq, ws, a.B, a.S, a.H);
     dk.q = c.v, dk.k = c.d_o, dk.v = c.q;
     dk.out = G > 1 ? gk : c.dk_out, dk.out_f32 = G > 1;
     dk.X0 = c.dS_T, dk.kd = c.dv, dk.vd = c.dk, dk.rs = dk.srs = 1, dk.cs = dk.scs = c.dv;
-    dk.of_p = dk.of_u = c.scale, dk.of_x = 1.f, dk.rev = 1, dk.seg = ws + seg;
+    dk.of_p = dk.of_u = c.scale, dk.of_x = 1.f, dk.rev = 1;
+    set_handed(dk, ws + seg, a.B, a.S, a.H);
     dv.q = c.k, dv.k = c.q, dv.v = c.d_o;
     dv.out = c.dv_out, dv.X0 = c.dS_T, dv.XT = c.dS0;
     dv.kd = c.dk, dv.vd = c.dv, dv.rs = dv.srs = c.dv, dv.cs = dv.scs = 1;
-    dv.of_p = dv.of_u = c.scale, dv.of_x = 1.f, dv.rev = 1, dv.seg = ws + seg;
+    dv.of_p = dv.of_u = c.scale, dv.of_x = 1.f, dv.rev = 1;
+    set_handed(dv, ws + seg, a.B, a.S, a.H);
 
     a.role[0] = dv;
     empty_states(a, c.dS_T, c.dS0, stream);
@@ -1076,7 +1128,8 @@ static hipError_t linattn_bwd(const LinCall& c, hipStream_t stream)
         LinRole& fwd = a.role[1];
         fwd = dv;
         fwd.q = c.q, fwd.k = c.k, fwd.v = c.v;
-        fwd.X0 = c.S0, fwd.of_u = 1.f, fwd.rev = 0, fwd.seg = ws;
+        fwd.X0 = c.S0, fwd.of_u = 1.f, fwd.rev = 0;
+        set_handed(fwd, ws, a.B, a.S, a.H);
         launch_states<IO>(a, 2, stream);
     }
     if (padded(c.dk) == padded(c.dv)) {
@@ -1108,10 +1161,14 @@ hipError_t launch_linattn_bwd(const LinCall& c, bool bf, hipStream_t stream)
 hipError_t launch_linattn_step(const LinStepArgs& a, bool bf, hipStream_t stream)
 {
     const unsigned groups = (unsigned)a.B * a.H * slices_of(a.dv);
-    if (bf)
-        linattn_step_kernel<bf16><<<groups, 256, 0, stream>>>(a);
-    else
-        linattn_step_kernel<float><<<groups, 256, 0, stream>>>(a);
+    auto run = [&](auto io) {
+        typedef decltype(io) IO;
+        if (a.dv % 4 == 0)
+            linattn_step_kernel<IO, 4, 8><<<groups, 256, 0, stream>>>(a);
+        else
+            linattn_step_kernel<IO, 1, 8><<<groups, 256, 0, stream>>>(a);
+    };
+    bf ? run(bf16{}) : run(0.f);
     return hipGetLastError();
 }
 
