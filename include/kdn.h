@@ -641,6 +641,71 @@ kdn_status kdn_linattn_step(int B, int H, int Hk, int dk, int dv, int io_dtype, 
                             const void* v, long long v_stride, long long v_head_stride,
                             const float* decay, float* state, void* o, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Group norm with an activation, channels last: x [N,S,C], N samples of S
+ * positions, G groups of C / G adjacent channels.  Over the positions and a
+ * group's channels of a sample,
+ *   mean = sum(x) / n, rstd = 1 / sqrt(sum((x - mean)^2) / n + eps),  n = S C / G
+ *   z = (x - mean) rstd weight + bias,   y = z, or z sigmoid(z) (KDN_ACT_SILU)
+ * S = 1 with a head's outputs as a group normalises each head of a token.
+ *   x      rows of C, x_stride apart (N S of them), io dtype;  y [N,S,C] io dtype
+ *   weight, bias [C] fp32, each nullable (ones, zeros)
+ *   mean, rstd   [N,G] fp32, written; each nullable
+ *   eps    finite, >= 0;  N G below 2^24
+ *   workspace    kdn_group_norm_fwd_workspace_size bytes (0 unless a group is
+ *          too large for one workgroup)
+ */
+size_t kdn_group_norm_fwd_workspace_size(int N, int S, int C, int G);
+kdn_status kdn_group_norm_fwd(int N, int S, int C, int G, int io_dtype, int activation, float eps,
+                              const void* x, long long x_stride, const float* weight,
+                              const float* bias, void* y, float* mean, float* rstd, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * Backward of kdn_group_norm_fwd with its mean and rstd, weight and bias (which
+ * the activation's slope needs).  With g = dy, or dy times the slope at z, and
+ * xh = (x - mean) rstd:
+ *   dx = rstd (g w - mean(g w) - xh mean(g w xh)), means over the group
+ *   dweight = sum of g xh, dbias = sum of g, over samples and positions
+ *   dy, dx [N,S,C] io dtype; dweight, dbias [C] fp32, each nullable
+ */
+size_t kdn_group_norm_bwd_workspace_size(int N, int S, int C, int G);
+kdn_status kdn_group_norm_bwd(int N, int S, int C, int G, int io_dtype, int activation,
+                              const void* dy, const void* x, long long x_stride, const float* mean,
+                              const float* rstd, const float* weight, const float* bias, void* dx,
+                              float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/*
+ * Dropout from a counter-based generator, with the residual stream added:
+ *   y = (kept ? x / (1 - p') : 0) + residual
+ * Element i of [rows,D] is kept where its 16 random bits are at least p' 2^16,
+ * p' being p (0 <= p <= 1) rounded to a multiple of 2^-16, ties to even.  The
+ * bits are word (i % 8) / 2, half i % 2 (0: the low one) of Philox4x32-10
+ * (Salmon, Moraes, Dror, Shaw 2011) for the counter {i / 8 (64 bits), offset
+ * (64 bits)} under the key `seed`, low words first: they depend on nothing but
+ * seed, offset and i.  Calls that are to be independent take offsets (or
+ * seeds) of their own.
+ *   seed_offset  nullable; device, int64 {seed, offset}, read by the kernel in
+ *        place of the two arguments: a captured graph that is replayed takes
+ *        what stands there then
+ *   x    rows of D, x_stride apart, io dtype; residual [rows,D] io dtype,
+ *        nullable; y [rows,D] io dtype
+ * What is dropped may be infinite or NaN: it leaves no trace.
+ */
+kdn_status kdn_dropout_fwd(int rows, int D, int io_dtype, double p, unsigned long long seed,
+                           unsigned long long offset, const long long* seed_offset, const void* x,
+                           long long x_stride, const void* residual, void* y, void* stream);
+
+/*
+ * Backward of kdn_dropout_fwd by x, for the same p, seed and offset: dx = kept ?
+ * dy / (1 - p') : 0.  (The residual's gradient is dy.)  dy, dx [rows,D].
+ */
+kdn_status kdn_dropout_bwd(int rows, int D, int io_dtype, double p, unsigned long long seed,
+                           unsigned long long offset, const long long* seed_offset, const void* dy,
+                           void* dx, void* stream);
+
 const char* kdn_status_string(int status);
 const char* kdn_last_error_message(void);
 

@@ -128,6 +128,19 @@ def lib():
                                   + [fp, vp, sz, vp])
     L.kdn_linattn_step.restype = i
     L.kdn_linattn_step.argtypes = [i] * 6 + [f] + rows * 3 + [fp] * 2 + [vp, vp]
+    for name in ("kdn_group_norm_fwd_workspace_size", "kdn_group_norm_bwd_workspace_size"):
+        fn = getattr(L, name)
+        fn.restype = sz
+        fn.argtypes = [i] * 4
+    L.kdn_group_norm_fwd.restype = i
+    L.kdn_group_norm_fwd.argtypes = [i] * 6 + [f, vp, ll] + [fp] * 2 + [vp] + [fp] * 2 + [vp, sz, vp]
+    L.kdn_group_norm_bwd.restype = i
+    L.kdn_group_norm_bwd.argtypes = [i] * 6 + [vp, vp, ll] + [fp] * 4 + [vp] + [fp] * 2 + [vp, sz, vp]
+    u64 = ctypes.c_ulonglong
+    L.kdn_dropout_fwd.restype = i
+    L.kdn_dropout_fwd.argtypes = [i] * 3 + [ctypes.c_double, u64, u64, vp, vp, ll, vp, vp, vp]
+    L.kdn_dropout_bwd.restype = i
+    L.kdn_dropout_bwd.argtypes = [i] * 3 + [ctypes.c_double, u64, u64, vp, vp, vp, vp]
     L.kdn_status_string.restype = ctypes.c_char_p
     L.kdn_status_string.argtypes = [i]
     L.kdn_last_error_message.restype = ctypes.c_char_p
@@ -148,7 +161,9 @@ EXPORTED = ("kdn_fwd_workspace_size", "kdn_diag_fwd", "kdn_iso_fwd", "kdn_step",
             "kdn_conv_step", "kdn_rec_fwd_workspace_size", "kdn_rec_fwd",
             "kdn_rec_bwd_workspace_size", "kdn_rec_bwd", "kdn_rec_step",
             "kdn_linattn_fwd_workspace_size", "kdn_linattn_fwd", "kdn_linattn_bwd_workspace_size",
-            "kdn_linattn_bwd", "kdn_linattn_step", "kdn_status_string",
+            "kdn_linattn_bwd", "kdn_linattn_step", "kdn_group_norm_fwd_workspace_size",
+            "kdn_group_norm_fwd", "kdn_group_norm_bwd_workspace_size", "kdn_group_norm_bwd",
+            "kdn_dropout_fwd", "kdn_dropout_bwd", "kdn_status_string",
             "kdn_last_error_message", "kdn_version")
 
 

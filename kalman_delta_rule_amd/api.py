@@ -1015,3 +1015,120 @@ def kdn_linattn_step(q, k, v, decay, state, scale=None, o=None) -> torch.Tensor:
     _launch(dev, L.kdn_linattn_step, B, H, Hk, dk, dv, io, _scale(scale, dk), *qh, *kh, *vh,
             decay.data_ptr(), state.data_ptr(), o.data_ptr())
     return o
+
+
+def _group_sizes(x, groups):
+    """Device, io code and (N, S, C, G) of x [N, ..., C]."""
+    dev, io = _first(x, "x", None)
+    if x.dim() < 2:
+        raise ValueError("x must have at least two axes [N, ..., C], got shape %s" % (tuple(x.shape),))
+    if not isinstance(groups, int) or groups < 1:
+        raise ValueError("groups must be a positive int, got %r" % (groups,))
+    N, C = x.shape[0], x.shape[-1]
+    S = 1
+    for n in x.shape[1:-1]:
+        S *= n
+    return dev, io, (N, S, C, groups)
+
+
+def kdn_group_norm_fwd(x, groups: int, weight=None, bias=None, eps: float = 1e-5, activation=None,
+                       y=None, want_stats: bool = False, workspace=None):
+    """Group norm over x [N, ..., C] (a slice of wider rows is fine): each
+    sample's positions and the C / groups adjacent channels of a group share a
+    mean and a variance; then weight and bias ([C] fp32, each optional) and the
+    ``activation``, None or "silu".  A head's outputs of a token are normalised
+    by x [tokens, H dv] with H groups.  Returns (y, mean, rstd): y in x's dtype,
+    and with ``want_stats`` the fp32 statistics [N, groups] that
+    kdn_group_norm_bwd reads (None, None otherwise)."""
+    L = _lib.lib()
+    dev, io, sizes = _group_sizes(x, groups)
+    N, C = sizes[0], sizes[2]
+    stride = _row_stride(x, "x")
+    act = _activation(activation)
+    f32 = torch.float32
+    _optional(dev, (weight, "weight", (C,), f32), (bias, "bias", (C,), f32))
+    y = _given(y, "y", x)
+    mean = rstd = None
+    if want_stats:
+        mean = torch.empty((N, groups), dtype=f32, device=dev)
+        rstd = torch.empty((N, groups), dtype=f32, device=dev)
+    ws, ws_bytes = _workspace(workspace, L.kdn_group_norm_fwd_workspace_size(*sizes), dev)
+    _launch(dev, L.kdn_group_norm_fwd, *sizes, io, act, float(eps), x.data_ptr(), stride, _ptr(weight),
+            _ptr(bias), y.data_ptr(), _ptr(mean), _ptr(rstd), _ptr(ws), ws_bytes)
+    return y, mean, rstd
+
+
+def kdn_group_norm_bwd(dy, x, mean, rstd, weight=None, bias=None, activation=None,
+                       want_param_grads: bool = True, dx=None, workspace=None) -> dict:
+    """Backward of kdn_group_norm_fwd with its mean and rstd [N, groups], and its
+    weight, bias and activation.  Returns a dict with dx (x's dtype) and, with
+    ``want_param_grads``, dweight and dbias [C] (fp32, summed over samples and
+    positions)."""
+    L = _lib.lib()
+    if not isinstance(mean, torch.Tensor) or mean.dim() != 2:
+        raise ValueError("mean must be a tensor [N, groups]")
+    dev, io, sizes = _group_sizes(x, mean.shape[1])
+    N, C = sizes[0], sizes[2]
+    stride = _row_stride(x, "x")
+    act = _activation(activation)
+    f32 = torch.float32
+    _need(dy, "dy", x.shape, x.dtype, dev)
+    _need(mean, "mean", (N, sizes[3]), f32, dev)
+    _need(rstd, "rstd", (N, sizes[3]), f32, dev)
+    _optional(dev, (weight, "weight", (C,), f32), (bias, "bias", (C,), f32))
+    g = {"dx": _given(dx, "dx", x)}
+    if want_param_grads:
+        g["dweight"] = torch.empty(C, dtype=f32, device=dev)
+        g["dbias"] = torch.empty(C, dtype=f32, device=dev)
+    ws, ws_bytes = _workspace(workspace, L.kdn_group_norm_bwd_workspace_size(*sizes), dev)
+    _launch(dev, L.kdn_group_norm_bwd, *sizes, io, act, dy.data_ptr(), x.data_ptr(), stride,
+            mean.data_ptr(), rstd.data_ptr(), _ptr(weight), _ptr(bias), g["dx"].data_ptr(),
+            _ptr(g.get("dweight")), _ptr(g.get("dbias")), _ptr(ws), ws_bytes)
+    return g
+
+
+def _seed(seed, offset, dev):
+    """(seed, offset, pointer to both on the device) of a call's random numbers."""
+    if isinstance(seed, torch.Tensor):
+        _need(seed, "seed", (2,), torch.int64, dev)
+        if offset:
+            raise ValueError("a seed tensor holds the offset too: offset must be 0")
+        return 0, 0, seed.data_ptr()
+    for v, name in ((seed, "seed"), (offset, "offset")):
+        if not isinstance(v, int) or isinstance(v, bool) or not 0 <= v < 1 << 64:
+            raise ValueError("%s must be an int of 64 bits, got %r" % (name, v))
+    return seed, offset, None
+
+
+def kdn_dropout_fwd(x, p: float, seed, offset: int = 0, residual=None, y=None) -> torch.Tensor:
+    """Dropout of x [..., D] (a slice of wider rows is fine) with probability p
+    (rounded to a multiple of 2^-16): kept elements are divided by the share
+    that is kept, and ``residual`` (x's shape and dtype) is added.  What is kept
+    goes by seed, offset and an element's place alone, so nothing is stored for
+    the backward; calls that are to be independent take offsets of their own.
+    ``seed`` may be an int64 tensor {seed, offset} on the device, which the
+    kernel reads: a replayed graph takes what it holds then.  Returns y."""
+    L = _lib.lib()
+    dev, io = _first(x, "x", None)
+    D = x.shape[-1]
+    stride = _row_stride(x, "x")
+    number, offset, state = _seed(seed, offset, dev)
+    _optional(dev, (residual, "residual", x.shape, x.dtype))
+    y = _given(y, "y", x)
+    _launch(dev, L.kdn_dropout_fwd, x.numel() // D if D else 0, D, io, float(p), number, offset, state,
+            x.data_ptr(), stride, _ptr(residual), y.data_ptr())
+    return y
+
+
+def kdn_dropout_bwd(dy, p: float, seed, offset: int = 0, dx=None) -> torch.Tensor:
+    """Gradient of kdn_dropout_fwd by x, for the same p, seed and offset (the
+    residual's is dy itself).  Returns dx."""
+    L = _lib.lib()
+    dev, io = _first(dy, "dy", None)
+    D = dy.shape[-1]
+    _need(dy, "dy", dy.shape, dy.dtype, dev)
+    number, offset, state = _seed(seed, offset, dev)
+    dx = _given(dx, "dx", dy)
+    _launch(dev, L.kdn_dropout_bwd, dy.numel() // D if D else 0, D, io, float(p), number, offset, state,
+            dy.data_ptr(), dx.data_ptr())
+    return dx

@@ -18,7 +18,8 @@ SOURCES = ["kdn_api.cpp", "kdn_walk.hip", "kdn_chunk.hip", "kdn_step.hip", "kdn_
            "kdn_dense.hip", "kdn_bwd.hip", "kdn_bwd_chunk.hip",
            "kdn_prologue.hip", "kdn_seqpar.hip", "kdn_plan.cpp",
            "kdn_block_api.cpp", "kdn_norm.hip", "kdn_conv.hip", "kdn_rec.hip",
-           "kdn_linattn_api.cpp", "kdn_linattn.hip"]
+           "kdn_linattn_api.cpp", "kdn_linattn.hip", "kdn_layer_ops_api.cpp",
+           "kdn_group_norm.hip", "kdn_dropout.hip"]
 # sources whose kernels use the matrix cores (checked by isa_check)
 MFMA_SOURCES = ["kdn_walk.hip", "kdn_chunk.hip", "kdn_bwd_chunk.hip", "kdn_linattn.hip"]
 ARCH = os.environ.get("KDN_OFFLOAD_ARCH", "gfx950")

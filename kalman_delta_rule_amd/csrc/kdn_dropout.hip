@@ -1,0 +1,136 @@
+// kdn_dropout.hip -- dropout from a counter-based generator, gfx950.
+//
+//   y = (kept ? x scale : 0) + residual
+//
+// Eight elements take the 128 bits that Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel
+// random numbers: as easy as 1, 2, 3", 2011) gives for their number: 16 bits an element, so
+// that its 20 products of 32 bits cost less than the memory they run beside.  The mask is
+// never stored: the backward forms it again.  Bound by HBM.
+#include "kdn_common.h"
+#include "kdn_layer_ops.h"
+#include "kdn_stream.h"
+
+namespace kdn {
+
+namespace {
+
+struct Words4 {
+    uint32_t w[4];
+};
+
+__device__ __forceinline__ Words4 philox(uint64_t block, uint64_t offset, uint64_t seed)
+{
+    uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32), c2 = (uint32_t)offset, c3 = (uint32_t)(offset >> 32);
+    uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+        const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+        c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+        c1 = (uint32_t)b;
+        c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+        c3 = (uint32_t)a;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return {{c0, c1, c2, c3}};
+}
+
+// DENSE: x's rows follow one another, or a block of eight lies in one row (D a multiple of 8)
+template <typename IO, bool DENSE>
+__global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a)
+{
+    constexpr int VE = 16 / sizeof(IO);
+    const long long n = (long long)a.rows * a.D, block = (long long)blockIdx.x * 256 + threadIdx.x, i0 = block * 8;
+    if (i0 >= n)
+        return;
+    uint64_t seed = a.seed, offset = a.offset;
+    if (a.state) {
+        seed = (uint64_t)a.state[0];
+        offset = (uint64_t)a.state[1];
+    }
+    const int count = (int)min(n - i0, 8ll);
+    long long row = (uint32_t)i0 / (uint32_t)a.D;
+    int col = (int)(i0 - row * a.D);
+    const IO* x = static_cast<const IO*>(a.x);
+    const IO* res = static_cast<const IO*>(a.residual);
+    IO* y = static_cast<IO*>(a.y) + i0;
+    float v[8], r[8] = {};
+    const bool whole = DENSE && count == 8;
+    if (whole) {
+        const IO* p = x + row * a.xs + col;
+#pragma unroll
+        for (int k = 0; k < 8 / VE; ++k) {
+            const Raw<IO, VE> t = load_raw<false, IO, VE>(p + k * VE);
+#pragma unroll
+            for (int j = 0; j < VE; ++j)
+                v[k * VE + j] = t.get(j);
+        }
+        if (res) {
+#pragma unroll
+            for (int k = 0; k < 8 / VE; ++k) {
+                const Raw<IO, VE> t = load_raw<false, IO, VE>(res + i0 + k * VE);
+#pragma unroll
+                for (int j = 0; j < VE; ++j)
+                    r[k * VE + j] = t.get(j);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] = 0.f;
+            if (j < count) {
+                v[j] = to_f32(x[row * a.xs + col]);
+                if (res)
+                    r[j] = to_f32(res[i0 + j]);
+            }
+            if (++col == a.D)
+                col = 0, ++row;
+        }
+    }
+    const Words4 bits = philox((uint64_t)block, offset, seed);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t u = j & 1 ? bits.w[j / 2] >> 16 : bits.w[j / 2] & 0xFFFFu;
+        // a choice, not a product: what is dropped may be infinite
+        v[j] = (u >= a.least ? v[j] * a.scale : 0.f);
+        if (res)
+            v[j] += r[j];
+    }
+    if (whole) {
+#pragma unroll
+        for (int k = 0; k < 8 / VE; ++k) {
+            float t[VE];
+#pragma unroll
+            for (int j = 0; j < VE; ++j)
+                t[j] = v[k * VE + j];
+            store_raw<IO, VE>(y + k * VE, t);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < count)
+                y[j] = from_f32<IO>(v[j]);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_dropout(const DropoutArgs& a, bool bf, hipStream_t stream)
+{
+    const long long n = (long long)a.rows * a.D;
+    if (n == 0)
+        return hipSuccess;
+    const unsigned groups = (unsigned)((n + 2047) / 2048);
+    const bool dense = a.xs == a.D || a.rows == 1 || a.D % 8 == 0;
+    auto run = [&](auto io) {
+        typedef decltype(io) IO;
+        if (dense)
+            dropout_kernel<IO, true><<<groups, 256, 0, stream>>>(a);
+        else
+            dropout_kernel<IO, false><<<groups, 256, 0, stream>>>(a);
+    };
+    bf ? run(bf16{}) : run(0.f);
+    return hipGetLastError();
+}
+
+}  // namespace kdn
