@@ -12,6 +12,7 @@
 // the mean is corrected by what is left around it.  Larger units, and few large ones, are
 // read twice by many workgroups, whose sums by channel are joined in between.
 #include "kdn_common.h"
+#include "kdn_lanes.h"
 #include "kdn_layer_ops.h"
 #include "kdn_stream.h"
 
@@ -37,11 +38,8 @@ template <int TPR>
 __device__ __forceinline__ float2 unit_sum(float a, float b, float2* red)
 {
     constexpr int N = TPR < 64 ? TPR : 64;
-#pragma unroll
-    for (int o = 1; o < N; o *= 2) {
-        a += __shfl_xor(a, o);
-        b += __shfl_xor(b, o);
-    }
+    a = lane_sum<N>(a);
+    b = lane_sum<N>(b);
     if constexpr (TPR > 64) {
         constexpr int W = TPR / 64;
         __syncthreads();  // the last sum's reads are done
@@ -145,9 +143,9 @@ struct Part {
     }
     // elements that there are of vector v
     __device__ __forceinline__ int there(int S, int v) const { return s0 + v * ds < S ? width : 0; }
-    __device__ __forceinline__ size_t at(const GroupNormArgs& a, int v, long long stride) const
+    __device__ __forceinline__ size_t at(const GroupNormArgs& a, int v, long long stride, int sample) const
     {
-        return ((size_t)n * a.S + s0 + v * ds) * stride + col;
+        return ((size_t)sample * a.S + s0 + v * ds) * stride + col;
     }
 };
 
@@ -165,16 +163,32 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void group_norm_fwd_kernel(G
     load_param(a.bias ? a.bias + part.col : nullptr, 0.f, part.on ? part.width : 0, b);
     const IO* x = static_cast<const IO*>(a.x);
     IO* y = static_cast<IO*>(a.y);
-    // all sets walk as many units; those behind the last sample hold nothing
-    for (long long u = P::SETS == 1 ? part.set : blockIdx.x * (long long)P::SETS; u < (long long)a.N * a.G; u += part.step, part.n += part.step / a.G) {
-        const bool on = part.n < a.N;
-        Raw<IO, VE> raw[NV];
-        float s = 0.f;
+    // Small units are loaded one ahead (524288 units of 128 bf16: 73 us without).
+    constexpr bool AHEAD = NV <= 2;
+    const long long units = (long long)a.N * a.G;
+    Raw<IO, VE> raw[NV], next[AHEAD ? NV : 1];
+    auto load = [&](Raw<IO, VE>(&to)[NV], int sample) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int n = on ? part.there(a.S, v) : 0;
-            raw[v] = load_some<IO, VE>(x + (n ? part.at(a, v, a.xs) : 0), n);
+            const int n = sample < a.N ? part.there(a.S, v) : 0;
+            to[v] = load_some<IO, VE>(x + (n ? part.at(a, v, a.xs, sample) : 0), n);
         }
+    };
+    if constexpr (AHEAD)
+        load(next, part.n);
+    // all sets walk as many units; those behind the last sample hold nothing
+    for (long long u = P::SETS == 1 ? part.set : blockIdx.x * (long long)P::SETS; u < units; u += part.step, part.n += part.step / a.G) {
+        const bool on = part.n < a.N;
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                raw[v] = next[v];
+            if (u + part.step < units)
+                load(next, part.n + part.step / a.G);
+        } else {
+            load(raw, part.n);
+        }
+        float s = 0.f;
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -210,7 +224,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void group_norm_fwd_kernel(G
                 const float z = fmaf((raw[v].get(j) - near - off) * rstd, w[j], b[j]);
                 o[j] = a.silu ? silu_of(z) : z;
             }
-            store_some<IO, VE>(y + part.at(a, v, a.C), o, n);
+            store_some<IO, VE>(y + part.at(a, v, a.C, part.n), o, n);
         }
         if (on && threadIdx.x % TPR == 0) {
             const size_t i = (size_t)part.n * a.G + part.g;
@@ -244,15 +258,28 @@ __global__ __launch_bounds__(kBwdThreads) void group_norm_bwd_kernel(GroupNormAr
     const IO* x = static_cast<const IO*>(a.x);
     const IO* dy = static_cast<const IO*>(a.dy);
     IO* dx = static_cast<IO*>(a.dx);
-    for (long long u = SETS == 1 ? part.set : blockIdx.x * (long long)SETS; u < (long long)a.N * a.G; u += part.step, part.n += part.step / a.G) {
-        const bool on = part.n < a.N;
-        Raw<IO, VE> rx[NV], ry[NV];
-        float kept[KEEP ? NV : 1][VE];
+    constexpr bool AHEAD = NV == 1;
+    const long long units = (long long)a.N * a.G;
+    Raw<IO, VE> rx[NV], ry[NV], nx[AHEAD ? NV : 1], ny[AHEAD ? NV : 1];
+    auto load = [&](Raw<IO, VE>(&tx)[NV], Raw<IO, VE>(&ty)[NV], int sample) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int n = on ? part.there(a.S, v) : 0;
-            rx[v] = load_some<IO, VE>(x + (n ? part.at(a, v, a.xs) : 0), n);
-            ry[v] = load_some<IO, VE>(dy + (n ? part.at(a, v, a.C) : 0), n);
+            const int n = sample < a.N ? part.there(a.S, v) : 0;
+            tx[v] = load_some<IO, VE>(x + (n ? part.at(a, v, a.xs, sample) : 0), n);
+            ty[v] = load_some<IO, VE>(dy + (n ? part.at(a, v, a.C, sample) : 0), n);
+        }
+    };
+    if constexpr (AHEAD)
+        load(nx, ny, part.n);
+    for (long long u = SETS == 1 ? part.set : blockIdx.x * (long long)SETS; u < units; u += part.step, part.n += part.step / a.G) {
+        const bool on = part.n < a.N;
+        float kept[KEEP ? NV : 1][VE];
+        if constexpr (AHEAD) {
+            rx[0] = nx[0], ry[0] = ny[0];
+            if (u + part.step < units)
+                load(nx, ny, part.n + part.step / a.G);
+        } else {
+            load(rx, ry, part.n);
         }
         const size_t i = (size_t)(on ? part.n : 0) * a.G + part.g;
         const float mean = a.mean[i], rstd = a.rstd[i];
@@ -298,7 +325,7 @@ __global__ __launch_bounds__(kBwdThreads) void group_norm_bwd_kernel(GroupNormAr
                     g = slope(v, j, xh);
                 o[j] = rstd * (g * w[j] - m1 - xh * m2);
             }
-            store_some<IO, VE>(dx + part.at(a, v, a.C), o, n);
+            store_some<IO, VE>(dx + part.at(a, v, a.C, part.n), o, n);
         }
     }
     if (!a.ws)
@@ -472,11 +499,13 @@ __global__ __launch_bounds__(256) void group_norm_join_kernel(GroupNormArgs a, S
     };
     float s = 0.f, q = 0.f, positions;
     const float first = from[0].x;  // sums around it: means far from zero cancel exactly
+#pragma unroll 4
     for (int i = threadIdx.x; i < items; i += 256) {
         const float2 x = item(i, positions);
         s = fmaf(positions, x.x - first, s);
     }
     const float mean = first + unit_sum<256>(s, 0.f, red).x / count;
+#pragma unroll 4
     for (int i = threadIdx.x; i < items; i += 256) {
         const float2 x = item(i, positions);
         const float d = x.x - mean;
@@ -581,6 +610,7 @@ __global__ __launch_bounds__(256) void group_norm_means_kernel(GroupNormArgs a, 
     __shared__ float2 red[4];
     const int n = blockIdx.x / a.G, g = blockIdx.x % a.G, Cg = a.C / a.G, items = p.tiles * Cg;
     float s1 = 0.f, s2 = 0.f;
+#pragma unroll 4
     for (int i = threadIdx.x; i < items; i += 256) {
         const int c = g * Cg + i % Cg;
         const float* from = ws + ((size_t)n * p.tiles + i / Cg) * 2 * a.C + c;
@@ -617,11 +647,11 @@ Held held_shape(int N, int S, int C, int G, bool bf, bool backward)
     Held h{};
     h.pad = power_of_two(ceil_div(Cg, VE));
     const long long pieces = (long long)S * h.pad;
-    if (h.pad > 1024 || pieces > 8 * 1024 || (units < 128 && pieces > 1024))
+    if (h.pad > 1024 || pieces > (backward ? 4 : 8) * 1024 || (units < 128 && pieces > 1024))
         return h;
     const int sizes[] = {8, 16, 32, 64, 256, 1024};
     int k = 0;
-    auto fits = [&](int k) { return sizes[k] >= h.pad && (long long)sizes[k] * (sizes[k] == 1024 ? 8 : 4) >= pieces; };
+    auto fits = [&](int k) { return sizes[k] >= h.pad && (long long)sizes[k] * (sizes[k] == 1024 && !backward ? 8 : 4) >= pieces; };
     while (!fits(k))
         ++k;
     while (k < 5 && sizes[k] < pieces && units * sizes[k] < 64 * 1024)
@@ -652,7 +682,7 @@ Split split_shape(int N, int S, int C, bool bf)
     p.blocks = ceil_div(C, p.lanes * VE);
     const int at_once = 256 / p.lanes;
     const long long others = (long long)N * p.blocks;
-    long long tiles = others >= 2048 ? 1 : 2048 / others;
+    long long tiles = others >= 1024 ? 1 : 1024 / others;
     const int most = ceil_div(S, at_once * 4);
     tiles = tiles < most ? tiles : most;
     p.rows = ceil_div(ceil_div(S, tiles), at_once) * at_once;
@@ -715,7 +745,9 @@ hipError_t group_norm_bwd(const GroupNormArgs& args, hipStream_t stream)
         units = sets >= a.G ? 0 : h.grid * sets;
         if (a.N && a.S)
             with_held(h, [&](auto t, auto v) {
-                group_norm_bwd_kernel<IO, decltype(t)::value, decltype(v)::value><<<h.grid, kBwdThreads, 0, stream>>>(a, h);
+                constexpr int V = decltype(v)::value;
+                if constexpr (V <= 4)
+                    group_norm_bwd_kernel<IO, decltype(t)::value, V><<<h.grid, kBwdThreads, 0, stream>>>(a, h);
             });
     } else if (a.N && a.S) {
         const Split p = split_shape(a.N, a.S, a.C, sizeof(IO) == 2);
