@@ -71,6 +71,19 @@ __device__ __forceinline__ Raw<E, VE> load_some(const E* p, int n)
     __builtin_memcpy(r.w, v, sizeof(v));
     return r;
 }
+// all of them, or none
+template <bool WHOLE, typename E, int VE>
+__device__ __forceinline__ Raw<E, VE> load_part(const E* p, int n)
+{
+    if constexpr (WHOLE) {
+        Raw<E, VE> r{};
+        if (n)
+            r = load_raw<false, E, VE>(p);
+        return r;
+    } else {
+        return load_some<E, VE>(p, n);
+    }
+}
 template <typename E, int VE>
 __device__ __forceinline__ void store_some(E* p, const float (&v)[VE], int n)
 {
@@ -149,7 +162,8 @@ struct Part {
     }
 };
 
-template <typename IO, int TPR, int NV>
+// WHOLE: a group's channels are whole vectors
+template <typename IO, int TPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void group_norm_fwd_kernel(GroupNormArgs a, Held held)
 {
     constexpr int THREADS = TPR > 256 ? TPR : 256;
@@ -171,7 +185,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void group_norm_fwd_kernel(G
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int n = sample < a.N ? part.there(a.S, v) : 0;
-            to[v] = load_some<IO, VE>(x + (n ? part.at(a, v, a.xs, sample) : 0), n);
+            to[v] = load_part<WHOLE, IO, VE>(x + (n ? part.at(a, v, a.xs, sample) : 0), n);
         }
     };
     if constexpr (AHEAD)
@@ -201,9 +215,11 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void group_norm_fwd_kernel(G
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int n = on ? part.there(a.S, v) : 0;
+            if (n == 0)
+                continue;
 #pragma unroll
             for (int j = 0; j < VE; ++j) {
-                const float d = j < n ? raw[v].get(j) - near : 0.f;
+                const float d = WHOLE || j < n ? raw[v].get(j) - near : 0.f;
                 d1 += d;
                 d2 = fmaf(d, d, d2);
             }
@@ -224,7 +240,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void group_norm_fwd_kernel(G
                 const float z = fmaf((raw[v].get(j) - near - off) * rstd, w[j], b[j]);
                 o[j] = a.silu ? silu_of(z) : z;
             }
-            store_some<IO, VE>(y + part.at(a, v, a.C, part.n), o, n);
+            store_some<IO, VE>(y + part.at(a, v, a.C, part.n), o, WHOLE ? VE : n);
         }
         if (on && threadIdx.x % TPR == 0) {
             const size_t i = (size_t)part.n * a.G + part.g;
@@ -242,7 +258,7 @@ constexpr int kBwdThreads = 1024;
 // groups, else one for every G units side by side.
 __host__ __device__ inline int slots_of(int grid, int sets, int G) { return sets >= G ? grid : (grid * sets + G - 1) / G; }
 
-template <typename IO, int TPR, int NV>
+template <typename IO, int TPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(kBwdThreads) void group_norm_bwd_kernel(GroupNormArgs a, Held held)
 {
     typedef Part<IO, TPR, NV, kBwdThreads> P;
@@ -265,8 +281,8 @@ __global__ __launch_bounds__(kBwdThreads) void group_norm_bwd_kernel(GroupNormAr
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int n = sample < a.N ? part.there(a.S, v) : 0;
-            tx[v] = load_some<IO, VE>(x + (n ? part.at(a, v, a.xs, sample) : 0), n);
-            ty[v] = load_some<IO, VE>(dy + (n ? part.at(a, v, a.C, sample) : 0), n);
+            tx[v] = load_part<WHOLE, IO, VE>(x + (n ? part.at(a, v, a.xs, sample) : 0), n);
+            ty[v] = load_part<WHOLE, IO, VE>(dy + (n ? part.at(a, v, a.C, sample) : 0), n);
         }
     };
     if constexpr (AHEAD)
@@ -291,13 +307,15 @@ __global__ __launch_bounds__(kBwdThreads) void group_norm_bwd_kernel(GroupNormAr
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int n = on ? part.there(a.S, v) : 0;
+            if (n == 0)
+                continue;
 #pragma unroll
             for (int j = 0; j < VE; ++j) {
                 const float xh = (rx[v].get(j) - mean) * rstd;
-                const float g = j < n ? slope(v, j, xh) : 0.f;
+                const float g = WHOLE || j < n ? slope(v, j, xh) : 0.f;
                 if constexpr (KEEP)
                     kept[v][j] = g;
-                if (j < n) {
+                if (WHOLE || j < n) {
                     s1 = fmaf(g, w[j], s1);
                     s2 = fmaf(g * w[j], xh, s2);
                     dw[j] = fmaf(g, xh, dw[j]);
@@ -325,7 +343,7 @@ __global__ __launch_bounds__(kBwdThreads) void group_norm_bwd_kernel(GroupNormAr
                     g = slope(v, j, xh);
                 o[j] = rstd * (g * w[j] - m1 - xh * m2);
             }
-            store_some<IO, VE>(dx + part.at(a, v, a.C, part.n), o, n);
+            store_some<IO, VE>(dx + part.at(a, v, a.C, part.n), o, WHOLE ? VE : n);
         }
     }
     if (!a.ws)
@@ -712,10 +730,14 @@ template <typename IO>
 hipError_t group_norm_fwd(const GroupNormArgs& a, hipStream_t stream)
 {
     const Held h = held_shape(a.N, a.S, a.C, a.G, sizeof(IO) == 2, false);
+    const bool whole = a.C / a.G % (16 / sizeof(IO)) == 0;
     if (h.tpr) {
         with_held(h, [&](auto t, auto v) {
             constexpr int T = decltype(t)::value, V = decltype(v)::value;
-            group_norm_fwd_kernel<IO, T, V><<<h.grid, T > 256 ? T : 256, 0, stream>>>(a, h);
+            if (whole)
+                group_norm_fwd_kernel<IO, T, V, true><<<h.grid, T > 256 ? T : 256, 0, stream>>>(a, h);
+            else
+                group_norm_fwd_kernel<IO, T, V, false><<<h.grid, T > 256 ? T : 256, 0, stream>>>(a, h);
         });
         return hipGetLastError();
     }
@@ -735,6 +757,7 @@ hipError_t group_norm_bwd(const GroupNormArgs& args, hipStream_t stream)
     GroupNormArgs a = args;
     const bool sums = a.dweight || a.dbias;
     const Held h = held_shape(a.N, a.S, a.C, a.G, sizeof(IO) == 2, true);
+    const bool whole = a.C / a.G % (16 / sizeof(IO)) == 0;
     float* ws = static_cast<float*>(a.ws);
     int slots = 0, units = 0;
     if (h.tpr) {
@@ -745,9 +768,13 @@ hipError_t group_norm_bwd(const GroupNormArgs& args, hipStream_t stream)
         units = sets >= a.G ? 0 : h.grid * sets;
         if (a.N && a.S)
             with_held(h, [&](auto t, auto v) {
-                constexpr int V = decltype(v)::value;
-                if constexpr (V <= 4)
-                    group_norm_bwd_kernel<IO, decltype(t)::value, V><<<h.grid, kBwdThreads, 0, stream>>>(a, h);
+                constexpr int T = decltype(t)::value, V = decltype(v)::value;
+                if constexpr (V <= 4) {
+                    if (whole)
+                        group_norm_bwd_kernel<IO, T, V, true><<<h.grid, kBwdThreads, 0, stream>>>(a, h);
+                    else
+                        group_norm_bwd_kernel<IO, T, V, false><<<h.grid, kBwdThreads, 0, stream>>>(a, h);
+                }
             });
     } else if (a.N && a.S) {
         const Split p = split_shape(a.N, a.S, a.C, sizeof(IO) == 2);
