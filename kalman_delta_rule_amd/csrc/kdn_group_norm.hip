@@ -32,6 +32,13 @@ __device__ __forceinline__ float silu_slope(float z)
 // (a NaN stays one)
 __device__ __forceinline__ float not_below_zero(float x) { return x < 0.f ? 0.f : x; }
 
+// 1 / sqrt(x) within 1 ulp, denormal numbers included
+__device__ __forceinline__ float rsqrt_of(float x)
+{
+    const bool tiny = x < 0x1p-100f;
+    return __builtin_amdgcn_rsqf(tiny ? x * 0x1p100f : x) * (tiny ? 0x1p50f : 1.f);
+}
+
 // The sums of two values over the TPR threads of a unit, in all of them; `red` holds a
 // slot for each wave of the workgroup.
 template <int TPR>
@@ -171,7 +178,9 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void group_norm_fwd_kernel(G
     constexpr int VE = P::VE;
     __shared__ float2 red[THREADS / 64];
     P part(a, held);
-    const float count = (float)a.S * (a.C / a.G);
+    // the first mean is divided by the count, not multiplied with its reciprocal: that of
+    // equal values is that value
+    const float count = (float)a.S * (a.C / a.G), inv = 1.f / count;
     float w[VE], b[VE];
     load_param(a.weight ? a.weight + part.col : nullptr, 1.f, part.on ? part.width : 0, w);
     load_param(a.bias ? a.bias + part.col : nullptr, 0.f, part.on ? part.width : 0, b);
@@ -227,8 +236,8 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void group_norm_fwd_kernel(G
         const float2 m = unit_sum<TPR>(d1, d2, red);
         if constexpr (NV > 2)
             anew(raw);
-        const float off = m.x / count, mean = near + off;
-        const float rstd = 1.f / sqrtf(not_below_zero(m.y / count - off * off) + a.eps);
+        const float off = m.x * inv, mean = near + off;
+        const float rstd = rsqrt_of(not_below_zero(m.y * inv - off * off) + a.eps);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int n = on ? part.there(a.S, v) : 0;
@@ -236,9 +245,12 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void group_norm_fwd_kernel(G
                 continue;
             float o[VE];
 #pragma unroll
-            for (int j = 0; j < VE; ++j) {
-                const float z = fmaf((raw[v].get(j) - near - off) * rstd, w[j], b[j]);
-                o[j] = a.silu ? silu_of(z) : z;
+            for (int j = 0; j < VE; ++j)
+                o[j] = fmaf((raw[v].get(j) - near - off) * rstd, w[j], b[j]);
+            if (a.silu) {
+#pragma unroll
+                for (int j = 0; j < VE; ++j)
+                    o[j] = silu_of(o[j]);
             }
             store_some<IO, VE>(y + part.at(a, v, a.C, part.n), o, WHOLE ? VE : n);
         }
@@ -252,20 +264,21 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void group_norm_fwd_kernel(G
     }
 }
 
-constexpr int kBwdThreads = 1024;
+constexpr int bwd_threads(int tpr) { return tpr > 512 ? tpr : 512; }
 
 // Slots of sums by channel that a backward launch leaves: a workgroup's where it holds all
 // groups, else one for every G units side by side.
 __host__ __device__ inline int slots_of(int grid, int sets, int G) { return sets >= G ? grid : (grid * sets + G - 1) / G; }
 
 template <typename IO, int TPR, int NV, bool WHOLE>
-__global__ __launch_bounds__(kBwdThreads) void group_norm_bwd_kernel(GroupNormArgs a, Held held)
+__global__ __launch_bounds__(bwd_threads(TPR)) void group_norm_bwd_kernel(GroupNormArgs a, Held held)
 {
-    typedef Part<IO, TPR, NV, kBwdThreads> P;
+    constexpr int THREADS = bwd_threads(TPR);
+    typedef Part<IO, TPR, NV, THREADS> P;
     constexpr int VE = P::VE, SETS = P::SETS;
     constexpr bool KEEP = NV * VE <= 16;  // g is kept, not formed again
-    __shared__ float2 red[kBwdThreads / 64];
-    __shared__ float sums[kBwdThreads * VE];
+    __shared__ float2 red[THREADS / 64];
+    __shared__ float sums[THREADS * VE];
     P part(a, held);
     const float inv = 1.f / ((float)a.S * (a.C / a.G));
     float w[VE], b[VE], dw[VE] = {}, db[VE] = {};
@@ -274,7 +287,7 @@ __global__ __launch_bounds__(kBwdThreads) void group_norm_bwd_kernel(GroupNormAr
     const IO* x = static_cast<const IO*>(a.x);
     const IO* dy = static_cast<const IO*>(a.dy);
     IO* dx = static_cast<IO*>(a.dx);
-    constexpr bool AHEAD = NV == 1;
+    constexpr bool AHEAD = false;
     const long long units = (long long)a.N * a.G;
     Raw<IO, VE> rx[NV], ry[NV], nx[AHEAD ? NV : 1], ny[AHEAD ? NV : 1];
     auto load = [&](Raw<IO, VE>(&tx)[NV], Raw<IO, VE>(&ty)[NV], int sample) {
@@ -367,7 +380,7 @@ __global__ __launch_bounds__(kBwdThreads) void group_norm_bwd_kernel(GroupNormAr
         __syncthreads();
         // of a set: TPR / LANES parts of `row` threads; part i holds pieces i row .. modulo pad
         const int groups = SETS < a.G ? SETS : a.G, cols = groups * Cg;
-        for (int i = threadIdx.x; i < cols; i += kBwdThreads) {
+        for (int i = threadIdx.x; i < cols; i += THREADS) {
             const int q = i / Cg, c = i % Cg, piece = c / VE, j = c % VE;
             float s = 0.f;
             for (int set = q; set < SETS; set += a.G)
@@ -529,7 +542,7 @@ __global__ __launch_bounds__(256) void group_norm_join_kernel(GroupNormArgs a, S
         const float d = x.x - mean;
         q += fmaf(positions * d, d, x.y);
     }
-    const float rstd = 1.f / sqrtf(unit_sum<256>(q, 0.f, red).x / count + a.eps);
+    const float rstd = rsqrt_of(unit_sum<256>(q, 0.f, red).x / count + a.eps);
     if (threadIdx.x == 0) {
         stats[blockIdx.x] = float2{mean, rstd};
         if (a.mean)
@@ -562,9 +575,12 @@ __global__ __launch_bounds__(256) void group_norm_apply_kernel(GroupNormArgs a, 
         const Raw<IO, VE> r = load_some<IO, VE>(x + (size_t)s * a.xs, at.width);
         float o[VE];
 #pragma unroll
-        for (int j = 0; j < VE; ++j) {
-            const float z = fmaf((r.get(j) - mean[j]) * rstd[j], w[j], b[j]);
-            o[j] = a.silu ? silu_of(z) : z;
+        for (int j = 0; j < VE; ++j)
+            o[j] = fmaf((r.get(j) - mean[j]) * rstd[j], w[j], b[j]);
+        if (a.silu) {
+#pragma unroll
+            for (int j = 0; j < VE; ++j)
+                o[j] = silu_of(o[j]);
         }
         store_some<IO, VE>(y + (size_t)s * a.C, o, at.width);
     }
@@ -676,8 +692,8 @@ Held held_shape(int N, int S, int C, int G, bool bf, bool backward)
         ++k;
     h.tpr = sizes[k];
     h.nv = power_of_two(ceil_div(pieces, h.tpr));
-    const int threads = backward ? kBwdThreads : h.tpr > 256 ? h.tpr : 256, sets = threads / h.tpr;
-    const int full = ceil_div(units, sets), most = backward ? 512 : 2048;
+    const int threads = backward ? bwd_threads(h.tpr) : h.tpr > 256 ? h.tpr : 256, sets = threads / h.tpr;
+    const int full = ceil_div(units, sets), most = backward ? 768 : 2048;
     h.grid = full;
     if (full > most) {
         // every set keeps its group: sets of a launch are a multiple of G
@@ -763,7 +779,7 @@ hipError_t group_norm_bwd(const GroupNormArgs& args, hipStream_t stream)
     if (h.tpr) {
         if (!sums)
             a.ws = nullptr;
-        const int sets = kBwdThreads / h.tpr;
+        const int sets = bwd_threads(h.tpr) / h.tpr;
         slots = a.S ? slots_of(h.grid, sets, a.G) : 0;
         units = sets >= a.G ? 0 : h.grid * sets;
         if (a.N && a.S)
@@ -771,9 +787,9 @@ hipError_t group_norm_bwd(const GroupNormArgs& args, hipStream_t stream)
                 constexpr int T = decltype(t)::value, V = decltype(v)::value;
                 if constexpr (V <= 4) {
                     if (whole)
-                        group_norm_bwd_kernel<IO, T, V, true><<<h.grid, kBwdThreads, 0, stream>>>(a, h);
+                        group_norm_bwd_kernel<IO, T, V, true><<<h.grid, bwd_threads(T), 0, stream>>>(a, h);
                     else
-                        group_norm_bwd_kernel<IO, T, V, false><<<h.grid, kBwdThreads, 0, stream>>>(a, h);
+                        group_norm_bwd_kernel<IO, T, V, false><<<h.grid, bwd_threads(T), 0, stream>>>(a, h);
                 }
             });
     } else if (a.N && a.S) {
@@ -817,7 +833,7 @@ size_t group_norm_bwd_workspace_bytes(int N, int S, int C, int G)
         if (!N || !S)
             continue;
         const Held h = held_shape(N, S, C, G, bf, true);
-        const size_t n = h.tpr ? (size_t)slots_of(h.grid, kBwdThreads / h.tpr, G) * 2 * C * sizeof(float)
+        const size_t n = h.tpr ? (size_t)slots_of(h.grid, bwd_threads(h.tpr) / h.tpr, G) * 2 * C * sizeof(float)
                                : split_bytes(N, S, C, G, bf);
         most = most > n ? most : n;
     }
