@@ -46,7 +46,8 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 // A matrix in LDS, rows of W elements without a gap.  Its 16-byte blocks are exchanged
 // within a row by a number that goes by the row, so that all banks are busy in each of
-// the ways it is read: one block of 16 rows, and
+// the ways it is read: one block of 16 rows (where lanes 0 to 3 and 20 to 23, 4 to 7 and 16
+// to 19, .. read at once), and
 // - bf16, read transposed: pieces of 4 to 16 bytes of 4 adjacent rows;
 // - fp32, read by columns: 4 blocks of rows that lie 4 apart.
 // (256 bytes are all banks: of rows of 128 or 64 bytes, two or four lie side by side.)
@@ -61,9 +62,7 @@ struct Lds {
         if constexpr (sizeof(IO) == 4)
             return BLOCKS == 8 ? (row >> 1 & 1) | (row >> 1 & 6) : (row >> 2 & 3) << 2 | (row & 3);
         else
-            return BLOCKS == 4   ? row >> 2 & 3
-                   : BLOCKS == 8 ? (row >> 1 & 1) << 2 | (row >> 2 & 3)
-                                 : (row & 3) << 2 | (row >> 2 & 3);
+            return (row >> 1 & 2) | (row >> 3 & 1) | (BLOCKS == 4 ? 0 : BLOCKS == 8 ? row << 1 & 4 : row << 2 & 12);
     }
     // bytes from the matrix's front, which is a multiple of 256
     static __device__ __forceinline__ uint32_t at(int row, int block)
@@ -644,26 +643,27 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                     ahead(u, NT * NG);
                     if (s0 == 0)
                         acc[it] = p = zero4();
+                    // (two sums at a time: a product waits for the one before of its own sum)
 #pragma unroll
-                    for (int s = 0; s < GS; ++s)
+                    for (int s = 0; s < GS; ++s) {
                         O::mma(acc[it], fx[s0 + s], fq[u % 2][s]);
-                    if (mixed) {
+                        if constexpr (NT == 4)
+                            O::mma(p, fk[s0 + s], fq[u % 2][s]);
+                    }
+                    if constexpr (NT != 4) {
+                        if (mixed) {
 #pragma unroll
-                        for (int s = 0; s < GS; ++s) {
-                            if constexpr (NT == 4)
-                                O::mma(p, fk[s0 + s], fq[u % 2][s]);
-                            else
+                            for (int s = 0; s < GS; ++s)
                                 O::mma(p, rows<IO, KD>(krow, 0, s0 + s), fq[u % 2][s]);
                         }
                     }
                     if (mixed && s0 + GS == KS) {
                         typedef IO Four __attribute__((ext_vector_type(4)));
-                        Four out;
+                        p *= pdecay[NT == 4 ? it : 0];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {  // a choice, not a product with zero: k may be infinite
-                            const bool before = it > jt || (it == jt && c >= 4 * g + e);
-                            out[e] = from_f32<IO>(before ? p[e] * pdecay[NT == 4 ? it : 0][e] : 0.f);
-                        }
+                        for (int e = 0; e < 4; ++e)  // a choice, not a product with zero: k may be infinite
+                            p[e] = it > jt || (it == jt && c >= 4 * g + e) ? p[e] : 0.f;
+                        const Four out = __builtin_convertvector(p, Four);
                         lds_write(LP::further(pput, 16 * it, 0), out);
                     }
                 }
@@ -692,12 +692,26 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                 O::mma(none, frag{}, fv[s]);
                 if (!STATE && !odd && more > 0)
                     q2.share(qfrom, s, CS);
+                typedef IO Four __attribute__((ext_vector_type(4)));
 #pragma unroll
-                for (int e = 0; e < FE; ++e) {
-                    const float y = to_f32(fv[s][e]) * weight[e / 4][e % 4];
-                    hi[s][e] = from_f32<IO>(y);
-                    if constexpr (BF)
-                        lo[s][e] = static_cast<bf16>(y - to_f32(hi[s][e]));
+                for (int i = 0; i < FE / 4; ++i) {
+                    f32x4 y;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        y[e] = to_f32(fv[s][4 * i + e]) * weight[i][e];
+                    const Four high = __builtin_convertvector(y, Four);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        hi[s][4 * i + e] = high[e];
+                        if constexpr (BF)
+                            y[e] -= to_f32(high[e]);
+                    }
+                    if constexpr (BF) {
+                        const Four low = __builtin_convertvector(y, Four);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            lo[s][4 * i + e] = low[e];
+                    }
                 }
             }
             const bool bad = __ballot(none[0] != 0.f);
@@ -724,9 +738,9 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                         }
                 }
 #pragma unroll
-                for (int it = 0; it < NT; ++it)
+                for (int s = 0; s < CS; ++s)
 #pragma unroll
-                    for (int s = 0; s < CS; ++s)
+                    for (int it = 0; it < NT; ++it)
                         if (s * O::K < 16 * (it + 1))
                             O::mma(acc[it], fv[s], rows<IO, C>(prow, 16 * it, s));
                 if (bad) {
@@ -752,25 +766,31 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                 }
             }
             const uint32_t kc = kcol + turn * W::kTileK;
-            frag fk[2][CS];
-            auto read = [&](int t) KDN_INLINE {
+            frag fk[2][2][CS];
+            auto read = [&](int t) KDN_INLINE {  // of tiles t, t + 1
 #pragma unroll
-                for (int s = 0; s < CS; ++s)
-                    fk[t % 2][s] = O::template state_cols<KD>(kc, s, t);
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int s = 0; s < CS; ++s)
+                        fk[t / 2 % 2][i][s] = O::template state_cols<KD>(kc, s, t + i);
             };
             read(0);
 #pragma unroll
-            for (int t = 0; t < ST; ++t) {
-                if (t + 1 < ST)
-                    read(t + 1);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    X[t][e] *= whole;
+            for (int t = 0; t < ST; t += 2) {
+                if (t + 2 < ST)
+                    read(t + 2);
+                X[t] *= whole;
+                X[t + 1] *= whole;
 #pragma unroll
                 for (int s = 0; s < CS; ++s) {
-                    O::mma(X[t], fk[t % 2][s], hi[s]);
-                    if constexpr (BF)
-                        O::mma(X[t], fk[t % 2][s], lo[s]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        O::mma(X[t + i], fk[t / 2 % 2][i][s], hi[s]);
+                    if constexpr (BF) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            O::mma(X[t + i], fk[t / 2 % 2][i][s], lo[s]);
+                    }
                 }
             }
             if constexpr (!STATE) {
