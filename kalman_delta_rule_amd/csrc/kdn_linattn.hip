@@ -384,7 +384,7 @@ struct Walk {
     static constexpr bool BF = sizeof(IO) == 2;
     static constexpr int E = sizeof(IO), kTileK = C * KD * E, kTileV = C * kCols * E, kTileP = C * C * E;  // bytes
     // q once, k and v twice, the decayed product, the tokens' decays
-    static constexpr int lds(bool state) { return (state ? 2 : 3) * kTileK + 2 * kTileV + (state ? 0 : kTileP) + C * 4; }
+    static constexpr int lds(bool state) { return (state ? 2 : 3) * kTileK + 2 * kTileV + (state ? 0 : kTileP) + C * 4 + (C + 1) * 4; }
 };
 
 // STATE: the states that segments hand on, nothing else
@@ -426,18 +426,34 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
     const IO* k = static_cast<const IO*>(r.k.p) + (long long)(h / r.k.div) * r.k.hs;
     const IO* v = static_cast<const IO*>(r.v.p) + (long long)(h / r.v.div) * r.v.hs + col0;
 
-    const Decay decay{log((double)a.decay[h])};
+    // Powers of the decay to C are formed once, a thread each, while the first copies are on
+    // their way.
     // C = 64: a wave forms q k^T for 16 tokens' k (block jt) and every q; C = 32: for one block
     // of q.  Lane (g, c) holds q k^T of k's tokens j = 4 g + e of a block and q's token i = c.
     const int jt = NT == 4 ? wave : wave & 1;
+    const uint32_t Ts = Ws + 4 * C;
     f32x4 pdecay[NT == 4 ? 4 : 1];
+    float front = 0.f, g16 = 0.f;
+    bool ready = false;
+    auto power = [&](int n) KDN_INLINE { return lds_read<float>(Ts + 4 * max(n, 0)); };
+    auto powers = [&]() KDN_INLINE {
+        if (ready)
+            return;
+        ready = true;
+        const Decay decay{log((double)a.decay[h])};
+        if (threadIdx.x <= C)
+            lds_write(Ts + 4 * threadIdx.x, decay.power(threadIdx.x));
+        lds_barrier();
+        if constexpr (!STATE) {
 #pragma unroll
-    for (int i = 0; i < (NT == 4 ? 4 : 1); ++i)
+            for (int i = 0; i < (NT == 4 ? 4 : 1); ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            pdecay[i][e] = r.of_p * decay.power(16 * ((NT == 4 ? i : wave >> 1) - jt) + c - 4 * g - e);
-    const float front = r.of_x * decay.power(c + 1 - rev);
-    const float g16 = decay.power(16);
+                for (int e = 0; e < 4; ++e)
+                    pdecay[i][e] = r.of_p * power(16 * ((NT == 4 ? i : wave >> 1) - jt) + c - 4 * g - e);
+            front = r.of_x * power(c + 1 - rev);
+            g16 = power(16);
+        }
+    };
     int held = -1;  // tokens of the chunk that Ws is for
     float whole = 0.f;
 
@@ -555,6 +571,7 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
             copies(TK{}, Ks, kp, kts, kd, some).share(kfrom, 0, 1);
             copies(TV{}, Vs, vp, vts, width, some).share(vfrom, 0, 1);
         }
+        powers();
         arrived<0>();
         for (; left > 0; turn ^= 1) {
             const int len = min(left, C), more = min(left - C, C);
@@ -576,10 +593,10 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                     if (width % O::VE)
                         TV::end_row(V, x, width);
                     if (len != held)
-                        lds_write(Ws + 4 * x, r.of_u * decay.power(len - 1 - x + rev));
+                        lds_write(Ws + 4 * x, r.of_u * power(len - 1 - x + rev));
                 }
                 if (len != held)
-                    whole = decay.power(len);
+                    whole = power(len);
                 held = len;
                 lds_barrier();
             }
@@ -1077,7 +1094,9 @@ size_t linattn_fwd_workspace_bytes(int B, int T, int H, int dk, int dv)
 
 static size_t bwd_segments_bytes(int B, int T, int H, int dk, int dv, int& S, int& L)
 {
-    S = segments(B, T, H, slices_of(dk) * 2 + slices_of(dv), L);
+    // walks of the same width go in one launch
+    const int of_dv = slices_of(dv), of_dk = 2 * slices_of(dk);
+    S = segments(B, T, H, padded(dk) == padded(dv) ? of_dv + of_dk : of_dv < of_dk ? of_dv : of_dk, L);
     return handed_bytes(B, S, H, dk, dv);
 }
 
