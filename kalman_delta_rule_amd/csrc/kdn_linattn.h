@@ -49,6 +49,7 @@ struct LinRole {
     int4* spans;      // [B,S] the tokens they are of, and the sequence if it begins there (or -1)
     int srs, scs;     // strides of an element in seg
     int kd, vd, rs, cs, rev;
+    bool exact;  // its state is an fp32 output
     float of_p, of_x, of_u;
 };
 struct LinArgs {

@@ -23,8 +23,14 @@
 // bf16: the products' operands are bf16, sums and states fp32.  q, k, v are exact.  What
 // is rounded to an operand once: the decayed q k (2^-8 of each term of a y that is
 // itself rounded to 2^-8) and X where y is formed from it (the same).  X itself is summed
-// from v's decayed values as two bf16 parts (2^-16 of each term), since states are fp32
-// outputs.  fp32: matrix instructions with fp32 operands throughout.
+// from v's decayed values as two bf16 parts (2^-16 of each term).  Where it is an fp32
+// output a third part follows (2^-24), for the tokens before its last that still have an
+// eighth of their weight in it; of the others the two parts' error is as small.  The third
+// part costs 0 to 8% of a call (B8 T4096, 16 heads of 128: 134 us without a state out, 148
+// with, at one workgroup a compute unit, where the slowest decay's walk sets the time; B16
+// T2048, at two: 137 and 141), so walks that hand no state out do not form it, and are
+// kernels of their own: the branch alone cost them 2%.
+// fp32: matrix instructions with fp32 operands throughout.
 #include "kdn_common.h"
 #include "kdn_linattn.h"
 #include "kdn_sequences.h"
@@ -41,6 +47,7 @@ namespace {
 
 constexpr int kThreads = 256, kCols = 64;  // columns of v a workgroup
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
@@ -186,6 +193,19 @@ struct Decay {
 };
 
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// two values in a word as bf16, and they as fp32.  (The word is made opaque: values taken
+// from it one by one would be rounded one by one too.)
+__device__ __forceinline__ uint32_t two_bf16(float a, float b)
+{
+    typedef float two __attribute__((ext_vector_type(2)));
+    typedef bf16 out __attribute__((ext_vector_type(2)));
+    uint32_t w = __builtin_bit_cast(uint32_t, __builtin_convertvector(two{a, b}, out));
+    asm volatile("" : "+v"(w));
+    return w;
+}
+__device__ __forceinline__ float low_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
 // What this wave copies into LDS, loads and stores has arrived, but for the last N asked
 // for.  (The compiler has to know: it would otherwise wait for loads of before the walk
 // inside it, and so for the copies.)
@@ -389,7 +409,7 @@ struct Walk {
 
 // STATE: the states that segments hand on, nothing else
 // EDGE: rows that are not whole pieces of 16 bytes, or y's not whole words
-template <typename IO, int KD, int C, bool STATE, bool EDGE>
+template <typename IO, int KD, int C, bool STATE, bool EDGE, bool EXACT>
 __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linattn_kernel(LinArgs a)
 {
     typedef Walk<IO, KD, C> W;
@@ -435,12 +455,15 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
     f32x4 pdecay[NT == 4 ? 4 : 1];
     float front = 0.f, g16 = 0.f;
     bool ready = false;
+    // tokens until a term of the state has decayed to an eighth
+    int reach = 0;
     auto power = [&](int n) KDN_INLINE { return lds_read<float>(Ts + 4 * max(n, 0)); };
     auto powers = [&]() KDN_INLINE {
         if (ready)
             return;
         ready = true;
         const Decay decay{log((double)a.decay[h])};
+        reach = __builtin_amdgcn_readfirstlane(decay.log < 0 ? (int)fminf(-2.1f / (float)decay.log, 2e9f) : 2000000000);
         if (threadIdx.x <= C)
             lds_write(Ts + 4 * threadIdx.x, decay.power(threadIdx.x));
         lds_barrier();
@@ -572,6 +595,8 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
             copies(TV{}, Vs, vp, vts, width, some).share(vfrom, 0, 1);
         }
         powers();
+        // of a state that is an output: tokens before its last that a third part is formed of
+        const int near = __builtin_amdgcn_readfirstlane(EXACT && r.exact && (STATE || span.last) ? reach : -1);
         arrived<0>();
         for (; left > 0; turn ^= 1) {
             const int len = min(left, C), more = min(left - C, C);
@@ -698,7 +723,7 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
             }
             const auto q2 = copies(TK{}, Qs, qp, qts, kd, more);
             // v's decayed values, in two parts where they are rounded
-            frag hi[CS], lo[BF ? CS : 1];
+            frag hi[CS], lo[BF ? CS : 1], rest[EXACT ? CS : 1];
             f32x4 none = zero4();  // zero times v: what is not finite shows
 #pragma unroll
             for (int s = 0; s < CS; ++s) {
@@ -709,28 +734,35 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                 O::mma(none, frag{}, fv[s]);
                 if (!STATE && !odd && more > 0)
                     q2.share(qfrom, s, CS);
-                typedef IO Four __attribute__((ext_vector_type(4)));
+                if constexpr (BF) {
+                    u32x4 high, low, x = __builtin_bit_cast(u32x4, fv[s]);
 #pragma unroll
-                for (int i = 0; i < FE / 4; ++i) {
-                    f32x4 y;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        y[e] = to_f32(fv[s][4 * i + e]) * weight[i][e];
-                    const Four high = __builtin_convertvector(y, Four);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        hi[s][4 * i + e] = high[e];
-                        if constexpr (BF)
-                            y[e] -= to_f32(high[e]);
+                    for (int i = 0; i < 4; ++i) {
+                        const float w0 = weight[i / 2][i % 2 * 2], w1 = weight[i / 2][i % 2 * 2 + 1];
+                        high[i] = two_bf16(low_bf16(x[i]) * w0, high_bf16(x[i]) * w1);
+                        low[i] = two_bf16(fmaf(low_bf16(x[i]), w0, -low_bf16(high[i])),
+                                          fmaf(high_bf16(x[i]), w1, -high_bf16(high[i])));
                     }
-                    if constexpr (BF) {
-                        const Four low = __builtin_convertvector(y, Four);
+                    hi[s] = __builtin_bit_cast(frag, high);
+                    lo[s] = __builtin_bit_cast(frag, low);
+                    if constexpr (EXACT) {
+                        u32x4 last;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            lo[s][4 * i + e] = low[e];
+                        for (int i = 0; i < 4; ++i) {
+                            const float w0 = weight[i / 2][i % 2 * 2], w1 = weight[i / 2][i % 2 * 2 + 1];
+                            last[i] = two_bf16(
+                                fmaf(low_bf16(x[i]), w0, -low_bf16(high[i])) - low_bf16(low[i]),
+                                fmaf(high_bf16(x[i]), w1, -high_bf16(high[i])) - high_bf16(low[i]));
+                        }
+                        rest[s] = __builtin_bit_cast(frag, last);
                     }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < FE; ++e)
+                        hi[s][e] = fv[s][e] * weight[0][e];
                 }
             }
+            const bool exact = EXACT && left - len <= near;
             const bool bad = __ballot(none[0] != 0.f);
             if constexpr (BF) {
                 if (bad) {  // the second part of an infinity is none, not a NaN
@@ -740,6 +772,14 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                         for (int e = 0; e < FE; ++e)
                             if (lo[s][e] != lo[s][e])
                                 lo[s][e] = bf16(0.f);
+                    if constexpr (EXACT) {
+#pragma unroll
+                        for (int s = 0; s < CS; ++s)
+#pragma unroll
+                            for (int e = 0; e < FE; ++e)
+                                if (rest[s][e] != rest[s][e])
+                                    rest[s][e] = bf16(0.f);
+                    }
                 }
             }
             if constexpr (!STATE) {
@@ -791,24 +831,30 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                     for (int s = 0; s < CS; ++s)
                         fk[t / 2 % 2][i][s] = O::template state_cols<KD>(kc, s, t + i);
             };
-            read(0);
+            auto add = [&](auto parts) KDN_INLINE {
+                read(0);
 #pragma unroll
-            for (int t = 0; t < ST; t += 2) {
-                if (t + 2 < ST)
-                    read(t + 2);
-                X[t] *= whole;
-                X[t + 1] *= whole;
+                for (int t = 0; t < ST; t += 2) {
+                    if (t + 2 < ST)
+                        read(t + 2);
+                    X[t] *= whole;
+                    X[t + 1] *= whole;
 #pragma unroll
-                for (int s = 0; s < CS; ++s) {
+                    for (int s = 0; s < CS; ++s)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        O::mma(X[t + i], fk[t / 2 % 2][i][s], hi[s]);
-                    if constexpr (BF) {
+                        for (int part = 0; part < parts; ++part)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            O::mma(X[t + i], fk[t / 2 % 2][i][s], lo[s]);
-                    }
+                            for (int i = 0; i < 2; ++i)
+                                O::mma(X[t + i], fk[t / 2 % 2][i][s], part == 0 ? hi[s] : part == 1 ? lo[s] : rest[EXACT ? s : 0]);
                 }
+            };
+            if constexpr (EXACT) {
+                if (exact)
+                    add(std::integral_constant<int, 3>{});
+                else
+                    add(std::integral_constant<int, 2>{});
+            } else {
+                add(std::integral_constant<int, BF ? 2 : 1>{});
             }
             if constexpr (!STATE) {
                 store(acc, yp, len);
@@ -1010,8 +1056,9 @@ void launch_walk(const LinArgs& a, int roles, hipStream_t stream)
     constexpr int VE = 16 / sizeof(IO);
     LinArgs b = a;
     b.roles = roles;
-    bool edge = false;
+    bool edge = false, exact = false;
     for (int i = 0; i < roles; ++i) {
+        exact = exact || a.role[i].exact;
         b.slices = b.slices > slices_of(a.role[i].vd) ? b.slices : slices_of(a.role[i].vd);
         edge = edge || a.role[i].kd % VE || a.role[i].vd % VE;
         if (sizeof(IO) == 2 && !(in_words(a.role[i].q) && in_words(a.role[i].k) && in_words(a.role[i].v)))
@@ -1020,10 +1067,17 @@ void launch_walk(const LinArgs& a, int roles, hipStream_t stream)
             edge = true;
     }
     const unsigned grid = ((unsigned)a.B * a.H * a.S + 7) / 8 * 8 * b.slices * roles;
-    if (edge || b.odd)
-        linattn_kernel<IO, KD, C, STATE, true><<<grid, kThreads, 0, stream>>>(b);
+    auto launch = [&](auto exactly) {
+        constexpr bool EXACT = decltype(exactly)::value;
+        if (edge || b.odd)
+            linattn_kernel<IO, KD, C, STATE, true, EXACT><<<grid, kThreads, 0, stream>>>(b);
+        else
+            linattn_kernel<IO, KD, C, STATE, false, EXACT><<<grid, kThreads, 0, stream>>>(b);
+    };
+    if (sizeof(IO) == 2 && exact)
+        launch(std::bool_constant<sizeof(IO) == 2>{});
     else
-        linattn_kernel<IO, KD, C, STATE, false><<<grid, kThreads, 0, stream>>>(b);
+        launch(std::false_type{});
 }
 
 template <typename IO, bool STATE>
@@ -1121,7 +1175,7 @@ hipError_t launch_linattn_fwd(const LinCall& c, bool bf, hipStream_t stream)
     a.S = segments(c.B, c.T, c.H, slices_of(c.dv), a.L);
     LinRole& r = a.role[0];
     r.q = c.q, r.k = c.k, r.v = c.v;
-    r.out = c.o, r.X0 = c.S0, r.XT = c.S_T;
+    r.out = c.o, r.X0 = c.S0, r.XT = c.S_T, r.exact = c.S_T != nullptr;
     r.kd = c.dk, r.vd = c.dv, r.rs = r.srs = c.dv, r.cs = r.scs = 1;
     r.of_p = r.of_x = c.scale, r.of_u = 1.f;
     set_handed(r, c.ws, a.B, a.S, a.H);
@@ -1153,7 +1207,7 @@ static hipError_t linattn_bwd(const LinCall& c, hipStream_t stream)
     dk.of_p = dk.of_u = c.scale, dk.of_x = 1.f, dk.rev = 1;
     set_handed(dk, ws + seg, a.B, a.S, a.H);
     dv.q = c.k, dv.k = c.q, dv.v = c.d_o;
-    dv.out = c.dv_out, dv.X0 = c.dS_T, dv.XT = c.dS0;
+    dv.out = c.dv_out, dv.X0 = c.dS_T, dv.XT = c.dS0, dv.exact = c.dS0 != nullptr;
     dv.kd = c.dk, dv.vd = c.dv, dv.rs = dv.srs = c.dv, dv.cs = dv.scs = 1;
     dv.of_p = dv.of_u = c.scale, dv.of_x = 1.f, dv.rev = 1;
     set_handed(dv, ws + seg, a.B, a.S, a.H);
@@ -1167,7 +1221,7 @@ static hipError_t linattn_bwd(const LinCall& c, hipStream_t stream)
         LinRole& fwd = a.role[1];
         fwd = dv;
         fwd.q = c.q, fwd.k = c.k, fwd.v = c.v;
-        fwd.X0 = c.S0, fwd.of_u = 1.f, fwd.rev = 0;
+        fwd.X0 = c.S0, fwd.of_u = 1.f, fwd.rev = 0, fwd.exact = 0;
         set_handed(fwd, ws, a.B, a.S, a.H);
         launch_states<IO>(a, 2, stream);
     }

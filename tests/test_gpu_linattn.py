@@ -227,6 +227,25 @@ def test_what_is_not_finite_reaches_no_earlier_token(io, bad):
             assert same(h[n][0, at + 1:], g[n][0, at + 1:]), (name, n)
 
 
+@pytest.mark.parametrize("T,shift,bound", [(128, 11, 2.0 ** -20), (128, 7, 2.0 ** -20), (1024, 6, 2.0 ** -19),
+                                           (1500, 5, 2.0 ** -19)])
+def test_states_of_bf16_are_as_exact_as_fp32_sums(T, shift, bound):
+    # Relative 2-norm of a state's error.  128 tokens are two chunks of a decay's product and
+    # six matrix products: 14 roundings of 2^-24 at most, under 2^-20.  Longer: what is summed
+    # last weighs most, and of the tokens that have decayed to an eighth the terms are rounded
+    # to 2^-16 (2^-18 in the 2-norm): 2^-21 and the 14 roundings together are under 2^-19.
+    # Terms of two bf16 parts alone are 2^-18.4 off.
+    d = data(2, T, 2, 2, 64, 64, "bf16", seed=T + shift)
+    d["g"] = dev(np.full(2, 1 - 2.0 ** -shift), "f32")
+    want = R.forward(d["q"][1], d["k"][1], d["v"][1], d["g"][1], 0.125, d["S0"][1], None, "bf16")["S_T"][0]
+    off = host(forward(d, 0.125)[1]) - want
+    assert np.linalg.norm(off) <= bound * np.linalg.norm(want)
+    g = backward(d, 0.125)
+    want = R.backward(d["do"][1], d["q"][1], d["k"][1], d["v"][1], d["g"][1], 0.125, d["S0"][1], d["dS"][1], None,
+                      "bf16")["dS0"][0]
+    assert np.linalg.norm(host(g["dS0"]) - want) <= bound * np.linalg.norm(want)
+
+
 def test_sequences_do_not_leak():
     cu = [0, 40, 100, 100, 130]
     d = data(1, 130, 2, 2, 32, 32, "bf16", 9, cu)
