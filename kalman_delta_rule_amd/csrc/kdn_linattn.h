@@ -58,6 +58,7 @@ struct LinArgs {
     const float* decay;
     bool clear;
     int S, L;  // segments of each row, and their tokens
+    int parts, tokens;  // of a segment that go to a workgroup each, by where sequences begin; tokens of one
     int roles, slices;  // walks of a launch, and the most slices that one has
     bool odd;  // rows of some input begin in the middle of a word
     LinRole role[3];

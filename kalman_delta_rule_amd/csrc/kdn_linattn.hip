@@ -269,16 +269,32 @@ struct Tile {
                     turn(from, i);
         }
     };
-    // the same where rows begin in the middle of a word: an element at a time
+    // the same where rows begin in the middle of a word, through registers
     static __device__ __forceinline__ void copy_odd(uint32_t lds, const IO* p, int ts, int len, int width, int dir)
     {
-        for (int x = threadIdx.x; x < C * W; x += kThreads) {
-            const int i = x / W, j = x % W;
-            IO v = IO(0.f);
-            if (i < len && j < width)
-                v = p[(ptrdiff_t)(dir < 0 ? len - 1 - i : i) * ts + j];
-            lds_write(lds + L::at(i, j / VE) + j % VE * E, v);
+        struct __attribute__((packed, aligned(2))) Piece {
+            uint32_t w[4];
+        };
+        typedef uint32_t four __attribute__((ext_vector_type(4)));
+        four x[NP];
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            const int i = row(n), j = (int)threadIdx.x % PER * VE;
+            const IO* from = p + (ptrdiff_t)(dir < 0 ? len - 1 - i : i) * ts + j;
+            x[n] = four{};
+            if (i < len && j + VE <= width) {
+                const Piece piece = *reinterpret_cast<const Piece*>(from);
+                x[n] = four{piece.w[0], piece.w[1], piece.w[2], piece.w[3]};
+            } else if (i < len && j < width) {
+#pragma unroll
+                for (int e = 0; e < VE; ++e)
+                    if (j + e < width)
+                        x[n][e / 2] |= (uint32_t) __builtin_bit_cast(uint16_t, (bf16)from[e]) << (e % 2 * 16);
+            }
         }
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+            lds_write(lds + L::at(row(n), (int)threadIdx.x % PER), x[n]);
     }
     // row i's piece that the row ends in: what follows is the next head's, or the next token's
     static __device__ __forceinline__ void end_row(uint32_t lds, int i, int width)
@@ -302,26 +318,33 @@ struct Span {
     bool first, last;
 };
 
-// The spans of one segment [t0, t1) of a row, in the order of the walk.  Offsets may hold
-// anything: spans lie in the segment and follow one another.
+// The spans of one segment [t0, t1) of a row, in the order of the walk; with offsets, those
+// that begin in a part of it.  Offsets may hold anything: spans lie in the segment and follow
+// one another.
 struct Spans {
     const int* cu;
     int N, t0, t1, rev, at, n;
+    int u0, u1;  // the part
 
     // (all threads) cu[n] <= token, the last such n
     __device__ __forceinline__ int holding(int token) const { return count_at_most<kThreads>(cu, N, token) - 1; }
 
-    __device__ __forceinline__ void start(const LinArgs& a, int b, int begin, int end, int backwards)
+    __device__ __forceinline__ void start(const LinArgs& a, int b, int begin, int end, int backwards, int part)
     {
         cu = a.cu, N = a.N, t0 = begin, t1 = end, rev = backwards;
-        at = rev ? t1 : t0;
-        n = -1;
-        if (!cu)
-            n = b;
+        u0 = min(t1, t0 + part * a.tokens), u1 = min(t1, u0 + a.tokens);
+        at = rev ? u1 : u0;
+        n = cu ? -1 : b;
+        if (cu && u0 < u1 && at != (rev ? t1 : t0)) {
+            // a sequence that goes on here is the neighbour's
+            const int m = holding(at - 1);
+            if (m >= 0 && cu[m + 1] > at)
+                at = rev ? max(min(cu[m], at), u0) : min(cu[m + 1], u1);
+        }
     }
     __device__ __forceinline__ bool next(Span& s, int T)
     {
-        if (rev ? at <= t0 : at >= t1)
+        if (rev ? at <= u0 : at >= u1)
             return false;
         if (!cu) {
             s = Span{n, t0, t1, rev ? t1 == T : t0 == 0, rev ? t0 == 0 : t1 == T};
@@ -338,7 +361,7 @@ struct Spans {
             if (!rev || m < 0)
                 return false;
             const int e = min(cu[m + 1], token);
-            if (e <= t0)
+            if (e <= u0)
                 return false;
             at = e;
             n = -1;
@@ -432,9 +455,9 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
     const int index = blockIdx.x / 8, each = a.slices * a.roles, unit = index / each * 8 + (int)(blockIdx.x & 7);
     const LinRole& r = a.role[index % each / a.slices];
     const int slice = index % a.slices;
-    if (unit >= a.B * a.H * a.S || slice * kCols >= r.vd)
+    if (unit >= a.B * a.H * a.S * a.parts || slice * kCols >= r.vd)
         return;
-    const int h = unit % a.H, s = unit / a.H % a.S, b = unit / a.H / a.S;
+    const int h = unit % a.H, piece = unit / a.H % a.parts, s = unit / a.H / a.parts % a.S, b = unit / a.H / a.parts / a.S;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, c = lane & 15;
     const int col0 = slice * kCols, width = min(r.vd - col0, kCols);  // of v
@@ -531,7 +554,7 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
     const typename TV::Places vfrom((int)tv.ts, width, dir);
     const uint32_t part = 1024 * wave;  // of a turn's copies, this wave's
     const bool ragged = EDGE && (kd % O::VE || width % O::VE);
-    const bool odd = EDGE && a.odd;  // some rows begin in the middle of a word
+    const bool odd = BF && EDGE && a.odd;  // some rows begin in the middle of a word
     auto copies = [&](auto tile, uint32_t to, const IO* p, int ts, int wide, int len) KDN_INLINE {
         return typename decltype(tile)::Copy(to + part, p, ts, len, wide, dir);
     };
@@ -881,7 +904,7 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
         const int t0 = s * a.L, t1 = min(a.T, t0 + a.L);
         Spans spans;
         Span span;
-        spans.start(a, b, t0, t1, rev);
+        spans.start(a, b, t0, t1, rev, piece);
         while (spans.next(span, a.T)) {
             const size_t n = ((size_t)__builtin_amdgcn_readfirstlane(span.n) * a.H + h) * dense;
             // (offsets that begin below zero claim a segment before the first one)
@@ -895,7 +918,7 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
         }
         if (a.cu && a.clear && !r.out_f32) {
             IO* y = static_cast<IO*>(r.out);
-            for (int t = max(t0, max(a.cu[a.N], 0)); t < t1; ++t)
+            for (int t = max(spans.u0, max(a.cu[a.N], 0)); t < spans.u1; ++t)
                 if ((int)threadIdx.x < width)
                     y[((row0 + t) * a.H + h) * r.vd + col0 + threadIdx.x] = IO(0.f);
         }
@@ -1066,7 +1089,16 @@ void launch_walk(const LinArgs& a, int roles, hipStream_t stream)
         if (reinterpret_cast<uintptr_t>(a.role[i].out) & 3)
             edge = true;
     }
-    const unsigned grid = ((unsigned)a.B * a.H * a.S + 7) / 8 * 8 * b.slices * roles;
+    // Sequences of a segment go to several workgroups where there are few: as many as let two
+    // stay on a compute unit.
+    const long long walks = (long long)a.B * a.H * a.S, wide = walks * b.slices * roles;
+    b.parts = 1;
+    if (!STATE && a.cu && wide < 512) {
+        const int most = a.N < a.L ? a.N : a.L;
+        b.parts = 512 / wide < most ? (int)(512 / wide) : most;
+    }
+    b.tokens = (a.L + b.parts - 1) / b.parts;
+    const unsigned grid = ((unsigned)walks * b.parts + 7) / 8 * 8 * b.slices * roles;
     auto launch = [&](auto exactly) {
         constexpr bool EXACT = decltype(exactly)::value;
         if (edge || b.odd)

@@ -124,6 +124,18 @@ def test_packed(name, io):
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("T,N,tail,H", [(90, 30, 0, 6), (41, 269, 0, 2), (700, 40, 13, 2), (1700, 23, 5, 1), (64, 64, 0, 40),
+                                        (5, 1, 2, 1)])
+def test_many_short_sequences(T, N, tail, H, io):
+    # several workgroups share a segment's sequences: cuts anywhere, empty ones, long ones
+    rng = np.random.default_rng(T + N)
+    cu = [0] + sorted(rng.integers(0, T - tail + 1, N - 1).tolist()) + [T - tail]
+    both(data(1, T, H, H, 49, 32, io, seed=T, cu=cu), io, None, cu)
+    one_by_one = list(range(T - tail + 1))
+    both(data(1, T, 1, 1, 16, 70, io, seed=N, cu=one_by_one), io, None, one_by_one)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
 @pytest.mark.parametrize("H,Hk", [(4, 4), (4, 2), (6, 2), (8, 1)])
 def test_shared_keys(H, Hk, io):
     both(data(2, 70, H, Hk, 32, 48, io, H + Hk), io, None)
