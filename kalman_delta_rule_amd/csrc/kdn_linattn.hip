@@ -269,32 +269,53 @@ struct Tile {
                     turn(from, i);
         }
     };
-    // the same where rows begin in the middle of a word, through registers
+    // the same where rows begin in the middle of a word, through registers: a row's last piece
+    // is read so that it ends with the row, and moved.  (One load after another, without a
+    // branch: what waits for one would wait for all.)
     static __device__ __forceinline__ void copy_odd(uint32_t lds, const IO* p, int ts, int len, int width, int dir)
     {
         struct __attribute__((packed, aligned(2))) Piece {
             uint32_t w[4];
         };
-        typedef uint32_t four __attribute__((ext_vector_type(4)));
-        four x[NP];
+        const int j = (int)threadIdx.x % PER * VE;
+        if (width < VE) {
 #pragma unroll
-        for (int n = 0; n < NP; ++n) {
-            const int i = row(n), j = (int)threadIdx.x % PER * VE;
-            const IO* from = p + (ptrdiff_t)(dir < 0 ? len - 1 - i : i) * ts + j;
-            x[n] = four{};
-            if (i < len && j + VE <= width) {
-                const Piece piece = *reinterpret_cast<const Piece*>(from);
-                x[n] = four{piece.w[0], piece.w[1], piece.w[2], piece.w[3]};
-            } else if (i < len && j < width) {
+            for (int n = 0; n < NP; ++n) {
+                const int i = min(row(n), len - 1);
+                const IO* from = p + (ptrdiff_t)(dir < 0 ? len - 1 - i : i) * ts;
+                IO x[VE];
 #pragma unroll
                 for (int e = 0; e < VE; ++e)
-                    if (j + e < width)
-                        x[n][e / 2] |= (uint32_t) __builtin_bit_cast(uint16_t, (bf16)from[e]) << (e % 2 * 16);
-            }
-        }
+                    x[e] = from[min(e, width - 1)];
+                u32x4 w = {};
 #pragma unroll
-        for (int n = 0; n < NP; ++n)
-            lds_write(lds + L::at(row(n), (int)threadIdx.x % PER), x[n]);
+                for (int e = 0; e < VE; ++e)
+                    if (j + e < width && row(n) < len)
+                        w[e * E / 4] |= (uint32_t) __builtin_bit_cast(uint16_t, (bf16)x[e]) << (e % 2 * 16);
+                lds_write(lds + L::at(row(n), j / VE), w);
+            }
+            return;
+        }
+        Piece x[NP];
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            const int i = min(row(n), len - 1);
+            x[n] = *reinterpret_cast<const Piece*>(p + (ptrdiff_t)(dir < 0 ? len - 1 - i : i) * ts + min(j, width - VE));
+        }
+        const int over = j + VE - width, by = (VE - width % VE) * 16;  // bits (where a piece is not whole)
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            u32x4 w = {x[n].w[0], x[n].w[1], x[n].w[2], x[n].w[3]};
+            if (over > 0) {
+                typedef uint64_t two __attribute__((ext_vector_type(2)));
+                two d = __builtin_bit_cast(two, w);
+                d = by < 64 ? two{d.x >> by | d.y << (64 - by), d.y >> by} : two{d.y >> (by - 64 & 63), 0};
+                w = over < VE ? __builtin_bit_cast(u32x4, d) : u32x4{};
+            }
+            if (row(n) >= len)
+                w = u32x4{};
+            lds_write(lds + L::at(row(n), j / VE), w);
+        }
     }
     // row i's piece that the row ends in: what follows is the next head's, or the next token's
     static __device__ __forceinline__ void end_row(uint32_t lds, int i, int width)
