@@ -9,7 +9,7 @@
 // 1024 threads it is read once: a thread holds NV vectors of 16 bytes, always of the same
 // channels of its group, so that w and b, and in the backward the channels' sums, stay in
 // registers over all the units that it walks.  The variance is taken around the mean, and
-// the mean is corrected by what is left around it.  Larger units, and few large ones, are
+// the mean is corrected by what is left around it.  Larger units are
 // read twice by many workgroups, whose sums by channel are joined in between.
 #include "kdn_common.h"
 #include "kdn_lanes.h"
@@ -78,18 +78,29 @@ __device__ __forceinline__ Raw<E, VE> load_some(const E* p, int n)
     __builtin_memcpy(r.w, v, sizeof(v));
     return r;
 }
-// all of them, or none
+// The same without a branch a value.  WHOLE: all of them are there, or none.  Else, and
+// where VE values end with the last one there (back), a vector that is not whole is read so,
+// and `settle` moves its values to the front once they are used: what waits for one load
+// would wait for all.  (2497 x 73 positions of 16 groups of 20, forward: 167 us without.)
 template <bool WHOLE, typename E, int VE>
-__device__ __forceinline__ Raw<E, VE> load_part(const E* p, int n)
+__device__ __forceinline__ Raw<E, VE> load_part(const E* p, int n, bool back)
 {
-    if constexpr (WHOLE) {
-        Raw<E, VE> r{};
-        if (n)
-            r = load_raw<false, E, VE>(p);
-        return r;
-    } else {
+    if (!WHOLE && !back)
         return load_some<E, VE>(p, n);
-    }
+    Raw<E, VE> r{};
+    if (n)
+        r = load_raw<false, E, VE>(WHOLE ? p : p - (VE - n));
+    return r;
+}
+template <bool WHOLE, typename E, int VE>
+__device__ __forceinline__ void settle(Raw<E, VE>& r, int n, bool back)
+{
+    if (WHOLE || !back || n == VE || n == 0)
+        return;
+    const int by = (VE - n) * (int)sizeof(E) * 8;  // under 128
+    const uint64_t low = r.w[0] | (uint64_t)r.w[1] << 32, high = r.w[2] | (uint64_t)r.w[3] << 32;
+    const uint64_t x = by < 64 ? low >> by | high << (64 - by) : high >> (by - 64), y = by < 64 ? high >> by : 0;
+    r.w[0] = (uint32_t)x, r.w[1] = (uint32_t)(x >> 32), r.w[2] = (uint32_t)y, r.w[3] = (uint32_t)(y >> 32);
 }
 template <typename E, int VE>
 __device__ __forceinline__ void store_some(E* p, const float (&v)[VE], int n)
@@ -98,10 +109,27 @@ __device__ __forceinline__ void store_some(E* p, const float (&v)[VE], int n)
         store_raw<E, VE>(p, v);
         return;
     }
+    // by halves, quarters, ..
+    E x[VE];
 #pragma unroll
     for (int j = 0; j < VE; ++j)
-        if (j < n)
-            p[j] = from_f32<E>(v[j]);
+        x[j] = from_f32<E>(v[j]);
+    if constexpr (VE == 8) {
+        if (n & 4) {
+            store_raw<E, 4>(p, {v[0], v[1], v[2], v[3]});
+            p += 4;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                x[j] = x[j + 4];
+        }
+    }
+    if (n & 2) {
+        p[0] = x[0], p[1] = x[1];
+        p += 2;
+        x[0] = x[2];
+    }
+    if (n & 1)
+        p[0] = x[0];
 }
 // Values are taken from their words again: kept as fp32 from one pass over a unit to the
 // next they would need twice the registers.
@@ -136,6 +164,7 @@ struct Part {
     int set, n, g, step;    // of units: this one's sample and group, sets of the launch
     int s0, ds, col, width; // this thread's first position, positions a turn, channels
     bool on;                // there is such a unit
+    bool back;              // VE values end with a group's last
 
     __device__ __forceinline__ Part(const GroupNormArgs& a, const Held& held)
     {
@@ -160,6 +189,7 @@ struct Part {
         s0 = t / held.pad, ds = TPR / held.pad;
         col = g * Cg + piece * VE;
         width = min(max(Cg - piece * VE, 0), VE);
+        back = Cg >= VE;
     }
     // elements that there are of vector v
     __device__ __forceinline__ int there(int S, int v) const { return s0 + v * ds < S ? width : 0; }
@@ -194,7 +224,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void group_norm_fwd_kernel(G
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int n = sample < a.N ? part.there(a.S, v) : 0;
-            to[v] = load_part<WHOLE, IO, VE>(x + (n ? part.at(a, v, a.xs, sample) : 0), n);
+            to[v] = load_part<WHOLE, IO, VE>(x + (n ? part.at(a, v, a.xs, sample) : 0), n, part.back);
         }
     };
     if constexpr (AHEAD)
@@ -211,6 +241,9 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void group_norm_fwd_kernel(G
         } else {
             load(raw, part.n);
         }
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            settle<WHOLE>(raw[v], part.width, part.back);
         float s = 0.f;
 #pragma unroll
         for (int v = 0; v < NV; ++v)
@@ -287,28 +320,24 @@ __global__ __launch_bounds__(bwd_threads(TPR)) void group_norm_bwd_kernel(GroupN
     const IO* x = static_cast<const IO*>(a.x);
     const IO* dy = static_cast<const IO*>(a.dy);
     IO* dx = static_cast<IO*>(a.dx);
-    constexpr bool AHEAD = false;
     const long long units = (long long)a.N * a.G;
-    Raw<IO, VE> rx[NV], ry[NV], nx[AHEAD ? NV : 1], ny[AHEAD ? NV : 1];
+    Raw<IO, VE> rx[NV], ry[NV];
     auto load = [&](Raw<IO, VE>(&tx)[NV], Raw<IO, VE>(&ty)[NV], int sample) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int n = sample < a.N ? part.there(a.S, v) : 0;
-            tx[v] = load_part<WHOLE, IO, VE>(x + (n ? part.at(a, v, a.xs, sample) : 0), n);
-            ty[v] = load_part<WHOLE, IO, VE>(dy + (n ? part.at(a, v, a.C, sample) : 0), n);
+            tx[v] = load_part<WHOLE, IO, VE>(x + (n ? part.at(a, v, a.xs, sample) : 0), n, part.back);
+            ty[v] = load_part<WHOLE, IO, VE>(dy + (n ? part.at(a, v, a.C, sample) : 0), n, part.back);
         }
     };
-    if constexpr (AHEAD)
-        load(nx, ny, part.n);
     for (long long u = SETS == 1 ? part.set : blockIdx.x * (long long)SETS; u < units; u += part.step, part.n += part.step / a.G) {
         const bool on = part.n < a.N;
         float kept[KEEP ? NV : 1][VE];
-        if constexpr (AHEAD) {
-            rx[0] = nx[0], ry[0] = ny[0];
-            if (u + part.step < units)
-                load(nx, ny, part.n + part.step / a.G);
-        } else {
-            load(rx, ry, part.n);
+        load(rx, ry, part.n);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            settle<WHOLE>(rx[v], part.width, part.back);
+            settle<WHOLE>(ry[v], part.width, part.back);
         }
         const size_t i = (size_t)(on ? part.n : 0) * a.G + part.g;
         const float mean = a.mean[i], rstd = a.rstd[i];
@@ -433,6 +462,7 @@ struct Split {
 template <int VE>
 struct Place {
     int n, tile, c, width, s, s1, ds, lane;
+    bool back;  // VE values end with a row's last
     __device__ __forceinline__ Place(const GroupNormArgs& a, const Split& p)
     {
         int i = blockIdx.x;
@@ -442,6 +472,7 @@ struct Place {
         lane = threadIdx.x & (p.lanes - 1);
         c = (block * p.lanes + lane) * VE;
         width = min(max(a.C - c, 0), VE);
+        back = a.C >= VE;
         ds = 256 / p.lanes;
         s = tile * p.rows + threadIdx.x / p.lanes;
         s1 = min(a.S, (tile + 1) * p.rows);
@@ -481,7 +512,7 @@ __device__ __forceinline__ void channel_sums(const Place<VE>& at, const Split& p
 
 // A tile's mean and sum of squares around it, by channel: around the tile's first value, so
 // that nothing large cancels.  ws [N][tiles][C][2]
-template <typename IO>
+template <typename IO, bool WHOLE>
 __global__ __launch_bounds__(256) void group_norm_stats_kernel(GroupNormArgs a, Split p, float2* ws)
 {
     constexpr int VE = 16 / sizeof(IO);
@@ -499,7 +530,8 @@ __global__ __launch_bounds__(256) void group_norm_stats_kernel(GroupNormArgs a, 
     if (at.width)
 #pragma unroll 4
         for (int s = at.s; s < at.s1; s += at.ds) {
-            const Raw<IO, VE> r = load_some<IO, VE>(x + (size_t)s * a.xs, at.width);
+            Raw<IO, VE> r = load_part<WHOLE, IO, VE>(x + (size_t)s * a.xs, WHOLE ? VE : at.width, at.back);
+            settle<WHOLE>(r, at.width, at.back);
 #pragma unroll
             for (int j = 0; j < VE; ++j) {
                 const float d = r.get(j) - k[j];
@@ -552,7 +584,7 @@ __global__ __launch_bounds__(256) void group_norm_join_kernel(GroupNormArgs a, S
     }
 }
 
-template <typename IO>
+template <typename IO, bool WHOLE>
 __global__ __launch_bounds__(256) void group_norm_apply_kernel(GroupNormArgs a, Split p, const float2* stats)
 {
     constexpr int VE = 16 / sizeof(IO);
@@ -572,7 +604,8 @@ __global__ __launch_bounds__(256) void group_norm_apply_kernel(GroupNormArgs a, 
     IO* y = static_cast<IO*>(a.y) + (size_t)at.n * a.S * a.C + at.c;
 #pragma unroll 4
     for (int s = at.s; s < at.s1; s += at.ds) {
-        const Raw<IO, VE> r = load_some<IO, VE>(x + (size_t)s * a.xs, at.width);
+        Raw<IO, VE> r = load_part<WHOLE, IO, VE>(x + (size_t)s * a.xs, WHOLE ? VE : at.width, at.back);
+        settle<WHOLE>(r, at.width, at.back);
         float o[VE];
 #pragma unroll
         for (int j = 0; j < VE; ++j)
@@ -582,13 +615,13 @@ __global__ __launch_bounds__(256) void group_norm_apply_kernel(GroupNormArgs a, 
             for (int j = 0; j < VE; ++j)
                 o[j] = silu_of(o[j]);
         }
-        store_some<IO, VE>(y + (size_t)s * a.C, o, at.width);
+        store_some<IO, VE>(y + (size_t)s * a.C, o, WHOLE ? VE : at.width);
     }
 }
 
 // The backward's first pass (APPLY false): sums of g and g xh by channel of a tile, ws
 // [N][tiles][2][C]; and its second: dx, with the groups' means of g w and g w xh in `means`.
-template <typename IO, bool APPLY>
+template <typename IO, bool APPLY, bool WHOLE>
 __global__ __launch_bounds__(256) void group_norm_bwd_split_kernel(GroupNormArgs a, Split p, float* ws, const float2* means)
 {
     constexpr int VE = 16 / sizeof(IO);
@@ -612,8 +645,10 @@ __global__ __launch_bounds__(256) void group_norm_bwd_split_kernel(GroupNormArgs
     if (at.width)
 #pragma unroll 2
         for (int s = at.s; s < at.s1; s += at.ds) {
-            const Raw<IO, VE> rx = load_some<IO, VE>(x + (size_t)s * a.xs, at.width);
-            const Raw<IO, VE> ry = load_some<IO, VE>(dy + (size_t)s * a.C, at.width);
+            Raw<IO, VE> rx = load_part<WHOLE, IO, VE>(x + (size_t)s * a.xs, WHOLE ? VE : at.width, at.back);
+            Raw<IO, VE> ry = load_part<WHOLE, IO, VE>(dy + (size_t)s * a.C, WHOLE ? VE : at.width, at.back);
+            settle<WHOLE>(rx, at.width, at.back);
+            settle<WHOLE>(ry, at.width, at.back);
             float o[VE];
 #pragma unroll
             for (int j = 0; j < VE; ++j) {
@@ -627,7 +662,7 @@ __global__ __launch_bounds__(256) void group_norm_bwd_split_kernel(GroupNormArgs
                 }
             }
             if constexpr (APPLY)
-                store_some<IO, VE>(dx + (size_t)s * a.C, o, at.width);
+                store_some<IO, VE>(dx + (size_t)s * a.C, o, WHOLE ? VE : at.width);
         }
     if constexpr (!APPLY) {
         float* out = ws + ((size_t)at.n * p.tiles + at.tile) * 2 * a.C;
@@ -672,8 +707,16 @@ int power_of_two(int n)
 
 int common(int a, int b) { return b ? common(b, a % b) : a; }
 
-// The fewest threads whose registers hold a unit, up to 4 vectors each (8 of 1024); more
-// threads where units are few.  Few large units are split instead.
+// The fewest threads whose registers hold a unit, up to 4 vectors each (8 of 1024, forward);
+// more threads where units are few.  Larger units are split.  (bf16 with SiLU, held against
+// split: units of 65536 values forward, 512 of them 41 us against 48, 32 of them 15 against
+// 18, one 14.5 against 17.  The backward holds two tensors, 4 vectors of each.)
+//
+// Groups that are not whole vectors leave threads without one: large calls are split from as
+// many positions on as the sums by channel then cost less.  (320 channels, held against split:
+// 512 x 256 positions, 16 groups: forward 62 us against 60, backward 155 against 87; 256 x 256
+// positions, 64 groups, 101 and 168 against 48 and 63; 1024 x 64 positions 56 and 117 against 88
+// and 87; of 6 MB, 32 x 256 positions of 352 channels, 12 and 19 against 18 and 24.)
 Held held_shape(int N, int S, int C, int G, bool bf, bool backward)
 {
     const int VE = bf ? 8 : 4, Cg = C / G;
@@ -681,7 +724,8 @@ Held held_shape(int N, int S, int C, int G, bool bf, bool backward)
     Held h{};
     h.pad = power_of_two(ceil_div(Cg, VE));
     const long long pieces = (long long)S * h.pad;
-    if (h.pad > 1024 || pieces > (backward ? 4 : 8) * 1024 || (units < 128 && pieces > 1024))
+    const bool uneven = Cg % VE && S >= (backward ? 64 : 256) && (long long)N * S * C * (bf ? 2 : 4) >= 32 << 20;
+    if (h.pad > 1024 || pieces > (backward ? 4 : 8) * 1024 || uneven)
         return h;
     const int sizes[] = {8, 16, 32, 64, 256, 1024};
     int k = 0;
@@ -742,6 +786,16 @@ void with_held(const Held& h, F f)
         with<1024, 1>(h, f) || with<1024, 2>(h, f) || with<1024, 4>(h, f) || with<1024, 8>(h, f);
 }
 
+// calls f with whether rows of C values are whole vectors
+template <typename IO, typename F>
+void with_whole(int C, F f)
+{
+    if (C % (16 / sizeof(IO)) == 0)
+        f(std::true_type{});
+    else
+        f(std::false_type{});
+}
+
 template <typename IO>
 hipError_t group_norm_fwd(const GroupNormArgs& a, hipStream_t stream)
 {
@@ -761,9 +815,12 @@ hipError_t group_norm_fwd(const GroupNormArgs& a, hipStream_t stream)
     const unsigned grid = (unsigned)a.N * p.tiles * p.blocks;
     float2* ws = static_cast<float2*>(a.ws);
     float2* stats = ws + (size_t)a.N * p.tiles * a.C;
-    group_norm_stats_kernel<IO><<<grid, 256, 0, stream>>>(a, p, ws);
-    group_norm_join_kernel<<<(unsigned)a.N * a.G, 256, 0, stream>>>(a, p, ws, stats);
-    group_norm_apply_kernel<IO><<<grid, 256, 0, stream>>>(a, p, stats);
+    with_whole<IO>(a.C, [&](auto w) {
+        constexpr bool WHOLE = decltype(w)::value;
+        group_norm_stats_kernel<IO, WHOLE><<<grid, 256, 0, stream>>>(a, p, ws);
+        group_norm_join_kernel<<<(unsigned)a.N * a.G, 256, 0, stream>>>(a, p, ws, stats);
+        group_norm_apply_kernel<IO, WHOLE><<<grid, 256, 0, stream>>>(a, p, stats);
+    });
     return hipGetLastError();
 }
 
@@ -796,9 +853,12 @@ hipError_t group_norm_bwd(const GroupNormArgs& args, hipStream_t stream)
         const Split p = split_shape(a.N, a.S, a.C, sizeof(IO) == 2);
         const unsigned grid = (unsigned)a.N * p.tiles * p.blocks;
         float2* means = reinterpret_cast<float2*>(ws + (size_t)a.N * p.tiles * 2 * a.C);
-        group_norm_bwd_split_kernel<IO, false><<<grid, 256, 0, stream>>>(a, p, ws, nullptr);
-        group_norm_means_kernel<<<(unsigned)a.N * a.G, 256, 0, stream>>>(a, p, ws, means);
-        group_norm_bwd_split_kernel<IO, true><<<grid, 256, 0, stream>>>(a, p, ws, means);
+        with_whole<IO>(a.C, [&](auto w) {
+            constexpr bool WHOLE = decltype(w)::value;
+            group_norm_bwd_split_kernel<IO, false, WHOLE><<<grid, 256, 0, stream>>>(a, p, ws, nullptr);
+            group_norm_means_kernel<<<(unsigned)a.N * a.G, 256, 0, stream>>>(a, p, ws, means);
+            group_norm_bwd_split_kernel<IO, true, WHOLE><<<grid, 256, 0, stream>>>(a, p, ws, means);
+        });
         slots = a.N * p.tiles;
     }
     if (sums)

@@ -66,6 +66,15 @@ def test_group_norm(N, S, C, G, io):
     assert set(only) == {"dx"} and same(only["dx"], g["dx"])
 
 
+# groups whose last vector holds one to all but one of its values; large calls of such
+# groups, whose sums go by channel
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("N,S,C,G", [(50, 3, 3 * n, 3) for n in range(5, 24)] + [(2, 9000, 2 * n, 2) for n in (5, 9, 14, 23)] +
+                         [(1, 9000, n, 1) for n in (3, 5, 7, 9, 13)] + [(64, 260, 1029, 7), (300, 70, 900, 36)])
+def test_group_norm_of_uneven_groups(N, S, C, G, io):
+    test_group_norm(N, S, C, G, io)
+
+
 def test_one_group_of_a_row_is_layer_norm():
     x = torch.randn(300, 1000, device="cuda")
     w, b = torch.randn(1000, device="cuda"), torch.randn(1000, device="cuda")
