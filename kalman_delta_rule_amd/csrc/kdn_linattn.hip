@@ -1156,12 +1156,19 @@ void launch_states(const LinArgs& a, int roles, hipStream_t stream)
     linattn_join_kernel<<<dim3((unsigned)((dense + kThreads - 1) / kThreads), a.B * a.H, roles), kThreads, 0, stream>>>(a);
 }
 
-// Segments of a row and the tokens of one, a multiple of 64: one where the walks fill the
-// chip, else as many as let two workgroups stay on a compute unit, of 128 tokens at least.
-int segments(int B, int T, int H, int slices, int& L)
+// Segments of a row and the tokens of one, a multiple of 64, of 128 at least: one where the
+// walks fill the chip, else as many as let two workgroups stay on a compute unit.  The
+// backward's walks, which meet each other's inputs in the caches, take half as many again
+// where segments stay long.  (us, heads of 128 in bf16.  From 256 walks on, 8 x 4096 tokens of
+// 16 heads: 134 forward in one segment, 197 in two.  65536 tokens of 16 heads: 397 forward by
+// 512 workgroups, 426 by 256, 436 by 1024; backward 941 by 512, 901 by 768, 945 by 1024.
+// 2 x 16384 tokens backward 537 by 512, 454 by 768; 2 x 2048 79 and 83.  512 tokens of 4 heads
+// in fp32: 29 forward in segments, 52 in one; of 256 tokens at least, 2 x 2047 tokens of 6
+// heads in fp32 take 74 instead of 62.)
+int segments(int B, int T, int H, int slices, bool backward, int& L)
 {
-    const long long groups = (long long)B * H * slices;
-    const long long want = groups >= 256 ? 1 : 512 / groups, most = T < 512 ? 1 : T / 128;
+    const long long groups = (long long)B * H * slices, wanted = backward && T * groups >= 2048 * 768 ? 768 : 512;
+    const long long want = groups >= 256 ? 1 : wanted / groups, most = T < 512 ? 1 : T / 128;
     const long long S = want < most ? want : most;
     L = S <= 1 ? (T > 0 ? T : 1) : (int)(((T + S - 1) / S + 63) / 64 * 64);
     return T > 0 ? (T + L - 1) / L : 1;
@@ -1195,7 +1202,7 @@ hipError_t linattn_fwd(const LinArgs& a, hipStream_t stream)
 size_t linattn_fwd_workspace_bytes(int B, int T, int H, int dk, int dv)
 {
     int L;
-    const int S = segments(B, T, H, slices_of(dv), L);
+    const int S = segments(B, T, H, slices_of(dv), false, L);
     return handed_bytes(B, S, H, dk, dv);
 }
 
@@ -1203,7 +1210,7 @@ static size_t bwd_segments_bytes(int B, int T, int H, int dk, int dv, int& S, in
 {
     // walks of the same width go in one launch
     const int of_dv = slices_of(dv), of_dk = 2 * slices_of(dk);
-    S = segments(B, T, H, padded(dk) == padded(dv) ? of_dv + of_dk : of_dv < of_dk ? of_dv : of_dk, L);
+    S = segments(B, T, H, padded(dk) == padded(dv) ? of_dv + of_dk : of_dv < of_dk ? of_dv : of_dk, true, L);
     return handed_bytes(B, S, H, dk, dv);
 }
 
@@ -1225,7 +1232,7 @@ hipError_t launch_linattn_fwd(const LinCall& c, bool bf, hipStream_t stream)
 {
     LinArgs a{};
     a.B = c.B, a.T = c.T, a.H = c.H, a.N = c.N, a.cu = c.cu, a.decay = c.decay, a.clear = c.clear;
-    a.S = segments(c.B, c.T, c.H, slices_of(c.dv), a.L);
+    a.S = segments(c.B, c.T, c.H, slices_of(c.dv), false, a.L);
     LinRole& r = a.role[0];
     r.q = c.q, r.k = c.k, r.v = c.v;
     r.out = c.o, r.X0 = c.S0, r.XT = c.S_T, r.exact = c.S_T != nullptr;
