@@ -595,8 +595,9 @@ kdn_status kdn_rec_step(int B, int D, int io_dtype, int gate, int blend, const v
  *         many tokens: the states handed between pieces of a sequence)
  * bf16: products of bf16 operands, summed in fp32; the products' own operands
  * that are not inputs (the decayed q k^T, and the state where o is formed from
- * it) are rounded to bf16, those that states are summed from to 16 bits.  fp32:
- * products of fp32 operands.
+ * it) are rounded to bf16, those that states are summed from to 16 bits, and to
+ * 24 where the state is an output and the token still has an eighth of its weight
+ * in it.  fp32: products of fp32 operands.
  * What is not finite stays in its sequence and head and reaches no earlier
  * token; an infinity may become a NaN later in the sequence.
  */
@@ -654,7 +655,7 @@ kdn_status kdn_linattn_step(int B, int H, int Hk, int dk, int dv, int io_dtype, 
  *   mean, rstd   [N,G] fp32, written; each nullable
  *   eps    finite, >= 0;  N G below 2^24
  *   workspace    kdn_group_norm_fwd_workspace_size bytes (0 unless a group is
- *          too large for one workgroup)
+ *          too large for one workgroup, or not whole vectors in a large call)
  */
 size_t kdn_group_norm_fwd_workspace_size(int N, int S, int C, int G);
 kdn_status kdn_group_norm_fwd(int N, int S, int C, int G, int io_dtype, int activation, float eps,
