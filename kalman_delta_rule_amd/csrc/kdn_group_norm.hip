@@ -65,43 +65,62 @@ __device__ __forceinline__ float2 unit_sum(float a, float b, float2* red)
     return float2{a, b};
 }
 
-// VE adjacent values, the first n of them there
-template <typename E, int VE>
-__device__ __forceinline__ Raw<E, VE> load_some(const E* p, int n)
-{
-    if (n >= VE)
-        return load_raw<false, E, VE>(p);
-    E v[VE];
-#pragma unroll
-    for (int j = 0; j < VE; ++j)
-        v[j] = j < n ? p[j] : E(0.f);
-    Raw<E, VE> r;
-    __builtin_memcpy(r.w, v, sizeof(v));
-    return r;
-}
-// The same without a branch a value.  WHOLE: all of them are there, or none.  Else, and
-// where VE values end with the last one there (back), a vector that is not whole is read so,
-// and `settle` moves its values to the front once they are used: what waits for one load
-// would wait for all.  (2497 x 73 positions of 16 groups of 20, forward: 167 us without.)
+// VE adjacent values, the first n of them there (WHOLE: all or none), without a branch a value.
+// A vector that is not whole is read so that it ends with its last value, if VE values end there
+// (back), else in halves, quarters, ..; `settle` puts its values in place once they are used,
+// since what waits for one load would wait for all.  (2497 x 73 positions of 16 groups of 20,
+// forward: 164 us a value at a time, 102 so.)
 template <bool WHOLE, typename E, int VE>
 __device__ __forceinline__ Raw<E, VE> load_part(const E* p, int n, bool back)
 {
-    if (!WHOLE && !back)
-        return load_some<E, VE>(p, n);
     Raw<E, VE> r{};
-    if (n)
-        r = load_raw<false, E, VE>(WHOLE ? p : p - (VE - n));
+    if (WHOLE || back) {
+        if (n)
+            r = load_raw<false, E, VE>(WHOLE ? p : p - (VE - n));
+    } else if (n == VE) {
+        r = load_raw<false, E, VE>(p);
+    } else if constexpr (VE == 8) {
+        if (n & 4) {
+            const auto x = load_raw<false, E, 4>(p);
+            r.w[0] = x.w[0], r.w[1] = x.w[1];
+        }
+        if (n & 2)
+            r.w[2] = load_raw<false, E, 2>(p + (n & 4)).w[0];
+        if (n & 1)
+            r.w[3] = load_raw<false, E, 1>(p + (n & 6)).w[0];
+    } else {
+        if (n & 2) {
+            const auto x = load_raw<false, E, 2>(p);
+            r.w[0] = x.w[0], r.w[1] = x.w[1];
+        }
+        if (n & 1)
+            r.w[3] = load_raw<false, E, 1>(p + (n & 2)).w[0];
+    }
     return r;
 }
 template <bool WHOLE, typename E, int VE>
 __device__ __forceinline__ void settle(Raw<E, VE>& r, int n, bool back)
 {
-    if (WHOLE || !back || n == VE || n == 0)
+    if (WHOLE || n == VE || n == 0)
         return;
-    const int by = (VE - n) * (int)sizeof(E) * 8;  // under 128
-    const uint64_t low = r.w[0] | (uint64_t)r.w[1] << 32, high = r.w[2] | (uint64_t)r.w[3] << 32;
-    const uint64_t x = by < 64 ? low >> by | high << (64 - by) : high >> (by - 64), y = by < 64 ? high >> by : 0;
-    r.w[0] = (uint32_t)x, r.w[1] = (uint32_t)(x >> 32), r.w[2] = (uint32_t)y, r.w[3] = (uint32_t)(y >> 32);
+    if (back) {
+        const int by = (VE - n) * (int)sizeof(E) * 8;  // under 128
+        const uint64_t low = r.w[0] | (uint64_t)r.w[1] << 32, high = r.w[2] | (uint64_t)r.w[3] << 32;
+        const uint64_t x = by < 64 ? low >> by | high << (64 - by) : high >> (by - 64), y = by < 64 ? high >> by : 0;
+        r.w[0] = (uint32_t)x, r.w[1] = (uint32_t)(x >> 32), r.w[2] = (uint32_t)y, r.w[3] = (uint32_t)(y >> 32);
+    } else if constexpr (VE == 8) {
+        const uint32_t two = r.w[2], one = r.w[3], x = n & 2 ? two : one, y = n & 2 ? one : 0;
+        if (n & 4)
+            r.w[2] = x, r.w[3] = y;
+        else
+            r.w[0] = x, r.w[1] = y, r.w[2] = r.w[3] = 0;
+    } else {
+        if (n & 2)
+            r.w[2] = r.w[3];
+        else
+            r.w[0] = r.w[3];
+        r.w[3] = 0;
+    }
 }
 template <typename E, int VE>
 __device__ __forceinline__ void store_some(E* p, const float (&v)[VE], int n)
@@ -525,7 +544,8 @@ __global__ __launch_bounds__(256) void group_norm_stats_kernel(GroupNormArgs a, 
     const int s0 = at.tile * p.rows;
     float k[VE], d1[VE] = {}, d2[VE] = {};
     {
-        const Raw<IO, VE> r = load_some<IO, VE>(x + (at.width ? (size_t)s0 * a.xs : 0), at.width);
+        Raw<IO, VE> r = load_part<WHOLE, IO, VE>(x + (at.width ? (size_t)s0 * a.xs : 0), at.width, at.back);
+        settle<WHOLE>(r, at.width, at.back);
 #pragma unroll
         for (int j = 0; j < VE; ++j)
             k[j] = r.get(j);
@@ -718,7 +738,7 @@ int common(int a, int b) { return b ? common(b, a % b) : a; }
 // Groups that are not whole vectors leave threads without one: large calls are split from as
 // many positions on as the sums by channel then cost less.  (320 channels, held against split:
 // 512 x 256 positions, 16 groups: forward 62 us against 60, backward 155 against 87; 256 x 256
-// positions, 64 groups, 101 and 168 against 48 and 63; 1024 x 64 positions 56 and 117 against 88
+// positions, 64 groups, 101 and 168 against 48 and 63; 1024 x 64 positions 41 and 117 against 88
 // and 87; of 6 MB, 32 x 256 positions of 352 channels, 12 and 19 against 18 and 24.)
 Held held_shape(int N, int S, int C, int G, bool bf, bool backward)
 {
