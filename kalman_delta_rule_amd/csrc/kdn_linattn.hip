@@ -33,6 +33,7 @@
 // fp32: matrix instructions with fp32 operands throughout.
 #include "kdn_common.h"
 #include "kdn_linattn.h"
+#include "kdn_linattn_spans.h"
 #include "kdn_sequences.h"
 #include "kdn_stream.h"
 
@@ -333,111 +334,10 @@ struct Tile {
     }
 };
 
-// Tokens [from, to) of sequence n, and whether they hold its first and last token in
-// the order of the walk
-struct Span {
-    int n, from, to;
-    bool first, last;
+// of the spans' offsets: by all threads
+struct Counted {
+    static __device__ __forceinline__ int at_most(const int* p, int n, int x) { return count_at_most<kThreads>(p, n, x); }
 };
-
-// The spans of one segment [t0, t1) of a row, in the order of the walk; with offsets, those
-// that begin in a part of it.  Offsets may hold anything: spans lie in the segment and follow
-// one another.
-struct Spans {
-    const int* cu;
-    int N, t0, t1, rev, at, n;
-    int u0, u1;  // the part
-
-    // (all threads) cu[n] <= token, the last such n
-    __device__ __forceinline__ int holding(int token) const { return count_at_most<kThreads>(cu, N, token) - 1; }
-
-    __device__ __forceinline__ void start(const LinArgs& a, int b, int begin, int end, int backwards, int part)
-    {
-        cu = a.cu, N = a.N, t0 = begin, t1 = end, rev = backwards;
-        u0 = min(t1, t0 + part * a.tokens), u1 = min(t1, u0 + a.tokens);
-        at = rev ? u1 : u0;
-        n = cu ? -1 : b;
-        if (cu && u0 < u1 && at != (rev ? t1 : t0)) {
-            // a sequence that goes on here is the neighbour's
-            const int m = holding(at - 1);
-            if (m >= 0 && cu[m + 1] > at)
-                at = rev ? max(min(cu[m], at), u0) : min(cu[m + 1], u1);
-        }
-    }
-    __device__ __forceinline__ bool next(Span& s, int T)
-    {
-        if (rev ? at <= u0 : at >= u1)
-            return false;
-        if (!cu) {
-            s = Span{n, t0, t1, rev ? t1 == T : t0 == 0, rev ? t0 == 0 : t1 == T};
-            at = rev ? t0 : t1;
-            return true;
-        }
-        // the sequence of the next token: mostly the neighbour of the last one
-        const int token = rev ? at - 1 : at;
-        int m = rev ? n - 1 : n + 1;
-        if (n < 0 || m < 0 || m >= N || cu[m] > token || cu[m + 1] <= token)
-            m = holding(token);
-        if (m < 0 || cu[m + 1] <= token) {
-            // behind the last sequence; backwards there may be sequences before
-            if (!rev || m < 0)
-                return false;
-            const int e = min(cu[m + 1], token);
-            if (e <= u0)
-                return false;
-            at = e;
-            n = -1;
-            return next_of(s, holding(e - 1));
-        }
-        return next_of(s, m);
-    }
-    __device__ __forceinline__ bool next_of(Span& s, int m)
-    {
-        if (m < 0)
-            return false;
-        const int p = cu[m], e = cu[m + 1];
-        s.n = m;
-        if (rev) {
-            s.to = at, s.from = max(p, t0);
-            if (s.from >= s.to || e < at)
-                return false;
-            s.first = e == s.to, s.last = p == s.from;
-            at = s.from;
-        } else {
-            s.from = at, s.to = min(e, t1);
-            if (s.to <= s.from || p > at)
-                return false;
-            s.first = p == s.from, s.last = e == s.to;
-            at = s.to;
-        }
-        n = m;
-        return true;
-    }
-};
-
-// Which tokens of the segment before (in the order of the walk) the state handed on to
-// segment s comes from: false where s begins with a sequence of its own.
-__device__ __forceinline__ bool handed_on(const LinArgs& a, int b, int s, int rev, Span& x)
-{
-    // the border between segment s and the next one in the order of the walk
-    const int border = rev ? s * a.L : (s + 1) * a.L;
-    const int t0 = s * a.L, t1 = min(a.T, t0 + a.L);
-    x.n = b;
-    int p = 0, e = a.T;
-    if (a.cu) {
-        x.n = count_at_most<kThreads>(a.cu, a.N, border - 1) - 1;
-        if (x.n < 0)
-            return false;
-        p = a.cu[x.n], e = a.cu[x.n + 1];
-    }
-    if (p >= border || e <= border)
-        return false;
-    x.from = rev ? border : max(p, t0);
-    x.to = rev ? min(e, t1) : border;
-    x.first = rev ? e <= t1 : p >= t0;
-    x.last = false;
-    return true;
-}
 
 // What bounds a walk (B8 T4096, 16 heads of 128 in bf16, forward, 134 us): a chunk of 64
 // tokens takes a compute unit 2 us, of which the matrix units are busy a fifth.  With copies
@@ -922,7 +822,7 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
 
     if constexpr (STATE) {
         Span span;
-        const bool some = handed_on(a, b, s, rev, span);
+        const bool some = handed_on<Counted>(a, b, s, rev, span);
         if (h == 0 && slice == 0 && threadIdx.x == 0)
             r.spans[b * a.S + s] = int4{some ? span.to - span.from : 0, span.first ? span.n : -1, 0, 0};
         if (some) {
@@ -932,7 +832,7 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
         }
     } else {
         const int t0 = s * a.L, t1 = min(a.T, t0 + a.L);
-        Spans spans;
+        Spans<Counted> spans;
         Span span;
         spans.start(a, b, t0, t1, rev, piece);
         while (spans.next(span, a.T)) {
