@@ -593,11 +593,11 @@ kdn_status kdn_rec_step(int B, int D, int io_dtype, int gate, int blend, const v
  *         each sequence (S0 for an empty one)
  *   workspace  kdn_linattn_fwd_workspace_size bytes (0 unless few heads have
  *         many tokens: the states handed between pieces of a sequence)
- * bf16: products of bf16 operands, summed in fp32; the products' own operands
- * that are not inputs (the decayed q k^T, and the state where o is formed from
- * it) are rounded to bf16, those that states are summed from to 16 bits, and to
- * 24 where the state is an output and the token still has an eighth of its weight
- * in it.  fp32: products of fp32 operands.
+ * bf16: products of bf16 operands, summed in fp32; operands that are not inputs
+ * (the decayed q k^T, the state where o is formed from it, the decayed v that
+ * states are summed from) are held to 16 bits, as two bf16 parts, the last to 24
+ * where the state is an output and the token still has an eighth of its weight in
+ * it: o is off by its own rounding.  fp32: products of fp32 operands.
  * What is not finite stays in its sequence and head and reaches no earlier
  * token; an infinity may become a NaN later in the sequence.
  */

@@ -20,16 +20,20 @@
 // a lane's four values are adjacent in a row of the decayed product, which goes through
 // LDS to all waves.  The token's decay is put on v, in registers, not on k.
 //
-// bf16: the products' operands are bf16, sums and states fp32.  q, k, v are exact.  What
-// is rounded to an operand once: the decayed q k (2^-8 of each term of a y that is
-// itself rounded to 2^-8) and X where y is formed from it (the same).  X itself is summed
-// from v's decayed values as two bf16 parts (2^-16 of each term).  Where it is an fp32
-// output a third part follows (2^-24), for the tokens before its last that still have an
-// eighth of their weight in it; of the others the two parts' error is as small.  The third
-// part costs 0 to 8% of a call (B8 T4096, 16 heads of 128: 134 us without a state out, 148
-// with, at one workgroup a compute unit, where the slowest decay's walk sets the time; B16
-// T2048, at two: 137 and 141), so walks that hand no state out do not form it, and are
-// kernels of their own: the branch alone cost them 2%.
+// bf16: the products' operands are bf16, sums and states fp32.  q, k, v are exact.  Every
+// other operand is two bf16 parts (2^-16 of each term), so that a y is off by its own rounding
+// alone: the decayed q k, X where y is formed from it, and v's decayed values that X is summed
+// from.  (With one part of the first two y was 2.3e-3 off in the 2-norm, instead of 1.7e-3.
+// Their second parts take vector instructions, which bound a walk at one workgroup a compute
+// unit: B8 T4096, 16 heads of 128, forward 147 us with one part, 177 with two; B16 T2048, at
+// two workgroups, 138 and 146; backward of the first 355 and 418, of 65536 tokens 893 and
+// 1010; B2 T2048, 16 heads of 256, backward 143 and 202.)
+// Where X is an fp32 output v has a third part (2^-24), for the tokens before its last that
+// still have an eighth of their weight in it; of the others the two parts' error is as small.
+// It costs 6% at two workgroups a compute unit (B16 T2048 forward 146 us without a state out,
+// 155 with), 15 to 20% at one, where the slowest decay's walk sets the time (B8 T4096 177 and
+// 205), so walks that hand no state out do not form it, and are kernels of their own: the
+// branch alone cost them 2%.
 // fp32: matrix instructions with fp32 operands throughout.
 #include "kdn_common.h"
 #include "kdn_linattn.h"
@@ -207,6 +211,15 @@ __device__ __forceinline__ uint32_t two_bf16(float a, float b)
 }
 __device__ __forceinline__ float low_bf16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// What is left of two values whose words as bf16 `near` is, as bf16.  An infinity leaves a
+// NaN, which the larger of two drops: some finite value, which no sum with an infinity shows.
+__device__ __forceinline__ uint32_t rest_bf16(float a, float b, uint32_t near)
+{
+    typedef float two __attribute__((ext_vector_type(2)));
+    typedef bf16 out __attribute__((ext_vector_type(2)));
+    const two rest{fmaxf(a - low_bf16(near), -0x1p120f), fmaxf(b - high_bf16(near), -0x1p120f)};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, out));
+}
 
 // What this wave copies into LDS, loads and stores has arrived, but for the last N asked
 // for.  (The compiler has to know: it would otherwise wait for loads of before the walk
@@ -355,7 +368,13 @@ struct Walk {
     typedef Tile<IO, C, kCols> TV;
     static constexpr int NT = C / 16, ST = KD / 16, KS = KD / O::K, CS = C / O::K, FE = O::K / 4;
     static constexpr bool BF = sizeof(IO) == 2;
-    static constexpr int E = sizeof(IO), kTileK = C * KD * E, kTileV = C * kCols * E, kTileP = C * C * E;  // bytes
+    static constexpr int E = sizeof(IO), kTileK = C * KD * E, kTileV = C * kCols * E;  // bytes
+    // The decayed product.  fp32: rows of C tokens j.  bf16: for each step of 32 tokens j the rows
+    // i from there on, the 32 values of the first part beside those of the second.
+    static constexpr int PW = BF ? 64 : C, kTileP = (BF && C == 64 ? 64 + 32 : C) * PW * E;
+    // bytes to step s, and the rows that it leaves out
+    static constexpr int step_at(int s) { return BF ? s * C * PW * E : 0; }
+    static constexpr int step_row(int s) { return BF ? 32 * s : 0; }
     // q once, k and v twice, the decayed product, the tokens' decays
     static constexpr int lds(bool state) { return (state ? 2 : 3) * kTileK + 2 * kTileV + (state ? 0 : kTileP) + C * 4 + (C + 1) * 4; }
 };
@@ -371,7 +390,7 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
     typedef typename W::TK TK;
     typedef typename W::TV TV;
     typedef Lds<IO, kCols> LV;
-    typedef Lds<IO, C> LP;
+    typedef Lds<IO, W::PW> LP;
     typedef Lds<IO, KD> LK;
     constexpr int NT = W::NT, ST = W::ST, KS = W::KS, CS = W::CS, FE = W::FE;
     constexpr bool BF = W::BF;
@@ -406,7 +425,6 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
     const int jt = NT == 4 ? wave : wave & 1;
     const uint32_t Ts = Ws + 4 * C;
     f32x4 pdecay[NT == 4 ? 4 : 1];
-    float front = 0.f, g16 = 0.f;
     bool ready = false;
     // tokens until a term of the state has decayed to an eighth
     int reach = 0;
@@ -426,8 +444,6 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     pdecay[i][e] = r.of_p * power(16 * ((NT == 4 ? i : wave >> 1) - jt) + c - 4 * g - e);
-            front = r.of_x * power(c + 1 - rev);
-            g16 = power(16);
         }
     };
     int held = -1;  // tokens of the chunk that Ws is for
@@ -473,10 +489,12 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
     }
 
     // places in LDS of a lane, in the first row or tile that it touches
-    uint32_t qrow = Qs + rows_at<IO, KD>(lane), prow = Ps + rows_at<IO, C>(lane);
+    uint32_t qrow = Qs + rows_at<IO, KD>(lane), prow = Ps + rows_at<IO, W::PW>(lane);
     const uint32_t kcol = Ks + O::template cols_at<KD>(0, O::kApart, lane);
     const uint32_t vcol = Vs + O::template cols_at<kCols>(16 * wave, 4, lane);
-    uint32_t pput = Ps + LP::at(c, (16 * jt + 4 * g) / O::VE) + 4 * g % O::VE * W::E;
+    const int js = BF ? jt / 2 : 0;  // the step that this wave's tokens j belong to
+    uint32_t pput = Ps + W::step_at(js) - W::step_row(js) * LP::BYTES
+                    + LP::at(c, (16 * (jt - 2 * js) + 4 * g) / O::VE) + 4 * g % O::VE * W::E;
 
     const LinTensor tq = r.q, tk = r.k, tv = r.v;
     const int kd = r.kd;
@@ -601,20 +619,11 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                 fv[s] = O::template cols<kCols>(vcol + turn * W::kTileV, s, 0);
             f32x4 acc[NT];
             if constexpr (!STATE) {
-                frag fx[KS];
-#pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    if constexpr (BF) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            fx[s][e] = static_cast<bf16>(X[2 * s + e / 4][e % 4]);
-                    } else {
-                        fx[s] = X[s];
-                    }
-                }
                 const uint32_t krow = K + (qrow - Qs) + 16 * jt * LK::BYTES;
-                // q's operands are read a group ahead of their products
+                // q's operands are read a group of steps ahead of their products
                 constexpr int GS = KS < 4 ? KS : 4, NG = KS / GS;
+                static_assert(NT == 2 || NG == 1, "p is one block's");
+                frag fx[GS], fl[BF ? GS : 1];  // X as operands, in two parts where they are rounded
                 frag fk[NT == 4 ? KS : 1], fq[2][GS];
                 if constexpr (NT == 4) {
 #pragma unroll
@@ -624,26 +633,48 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                 auto read = [&](int u) KDN_INLINE {
 #pragma unroll
                     for (int s = 0; s < GS; ++s)
-                        fq[u % 2][s] = rows<IO, KD>(qrow, 16 * (u / NG), u % NG * GS + s);
+                        fq[u % 2][s] = rows<IO, KD>(qrow, 16 * (u % NT), u / NT * GS + s);
                 };
                 read(0);
                 f32x4 p;
 #pragma unroll
                 for (int u = 0; u < NT * NG; ++u) {
-                    const int it = u / NG, s0 = u % NG * GS;
+                    const int it = u % NT, s0 = u / NT * GS;
                     // (C = 32: two waves form a block each)
                     const bool mixed = NT == 4 || it == wave >> 1;
                     if (u + 1 < NT * NG)
                         read(u + 1);
                     ahead(u, NT * NG);
                     if (s0 == 0)
-                        acc[it] = p = zero4();
-                    // (two sums at a time: a product waits for the one before of its own sum)
+                        acc[it] = zero4();
+                    if (NT == 4 || u == 0)
+                        p = zero4();
+                    if (it == 0) {
+#pragma unroll
+                        for (int s = 0; s < GS; ++s) {
+                            if constexpr (BF) {
+                                u32x4 high, low;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const f32x4& x = X[2 * (s0 + s) + i / 2];
+                                    high[i] = two_bf16(x[i % 2 * 2], x[i % 2 * 2 + 1]);
+                                    low[i] = rest_bf16(x[i % 2 * 2], x[i % 2 * 2 + 1], high[i]);
+                                }
+                                fx[s] = __builtin_bit_cast(frag, high);
+                                fl[s] = __builtin_bit_cast(frag, low);
+                            } else {
+                                fx[s] = X[s0 + s];
+                            }
+                        }
+                    }
+                    // (sums by turns: a product waits for the one before of its own sum)
 #pragma unroll
                     for (int s = 0; s < GS; ++s) {
-                        O::mma(acc[it], fx[s0 + s], fq[u % 2][s]);
+                        O::mma(acc[it], fx[s], fq[u % 2][s]);
                         if constexpr (NT == 4)
                             O::mma(p, fk[s0 + s], fq[u % 2][s]);
+                        if constexpr (BF)
+                            O::mma(acc[it], fl[s], fq[u % 2][s]);
                     }
                     if constexpr (NT != 4) {
                         if (mixed) {
@@ -652,22 +683,26 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                                 O::mma(p, rows<IO, KD>(krow, 0, s0 + s), fq[u % 2][s]);
                         }
                     }
-                    if (mixed && s0 + GS == KS) {
-                        typedef IO Four __attribute__((ext_vector_type(4)));
+                    // (the blocks that no step reads are not there)
+                    if (mixed && s0 + GS == KS && (NT != 4 || it >= 2 * js)) {
                         p *= pdecay[NT == 4 ? it : 0];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)  // a choice, not a product with zero: k may be infinite
                             p[e] = it > jt || (it == jt && c >= 4 * g + e) ? p[e] : 0.f;
-                        const Four out = __builtin_convertvector(p, Four);
-                        lds_write(LP::further(pput, 16 * it, 0), out);
+                        const uint32_t to = LP::further(pput, 16 * it, 0);
+                        if constexpr (BF) {
+                            typedef uint32_t two __attribute__((ext_vector_type(2)));
+                            const two high{two_bf16(p[0], p[1]), two_bf16(p[2], p[3])};
+                            lds_write(to, high);
+                            lds_write(LP::further(to, 0, 4), two{rest_bf16(p[0], p[1], high.x), rest_bf16(p[2], p[3], high.y)});
+                        } else {
+                            lds_write(to, p);
+                        }
                     }
                 }
-                float decayed = front;
 #pragma unroll
-                for (int it = 0; it < NT; ++it) {
-                    acc[it] *= decayed;
-                    decayed *= g16;
-                }
+                for (int it = 0; it < NT; ++it)
+                    acc[it] *= r.of_x * power(16 * it + c + 1 - rev);
             }
             if constexpr (!STATE) {
                 lds_barrier();  // Ps is whole, q is read
@@ -750,9 +785,11 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
 #pragma unroll
                 for (int s = 0; s < CS; ++s)
 #pragma unroll
-                    for (int it = 0; it < NT; ++it)
-                        if (s * O::K < 16 * (it + 1))
-                            O::mma(acc[it], fv[s], rows<IO, C>(prow, 16 * it, s));
+                    for (int part = 0; part < (BF ? 2 : 1); ++part)
+#pragma unroll
+                        for (int it = 0; it < NT; ++it)
+                            if (s * O::K < 16 * (it + 1))
+                                O::mma(acc[it], fv[s], rows<IO, W::PW>(prow + W::step_at(s), 16 * it - W::step_row(s), BF ? part : s));
                 if (bad) {
                     typedef IO Four __attribute__((ext_vector_type(4)));
                     int i = c, four = 16 * wave + 4 * g;  // of v's columns, this lane's
@@ -766,7 +803,11 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
                             x[e] = to_f32(vj[e]);
 #pragma unroll
                         for (int it = 0; it < NT; ++it) {
-                            const float pj = to_f32(lds_read<IO>(Ps + LP::at(16 * it + i, j / O::VE) + j % O::VE * W::E));
+                            const int s = BF ? j / 32 : 0, row = max(16 * it + i - W::step_row(s), 0), col = j - W::step_row(s);
+                            const uint32_t at = Ps + W::step_at(s) + LP::at(row, col / O::VE) + col % O::VE * W::E;
+                            float pj = to_f32(lds_read<IO>(at));
+                            if constexpr (BF)
+                                pj += to_f32(lds_read<IO>(LP::further(at, 0, 4)));
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 if (16 * it + i >= j && x[e] - x[e] != 0.f)
