@@ -1,5 +1,6 @@
-"""bf16 linear attention against its 64-bit definition: outputs by token are off by
-their own rounding and by terms of 16 bits, not of 8; what is infinite stays so."""
+"""Linear attention's roundings: outputs by token in bf16 are off by their own
+rounding and by terms of 16 bits, not of 8; what is infinite stays so; states are
+rounded once a chunk."""
 import numpy as np
 import pytest
 import torch
@@ -92,3 +93,18 @@ def test_infinities_of_states_and_products(T, dk):
     got, _ = forward(dict(d, k=(k,), v=(v,)), 1.0)
     assert (got[0, 9, 0] == (q[0, 9, 0, 2].float() * float("inf"))).all()
     assert torch.isfinite(got[0, :9]).all() and not torch.isfinite(got[0, 9:, 0]).any()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("T,dk", [(32, 64), (64, 128), (320, 64), (320, 256), (2560, 32)])
+def test_small_terms_reach_a_large_state(T, dk, io):
+    """A state of 2^24, where floats are 2 apart, and terms of 3/4 without decay: their sum over
+    a chunk is exact, and adding it rounds by 1 at most.  A chunk is 32 tokens at least; the
+    segments of 2560 tokens start from states of their own, whose sums are joined alike."""
+    one = lambda *s: dev(np.ones(s), io)
+    d = {"q": one(1, T, 2, dk), "k": one(1, T, 2, dk), "v": dev(np.full((1, T, 2, 32), 0.75), io),
+         "do": dev(np.full((1, T, 2, 32), 0.75), io), "g": dev(np.ones(2)),
+         "S0": dev(np.full((1, 2, dk, 32), 2.0 ** 24)), "dS": dev(np.full((1, 2, dk, 32), 2.0 ** 24))}
+    want = 2.0 ** 24 + 0.75 * T
+    for got in (forward(d, 1.0)[1], backward(d, 1.0)["dS0"]):
+        assert np.abs(host(got) - want).max() <= T / 32
