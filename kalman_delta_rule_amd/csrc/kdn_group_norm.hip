@@ -528,8 +528,9 @@ __device__ __forceinline__ void channel_sum(const Split& p, int lane, float (&a)
 // are added, so that nothing cancels wherever single values lie.  (Sums around one of the
 // values left rstd 1.3e-3 off where that one lay far from the others, 1030 x 100000 positions,
 // the first at 10000, and took as long: 64 x 4096 positions of 256 channels fp32 forward 171
-// us, 168 so; 2497 x 292 of 320 in groups of 20, bf16, 370 and 354.)  Values are taken from one of the tile's, the middle one
-// of three: what lies far from zero keeps its digits.  ws [N][tiles][C][2]
+// us, 168 so; 2497 x 292 of 320 in groups of 20, bf16, 370 and 354.)  Values are taken from
+// one of the tile's, the middle one of three: what lies far from zero keeps its digits.
+// ws [N][tiles][C][2]
 template <typename IO, bool WHOLE>
 __global__ __launch_bounds__(256) void group_norm_stats_kernel(GroupNormArgs a, Split p, float2* ws)
 {

@@ -52,18 +52,20 @@ __device__ __forceinline__ SequenceRange sequences_at(const int* cu, int N, int 
 constexpr int kStatesOfRun = 20;
 
 // to[n] = from[n] (zeros where that is not given), rows of `width`, for empty sequences n:
-// of cu, or all of them without.  16 sequences a wave and time, 256 columns a workgroup.
+// of cu, or all of them without.  16 sequences a wave and time, 256 columns a workgroup and
+// time (rows may be wider than a grid's second axis holds workgroups).
 template <typename E>
 __global__ __launch_bounds__(256) void empty_states_kernel(const int* cu, int N, int width, const E* from, E* to)
 {
-    const int lane = threadIdx.x & 63, c0 = blockIdx.y * 256, c1 = min(c0 + 256, width);
+    const int lane = threadIdx.x & 63;
     for (long long n0 = (blockIdx.x * 4ll + (threadIdx.x >> 6)) * 16; n0 < N; n0 += gridDim.x * 64ll) {
         const long long n = n0 + lane;
         const bool empty = lane < 16 && n < N && (!cu || cu[n] >= cu[n + 1]);
         for (unsigned long long left = __ballot(empty); left; left &= left - 1) {
             const size_t row = (size_t)(n0 + __builtin_ctzll(left)) * width;
-            for (int c = c0 + lane; c < c1; c += 64)
-                to[row + c] = from ? from[row + c] : E(0);
+            for (int c0 = blockIdx.y * 256; c0 < width; c0 += gridDim.y * 256)
+                for (int c = c0 + lane; c < min(c0 + 256, width); c += 64)
+                    to[row + c] = from ? from[row + c] : E(0);
         }
     }
 }
@@ -72,7 +74,8 @@ template <typename E>
 void launch_empty_states(const int* cu, int N, int width, const void* from, void* to, hipStream_t stream)
 {
     const long long groups = ((long long)N + 63) / 64;
-    const dim3 grid(groups < 4096 ? (unsigned)groups : 4096u, (width + 255) / 256);
+    const unsigned columns = ((unsigned)width + 255) / 256;
+    const dim3 grid(groups < 4096 ? (unsigned)groups : 4096u, columns < 4096 ? columns : 4096u);
     empty_states_kernel<E><<<grid, 256, 0, stream>>>(cu, N, width, static_cast<const E*>(from), static_cast<E*>(to));
 }
 
