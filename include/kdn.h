@@ -652,7 +652,7 @@ kdn_status kdn_linattn_step(int B, int H, int Hk, int dk, int dv, int io_dtype, 
  * S = 1 with a head's outputs as a group normalises each head of a token.
  *   x      rows of C, x_stride apart (N S of them), io dtype;  y [N,S,C] io dtype
  *   weight, bias [C] fp32, each nullable (ones, zeros)
- *   mean, rstd   [N,G] fp32, written; each nullable
+ *   mean, rstd   [N,G] fp32, written (zeros where S = 0); each nullable
  *   eps    finite, >= 0;  N G below 2^24
  *   workspace    kdn_group_norm_fwd_workspace_size bytes (0 unless a group is
  *          too large for one workgroup, or not whole vectors in a large call)

@@ -760,6 +760,18 @@ __global__ __launch_bounds__(256) void group_norm_means_kernel(GroupNormArgs a, 
         means[blockIdx.x] = float2{m.x * inv, m.y * inv};
 }
 
+// samples without positions: statistics of nothing
+__global__ __launch_bounds__(256) void group_norm_none_kernel(int units, float* mean, float* rstd)
+{
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= units)
+        return;
+    if (mean)
+        mean[i] = 0.f;
+    if (rstd)
+        rstd[i] = 0.f;
+}
+
 // ---- which kernels --------------------------------------------------------------------
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
@@ -969,8 +981,13 @@ size_t group_norm_bwd_workspace_bytes(int N, int S, int C, int G)
 
 hipError_t launch_group_norm_fwd(const GroupNormArgs& a, bool bf, hipStream_t stream)
 {
-    if (a.N == 0 || a.S == 0)
+    if (a.N == 0)
         return hipSuccess;
+    if (a.S == 0) {
+        if (a.mean || a.rstd)
+            group_norm_none_kernel<<<(unsigned)ceil_div((long long)a.N * a.G, 256), 256, 0, stream>>>(a.N * a.G, a.mean, a.rstd);
+        return hipGetLastError();
+    }
     return bf ? group_norm_fwd<bf16>(a, stream) : group_norm_fwd<float>(a, stream);
 }
 
