@@ -352,14 +352,16 @@ struct Counted {
     static __device__ __forceinline__ int at_most(const int* p, int n, int x) { return count_at_most<kThreads>(p, n, x); }
 };
 
-// What bounds a walk (B8 T4096, 16 heads of 128 in bf16, forward, 134 us): a chunk of 64
-// tokens takes a compute unit 2 us, of which the matrix units are busy a fifth.  With copies
-// and stores left out it is 1.2 us at two workgroups (1.9 at one), with the arithmetic left
-// out 1.9: the copies arrive at 3.9 TB/s, since a chunk's are asked for while the one before
-// is computed, and no earlier.  A third tile of q would let them go further ahead, and takes
-// the LDS of the second workgroup.  C = 32 leaves room for both: with three workgroups the
-// backward of 8 x 4096 tokens took 338 us instead of 350, the forward, which has one, more
-// than with 64.  Heads of 256, and fp32, have 32, as their tiles would not fit twice.
+// What bounds a walk (16 heads of 128 in bf16, forward, no state out).  With one workgroup a
+// compute unit (B8 T4096, 180 us) the chain of a chunk's instructions: a chunk of 64 tokens
+// takes 2.8 us, 2.4 with copies and stores left out, 1.9 with the arithmetic left out; the
+// matrix units are busy a fifth of it.  With two (B16 T2048, 143 us) the copies: 2.2 us, 1.6
+// and 2.0.  A chunk's copies are asked for while the one before is computed, and no earlier: a
+// further tile of q, k and v takes the LDS of the second workgroup where there are two, and
+// where there is one (it would fit: 118 KB) the copies are not what sets the time.  C = 32
+// leaves room for both: with three workgroups the backward of 8 x 4096 tokens took 338 us
+// instead of 350, the forward, which has one, more than with 64 (the operands that are not
+// inputs in one part).  Heads of 256, and fp32, have 32, as their tiles would not fit twice.
 template <typename IO, int KD, int C>
 struct Walk {
     typedef Op<IO> O;
@@ -909,8 +911,8 @@ __global__ __launch_bounds__(kThreads, sizeof(IO) * KD > 512 ? 1 : 2) void linat
 
 // The states handed on, one segment after another: what a segment adds, and what it got,
 // decayed over its tokens.  A thread has one element of one head's state; what the next
-// segments add is loaded ahead.  (65536 tokens of 16 heads, forward and backward: 14 + 9 us of
-// 1290.)
+// segments add is loaded ahead.  (65536 tokens of 16 heads, forward and backward: 13 + 11 us of
+// 1467.)
 __global__ __launch_bounds__(kThreads) void linattn_join_kernel(LinArgs a)
 {
     const LinRole& r = a.role[blockIdx.z];
@@ -1125,9 +1127,9 @@ void launch_states(const LinArgs& a, int roles, hipStream_t stream)
 // walks fill the chip, else as many as let two workgroups stay on a compute unit.  The
 // backward's walks, which meet each other's inputs in the caches, take half as many again
 // where segments stay long.  (us, heads of 128 in bf16.  From 256 walks on, 8 x 4096 tokens of
-// 16 heads: 134 forward in one segment, 197 in two.  65536 tokens of 16 heads: 397 forward by
-// 512 workgroups, 426 by 256, 436 by 1024; backward 941 by 512, 901 by 768, 945 by 1024.
-// 2 x 16384 tokens backward 537 by 512, 454 by 768; 2 x 2048 79 and 83.  512 tokens of 4 heads
+// 16 heads: 181 forward in one segment, 205 in two.  65536 tokens of 16 heads: 432 forward by
+// 512 workgroups, 493 by 256, 467 by 1024; backward 1043 by 512, 1038 by 768, 1064 by 1024.
+// 2 x 16384 tokens backward 586 by 512, 518 by 768; 2 x 2048 90 and 92.  512 tokens of 4 heads
 // in fp32: 29 forward in segments, 52 in one; of 256 tokens at least, 2 x 2047 tokens of 6
 // heads in fp32 take 74 instead of 62.)
 int segments(int B, int T, int H, int slices, bool backward, int& L)
